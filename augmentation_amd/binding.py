@@ -25,7 +25,7 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 FN_OK, FN_EINVAL, FN_EOVERFLOW, FN_EHIP = 0, -1, -2, -3
-FN_OUT_FP32, FN_OUT_FP16, FN_OUT_FP16_PAD4 = 0, 1, 2
+FN_OUT_FP32, FN_OUT_FP16, FN_OUT_FP16_PAD4, FN_OUT_BF16 = 0, 1, 2, 3
 
 # fn_sample_params: eight int32 fields, 32 bytes
 PARAMS_DTYPE = np.dtype(
@@ -42,6 +42,14 @@ _SIGS = {
                               _f32, _f32, _f32, _u64, _i64, _i32, _P, _P],
     "fn_params": [_u64, _i64, _i32, _i32, _f32, _f32, _f32, _f32, _f32, _f32, _P, _P],
     "fn_params_ex": [_u64, _i64, _i64, _i32, _i32, _f32, _f32, _f32, _f32, _f32, _f32, _P, _P],
+    "fn_rms_norm": [_P, _i64, _P, _i64, _P, _i64, _i32, _f32, _i32, _P, _i64, _P, _i64, _P, _P],
+    "fn_rms_norm_q8": [_P, _i64, _P, _i64, _P, _i64, _i32, _f32, _i32, _P, _i64, _P, _i64, _P, _P,
+                       _P],
+    "fn_quantize_rows": [_P, _i64, _i64, _i32, _i32, _P, _i64, _P, _P],
+    "fn_rms_norm_backward": [_P, _i64, _P, _i64, _P, _P, _P, _i64, _i64, _i32, _i32, _P, _i64, _P,
+                             _P, _i64, _P],
+    "fn_rms_norm_backward_workspace": [_i64, _i32, _P],
+    "fn_matmul_q8": [_P, _i64, _P, _P, _i64, _P, _P, _i64, _i64, _i32, _i32, _P, _i64, _P],
     "fn_test_erase_dims": [_P, _P, _i64, _i32, _i32, _f32, _f32, _f32, _f32, _P, _P, _P, _P],
     "fn_test_cr_ops": [_i32, _P, _P, _i64, _P, _P],
     "fn_test_stream": [_P, _P, _i64, _i32, _P],
@@ -60,6 +68,8 @@ def _declare(lib) -> None:
 _declare(_lib)
 
 EXPORTED = ("fn_fused_normalize", "fn_fused_normalize_ex", "fn_params", "fn_params_ex",
+            "fn_rms_norm", "fn_rms_norm_q8", "fn_quantize_rows", "fn_rms_norm_backward",
+            "fn_rms_norm_backward_workspace", "fn_matmul_q8",
             "fn_last_error", "fn_test_erase_dims", "fn_test_cr_ops", "fn_test_stream",
             "fn_test_timeline")
 
@@ -163,6 +173,51 @@ def fn_params(seed, N, H, W, flip_p, erase_p, scale_min, scale_max, ratio_min, r
                                  _stream(stream)))
 
 
+def fn_rms_norm(x, x_stride, residual, residual_stride, weight, rows, width, eps, dtype, sum_out,
+                sum_stride, out, out_stride, rstd, stream=None) -> int:
+    return _check(_lib.fn_rms_norm(_addr(x), x_stride, _addr(residual), residual_stride,
+                                   _addr(weight), rows, width, eps, dtype, _addr(sum_out),
+                                   sum_stride, _addr(out), out_stride, _addr(rstd),
+                                   _stream(stream)))
+
+
+def fn_rms_norm_q8(x, x_stride, residual, residual_stride, weight, rows, width, eps, dtype,
+                   sum_out, sum_stride, codes, codes_stride, scales, rstd, stream=None) -> int:
+    return _check(_lib.fn_rms_norm_q8(_addr(x), x_stride, _addr(residual), residual_stride,
+                                      _addr(weight), rows, width, eps, dtype, _addr(sum_out),
+                                      sum_stride, _addr(codes), codes_stride, _addr(scales),
+                                      _addr(rstd), _stream(stream)))
+
+
+def fn_quantize_rows(x, x_stride, rows, width, dtype, codes, codes_stride, scales,
+                     stream=None) -> int:
+    return _check(_lib.fn_quantize_rows(_addr(x), x_stride, rows, width, dtype, _addr(codes),
+                                        codes_stride, _addr(scales), _stream(stream)))
+
+
+def fn_rms_norm_backward(dout, dout_stride, h, h_stride, weight, rstd, dsum, dsum_stride, rows,
+                         width, dtype, dx, dx_stride, dweight, workspace, workspace_bytes,
+                         stream=None) -> int:
+    return _check(_lib.fn_rms_norm_backward(
+        _addr(dout), dout_stride, _addr(h), h_stride, _addr(weight), _addr(rstd), _addr(dsum),
+        dsum_stride, rows, width, dtype, _addr(dx), dx_stride, _addr(dweight), _addr(workspace),
+        workspace_bytes, _stream(stream)))
+
+
+def fn_rms_norm_backward_workspace(rows, width) -> int:
+    """The workspace's size in bytes."""
+    n = _i64()
+    _check(_lib.fn_rms_norm_backward_workspace(rows, width, ctypes.byref(n)))
+    return n.value
+
+
+def fn_matmul_q8(a, a_stride, a_scales, b, b_stride, b_scales, bias, M, N, K, out_dtype, out,
+                 out_stride, stream=None) -> int:
+    return _check(_lib.fn_matmul_q8(_addr(a), a_stride, _addr(a_scales), _addr(b), b_stride,
+                                    _addr(b_scales), _addr(bias), M, N, K, out_dtype, _addr(out),
+                                    out_stride, _stream(stream)))
+
+
 def fn_test_erase_dims(w_scale, w_ratio, count, H, W, scale_min, scale_max, ratio_min, ratio_max,
                        eh, ew, accepted, stream=None) -> int:
     return _check(_lib.fn_test_erase_dims(_addr(w_scale), _addr(w_ratio), count, H, W, scale_min,
@@ -216,3 +271,173 @@ def sample_params(N, H, W, flip_p=0.5, erase_p=0.0, scale=(0.02, 0.33), ratio=(0
 def params_to_numpy(t: torch.Tensor) -> np.ndarray:
     """(N, 8) int32 tensor -> structured array with PARAMS_DTYPE fields."""
     return np.ascontiguousarray(t.cpu().numpy()).view(PARAMS_DTYPE).reshape(-1)
+
+
+# ------------------------------------- tensor helpers: the 8-bit linear layer
+
+_TYPE_CODES = {torch.float32: FN_OUT_FP32, torch.float16: FN_OUT_FP16, torch.bfloat16: FN_OUT_BF16}
+
+
+def _type_code(t: torch.Tensor) -> int:
+    code = _TYPE_CODES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"dtype {t.dtype}: float32, float16 or bfloat16 is needed")
+    return code
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """The row stride of a (..., D) tensor whose leading dimensions step by
+    one common stride (any contiguous tensor, a slice of its last dimension,
+    one row expanded to many) and whose last dimension is contiguous."""
+    if t.is_contiguous():
+        return t.size(-1)
+    shape, st = t.shape, t.stride()
+    stride = None
+    if shape[-1] <= 1 or st[-1] == 1:
+        for d in range(t.dim() - 2, -1, -1):
+            if shape[d] == 1:
+                continue
+            if stride is None:
+                stride, span = st[d], st[d] * shape[d]
+            elif st[d] == span:
+                span *= shape[d]
+            else:
+                break
+        else:
+            return shape[-1] if stride is None else stride
+    raise ValueError(f"{name}: the last dimension must be contiguous and the others one row stride "
+                     "(use .contiguous())")
+
+
+def _like(t, shape, dtype, ref: torch.Tensor, name: str) -> torch.Tensor:
+    """`t` if it has this shape, dtype and device; a new tensor if it is None."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=ref.device)
+    if t.dtype != dtype or t.shape != torch.Size(shape) or t.device != ref.device:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {ref.device}")
+    return t
+
+
+def _flat(t, shape, dtype, ref: torch.Tensor, name: str) -> torch.Tensor:
+    t = _like(t, shape, dtype, ref, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _rows_of(x: torch.Tensor) -> tuple[int, int]:
+    if x.dim() < 1 or not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor of at least one dimension")
+    width = x.size(-1)
+    return (x.numel() // width if width else 0), width
+
+
+def _norm_inputs(x, weight, residual, sum_out):
+    rows, width = _rows_of(x)
+    weight = _flat(weight, (width,), x.dtype, x, "weight")
+    if residual is None:
+        if sum_out is not None:
+            raise ValueError("sum_out without a residual")
+        return rows, width, weight, 0, None, 0
+    residual = _like(residual, x.shape, x.dtype, x, "residual")
+    sum_out = _like(sum_out, x.shape, x.dtype, x, "sum_out")
+    return (rows, width, weight, _row_stride(residual, "residual"), sum_out,
+            _row_stride(sum_out, "sum_out"))
+
+
+def rms_norm(x, weight, eps=1e-6, residual=None, out=None, sum_out=None, rstd=None, stream=None):
+    """fn_rms_norm on (..., D) CUDA tensors of one dtype.  Returns (out, rstd,
+    h): the norm of h = x + residual, each row's 1/rms (fp32), and h itself
+    (x when there is no residual).  out and sum_out may be x or residual."""
+    rows, width, weight, r_stride, sum_out, s_stride = _norm_inputs(x, weight, residual, sum_out)
+    out = _like(out, x.shape, x.dtype, x, "out")
+    rstd = _flat(rstd, x.shape[:-1], torch.float32, x, "rstd")
+    fn_rms_norm(x, _row_stride(x, "x"), residual, r_stride, weight, rows, width, eps,
+                _type_code(x), sum_out, s_stride, out, _row_stride(out, "out"), rstd, stream)
+    return out, rstd, x if sum_out is None else sum_out
+
+
+def rms_norm_q8(x, weight, eps=1e-6, residual=None, codes=None, scales=None, sum_out=None,
+                rstd=None, stream=None):
+    """fn_rms_norm_q8 on (..., D) CUDA tensors of one dtype.  Returns (codes,
+    scales, h): int8 codes of the shape of x, an fp32 scale per row, and h = x
+    + residual (x when there is no residual).  sum_out may be x or residual;
+    rstd, if given, receives each row's 1/rms."""
+    rows, width, weight, r_stride, sum_out, s_stride = _norm_inputs(x, weight, residual, sum_out)
+    codes = _like(codes, x.shape, torch.int8, x, "codes")
+    scales = _flat(scales, x.shape[:-1], torch.float32, x, "scales")
+    if rstd is not None:
+        rstd = _flat(rstd, x.shape[:-1], torch.float32, x, "rstd")
+    fn_rms_norm_q8(x, _row_stride(x, "x"), residual, r_stride, weight, rows, width, eps,
+                   _type_code(x), sum_out, s_stride, codes, _row_stride(codes, "codes"), scales,
+                   rstd, stream)
+    return codes, scales, x if sum_out is None else sum_out
+
+
+def quantize_rows(x, codes=None, scales=None, stream=None):
+    """fn_quantize_rows on a (..., D) CUDA tensor: (int8 codes of its shape,
+    an fp32 scale per row)."""
+    rows, width = _rows_of(x)
+    codes = _like(codes, x.shape, torch.int8, x, "codes")
+    scales = _flat(scales, x.shape[:-1], torch.float32, x, "scales")
+    fn_quantize_rows(x, _row_stride(x, "x"), rows, width, _type_code(x), codes,
+                     _row_stride(codes, "codes"), scales, stream)
+    return codes, scales
+
+
+def rms_norm_backward_workspace(rows, width, device="cuda") -> torch.Tensor:
+    """A workspace for rms_norm_backward on rows of this size."""
+    return torch.empty(fn_rms_norm_backward_workspace(rows, width) // 4, dtype=torch.float32,
+                       device=device)
+
+
+def rms_norm_backward(dout, h, weight, rstd, dsum=None, dx=None, dweight=None, workspace=None,
+                      stream=None):
+    """fn_rms_norm_backward on (..., D) CUDA tensors of one dtype; rstd and h
+    as rms_norm returned them.  Returns (dx, dweight): the gradient of x (and
+    of the residual) and the fp32 gradient of the weight.  dx may be dout, h
+    or dsum.  Without a workspace one is allocated for the call; with
+    `stream` other than the current one, pass a workspace that lives until
+    the stream has finished."""
+    rows, width = _rows_of(h)
+    weight = _flat(weight, (width,), h.dtype, h, "weight")
+    dout = _like(dout, h.shape, h.dtype, h, "dout")
+    rstd = _flat(rstd, h.shape[:-1], torch.float32, h, "rstd")
+    d_stride = 0
+    if dsum is not None:
+        dsum = _like(dsum, h.shape, h.dtype, h, "dsum")
+        d_stride = _row_stride(dsum, "dsum")
+    dx = _like(dx, h.shape, h.dtype, h, "dx")
+    dweight = _flat(dweight, (width,), torch.float32, h, "dweight")
+    if workspace is None:
+        workspace = rms_norm_backward_workspace(rows, width, h.device)
+    fn_rms_norm_backward(dout, _row_stride(dout, "dout"), h, _row_stride(h, "h"), weight, rstd,
+                         dsum, d_stride, rows, width, _type_code(h), dx, _row_stride(dx, "dx"),
+                         dweight, workspace, workspace.numel() * workspace.element_size(), stream)
+    return dx, dweight
+
+
+def matmul_q8(a, a_scales, b, b_scales, bias=None, out_dtype=FN_OUT_BF16, out=None, stream=None):
+    """fn_matmul_q8: the (..., N) product of int8 codes a (..., K) with a scale
+    per row and b (N, K) with a scale per row, plus an fp32 bias (N,).  Given
+    `out`, its dtype counts and not out_dtype."""
+    if a.dtype != torch.int8 or b.dtype != torch.int8 or a.dim() < 1 or b.dim() != 2 \
+            or not a.is_cuda or b.device != a.device or a.size(-1) != b.size(1):
+        raise ValueError("a must be an int8 (..., K) CUDA tensor and b an int8 (N, K) one beside it")
+    N, K = b.shape
+    lead = a.shape[:-1]
+    M = lead.numel()
+    if out is None:
+        tdt = {code: t for t, code in _TYPE_CODES.items()}.get(out_dtype)
+        if tdt is None:
+            raise ValueError(f"unknown out_dtype {out_dtype}")
+    else:
+        tdt = out.dtype
+    out = _like(out, (*lead, N), tdt, a, "out")
+    a_scales = _flat(a_scales, lead, torch.float32, a, "a_scales")
+    b_scales = _flat(b_scales, (N,), torch.float32, a, "b_scales")
+    if bias is not None:
+        bias = _flat(bias, (N,), torch.float32, a, "bias")
+    fn_matmul_q8(a, _row_stride(a, "a") if K else 0, a_scales, b, _row_stride(b, "b") if K else 0,
+                 b_scales, bias, M, N, K, _type_code(out), out, _row_stride(out, "out"), stream)
+    return out

@@ -14,14 +14,17 @@ from __future__ import annotations
 
 import os
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
-SOURCES = [os.path.join(HERE, "csrc", "fn_api.hip")]
-HEADERS = [os.path.join(HERE, "csrc", h) for h in ("fn_device.hpp", "fn_kernels.hpp",
-                                                   "exp2_table.inc")] + [
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("fn_api.hip", "q8_api.hip")]
+HEADERS = [os.path.join(HERE, "csrc", h) for h in ("fn_host.hpp", "fn_device.hpp",
+                                                   "fn_kernels.hpp", "row_kernels.hpp",
+                                                   "product_kernels.hpp", "exp2_table.inc")] + [
     os.path.join(ROOT, "include", "fn.h")]
 LIB_PATH = os.path.join(HERE, "libfn.so")
 # the instrumented build: the tiles kernel records per-tile clock stamps
@@ -29,7 +32,7 @@ LIB_PATH = os.path.join(HERE, "libfn.so")
 TIMELINE_LIB_PATH = os.path.join(HERE, "libfn_timeline.so")
 
 FLAGS = [
-    f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+    f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden",
     "-ffp-contract=off", "-fhip-fp32-correctly-rounded-divide-sqrt", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", f"-I{os.path.join(ROOT, 'include')}",
 ]
@@ -56,12 +59,8 @@ def build_cpu(verbose: bool = False) -> str:
     return CPU_LIB_PATH
 
 
-def build(verbose: bool = False, timeline: bool = False) -> str:
-    """Compile the library (always recompiles) and return its path;
-    timeline: the instrumented build libfn_timeline.so instead."""
-    path = TIMELINE_LIB_PATH if timeline else LIB_PATH
-    tmp = path + ".tmp"
-    cmd = [HIPCC, *FLAGS, *(["-DFN_TIMELINE=1"] if timeline else []), *SOURCES, "-o", tmp]
+def _hipcc(args: list[str], verbose: bool) -> None:
+    cmd = [HIPCC, *FLAGS, *args]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -71,6 +70,22 @@ def build(verbose: bool = False, timeline: bool = False) -> str:
         raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
     if verbose and msgs:
         print("\n".join(msgs))
+
+
+def build(verbose: bool = False, timeline: bool = False) -> str:
+    """Compile the library (always recompiles; the sources side by side) and
+    return its path; timeline: the instrumented build libfn_timeline.so
+    instead."""
+    path = TIMELINE_LIB_PATH if timeline else LIB_PATH
+    tmp = path + ".tmp"
+    defines = ["-DFN_TIMELINE=1"] if timeline else []
+    with tempfile.TemporaryDirectory() as objects, ThreadPoolExecutor(len(SOURCES)) as pool:
+        objs = [os.path.join(objects, os.path.basename(s) + ".o") for s in SOURCES]
+        jobs = [pool.submit(_hipcc, [*defines, "-c", s, "-o", o], verbose)
+                for s, o in zip(SOURCES, objs)]
+        for job in jobs:
+            job.result()
+        _hipcc(["-shared", *objs, "-o", tmp], verbose)
     os.replace(tmp, path)
     return path
 

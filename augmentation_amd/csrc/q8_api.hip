@@ -1,0 +1,418 @@
+// q8_api.hip -- the C ABI of the 8-bit linear layer's operators: argument
+// checks, the choice of kernel and the launches.  Declarations, argument
+// meaning, layouts and error behaviour are documented in include/fn.h.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "fn.h"
+#include "fn_host.hpp"
+#include "product_kernels.hpp"
+#include "row_kernels.hpp"
+
+namespace {
+
+using namespace fnhost;
+
+#define FN_TRY(call)        \
+  do {                      \
+    const int rc_ = (call); \
+    if (rc_) return rc_;    \
+  } while (0)
+
+constexpr int32_t kMaxWidth = 1 << 30;
+constexpr int32_t kMaxInRegisters = 32768;  // widest row that a work-group keeps in registers
+
+int type_bytes(int32_t dtype) {
+  return dtype == FN_OUT_FP32 ? 4 : dtype == FN_OUT_FP16 || dtype == FN_OUT_BF16 ? 2 : 0;
+}
+
+int check_type(int32_t dtype, const char* name) {
+  if (type_bytes(dtype) == 0) return fail(FN_EINVAL, "unknown %s %d", name, dtype);
+  return FN_OK;
+}
+
+// A buffer of a call: `rows` rows of `cols` elements, `stride` elements apart.
+struct Buffer {
+  const char* name;
+  const void* p;
+  int64_t rows, cols, stride;
+  int64_t element;       // bytes
+  bool output;
+  unsigned replaces = 0;  // outputs: bit i = may lie exactly on buffer i of the call
+
+  int64_t row_bytes() const { return cols * element; }
+  int64_t stride_bytes() const { return stride * element; }
+  int64_t span() const { return (rows - 1) * stride_bytes() + row_bytes(); }
+  bool empty() const { return rows == 0 || cols == 0; }
+};
+
+// Strides and spans that fit the index arithmetic; an output's rows may not
+// overlap each other, an input's may (stride 0: one row for all).
+int check_layout(const Buffer& b) {
+  if (b.stride < 0) return fail(FN_EINVAL, "%s: its row stride is negative", b.name);
+  if (b.output && b.rows > 1 && b.stride < b.cols)
+    return fail(FN_EINVAL, "%s: its row stride is shorter than a row", b.name);
+  const __int128 span = ((__int128)std::max<int64_t>(b.rows - 1, 0) * b.stride + b.cols) * b.element;
+  if (span > (__int128)1 << 62)
+    return fail(FN_EOVERFLOW, "%s: its rows span more than 2^62 bytes", b.name);
+  return FN_OK;
+}
+
+// True if some byte belongs to both.  Buffers of the same stride may lie side
+// by side as column ranges of one allocation.
+bool overlap(const Buffer& x, const Buffer& y) {
+  const uintptr_t a0 = (uintptr_t)x.p, a1 = a0 + (uintptr_t)x.span();
+  const uintptr_t b0 = (uintptr_t)y.p, b1 = b0 + (uintptr_t)y.span();
+  if (a1 <= b0 || b1 <= a0) return false;
+  const int64_t s = x.stride_bytes();
+  if (s != y.stride_bytes() || s < x.row_bytes() || s < y.row_bytes()) return true;
+  // where y's columns begin, counted from x's modulo the common stride
+  int64_t d = (int64_t)((b0 >= a0 ? b0 - a0 : a0 - b0) % (uintptr_t)s);
+  if (b0 < a0 && d != 0) d = s - d;
+  return !(d >= x.row_bytes() && d + y.row_bytes() <= s);
+}
+
+bool same_place(const Buffer& x, const Buffer& y) {
+  return x.p == y.p && x.rows == y.rows && x.row_bytes() == y.row_bytes() &&
+         (x.stride_bytes() == y.stride_bytes() || x.rows == 1);
+}
+
+// All buffers of a call; optional ones that are absent have rows = 0.
+template <int kCount>
+int check_buffers(const Buffer (&b)[kCount], int* dev) {
+  for (int i = 0; i < kCount; ++i) FN_TRY(check_layout(b[i]));
+  for (int i = 0; i < kCount; ++i) {
+    if (b[i].empty()) continue;
+    if (b[i].p != nullptr && (uintptr_t)b[i].p % (uintptr_t)b[i].element != 0)
+      return fail(FN_EINVAL, "%s must be aligned to its element size (%lld bytes)", b[i].name,
+                  (long long)b[i].element);
+    FN_TRY(check_device_range(b[i].p, (size_t)b[i].span(), b[i].name, dev));
+  }
+  for (int i = 0; i < kCount; ++i) {
+    if (!b[i].output || b[i].empty()) continue;
+    for (int j = 0; j < kCount; ++j) {
+      if (j == i || b[j].empty() || (b[j].output && j > i)) continue;
+      if ((b[i].replaces >> j & 1u) && same_place(b[i], b[j])) continue;
+      if (overlap(b[i], b[j])) return fail(FN_EINVAL, "%s and %s overlap", b[i].name, b[j].name);
+    }
+  }
+  return FN_OK;
+}
+
+int check_size(int64_t rows, int32_t width) {
+  if (rows < 0) return fail(FN_EINVAL, "rows must be >= 0");
+  if (rows > (int64_t)1 << 40) return fail(FN_EOVERFLOW, "rows exceeds 2^40");
+  if (width < 1) return fail(FN_EINVAL, "width must be >= 1 (got %d)", width);
+  if (width > kMaxWidth) return fail(FN_EOVERFLOW, "width %d exceeds 2^30", width);
+  return FN_OK;
+}
+
+// ------------------------------------------------------------- row kernels
+
+template <typename T, int kMode, int kThreads, int kChunks>
+void launch_rows_k(const fn::RowArgs& a, hipStream_t st) {
+  constexpr int kBlock = kThreads < 256 ? 256 : kThreads;
+  const int64_t groups = (a.rows + kBlock / kThreads - 1) / (kBlock / kThreads);
+  fn::rows_kernel<T, kMode, kThreads, kChunks>
+      <<<(unsigned)std::min<int64_t>(groups, 1 << 20), kBlock, 0, st>>>(a);
+}
+
+template <typename T, int kMode>
+void launch_rows(const fn::RowArgs& a, hipStream_t st) {
+  const int32_t w = a.width;
+  if (w <= 512)
+    launch_rows_k<T, kMode, 64, 1>(a, st);
+  else if (w <= 1024)
+    launch_rows_k<T, kMode, 64, 2>(a, st);
+  else if (w <= 2048)
+    launch_rows_k<T, kMode, 256, 1>(a, st);
+  else if (w <= 4096)
+    launch_rows_k<T, kMode, 256, 2>(a, st);
+  else if (w <= 8192)
+    launch_rows_k<T, kMode, 256, 4>(a, st);
+  else if (w <= 16384)
+    launch_rows_k<T, kMode, 1024, 2>(a, st);
+  else if (w <= kMaxInRegisters)
+    launch_rows_k<T, kMode, 1024, 4>(a, st);
+  else
+    fn::rows_wide_kernel<T, kMode>
+        <<<(unsigned)std::min<int64_t>(a.rows, 1 << 20), 1024, 0, st>>>(a);
+}
+
+template <int kMode>
+int launch_rows_type(const fn::RowArgs& a, int32_t dtype, void* stream) {
+  hipStream_t st = (hipStream_t)stream;
+  if (dtype == FN_OUT_FP32)
+    launch_rows<float, kMode>(a, st);
+  else if (dtype == FN_OUT_FP16)
+    launch_rows<_Float16, kMode>(a, st);
+  else
+    launch_rows<fn::BF16, kMode>(a, st);
+  return launch_status("rows_kernel launch");
+}
+
+// Both norms: out_dev (the input's type) or codes_dev and scales_dev.
+template <int kMode>
+int norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+         const void* weight, int64_t rows, int32_t width, float eps, int32_t dtype, void* sum,
+         int64_t sum_stride, void* out, int64_t out_stride, float* scales, float* rstd,
+         void* stream) {
+  constexpr bool kQ8 = kMode == fn::kRowNormQ8;
+  FN_TRY(check_size(rows, width));
+  FN_TRY(check_type(dtype, "dtype"));
+  if (!(eps > 0.0f && eps <= 3.4028234e38f))
+    return fail(FN_EINVAL, "eps must be positive and finite");
+  if ((residual == nullptr) != (sum == nullptr))
+    return fail(FN_EINVAL, "residual_dev and sum_dev come together or not at all");
+  const int64_t e = type_bytes(dtype), with_sum = residual != nullptr ? rows : 0;
+  // an output of the input's type may replace x or the residual: a thread
+  // has read its elements of a row before it writes them
+  const Buffer buffers[] = {
+      {"x_dev", x, rows, width, x_stride, e, false},
+      {"residual_dev", residual, with_sum, width, residual_stride, e, false},
+      {"weight_dev", weight, rows ? 1 : 0, width, 0, e, false},
+      {"sum_dev", sum, with_sum, width, sum_stride, e, true, 3u},
+      {kQ8 ? "codes_dev" : "out_dev", out, rows, width, out_stride, kQ8 ? 1 : e, true,
+       kQ8 ? 0u : 3u},
+      {"scales_dev", scales, kQ8 && rows ? 1 : 0, rows, 0, 4, true},
+      {"rstd_dev", rstd, rstd != nullptr && rows ? 1 : 0, rows, 0, 4, true},
+  };
+  int dev = -1;
+  FN_TRY(check_buffers(buffers, &dev));
+  if (rows == 0) return ok();
+  fn::RowArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.sum = sum;
+  a.out = kQ8 ? nullptr : out;
+  a.codes = kQ8 ? (int8_t*)out : nullptr;
+  a.scales = scales;
+  a.rstd = rstd;
+  a.rows = rows;
+  a.x_stride = x_stride;
+  a.residual_stride = residual_stride;
+  a.sum_stride = sum_stride;
+  a.out_stride = a.codes_stride = out_stride;
+  a.width = width;
+  a.eps = eps;
+  return launch_rows_type<kMode>(a, dtype, stream);
+}
+
+// Work-groups of the backward kernels, each with one row of partial sums:
+// about sixteen wavefronts per compute unit of a 256-unit device.  A function
+// of the sizes alone, so that results do not depend on the device.
+struct BackwardPlan {
+  int threads, chunks;  // of rows_backward_kernel; 0: the two-step kernels
+  int32_t partials;
+  int64_t rows_per_slice;
+  int64_t bytes;
+};
+
+BackwardPlan plan_backward(int64_t rows, int32_t width) {
+  BackwardPlan p{};
+  const int32_t limits[][3] = {{512, 64, 1},   {1024, 64, 2},   {2048, 256, 1},  {4096, 256, 2},
+                               {8192, 256, 4}, {16384, 1024, 2}, {32768, 1024, 4}};
+  for (const auto& l : limits) {
+    if (width <= l[0]) {
+      p.threads = l[1];
+      p.chunks = l[2];
+      const int block = std::max(256, p.threads);
+      const int64_t groups = (rows + block / p.threads - 1) / (block / p.threads);
+      p.partials = (int32_t)std::min<int64_t>(groups, 4096 / (block / 64));
+      p.bytes = (int64_t)p.partials * width * 4;
+      return p;
+    }
+  }
+  const int64_t slices = std::min<int64_t>(rows, 64);
+  p.rows_per_slice = slices ? (rows + slices - 1) / slices : 0;
+  p.partials = slices ? (int32_t)((rows + p.rows_per_slice - 1) / p.rows_per_slice) : 0;
+  p.bytes = (int64_t)p.partials * width * 4 + rows * 4;
+  return p;
+}
+
+template <typename T>
+void launch_backward(const fn::BackwardArgs& a, const BackwardPlan& p, hipStream_t st) {
+  const unsigned grid = (unsigned)p.partials;
+  switch (p.threads * 8 + p.chunks) {
+    case 64 * 8 + 1: fn::rows_backward_kernel<T, 64, 1><<<grid, 256, 0, st>>>(a); break;
+    case 64 * 8 + 2: fn::rows_backward_kernel<T, 64, 2><<<grid, 256, 0, st>>>(a); break;
+    case 256 * 8 + 1: fn::rows_backward_kernel<T, 256, 1><<<grid, 256, 0, st>>>(a); break;
+    case 256 * 8 + 2: fn::rows_backward_kernel<T, 256, 2><<<grid, 256, 0, st>>>(a); break;
+    case 256 * 8 + 4: fn::rows_backward_kernel<T, 256, 4><<<grid, 256, 0, st>>>(a); break;
+    case 1024 * 8 + 2: fn::rows_backward_kernel<T, 1024, 2><<<grid, 1024, 0, st>>>(a); break;
+    case 1024 * 8 + 4: fn::rows_backward_kernel<T, 1024, 4><<<grid, 1024, 0, st>>>(a); break;
+    default: {
+      fn::rows_backward_mean_kernel<T>
+          <<<(unsigned)std::min<int64_t>(a.rows, 1 << 20), 1024, 0, st>>>(a);
+      const unsigned columns = blocks_for(((int64_t)a.width + 7) / 8, 256);
+      fn::rows_backward_columns_kernel<T><<<dim3(columns, grid), 256, 0, st>>>(a);
+    }
+  }
+}
+
+template <typename T>
+void launch_product(const fn::ProductArgs& p, hipStream_t st) {
+  const int64_t tiles = ((p.M + 127) / 128) * (int64_t)p.tiles_n;
+  fn::product_any_kernel<T><<<(unsigned)tiles, 256, 0, st>>>(p);
+}
+
+}  // namespace
+
+FN_EXPORT int fn_rms_norm(const void* x_dev, int64_t x_stride, const void* residual_dev,
+                          int64_t residual_stride, const void* weight_dev, int64_t rows,
+                          int32_t width, float eps, int32_t dtype, void* sum_dev,
+                          int64_t sum_stride, void* out_dev, int64_t out_stride, float* rstd_dev,
+                          void* stream) {
+  return norm<fn::kRowNorm>(x_dev, x_stride, residual_dev, residual_stride, weight_dev, rows, width,
+                            eps, dtype, sum_dev, sum_stride, out_dev, out_stride, nullptr, rstd_dev,
+                            stream);
+}
+
+FN_EXPORT int fn_rms_norm_q8(const void* x_dev, int64_t x_stride, const void* residual_dev,
+                             int64_t residual_stride, const void* weight_dev, int64_t rows,
+                             int32_t width, float eps, int32_t dtype, void* sum_dev,
+                             int64_t sum_stride, int8_t* codes_dev, int64_t codes_stride,
+                             float* scales_dev, float* rstd_dev, void* stream) {
+  return norm<fn::kRowNormQ8>(x_dev, x_stride, residual_dev, residual_stride, weight_dev, rows,
+                              width, eps, dtype, sum_dev, sum_stride, codes_dev, codes_stride,
+                              scales_dev, rstd_dev, stream);
+}
+
+FN_EXPORT int fn_quantize_rows(const void* x_dev, int64_t x_stride, int64_t rows, int32_t width,
+                               int32_t dtype, int8_t* codes_dev, int64_t codes_stride,
+                               float* scales_dev, void* stream) {
+  FN_TRY(check_size(rows, width));
+  FN_TRY(check_type(dtype, "dtype"));
+  const int64_t e = type_bytes(dtype);
+  const Buffer buffers[] = {
+      {"x_dev", x_dev, rows, width, x_stride, e, false},
+      {"codes_dev", codes_dev, rows, width, codes_stride, 1, true},
+      {"scales_dev", scales_dev, rows ? 1 : 0, rows, 0, 4, true},
+  };
+  int dev = -1;
+  FN_TRY(check_buffers(buffers, &dev));
+  if (rows == 0) return ok();
+  fn::RowArgs a{};
+  a.x = x_dev;
+  a.codes = codes_dev;
+  a.scales = scales_dev;
+  a.rows = rows;
+  a.x_stride = x_stride;
+  a.codes_stride = codes_stride;
+  a.width = width;
+  return launch_rows_type<fn::kRowQuantize>(a, dtype, stream);
+}
+
+FN_EXPORT int fn_rms_norm_backward_workspace(int64_t rows, int32_t width, int64_t* bytes) {
+  FN_TRY(check_size(rows, width));
+  if (bytes == nullptr) return fail(FN_EINVAL, "bytes is NULL");
+  *bytes = plan_backward(rows, width).bytes;
+  return ok();
+}
+
+FN_EXPORT int fn_rms_norm_backward(const void* dout_dev, int64_t dout_stride, const void* h_dev,
+                                   int64_t h_stride, const void* weight_dev, const float* rstd_dev,
+                                   const void* dsum_dev, int64_t dsum_stride, int64_t rows,
+                                   int32_t width, int32_t dtype, void* dx_dev, int64_t dx_stride,
+                                   float* dweight_dev, void* workspace_dev,
+                                   int64_t workspace_bytes, void* stream) {
+  FN_TRY(check_size(rows, width));
+  FN_TRY(check_type(dtype, "dtype"));
+  const BackwardPlan plan = plan_backward(rows, width);
+  if (workspace_bytes < plan.bytes)
+    return fail(FN_EINVAL, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes,
+                (long long)plan.bytes);
+  const int64_t e = type_bytes(dtype);
+  const Buffer buffers[] = {
+      {"dout_dev", dout_dev, rows, width, dout_stride, e, false},
+      {"h_dev", h_dev, rows, width, h_stride, e, false},
+      {"dsum_dev", dsum_dev, dsum_dev != nullptr ? rows : 0, width, dsum_stride, e, false},
+      {"weight_dev", weight_dev, rows ? 1 : 0, width, 0, e, false},
+      {"rstd_dev", rstd_dev, rows ? 1 : 0, rows, 0, 4, false},
+      {"dx_dev", dx_dev, rows, width, dx_stride, e, true, 7u},
+      {"dweight_dev", dweight_dev, 1, width, 0, 4, true},
+      {"workspace_dev", workspace_dev, plan.bytes ? 1 : 0, plan.bytes / 4, 0, 4, true},
+  };
+  int dev = -1;
+  FN_TRY(check_buffers(buffers, &dev));
+  fn::BackwardArgs a{};
+  a.dout = dout_dev;
+  a.h = h_dev;
+  a.weight = weight_dev;
+  a.rstd = rstd_dev;
+  a.dsum = dsum_dev;
+  a.dx = dx_dev;
+  a.partial = (float*)workspace_dev;
+  a.row_mean = (float*)workspace_dev + (int64_t)plan.partials * width;
+  a.rows = rows;
+  a.dout_stride = dout_stride;
+  a.h_stride = h_stride;
+  a.dsum_stride = dsum_stride;
+  a.dx_stride = dx_stride;
+  a.rows_per_slice = plan.rows_per_slice;
+  a.width = width;
+  a.partials = plan.partials;
+  hipStream_t st = (hipStream_t)stream;
+  if (rows > 0) {
+    if (dtype == FN_OUT_FP32)
+      launch_backward<float>(a, plan, st);
+    else if (dtype == FN_OUT_FP16)
+      launch_backward<_Float16>(a, plan, st);
+    else
+      launch_backward<fn::BF16>(a, plan, st);
+    FN_TRY(launch_status("rows_backward_kernel launch"));
+  }
+  // no rows: no partial sums, and a gradient of zero
+  fn::column_sum_kernel<<<blocks_for(width, 16), 1024, 0, st>>>(a.partial, a.partials, width,
+                                                                dweight_dev);
+  return launch_status("column_sum_kernel launch");
+}
+
+FN_EXPORT int fn_matmul_q8(const int8_t* a_dev, int64_t a_stride, const float* a_scales_dev,
+                           const int8_t* b_dev, int64_t b_stride, const float* b_scales_dev,
+                           const float* bias_dev, int64_t M, int64_t N, int32_t K,
+                           int32_t out_dtype, void* out_dev, int64_t out_stride, void* stream) {
+  if (M < 0 || N < 0 || K < 0) return fail(FN_EINVAL, "M, N and K must be >= 0");
+  if (K > 131071) return fail(FN_EOVERFLOW, "K = %d: sums fit 32 bits up to 131071", K);
+  if (M > (int64_t)1 << 40 || N > (int64_t)1 << 40) return fail(FN_EOVERFLOW, "M or N exceeds 2^40");
+  FN_TRY(check_type(out_dtype, "out_dtype"));
+  const bool none = M == 0 || N == 0;
+  const Buffer buffers[] = {
+      {"a_dev", a_dev, none ? 0 : M, K, a_stride, 1, false},
+      {"b_dev", b_dev, none ? 0 : N, K, b_stride, 1, false},
+      {"a_scales_dev", a_scales_dev, none ? 0 : 1, M, 0, 4, false},
+      {"b_scales_dev", b_scales_dev, none ? 0 : 1, N, 0, 4, false},
+      {"bias_dev", bias_dev, none || bias_dev == nullptr ? 0 : 1, N, 0, 4, false},
+      {"out_dev", out_dev, none ? 0 : M, N, out_stride, type_bytes(out_dtype), true},
+  };
+  int dev = -1;
+  FN_TRY(check_buffers(buffers, &dev));
+  const int64_t tiles_n = (N + 127) / 128;
+  if (((M + 127) / 128) * (__int128)tiles_n > 0x7FFFFFFF)
+    return fail(FN_EOVERFLOW, "grid size limit exceeded");
+  if (none) return ok();
+  fn::ProductArgs p{};
+  p.a = a_dev;
+  p.b = b_dev;
+  p.sa = a_scales_dev;
+  p.sb = b_scales_dev;
+  p.bias = bias_dev;
+  p.out = out_dev;
+  p.a_stride = a_stride;
+  p.b_stride = b_stride;
+  p.out_stride = out_stride;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.tiles_n = (uint32_t)tiles_n;
+  hipStream_t st = (hipStream_t)stream;
+  if (out_dtype == FN_OUT_FP32)
+    launch_product<float>(p, st);
+  else if (out_dtype == FN_OUT_FP16)
+    launch_product<_Float16>(p, st);
+  else
+    launch_product<fn::BF16>(p, st);
+  return launch_status("product kernel launch");
+}

@@ -1,0 +1,648 @@
+// row_kernels.hpp -- kernels that work on rows of D elements: RMS norm of
+// x + residual with its output in 8 bits or in the input's type, the norm's
+// gradients, and the quantisation of rows to 8 bits.
+//
+// Mathematics of one row:
+//   h = RN_T(x + residual)                        (RN_T: round to the type)
+//   rstd = 1 / sqrt(mean(h^2) + eps)              (NaN if the mean is not finite)
+//   norm:      out_j = RN_T(h_j rstd w_j)
+//   8 bits:    t_j = RN32(h_j w_j), A = max |t_j|,
+//              code_j = rint(RN32(t_j RN32(127 / A))), scale = A rstd / 127
+// rstd is a common factor of the row, so it cancels in code_j: the codes need
+// the maximum alone, which no order of evaluation changes, and h_j w_j is
+// exact in fp32 for 16-bit types.  The sum of squares and the maximum are
+// taken in the same pass, so one reduction serves both.
+//
+// Every element is read once and written once: a row stays in registers
+// between the reduction and the output (rows of more than 32,768 elements
+// are read twice).  The kernels are bound by memory.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace fn {
+
+struct BF16 {
+  uint16_t bits;
+};
+
+enum RowMode { kRowNorm = 0, kRowNormQ8 = 1, kRowQuantize = 2 };
+
+struct RowArgs {
+  const void* x;
+  const void* residual;  // or null
+  const void* weight;    // null when quantising
+  void* sum;             // null without a residual
+  void* out;             // kRowNorm
+  int8_t* codes;         // kRowNormQ8, kRowQuantize
+  float* scales;
+  float* rstd;  // or null
+  int64_t rows;
+  int64_t x_stride, residual_stride, sum_stride, out_stride, codes_stride;  // in elements
+  int32_t width;
+  float eps;
+};
+
+// ------------------------------------------------------------- vector access
+// Eight consecutive elements, at any alignment of the element's size: the
+// hardware's global loads and stores take unaligned addresses.
+
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ float bf16_to_float(uint32_t bits) {
+  return __builtin_bit_cast(float, bits << 16);
+}
+
+// float -> bfloat16 bits, to nearest even (the type's own conversion
+// instruction); NaN stays NaN
+__device__ __forceinline__ uint32_t float_to_bf16(float v) {
+  return __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+
+template <typename T>
+struct Vec8;  // eight elements as they lie in memory
+
+template <>
+struct Vec8<float> {
+  u32x4 a, b;
+  __device__ __forceinline__ void zero() { a = b = u32x4{0, 0, 0, 0}; }
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const u32x4_any*>(p);
+    b = *reinterpret_cast<const u32x4_any*>(p + 4);
+  }
+  __device__ __forceinline__ void load_some(const float* p, int n) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      a[j] = j < n ? __builtin_bit_cast(uint32_t, p[j]) : 0u;
+      b[j] = j + 4 < n ? __builtin_bit_cast(uint32_t, p[j + 4]) : 0u;
+    }
+  }
+  __device__ __forceinline__ float get(int j) const {
+    return __builtin_bit_cast(float, j < 4 ? a[j & 3] : b[j & 3]);
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      a[j] = __builtin_bit_cast(uint32_t, v[j]);
+      b[j] = __builtin_bit_cast(uint32_t, v[j + 4]);
+    }
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    *reinterpret_cast<u32x4_any*>(p) = a;
+    *reinterpret_cast<u32x4_any*>(p + 4) = b;
+  }
+  __device__ __forceinline__ void store_some(float* p, int n) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) p[j] = get(j);
+  }
+};
+
+// the 16-bit types differ in their conversions alone
+template <typename T>
+struct Half8 {
+  u32x4 a;
+  __device__ __forceinline__ void zero() { a = u32x4{0, 0, 0, 0}; }
+  __device__ __forceinline__ void load(const T* p) {
+    a = *reinterpret_cast<const u32x4_any*>(p);
+  }
+  __device__ __forceinline__ void load_some(const T* p, int n) {
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t lo = 2 * j < n ? q[2 * j] : 0u;
+      const uint32_t hi = 2 * j + 1 < n ? q[2 * j + 1] : 0u;
+      a[j] = lo | hi << 16;
+    }
+  }
+  __device__ __forceinline__ uint32_t bits(int j) const { return (a[j >> 1] >> (16 * (j & 1))) & 0xFFFFu; }
+  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<u32x4_any*>(p) = a; }
+  __device__ __forceinline__ void store_some(T* p, int n) const {
+    uint16_t* q = reinterpret_cast<uint16_t*>(p);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) q[j] = (uint16_t)bits(j);
+  }
+};
+
+template <>
+struct Vec8<_Float16> : Half8<_Float16> {
+  __device__ __forceinline__ float get(int j) const {
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)bits(j));
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t lo = __builtin_bit_cast(uint16_t, (_Float16)v[2 * j]);
+      const uint32_t hi = __builtin_bit_cast(uint16_t, (_Float16)v[2 * j + 1]);
+      a[j] = lo | hi << 16;
+    }
+  }
+};
+
+template <>
+struct Vec8<BF16> : Half8<BF16> {
+  __device__ __forceinline__ float get(int j) const {
+    return __builtin_bit_cast(float, j & 1 ? a[j >> 1] & 0xFFFF0000u : a[j >> 1] << 16);
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      a[j] = float_to_bf16(v[2 * j]) | float_to_bf16(v[2 * j + 1]) << 16;
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void load_chunk(Vec8<T>& v, const T* row, int32_t c, int32_t width) {
+  if (8 * c + 8 <= width)
+    v.load(row + 8 * c);
+  else if (8 * c < width)
+    v.load_some(row + 8 * c, width - 8 * c);
+  else
+    v.zero();
+}
+
+template <typename T>
+__device__ __forceinline__ void store_chunk(const Vec8<T>& v, T* row, int32_t c, int32_t width) {
+  if (8 * c + 8 <= width)
+    v.store(row + 8 * c);
+  else if (8 * c < width)
+    v.store_some(row + 8 * c, width - 8 * c);
+}
+
+// --------------------------------------------------------------- reductions
+// Sum (or unsigned maximum) over the 64 lanes of a wavefront, the same value
+// in every lane, without LDS: shifts inside rows of 16 lanes, then the row
+// broadcasts.  The order is fixed, so a result never changes from run to run.
+
+template <int kCtrl, int kRowMask>
+__device__ __forceinline__ uint32_t dpp_or_zero(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, kRowMask, 0xF, false);
+}
+
+template <int kCtrl, int kRowMask>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __builtin_bit_cast(float, dpp_or_zero<kCtrl, kRowMask>(__builtin_bit_cast(uint32_t, v)));
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+  v = add_dpp<0x111, 0xF>(v);  // lane - 1
+  v = add_dpp<0x112, 0xF>(v);  // lane - 2
+  v = add_dpp<0x114, 0xF>(v);
+  v = add_dpp<0x118, 0xF>(v);  // lane 15 of each row of 16 holds the row's sum
+  v = add_dpp<0x142, 0xA>(v);  // row 0 -> 1, row 2 -> 3
+  v = add_dpp<0x143, 0xC>(v);  // rows 0, 1 -> 2, 3
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max(v, dpp_or_zero<0x111, 0xF>(v));
+  v = max(v, dpp_or_zero<0x112, 0xF>(v));
+  v = max(v, dpp_or_zero<0x114, 0xF>(v));
+  v = max(v, dpp_or_zero<0x118, 0xF>(v));
+  v = max(v, dpp_or_zero<0x142, 0xA>(v));
+  v = max(v, dpp_or_zero<0x143, 0xC>(v));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// Over the wavefronts of a work-group that share a row.  `parity` alternates
+// between calls, so that one barrier per call is enough: a wavefront reaches
+// the next call's writes of the same half only after everyone has left this
+// call's reads, one barrier later.
+template <int kWaves>
+__device__ __forceinline__ void group_reduce(float& sum, uint32_t& top, int parity) {
+  sum = wave_sum(sum);
+  top = wave_max(top);
+  if constexpr (kWaves > 1) {
+    __shared__ float s_sum[2][kWaves];
+    __shared__ uint32_t s_top[2][kWaves];
+    const int wave = (int)(threadIdx.x >> 6);
+    if ((threadIdx.x & 63u) == 0) {
+      s_sum[parity][wave] = sum;
+      s_top[parity][wave] = top;
+    }
+    __syncthreads();
+    sum = s_sum[parity][0];
+    top = s_top[parity][0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) {
+      sum += s_sum[parity][w];
+      top = max(top, s_top[parity][w]);
+    }
+  }
+}
+
+// ------------------------------------------------------------ quantised rows
+
+// What a row's codes and scale come from.  `top` holds the bits of
+// max |t_j|: as unsigned integers, absolute values order like the numbers
+// and infinities and NaN above them all, so a NaN is never lost on the way.
+struct RowQuant {
+  float inverse;   // 127 / A, 0 for an empty row
+  float prescale;  // 1, or 2^100 for rows so small that 127 / A is infinite
+  float scale;
+  bool finite;
+};
+
+__device__ __forceinline__ RowQuant row_quant(uint32_t top, float factor) {
+  RowQuant q;
+  const float A = __builtin_bit_cast(float, top);
+  q.finite = top < 0x7F800000u && factor == factor;
+  q.prescale = A < 0x1p-100f ? 0x1p100f : 1.0f;
+  q.inverse = top == 0u || !q.finite ? 0.0f : 127.0f / (A * q.prescale);
+  q.scale = q.finite ? A * factor / 127.0f : __builtin_bit_cast(float, 0x7FC00000u);
+  return q;
+}
+
+// rint(v) as a byte, |v| <= 127: adding 1.5 * 2^23 rounds to an integer, to
+// nearest even, and leaves it in the low bits.
+__device__ __forceinline__ uint32_t code_bits(float v) {
+  return __builtin_bit_cast(uint32_t, v + 0x1.8p23f);
+}
+
+// Eight codes from t_0..t_7.
+__device__ __forceinline__ u32x2_any eight_codes(const float (&t)[8], const RowQuant& q) {
+  u32x2_any c;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint32_t b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b[j] = code_bits(t[4 * k + j] * q.prescale * q.inverse);
+    const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000C0Cu);
+    c[k] = q.finite ? lo | hi : 0u;
+  }
+  return c;
+}
+
+__device__ __forceinline__ void store_codes(u32x2_any v, int8_t* row, int32_t c, int32_t width) {
+  const int n = width - 8 * c;
+  if (n >= 8) {
+    *reinterpret_cast<u32x2_any*>(row + 8 * c) = v;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) row[8 * c + j] = (int8_t)(v[j >> 2] >> (8 * (j & 3)));
+  }
+}
+
+__device__ __forceinline__ float row_rstd(float sum_of_squares, int32_t width, float eps) {
+  const float ms = sum_of_squares / (float)width;
+  // a row that holds an infinity or a NaN, or whose squares overflow, has no
+  // norm: its output is NaN throughout rather than a plausible zero
+  return ms < __builtin_inff() ? 1.0f / sqrtf(ms + eps) : __builtin_bit_cast(float, 0x7FC00000u);
+}
+
+// ------------------------------------------------------------------ forward
+
+// kThreads work on one row, each on up to kChunks chunks of eight elements
+// (chunk k * kThreads + lane): width <= 8 * kThreads * kChunks.  A row of 64
+// threads is one wavefront and needs no barrier; four such rows make a
+// work-group.
+template <typename T, int kMode, int kThreads, int kChunks>
+__global__ __launch_bounds__(kThreads < 256 ? 256 : kThreads) void rows_kernel(RowArgs a) {
+  constexpr int kBlockThreads = kThreads < 256 ? 256 : kThreads;
+  constexpr int kRows = kBlockThreads / kThreads;
+  const int lane = (int)threadIdx.x % kThreads;
+  const int slot = (int)threadIdx.x / kThreads;
+  Vec8<T> w[kChunks];
+  if constexpr (kMode != kRowQuantize) {
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k)
+      load_chunk(w[k], (const T*)a.weight, k * kThreads + lane, a.width);
+  }
+  int parity = 0;
+  for (int64_t row = (int64_t)blockIdx.x * kRows + slot; row < a.rows;
+       row += (int64_t)gridDim.x * kRows, parity ^= 1) {
+    const T* x = (const T*)a.x + row * a.x_stride;
+    Vec8<T> h[kChunks];
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) load_chunk(h[k], x, k * kThreads + lane, a.width);
+    if (kMode != kRowQuantize && a.residual != nullptr) {
+      const T* r = (const T*)a.residual + row * a.residual_stride;
+      Vec8<T> v[kChunks];
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) load_chunk(v[k], r, k * kThreads + lane, a.width);
+      T* s = (T*)a.sum + row * a.sum_stride;
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) {
+        float t[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[j] = h[k].get(j) + v[k].get(j);
+        h[k].set(t);
+        store_chunk(h[k], s, k * kThreads + lane, a.width);
+      }
+    }
+    float sum = 0.0f;
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float v = h[k].get(j);
+        if constexpr (kMode != kRowQuantize) sum += v * v;
+        if constexpr (kMode != kRowNorm) {
+          const float t = kMode == kRowQuantize ? v : v * w[k].get(j);
+          top = max(top, __builtin_bit_cast(uint32_t, t) & 0x7FFFFFFFu);
+        }
+      }
+    }
+    group_reduce<kThreads / 64>(sum, top, parity);
+    float rstd = 1.0f;
+    if constexpr (kMode != kRowQuantize) {
+      rstd = row_rstd(sum, a.width, a.eps);
+      if (lane == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
+    }
+    if constexpr (kMode == kRowNorm) {
+      T* o = (T*)a.out + row * a.out_stride;
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) {
+        float t[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[j] = h[k].get(j) * rstd * w[k].get(j);
+        Vec8<T> v;
+        v.set(t);
+        store_chunk(v, o, k * kThreads + lane, a.width);
+      }
+    } else {
+      const RowQuant q = row_quant(top, rstd);
+      int8_t* o = a.codes + row * a.codes_stride;
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) {
+        float t[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          t[j] = kMode == kRowQuantize ? h[k].get(j) : h[k].get(j) * w[k].get(j);
+        store_codes(eight_codes(t, q), o, k * kThreads + lane, a.width);
+      }
+      if (lane == 0) a.scales[row] = q.scale;
+    }
+  }
+}
+
+// Rows of any width, one work-group of 1,024 threads each: the row is read a
+// second time (from the stored sum where there is one) instead of being kept.
+// A thread meets the same columns in both passes, so it may store over what
+// it reads.
+template <typename T, int kMode>
+__global__ __launch_bounds__(1024) void rows_wide_kernel(RowArgs a) {
+  constexpr int kThreads = 1024;
+  const int lane = (int)threadIdx.x;
+  const int32_t chunks = (int32_t)(((int64_t)a.width + 7) / 8);
+  int parity = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
+    const T* x = (const T*)a.x + row * a.x_stride;
+    const bool add = kMode != kRowQuantize && a.residual != nullptr;
+    const T* r = add ? (const T*)a.residual + row * a.residual_stride : nullptr;
+    T* s = add ? (T*)a.sum + row * a.sum_stride : nullptr;
+    float sum = 0.0f;
+    uint32_t top = 0;
+    for (int32_t c = lane; c < chunks; c += kThreads) {
+      Vec8<T> h, w;
+      load_chunk(h, x, c, a.width);
+      if (add) {
+        Vec8<T> v;
+        load_chunk(v, r, c, a.width);
+        float t[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[j] = h.get(j) + v.get(j);
+        h.set(t);
+        store_chunk(h, s, c, a.width);
+      }
+      if constexpr (kMode == kRowNormQ8) load_chunk(w, (const T*)a.weight, c, a.width);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float v = h.get(j);
+        if constexpr (kMode != kRowQuantize) sum += v * v;
+        if constexpr (kMode != kRowNorm) {
+          const float t = kMode == kRowQuantize ? v : v * w.get(j);
+          top = max(top, __builtin_bit_cast(uint32_t, t) & 0x7FFFFFFFu);
+        }
+      }
+    }
+    group_reduce<kThreads / 64>(sum, top, parity);
+    float rstd = 1.0f;
+    if constexpr (kMode != kRowQuantize) {
+      rstd = row_rstd(sum, a.width, a.eps);
+      if (lane == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
+    }
+    const RowQuant q = row_quant(top, rstd);
+    const T* from = add ? s : x;
+    for (int32_t c = lane; c < chunks; c += kThreads) {
+      Vec8<T> h, w;
+      load_chunk(h, from, c, a.width);
+      if constexpr (kMode != kRowQuantize) load_chunk(w, (const T*)a.weight, c, a.width);
+      float t[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float v = h.get(j);
+        t[j] = kMode == kRowQuantize ? v : kMode == kRowNorm ? v * rstd * w.get(j) : v * w.get(j);
+      }
+      if constexpr (kMode == kRowNorm) {
+        h.set(t);
+        store_chunk(h, (T*)a.out + row * a.out_stride, c, a.width);
+      } else {
+        store_codes(eight_codes(t, q), a.codes + row * a.codes_stride, c, a.width);
+      }
+    }
+    if (kMode != kRowNorm && lane == 0) a.scales[row] = q.scale;
+  }
+}
+
+// ----------------------------------------------------------------- backward
+//
+// With n = h rstd, g = dout w and m = mean(g n):
+//   dx = rstd (g - n m) [+ dsum],   dweight = sum over rows of dout n.
+// dx is the gradient of x and of the residual alike.
+
+struct BackwardArgs {
+  const void* dout;
+  const void* h;
+  const void* weight;
+  const float* rstd;
+  const void* dsum;  // or null
+  void* dx;
+  float* partial;   // [partials][width] sums of dout n, one row per work-group (or slice)
+  float* row_mean;  // rows of more than 32,768 elements: m of each row
+  int64_t rows;
+  int64_t dout_stride, h_stride, dsum_stride, dx_stride;  // in elements
+  int64_t rows_per_slice;
+  int32_t width;
+  int32_t partials;
+};
+
+template <typename T>
+__device__ __forceinline__ void backward_chunk(const Vec8<T>& d, const Vec8<T>& h,
+                                               const Vec8<T>& w, const Vec8<T>* s, float rstd,
+                                               float mean, Vec8<T>& out) {
+  float t[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float n = h.get(j) * rstd;
+    t[j] = rstd * (d.get(j) * w.get(j) - n * mean);
+    if (s != nullptr) t[j] += s->get(j);
+  }
+  out.set(t);
+}
+
+// Layout of threads and rows as in rows_kernel.  A work-group takes every
+// gridDim.x-th group of rows and keeps its columns' sums of dout n in
+// registers until the end: one row of partial sums per work-group.
+template <typename T, int kThreads, int kChunks>
+__global__ __launch_bounds__(kThreads < 256 ? 256 : kThreads) void rows_backward_kernel(
+    BackwardArgs a) {
+  constexpr int kBlockThreads = kThreads < 256 ? 256 : kThreads;
+  constexpr int kRows = kBlockThreads / kThreads;
+  const int lane = (int)threadIdx.x % kThreads;
+  const int slot = (int)threadIdx.x / kThreads;
+  Vec8<T> w[kChunks];
+  float dw[kChunks][8];
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k) {
+    load_chunk(w[k], (const T*)a.weight, k * kThreads + lane, a.width);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[k][j] = 0.0f;
+  }
+  int parity = 0;
+  for (int64_t row = (int64_t)blockIdx.x * kRows + slot; row < a.rows;
+       row += (int64_t)gridDim.x * kRows, parity ^= 1) {
+    const T* pd = (const T*)a.dout + row * a.dout_stride;
+    const T* ph = (const T*)a.h + row * a.h_stride;
+    Vec8<T> d[kChunks], h[kChunks], s[kChunks];
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+      load_chunk(d[k], pd, k * kThreads + lane, a.width);
+      load_chunk(h[k], ph, k * kThreads + lane, a.width);
+    }
+    const bool add = a.dsum != nullptr;
+    if (add) {
+      const T* ps = (const T*)a.dsum + row * a.dsum_stride;
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) load_chunk(s[k], ps, k * kThreads + lane, a.width);
+    }
+    const float rstd = a.rstd[row];
+    float sum = 0.0f;
+    uint32_t unused = 0;
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float dn = d[k].get(j) * (h[k].get(j) * rstd);
+        dw[k][j] += dn;
+        sum += dn * w[k].get(j);
+      }
+    }
+    group_reduce<kThreads / 64>(sum, unused, parity);
+    const float mean = sum / (float)a.width;
+    T* o = (T*)a.dx + row * a.dx_stride;
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+      Vec8<T> v;
+      backward_chunk(d[k], h[k], w[k], add ? &s[k] : nullptr, rstd, mean, v);
+      store_chunk(v, o, k * kThreads + lane, a.width);
+    }
+  }
+  if constexpr (kRows > 1) {
+    // the work-group's rows of sums, added in the order of the slots
+    __shared__ float s_dw[kRows - 1][kThreads * 8 * kChunks];
+    if (slot > 0) {
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s_dw[slot - 1][(k * 8 + j) * kThreads + lane] = dw[k][j];
+    }
+    __syncthreads();
+    if (slot > 0) return;
+#pragma unroll
+    for (int r = 0; r < kRows - 1; ++r)
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[k][j] += s_dw[r][(k * 8 + j) * kThreads + lane];
+  }
+  float* p = a.partial + (int64_t)blockIdx.x * a.width;
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k) {
+    Vec8<float> v;
+    v.set(dw[k]);
+    store_chunk(v, p, k * kThreads + lane, a.width);
+  }
+}
+
+// Rows of any width, first step: m = mean(g n) of each row.
+template <typename T>
+__global__ __launch_bounds__(1024) void rows_backward_mean_kernel(BackwardArgs a) {
+  const int32_t chunks = (int32_t)(((int64_t)a.width + 7) / 8);
+  int parity = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
+    const T* pd = (const T*)a.dout + row * a.dout_stride;
+    const T* ph = (const T*)a.h + row * a.h_stride;
+    const float rstd = a.rstd[row];
+    float sum = 0.0f;
+    uint32_t unused = 0;
+    for (int32_t c = (int32_t)threadIdx.x; c < chunks; c += 1024) {
+      Vec8<T> d, h, w;
+      load_chunk(d, pd, c, a.width);
+      load_chunk(h, ph, c, a.width);
+      load_chunk(w, (const T*)a.weight, c, a.width);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum += d.get(j) * (h.get(j) * rstd) * w.get(j);
+    }
+    group_reduce<16>(sum, unused, parity);
+    if (threadIdx.x == 0) a.row_mean[row] = sum / (float)a.width;
+  }
+}
+
+// Second step: a thread takes eight columns of a slice of the rows.
+template <typename T>
+__global__ __launch_bounds__(256) void rows_backward_columns_kernel(BackwardArgs a) {
+  const int32_t chunks = (int32_t)(((int64_t)a.width + 7) / 8);
+  const int32_t c = (int32_t)(blockIdx.x * 256u + threadIdx.x);
+  if (c >= chunks) return;
+  const int64_t first = (int64_t)blockIdx.y * a.rows_per_slice;
+  const int64_t end = min(first + a.rows_per_slice, a.rows);
+  Vec8<T> w;
+  load_chunk(w, (const T*)a.weight, c, a.width);
+  float dw[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int64_t row = first; row < end; ++row) {
+    Vec8<T> d, h, s, v;
+    load_chunk(d, (const T*)a.dout + row * a.dout_stride, c, a.width);
+    load_chunk(h, (const T*)a.h + row * a.h_stride, c, a.width);
+    const bool add = a.dsum != nullptr;
+    if (add) load_chunk(s, (const T*)a.dsum + row * a.dsum_stride, c, a.width);
+    const float rstd = a.rstd[row];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[j] += d.get(j) * (h.get(j) * rstd);
+    backward_chunk(d, h, w, add ? &s : nullptr, rstd, a.row_mean[row], v);
+    store_chunk(v, (T*)a.dx + row * a.dx_stride, c, a.width);
+  }
+  Vec8<float> v;
+  v.set(dw);
+  store_chunk(v, a.partial + (int64_t)blockIdx.y * a.width, c, a.width);
+}
+
+// dweight = the sum of the rows of partial sums: 16 columns per work-group,
+// 64 threads to a column, joined in a fixed order.
+__global__ __launch_bounds__(1024) void column_sum_kernel(const float* partial, int32_t partials,
+                                                          int32_t width, float* dweight) {
+  __shared__ float s_sum[64][17];
+  const int col = (int)(threadIdx.x & 15u), part = (int)(threadIdx.x >> 4);
+  const int64_t c = (int64_t)blockIdx.x * 16 + col;
+  float sum = 0.0f;
+  if (c < width) {
+#pragma unroll 8
+    for (int32_t p = part; p < partials; p += 64) sum += partial[(int64_t)p * width + c];
+  }
+  s_sum[part][col] = sum;
+  __syncthreads();
+  if (part == 0 && c < width) {
+#pragma unroll 8
+    for (int p = 1; p < 64; ++p) sum += s_sum[p][col];
+    dweight[c] = sum;
+  }
+}
+
+}  // namespace fn

@@ -52,6 +52,8 @@ extern "C" {
 #define FN_OUT_FP16_PAD4 2 /* binary16 with 4 channels per pixel: channels c < C as
                               FN_OUT_FP16, channels C..3 are +0 -- the page's
                               mixed-precision layout (page sec. 8) */
+#define FN_OUT_BF16 3 /* 2-byte bfloat16, rounded to nearest even: the row and
+                         product operators below, not the pixel operations     */
 
 /* One sample's random decisions (32 bytes, all int32):
  *   flip        1 if the image is mirrored left-right, else 0;
@@ -193,6 +195,107 @@ int fn_fused_normalize_ex(const uint8_t* in_u8_dev, int64_t in_row_stride,
 int fn_params_ex(uint64_t seed, int64_t first_sample_id, int64_t N, int32_t H, int32_t W,
                  float flip_p, float erase_p, float scale_min, float scale_max, float ratio_min,
                  float ratio_max, fn_sample_params* params_dev, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* The 8-bit linear layer: a norm that quantises, the quantisation of rows,   */
+/* the product of the codes, and the norm's gradients for training.           */
+/*                                                                            */
+/* A matrix is `rows` rows of contiguous elements, a row stride (in elements) */
+/* apart.  Bases and strides need the element's own alignment only.  An       */
+/* input's stride may be 0 (one row for all) or anything above; an output's   */
+/* is at least the row's length.  No output may overlap another buffer of the */
+/* call, except as each operator allows; column ranges of one buffer, with    */
+/* the same stride, do not overlap.  dtype is FN_OUT_FP32, FN_OUT_FP16 or     */
+/* FN_OUT_BF16.  Sums, statistics and scales are fp32 (integer sums 32-bit).  */
+/* Speed only: rows that start at multiples of 16 bytes are fastest.          */
+/*                                                                            */
+/* Errors of all: FN_EINVAL for a null, misaligned, too short or overlapping  */
+/* buffer, a negative size or stride, an output stride shorter than a row, an */
+/* unknown dtype; FN_EOVERFLOW for width > 2^30, rows > 2^40 or a span beyond */
+/* 2^62 bytes; FN_EHIP if a launch fails.  rows = 0 (M = 0 or N = 0) enqueues */
+/* nothing and needs no buffers, unless stated.                               */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * fn_rms_norm -- h = x + residual and its root-mean-square norm, per row:
+ *   h     = x + residual, rounded to dtype and stored in sum_dev (h = x and
+ *           nothing stored when residual_dev and sum_dev are NULL);
+ *   rstd  = 1 / sqrt(mean(h^2) + eps), stored if rstd_dev is not NULL (the
+ *           backward pass takes it);
+ *   out   = h * rstd * weight, rounded to dtype.
+ * weight_dev: `width` elements of dtype.  eps > 0.  sum_dev and out_dev may
+ * each be exactly x_dev or residual_dev (same stride), not each other.
+ * A row that holds a NaN or an infinity, or whose squares overflow fp32, has
+ * rstd = NaN and is NaN throughout.
+ */
+int fn_rms_norm(const void* x_dev, int64_t x_stride, const void* residual_dev,
+                int64_t residual_stride, const void* weight_dev, int64_t rows, int32_t width,
+                float eps, int32_t dtype, void* sum_dev, int64_t sum_stride, void* out_dev,
+                int64_t out_stride, float* rstd_dev, void* stream);
+
+/*
+ * fn_rms_norm_q8 -- the same norm with its output in 8 bits and a scale per
+ * row.  With t_j = h_j * weight_j and A = max |t_j|, each operation rounded to
+ * fp32:
+ *   code_j = rint(t_j * (127 / A)), ties to even, in -127..127;
+ *   scale  = A * rstd / 127,   so that   out_j ~ code_j * scale.
+ * rstd is common to a row and cancels in its codes, which therefore depend on
+ * no order of summation: they are the same bits on every run and device.
+ * (Where A < 2^-100, t and A are scaled by 2^100 first.)  A row of zeros has
+ * codes 0 and scale 0; a row without a norm (above), or with a NaN or an
+ * infinity among its t_j, has codes 0 and scale NaN.
+ * sum_dev may be exactly x_dev or residual_dev.
+ */
+int fn_rms_norm_q8(const void* x_dev, int64_t x_stride, const void* residual_dev,
+                   int64_t residual_stride, const void* weight_dev, int64_t rows, int32_t width,
+                   float eps, int32_t dtype, void* sum_dev, int64_t sum_stride,
+                   int8_t* codes_dev, int64_t codes_stride, float* scales_dev, float* rstd_dev,
+                   void* stream);
+
+/* fn_quantize_rows -- codes and scales of rows as they are: fn_rms_norm_q8's
+ * formulas with t = x and scale = A / 127.  For weights (a row per output
+ * channel) and for activations that come from no norm. */
+int fn_quantize_rows(const void* x_dev, int64_t x_stride, int64_t rows, int32_t width,
+                     int32_t dtype, int8_t* codes_dev, int64_t codes_stride, float* scales_dev,
+                     void* stream);
+
+/*
+ * fn_rms_norm_backward -- the gradients of fn_rms_norm.  dout is the gradient
+ * of out; dsum (or NULL) the gradient that reaches the stored sum by another
+ * way; h the sum (x if there was no residual) and rstd what the forward pass
+ * stored.  With n = h * rstd and g = dout * weight:
+ *   dx      = rstd * (g - n * mean(g * n)) + dsum, rounded to dtype: the
+ *             gradient of x and of the residual alike;
+ *   dweight = sum over the rows of dout * n, fp32, overwritten, joined in an
+ *             order that the sizes alone fix (no atomics).  rows = 0 writes
+ *             zeros.
+ * dx_dev may be exactly dout_dev, h_dev or dsum_dev.  workspace_dev: at least
+ * fn_rms_norm_backward_workspace(rows, width) bytes, 4-byte aligned, that no
+ * other call in flight uses.  For a norm whose output was quantised, dout is
+ * the gradient of code * scale, passed straight through the rounding.
+ */
+int fn_rms_norm_backward(const void* dout_dev, int64_t dout_stride, const void* h_dev,
+                         int64_t h_stride, const void* weight_dev, const float* rstd_dev,
+                         const void* dsum_dev, int64_t dsum_stride, int64_t rows, int32_t width,
+                         int32_t dtype, void* dx_dev, int64_t dx_stride, float* dweight_dev,
+                         void* workspace_dev, int64_t workspace_bytes, void* stream);
+
+/* Writes to *bytes (host) the workspace that fn_rms_norm_backward needs. */
+int fn_rms_norm_backward_workspace(int64_t rows, int32_t width, int64_t* bytes);
+
+/*
+ * fn_matmul_q8 -- the product of two matrices of codes:
+ *   out[m, n] = a_scales[m] * b_scales[n] * sum_k a[m, k] * b[n, k] + bias[n]
+ * a is M x K (tokens), b is N x K (output channels), out M x N of out_dtype.
+ * The sum is exact (32-bit integers; K <= 131071, else FN_EOVERFLOW; codes may
+ * be -128..127); the rest is ((sum * a_scale) * b_scale) + bias in fp32, one
+ * rounding per operation, then one rounding to out_dtype.  bias_dev may be
+ * NULL.  K = 0 gives bias (or 0), and needs no a_dev and b_dev.
+ */
+int fn_matmul_q8(const int8_t* a_dev, int64_t a_stride, const float* a_scales_dev,
+                 const int8_t* b_dev, int64_t b_stride, const float* b_scales_dev,
+                 const float* bias_dev, int64_t M, int64_t N, int32_t K, int32_t out_dtype,
+                 void* out_dev, int64_t out_stride, void* stream);
 
 /* The message of the last nonzero return on the calling thread ("" if none).
  * The pointer stays valid until the next call on the same thread. */

@@ -35,8 +35,32 @@ struct ProductArgs {
   int64_t out_stride;          // elements
   int64_t M, N;
   int32_t K;
-  uint32_t tiles_n;
+  uint32_t tiles_m, tiles_n;
 };
+
+// Waits until at most kLeft of this wavefront's loads are under way.
+template <int kLeft>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLeft) : "memory");
+}
+
+// Work-groups are dealt round-robin over the 8 XCDs, each with an L2 of its
+// own.  Every XCD takes one run of consecutive tiles, in an order that walks
+// kGroup token tiles for each channel tile, so that the tiles in flight on an
+// XCD share rows of both operands.
+struct TileAt {
+  uint32_t m, n;
+};
+
+__device__ __forceinline__ TileAt tile_at(uint32_t block, const ProductArgs& p) {
+  constexpr uint32_t kXcds = 8, kGroup = 8;
+  const uint32_t total = p.tiles_m * p.tiles_n;
+  const uint32_t xcd = block % kXcds, each = total / kXcds, more = total % kXcds;
+  const uint32_t t = xcd * each + min(xcd, more) + block / kXcds;
+  const uint32_t band = t / (kGroup * p.tiles_n), in = t % (kGroup * p.tiles_n);
+  const uint32_t height = min(kGroup, p.tiles_m - band * kGroup);
+  return {band * kGroup + in % height, in / height};
+}
 
 // Sixteen codes k0 .. k0 + 15 of a row, zeros from K on.
 __device__ __forceinline__ i32x4 load16(const int8_t* row, int32_t k0, int32_t K) {
@@ -109,9 +133,10 @@ __device__ __forceinline__ void store_strip(const ProductArgs& p, const i32x16 (
       bias[j] = j < left && p.bias != nullptr ? p.bias[n + j] : 0.0f;
     }
 #pragma unroll
-    for (int r = lane / kLanes; r < 32; r += kRowsAtOnce) {
+    for (int i = 0; i < 32 / kRowsAtOnce; ++i) {
+      const int r = i * kRowsAtOnce + lane / kLanes;
       const int64_t m = m0 + r;
-      if (m >= p.M) break;
+      if (m >= p.M) continue;
       int v[kE];
 #pragma unroll
       for (int j = 0; j < kE; j += 4) {
@@ -145,8 +170,8 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs p) {
   int8_t* s_a = s_tile;
   int8_t* s_b = s_tile + 128 * 64;
   const int lane = (int)(threadIdx.x & 63u), wave = (int)(threadIdx.x >> 6);
-  const int64_t m0 = (int64_t)(blockIdx.x / p.tiles_n) * 128;
-  const int64_t n0 = (int64_t)(blockIdx.x % p.tiles_n) * 128;
+  const TileAt tile = tile_at(blockIdx.x, p);
+  const int64_t m0 = (int64_t)tile.m * 128, n0 = (int64_t)tile.n * 128;
   const int row = (int)(threadIdx.x >> 2), piece = (int)(threadIdx.x & 3u);
   i32x4 ra[2], rb[2];
   auto load = [&](int32_t k0) {
@@ -191,6 +216,164 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs p) {
 #pragma unroll
   for (int i = 0; i < 2; ++i)
     store_strip<T, 2>(p, acc[i], strip, m0 + 64 * (wave >> 1) + 32 * i, n0 + 64 * (wave & 1));
+}
+
+// ---------------------------------------------------------------------------
+// Tiles through direct global-to-LDS loads, for rows that start at multiples
+// of 16 bytes.
+//
+// A stage is the next kBK codes of K of the tile's tokens and channels in LDS;
+// kStages of them are under way at once.  The loads are written out because
+// the compiler, which cannot tell a stage that is being read from one that is
+// being filled, would wait for all of them before every read; they have no
+// destination register, and every wait for them stands in the code below.
+// M0 holds the LDS address; nothing else in these kernels uses it.
+
+__device__ __forceinline__ void load_to_lds(i32x4 resource, uint32_t lds, int offset, int k0) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %2, %3 offen lds"
+      :
+      : "s"(lds), "v"(offset), "s"(resource), "s"(k0)
+      : "memory");
+}
+
+__device__ __forceinline__ i32x4 tile_resource(const int8_t* p, int64_t stride,
+                                                                int64_t rows, int32_t K) {
+  // bytes from the tile's first row to the end of the last one; loads beyond
+  // give zeros
+  const int64_t bytes = rows > 0 ? (rows - 1) * stride + K : 0;
+  const uint64_t at = (uint64_t)(uintptr_t)p;
+  return i32x4{(int)(uint32_t)at, (int)(uint32_t)(at >> 32),
+               (int)min(bytes, (int64_t)0x7FFFFFF0), 0x00027000};
+}
+
+constexpr int kOutside = 0x7FFFFFF8;  // an offset that lies beyond every tile
+
+// Position of a 16-byte piece in a staged row of kBK codes: piece c of row r
+// lies at c ^ (a hash of r), so that lanes that read the same piece of
+// neighbouring rows at once spread over all banks.
+template <int kBK>
+__device__ __forceinline__ int staged_piece(int row, int piece) {
+  return kBK == 64 ? piece ^ piece_swizzle(row) : piece ^ (row & 7);
+}
+
+// One tile of kBM tokens x kBN channels per work-group of kWM x kWN
+// wavefronts, each with kTM x kTN tiles of the 32x32x32 instruction.
+template <typename T, int kBM, int kBN, int kWM, int kWN, int kBK, int kStages, int kPerSimd>
+__global__ __launch_bounds__(64 * kWM * kWN, kPerSimd) void product_tile_kernel(ProductArgs p) {
+  constexpr int kWaves = kWM * kWN, kTM = kBM / kWM / 32, kTN = kBN / kWN / 32;
+  constexpr int kStageBytes = (kBM + kBN) * kBK;
+  constexpr int kPieces = kBK / 16;                    // 16-byte pieces of a staged row
+  constexpr int kRowsAtOnce = 64 / kPieces;            // rows that one load of a wavefront covers
+  constexpr int kLoadsA = kBM / kRowsAtOnce / kWaves;  // loads of a wavefront per stage
+  constexpr int kLoadsB = kBN / kRowsAtOnce / kWaves;
+  constexpr int kLoads = kLoadsA + kLoadsB;
+  constexpr int kSteps = kBK / 32;
+  __shared__ __align__(1024) int8_t s_stages[kStages * kStageBytes];
+  const int lane = (int)(threadIdx.x & 63u);
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+
+  const TileAt tile = tile_at(blockIdx.x, p);
+  const int64_t m0 = (int64_t)tile.m * kBM, n0 = (int64_t)tile.n * kBN;
+  const i32x4 src_a =
+      tile_resource(p.a + m0 * p.a_stride, p.a_stride, min(p.M - m0, (int64_t)kBM), p.K);
+  const i32x4 src_b =
+      tile_resource(p.b + n0 * p.b_stride, p.b_stride, min(p.N - n0, (int64_t)kBN), p.K);
+  // this lane's row and (swizzled) piece in each of the wavefront's loads
+  int off_a[kLoadsA], off_b[kLoadsB];
+  const int sub = lane / kPieces;
+  const int piece = staged_piece<kBK>(sub, lane % kPieces);
+#pragma unroll
+  for (int i = 0; i < kLoadsA; ++i) {
+    const int r = (wave * kLoadsA + i) * kRowsAtOnce + sub;
+    off_a[i] = m0 + r < p.M ? r * (int)p.a_stride + 16 * piece : kOutside;
+  }
+#pragma unroll
+  for (int i = 0; i < kLoadsB; ++i) {
+    const int r = (wave * kLoadsB + i) * kRowsAtOnce + sub;
+    off_b[i] = n0 + r < p.N ? r * (int)p.b_stride + 16 * piece : kOutside;
+  }
+  const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)s_stages;
+  auto issue = [&](int stage, int k0) {
+    const bool inside = k0 + 16 * piece < p.K;  // K is whole pieces
+    const uint32_t to = lds + stage * kStageBytes + wave * (kLoadsA * 1024);
+#pragma unroll
+    for (int i = 0; i < kLoadsA; ++i)
+      load_to_lds(src_a, to + i * 1024, inside ? off_a[i] : kOutside, k0);
+    const uint32_t to_b = lds + stage * kStageBytes + kBM * kBK + wave * (kLoadsB * 1024);
+#pragma unroll
+    for (int i = 0; i < kLoadsB; ++i)
+      load_to_lds(src_b, to_b + i * 1024, inside ? off_b[i] : kOutside, k0);
+  };
+  // fragments: lane l holds row l % 32, codes 16 (l / 32) .. + 15 of a step
+  const int frow = lane & 31, fhalf = lane >> 5;
+  const int at_a = ((wave / kWN) * kTM * 32 + frow) * kBK;
+  const int at_b = kBM * kBK + ((wave % kWN) * kTN * 32 + frow) * kBK;
+  int at_piece[kSteps];
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) at_piece[k] = 16 * staged_piece<kBK>(frow, 2 * k + fhalf);
+  i32x4 fa[2][kTM], fb[2][kTN];
+  auto fetch = [&](const int8_t* buf, int k, int slot) {
+#pragma unroll
+    for (int t = 0; t < kTM; ++t)
+      fa[slot][t] = *reinterpret_cast<const i32x4*>(buf + at_a + t * 32 * kBK + at_piece[k]);
+#pragma unroll
+    for (int t = 0; t < kTN; ++t)
+      fb[slot][t] = *reinterpret_cast<const i32x4*>(buf + at_b + t * 32 * kBK + at_piece[k]);
+  };
+  i32x16 acc[kTM][kTN] = {};
+  auto multiply = [&](int slot, int from, int to) {
+    // keeps the fetches above in front: they hide behind these products
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = from; i < to; ++i)
+#pragma unroll
+      for (int j = 0; j < kTN; ++j)
+        acc[i][j] =
+            __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[slot][j], fa[slot][i], acc[i][j], 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  const int iterations = (p.K + kBK - 1) / kBK;
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) issue(s, s * kBK);
+  wait_loads<(kStages - 1) * kLoads>();
+  __builtin_amdgcn_s_barrier();
+  fetch(s_stages, 0, 0);
+  int stage = 0;
+  for (int it = 0; it < iterations; ++it) {
+    const int next = stage + 1 == kStages ? 0 : stage + 1;
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      if (k + 1 < kSteps) {
+        fetch(s_stages + stage * kStageBytes, k + 1, (k + 1) & 1);
+        multiply(k & 1, 0, kTM);
+      } else {
+        multiply(k & 1, 0, kTM / 2);
+        // everyone's reads of this stage are done and everyone's loads of the
+        // next have landed: this buffer is free for the stage after the last
+        wait_loads<(kStages - 2) * kLoads>();
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        issue(stage, (it + kStages) * kBK);
+        fetch(s_stages + next * kStageBytes, 0, (k + 1) & 1);
+        multiply(k & 1, kTM / 2, kTM);
+      }
+    }
+    stage = next;
+  }
+  // loads of stages beyond K (they bring zeros) end before the buffers are
+  // used again
+  wait_loads<0>();
+  __syncthreads();
+  constexpr int kStripBytes = 32 * (32 * kTN + 4) * 4;
+  static_assert(kStripBytes * kWaves <= kStages * kStageBytes, "strips fit");
+  int8_t* strip = s_stages + wave * kStripBytes;
+#pragma unroll
+  for (int i = 0; i < kTM; ++i)
+    store_strip<T, kTN>(p, acc[i], reinterpret_cast<int*>(strip),
+                        m0 + ((wave / kWN) * kTM + i) * 32, n0 + (wave % kWN) * kTN * 32);
 }
 
 }  // namespace fn

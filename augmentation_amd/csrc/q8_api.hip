@@ -252,10 +252,36 @@ void launch_backward(const fn::BackwardArgs& a, const BackwardPlan& p, hipStream
   }
 }
 
+// Tiles of kBM tokens x kBN channels: the grid, or 0 if it has too many.
+template <int kBM, int kBN>
+unsigned tile_grid(fn::ProductArgs* p) {
+  const int64_t tm = (p->M + kBM - 1) / kBM, tn = (p->N + kBN - 1) / kBN;
+  if ((__int128)tm * tn > 0x7FFFFFFF) return 0;
+  p->tiles_m = (uint32_t)tm;
+  p->tiles_n = (uint32_t)tn;
+  return (unsigned)(tm * tn);
+}
+
 template <typename T>
-void launch_product(const fn::ProductArgs& p, hipStream_t st) {
-  const int64_t tiles = ((p.M + 127) / 128) * (int64_t)p.tiles_n;
-  fn::product_any_kernel<T><<<(unsigned)tiles, 256, 0, st>>>(p);
+int launch_product(fn::ProductArgs p, hipStream_t st) {
+  // whole 16-byte pieces from 16-byte aligned rows, a tile's rows within the
+  // 31-bit offsets of its buffer resource
+  const bool pieces = ((uintptr_t)p.a | (uintptr_t)p.b | (uint64_t)p.a_stride |
+                       (uint64_t)p.b_stride | (uint64_t)p.K) % 16 == 0 &&
+                      std::max(p.a_stride, p.b_stride) <= (0x7FFFFFF0 - 131072) / 256;
+  unsigned grid = 0;
+  if (pieces && p.M * (__int128)p.N >= (int64_t)256 * 256 * 200) {
+    grid = tile_grid<256, 256>(&p);
+    if (grid) fn::product_tile_kernel<T, 256, 256, 2, 2, 64, 4, 1><<<grid, 256, 0, st>>>(p);
+  } else if (pieces) {
+    grid = tile_grid<128, 128>(&p);
+    if (grid) fn::product_tile_kernel<T, 128, 128, 2, 2, 64, 4, 2><<<grid, 256, 0, st>>>(p);
+  } else {
+    grid = tile_grid<128, 128>(&p);
+    if (grid) fn::product_any_kernel<T><<<grid, 256, 0, st>>>(p);
+  }
+  if (grid == 0) return fail(FN_EOVERFLOW, "grid size limit exceeded");
+  return launch_status("product kernel launch");
 }
 
 }  // namespace
@@ -389,9 +415,6 @@ FN_EXPORT int fn_matmul_q8(const int8_t* a_dev, int64_t a_stride, const float* a
   };
   int dev = -1;
   FN_TRY(check_buffers(buffers, &dev));
-  const int64_t tiles_n = (N + 127) / 128;
-  if (((M + 127) / 128) * (__int128)tiles_n > 0x7FFFFFFF)
-    return fail(FN_EOVERFLOW, "grid size limit exceeded");
   if (none) return ok();
   fn::ProductArgs p{};
   p.a = a_dev;
@@ -406,13 +429,8 @@ FN_EXPORT int fn_matmul_q8(const int8_t* a_dev, int64_t a_stride, const float* a
   p.M = M;
   p.N = N;
   p.K = K;
-  p.tiles_n = (uint32_t)tiles_n;
   hipStream_t st = (hipStream_t)stream;
-  if (out_dtype == FN_OUT_FP32)
-    launch_product<float>(p, st);
-  else if (out_dtype == FN_OUT_FP16)
-    launch_product<_Float16>(p, st);
-  else
-    launch_product<fn::BF16>(p, st);
-  return launch_status("product kernel launch");
+  if (out_dtype == FN_OUT_FP32) return launch_product<float>(p, st);
+  if (out_dtype == FN_OUT_FP16) return launch_product<_Float16>(p, st);
+  return launch_product<fn::BF16>(p, st);
 }

@@ -7,7 +7,7 @@
 //   rstd = 1 / sqrt(mean(h^2) + eps)              (NaN if the mean is not finite)
 //   norm:      out_j = RN_T(h_j rstd w_j)
 //   8 bits:    t_j = RN32(h_j w_j), A = max |t_j|,
-//              code_j = rint(RN32(t_j RN32(127 / A))), scale = A rstd / 127
+//              code_j = rint(RN32(t_j RN32(127 RN32(1 / A)))), scale = A rstd / 127
 // rstd is a common factor of the row, so it cancels in code_j: the codes need
 // the maximum alone, which no order of evaluation changes, and h_j w_j is
 // exact in fp32 for 16-bit types.  The sum of squares and the maximum are
@@ -241,8 +241,8 @@ __device__ __forceinline__ void group_reduce(float& sum, uint32_t& top, int pari
 // max |t_j|: as unsigned integers, absolute values order like the numbers
 // and infinities and NaN above them all, so a NaN is never lost on the way.
 struct RowQuant {
-  float inverse;   // 127 / A, 0 for an empty row
-  float prescale;  // 1, or 2^100 for rows so small that 127 / A is infinite
+  float inverse;   // 127 (1 / A), 0 for an empty row
+  float prescale;  // 1, or 2^100 for rows so small that 1 / A is infinite
   float scale;
   bool finite;
 };
@@ -252,7 +252,7 @@ __device__ __forceinline__ RowQuant row_quant(uint32_t top, float factor) {
   const float A = __builtin_bit_cast(float, top);
   q.finite = top < 0x7F800000u && factor == factor;
   q.prescale = A < 0x1p-100f ? 0x1p100f : 1.0f;
-  q.inverse = top == 0u || !q.finite ? 0.0f : 127.0f / (A * q.prescale);
+  q.inverse = top == 0u || !q.finite ? 0.0f : 127.0f * (1.0f / (A * q.prescale));
   q.scale = q.finite ? A * factor / 127.0f : __builtin_bit_cast(float, 0x7FC00000u);
   return q;
 }

@@ -237,7 +237,7 @@ int fn_rms_norm(const void* x_dev, int64_t x_stride, const void* residual_dev,
  * fn_rms_norm_q8 -- the same norm with its output in 8 bits and a scale per
  * row.  With t_j = h_j * weight_j and A = max |t_j|, each operation rounded to
  * fp32:
- *   code_j = rint(t_j * (127 / A)), ties to even, in -127..127;
+ *   code_j = rint(t_j * (127 * (1 / A))), ties to even, in -127..127;
  *   scale  = A * rstd / 127,   so that   out_j ~ code_j * scale.
  * rstd is common to a row and cancels in its codes, which therefore depend on
  * no order of summation: they are the same bits on every run and device.

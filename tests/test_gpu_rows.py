@@ -61,7 +61,8 @@ def codes_of(t32: torch.Tensor):
     top = np.max(np.abs(t), axis=1)
     scale = np.where(top < np.float32(2.0 ** -100), np.float32(2.0 ** 100), np.float32(1))
     with np.errstate(divide="ignore", invalid="ignore", over="ignore"):
-        inv = np.where(top > 0, np.float32(127) / (top * scale), np.float32(0)).astype(np.float32)
+        inv = np.where(top > 0, np.float32(127) * (np.float32(1) / (top * scale)),
+                       np.float32(0)).astype(np.float32)
         q = np.rint(((t * scale[:, None]).astype(np.float32) * inv[:, None]).astype(np.float32))
     bad = ~np.isfinite(top)
     q[bad] = 0
@@ -127,7 +128,7 @@ def test_quantized_rows_match_their_formula(fn, width, t):
 @pytest.mark.parametrize("width", [5, 768, 1500, 4096, 33000])
 def test_rows_without_a_norm_and_empty_rows(fn, width, t):
     """Rows of zeros, NaN, infinities, the type's lowest value throughout,
-    squares that overflow, numbers too small for 127 / A, exact ties."""
+    squares that overflow, numbers too small for 1 / A, ties and near-ties."""
     n = 12
     x = rows(7, n, width, t, spread=0.0)
     fin = torch.finfo(t)
@@ -142,8 +143,8 @@ def test_rows_without_a_norm_and_empty_rows(fn, width, t):
     x[8] = 0
     x[8, 0] = 1.0
     x[9] = 254.0
-    x[9, : width // 2] = 1.0  # 1 * 127 / 254: a tie, to even
-    x[9, width // 2:width - 1] = -3.0  # -1.5: a tie
+    x[9, : width // 2] = 1.0  # 127 / 254: a half
+    x[9, width // 2:width - 1] = -3.0  # -1.5
     w = torch.ones(width, dtype=t, device="cuda")
     codes, scales = fn.quantize_rows(x)
     want, top = codes_of(x.float())
@@ -263,7 +264,7 @@ def test_many_rows(fn):
         x, w = torch.randn(n, width, device="cuda").to(t), weights(3, width, t)
         codes, scales = fn.quantize_rows(x)
         top = x.float().abs().amax(1)
-        inv = (127.0 / top.double()).float()
+        inv = 127.0 * (1.0 / top.double()).float()
         assert torch.equal(codes, torch.round(x.float() * inv[:, None]).to(torch.int8))
         out, rstd, _ = fn.rms_norm(x, w, EPS)
         want = 1 / torch.sqrt(x.double().square().mean(1) + EPS)

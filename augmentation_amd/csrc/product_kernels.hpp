@@ -15,6 +15,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "row_kernels.hpp"
 
@@ -23,6 +24,18 @@ namespace fn {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// Two numbers rounded to a 16-bit type, in one register.
+template <typename T>
+__device__ __forceinline__ uint32_t two_halves(float lo, float hi) {
+  if constexpr (std::is_same_v<T, BF16>)
+    return float_to_bf16(lo) | float_to_bf16(hi) << 16;
+  else
+    return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)lo) |
+           (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)hi) << 16;
+}
 
 struct ProductArgs {
   const int8_t* a;
@@ -37,6 +50,15 @@ struct ProductArgs {
   int32_t K;
   uint32_t tiles_m, tiles_n;
 };
+
+// f(0), f(1), ... f(kCount - 1), each with its number as a constant.
+template <int kCount, int kFirst = 0, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (kFirst < kCount) {
+    f(std::integral_constant<int, kFirst>{});
+    static_for<kCount, kFirst + 1>(f);
+  }
+}
 
 // Waits until at most kLeft of this wavefront's loads are under way.
 template <int kLeft>
@@ -108,7 +130,7 @@ __device__ __forceinline__ void store_outputs(const int (&acc)[kE], float sa, co
 // channel.  kPitch: 32-bit words from one token's row in LDS to the next; the
 // four words beyond the row keep a quad's 16-byte writes off the same banks.
 template <typename T, int kTn>
-__device__ __forceinline__ void store_strip(const ProductArgs& p, const i32x16 (&acc)[kTn],
+__device__ __forceinline__ void store_strip(const ProductArgs& p, const i32x16* acc,
                                             int* lds, int64_t m0, int64_t n0) {
   constexpr int kN = 32 * kTn, kPitch = kN + 4;
   constexpr int kE = 16 / (int)sizeof(T);  // outputs per 16-byte store
@@ -251,27 +273,125 @@ __device__ __forceinline__ i32x4 tile_resource(const int8_t* p, int64_t stride,
 
 constexpr int kOutside = 0x7FFFFFF8;  // an offset that lies beyond every tile
 
-// Position of a 16-byte piece in a staged row of kBK codes: piece c of row r
-// lies at c ^ (a hash of r), so that lanes that read the same piece of
-// neighbouring rows at once spread over all banks.
-template <int kBK>
+// Codes of a stage are rows of 128 (eight 16-byte pieces, one cache line, so a
+// load of 64 lanes touches eight whole lines; rows of 64 codes took twice the
+// time per byte).  Piece c of row r lies at position c ^ (r / 2 mod 8): the
+// sixteen rows of which lanes read the same piece at once spread over all
+// banks (measured: no conflicts; c ^ (r mod 8) had one conflict per read).
+constexpr int kBK = 128;
+
 __device__ __forceinline__ int staged_piece(int row, int piece) {
-  return kBK == 64 ? piece ^ piece_swizzle(row) : piece ^ (row & 7);
+  return piece ^ ((row >> 1) & 7);
 }
 
+// Rows of out from a wavefront's sums.  acc[i][j]: tile of 16 tokens x 16
+// channels; lane l holds channels 4 (l / 16) .. + 3 of token l % 16.  Scaled
+// and rounded where they are, 64 tokens at a time go through the wavefront's
+// own piece of LDS (rows of kPitch bytes; the 16 bytes beyond a row's
+// channels keep rows off the same banks) and leave as 16-byte stores along
+// rows.
+template <typename T, int kTM, int kTN>
+struct OutputTile {
+  static constexpr int kTokens = kTM < 4 ? 16 * kTM : 64;  // tokens that leave together
+  static constexpr int kPitch = 16 * kTN * (int)sizeof(T) + 16;
+  static constexpr int kBytes = kTokens * kPitch;
+  float sa[kTM], sb[kTN][4], bias[kTN][4];
+
+  // m0, n0: the wavefront's first token and channel
+  __device__ __forceinline__ void load_scales(const ProductArgs& p, int64_t m0, int64_t n0) {
+    const int lane = (int)(threadIdx.x & 63u);
+#pragma unroll
+    for (int i = 0; i < kTM; ++i) {
+      const int64_t m = m0 + 16 * i + (lane & 15);
+      sa[i] = m < p.M ? p.sa[m] : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < kTN; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int64_t n = n0 + 16 * j + 4 * (lane >> 4) + c;
+        sb[j][c] = n < p.N ? p.sb[n] : 0.0f;
+        bias[j][c] = n < p.N && p.bias != nullptr ? p.bias[n] : 0.0f;
+      }
+  }
+
+  __device__ __forceinline__ void store(const ProductArgs& p, const i32x4 (&acc)[kTM][kTN],
+                                        int8_t* lds, int64_t m0, int64_t n0) const {
+    constexpr int kE = 16 / (int)sizeof(T);    // outputs per 16-byte store
+    constexpr int kLanes = 16 * kTN / kE;      // lanes along a row
+    constexpr int kRowsAtOnce = 64 / kLanes;
+    constexpr int kTiles = kTokens / 16;
+    const int lane = (int)(threadIdx.x & 63u);
+    const int64_t n = n0 + kE * (lane % kLanes);
+    const int left = (int)min(p.N - n, (int64_t)kE);
+#pragma unroll
+    for (int i0 = 0; i0 < kTM; i0 += kTiles) {
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int j = 0; j < kTN; ++j) {
+          float v[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            v[c] = (float)acc[i0 + i][j][c] * sa[i0 + i] * sb[j][c] + bias[j][c];
+          int8_t* at = lds + (16 * i + (lane & 15)) * kPitch +
+                       (16 * j + 4 * (lane >> 4)) * (int)sizeof(T);
+          if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<f32x4*>(at) = f32x4{v[0], v[1], v[2], v[3]};
+          else
+            *reinterpret_cast<u32x2*>(at) =
+                u32x2{two_halves<T>(v[0], v[1]), two_halves<T>(v[2], v[3])};
+        }
+      // one wavefront's LDS operations take effect in their order
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+#pragma unroll
+      for (int i = 0; i < kTokens / kRowsAtOnce; ++i) {
+        const int r = i * kRowsAtOnce + lane / kLanes;
+        const int64_t m = m0 + 16 * i0 + r;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(lds + r * kPitch + 16 * (lane % kLanes));
+        T* to = (T*)p.out + m * p.out_stride + n;
+        if (m < p.M && left == kE) {
+          *reinterpret_cast<u32x4_any*>(to) = v;
+        } else if (m < p.M && left > 0) {
+          store_part(v, to, left);
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    }
+  }
+
+  static __device__ __forceinline__ void store_part(u32x4 v, T* to, int left) {
+#pragma unroll
+    for (int c = 0; c < 16 / (int)sizeof(T); ++c)
+      if (c < left) {
+        if constexpr (sizeof(T) == 4)
+          reinterpret_cast<uint32_t*>(to)[c] = v[c];
+        else
+          reinterpret_cast<uint16_t*>(to)[c] = (uint16_t)(v[c >> 1] >> (16 * (c & 1)));
+      }
+  }
+};
+
 // One tile of kBM tokens x kBN channels per work-group of kWM x kWN
-// wavefronts, each with kTM x kTN tiles of the 32x32x32 instruction.
-template <typename T, int kBM, int kBN, int kWM, int kWN, int kBK, int kStages, int kPerSimd>
+// wavefronts, each with kTM x kTN tiles of the 16x16x64 instruction (measured
+// against 32x32x32 on 8192^3: 2.54 against 2.42 POP/s; the smaller one moves
+// fewer accumulator registers per operation, and the power limit, not the
+// count of cycles, is what such a product meets first).
+//
+// A wavefront's products of one step (64 codes of K) are its time for
+// everything else: between them it reads the next step's fragments from LDS
+// and, in a stage's last step, issues its share of a later stage's loads.
+template <typename T, int kBM, int kBN, int kWM, int kWN, int kStages, int kPerSimd>
 __global__ __launch_bounds__(64 * kWM * kWN, kPerSimd) void product_tile_kernel(ProductArgs p) {
-  constexpr int kWaves = kWM * kWN, kTM = kBM / kWM / 32, kTN = kBN / kWN / 32;
+  constexpr int kWaves = kWM * kWN, kTM = kBM / kWM / 16, kTN = kBN / kWN / 16;
   constexpr int kStageBytes = (kBM + kBN) * kBK;
-  constexpr int kPieces = kBK / 16;                    // 16-byte pieces of a staged row
-  constexpr int kRowsAtOnce = 64 / kPieces;            // rows that one load of a wavefront covers
-  constexpr int kLoadsA = kBM / kRowsAtOnce / kWaves;  // loads of a wavefront per stage
-  constexpr int kLoadsB = kBN / kRowsAtOnce / kWaves;
+  constexpr int kLoadsA = kBM / 8 / kWaves, kLoadsB = kBN / 8 / kWaves;  // per wavefront and stage
   constexpr int kLoads = kLoadsA + kLoadsB;
-  constexpr int kSteps = kBK / 32;
-  __shared__ __align__(1024) int8_t s_stages[kStages * kStageBytes];
+  constexpr int kSteps = kBK / 64;
+  using Out = OutputTile<T, kTM, kTN>;
+  constexpr int kLds =
+      kStages * kStageBytes > kWaves * Out::kBytes ? kStages * kStageBytes : kWaves * Out::kBytes;
+  __shared__ __align__(1024) int8_t s_stages[kLds];
   const int lane = (int)(threadIdx.x & 63u);
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
 
@@ -281,99 +401,113 @@ __global__ __launch_bounds__(64 * kWM * kWN, kPerSimd) void product_tile_kernel(
       tile_resource(p.a + m0 * p.a_stride, p.a_stride, min(p.M - m0, (int64_t)kBM), p.K);
   const i32x4 src_b =
       tile_resource(p.b + n0 * p.b_stride, p.b_stride, min(p.N - n0, (int64_t)kBN), p.K);
-  // this lane's row and (swizzled) piece in each of the wavefront's loads
+  // load i of a wavefront brings eight rows; every other one has this lane's
+  // piece at the same place
+  static_assert(kLoadsA % 2 == 0 && kLoadsB % 2 == 0, "rows per wavefront: a multiple of 16");
+  const int sub = lane / 8;
+  const int piece[2] = {staged_piece(sub, lane % 8), staged_piece(8 + sub, lane % 8)};
   int off_a[kLoadsA], off_b[kLoadsB];
-  const int sub = lane / kPieces;
-  const int piece = staged_piece<kBK>(sub, lane % kPieces);
 #pragma unroll
   for (int i = 0; i < kLoadsA; ++i) {
-    const int r = (wave * kLoadsA + i) * kRowsAtOnce + sub;
-    off_a[i] = m0 + r < p.M ? r * (int)p.a_stride + 16 * piece : kOutside;
+    const int r = (wave * kLoadsA + i) * 8 + sub;
+    off_a[i] = m0 + r < p.M ? r * (int)p.a_stride + 16 * piece[i & 1] : kOutside;
   }
 #pragma unroll
   for (int i = 0; i < kLoadsB; ++i) {
-    const int r = (wave * kLoadsB + i) * kRowsAtOnce + sub;
-    off_b[i] = n0 + r < p.N ? r * (int)p.b_stride + 16 * piece : kOutside;
+    const int r = (wave * kLoadsB + i) * 8 + sub;
+    off_b[i] = n0 + r < p.N ? r * (int)p.b_stride + 16 * piece[i & 1] : kOutside;
   }
   const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)s_stages;
-  auto issue = [&](int stage, int k0) {
-    const bool inside = k0 + 16 * piece < p.K;  // K is whole pieces
-    const uint32_t to = lds + stage * kStageBytes + wave * (kLoadsA * 1024);
-#pragma unroll
-    for (int i = 0; i < kLoadsA; ++i)
-      load_to_lds(src_a, to + i * 1024, inside ? off_a[i] : kOutside, k0);
-    const uint32_t to_b = lds + stage * kStageBytes + kBM * kBK + wave * (kLoadsB * 1024);
-#pragma unroll
-    for (int i = 0; i < kLoadsB; ++i)
-      load_to_lds(src_b, to_b + i * 1024, inside ? off_b[i] : kOutside, k0);
+  // load i of the stage that begins at code k0; pieces from K on (K is whole
+  // pieces) bring zeros
+  auto issue = [&](int stage, int k0, int i, const bool (&inside)[2]) {
+    const uint32_t to = lds + stage * kStageBytes;
+    if (i < kLoadsA)
+      load_to_lds(src_a, to + (wave * kLoadsA + i) * 1024, inside[i & 1] ? off_a[i] : kOutside, k0);
+    else
+      load_to_lds(src_b, to + kBM * kBK + (wave * kLoadsB + i - kLoadsA) * 1024,
+                  inside[i & 1] ? off_b[i - kLoadsA] : kOutside, k0);
   };
-  // fragments: lane l holds row l % 32, codes 16 (l / 32) .. + 15 of a step
-  const int frow = lane & 31, fhalf = lane >> 5;
-  const int at_a = ((wave / kWN) * kTM * 32 + frow) * kBK;
-  const int at_b = kBM * kBK + ((wave % kWN) * kTN * 32 + frow) * kBK;
+
+  // fragments: lane l holds codes 16 (l / 16) .. + 15 of row l % 16
+  const int at_a = ((wave / kWN) * kTM * 16 + (lane & 15)) * kBK;
+  const int at_b = kBM * kBK + ((wave % kWN) * kTN * 16 + (lane & 15)) * kBK;
   int at_piece[kSteps];
 #pragma unroll
-  for (int k = 0; k < kSteps; ++k) at_piece[k] = 16 * staged_piece<kBK>(frow, 2 * k + fhalf);
+  for (int k = 0; k < kSteps; ++k) at_piece[k] = 16 * staged_piece(lane & 15, 4 * k + (lane >> 4));
   i32x4 fa[2][kTM], fb[2][kTN];
-  auto fetch = [&](const int8_t* buf, int k, int slot) {
-#pragma unroll
-    for (int t = 0; t < kTM; ++t)
-      fa[slot][t] = *reinterpret_cast<const i32x4*>(buf + at_a + t * 32 * kBK + at_piece[k]);
-#pragma unroll
-    for (int t = 0; t < kTN; ++t)
-      fb[slot][t] = *reinterpret_cast<const i32x4*>(buf + at_b + t * 32 * kBK + at_piece[k]);
+  auto fetch = [&](const int8_t* buf, int k, int slot, int i) {
+    if (i < kTN)
+      fb[slot][i] = *reinterpret_cast<const i32x4*>(buf + at_b + i * 16 * kBK + at_piece[k]);
+    else
+      fa[slot][i - kTN] =
+          *reinterpret_cast<const i32x4*>(buf + at_a + (i - kTN) * 16 * kBK + at_piece[k]);
   };
-  i32x16 acc[kTM][kTN] = {};
-  auto multiply = [&](int slot, int from, int to) {
-    // keeps the fetches above in front: they hide behind these products
-    __builtin_amdgcn_sched_barrier(0);
+  i32x4 acc[kTM][kTN] = {};
+
 #pragma unroll
-    for (int i = from; i < to; ++i)
+  for (int s = 0; s < kStages; ++s) {
+    const bool inside[2] = {s * kBK + 16 * piece[0] < p.K, s * kBK + 16 * piece[1] < p.K};
 #pragma unroll
-      for (int j = 0; j < kTN; ++j)
-        acc[i][j] =
-            __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[slot][j], fa[slot][i], acc[i][j], 0, 0, 0);
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  const int iterations = (p.K + kBK - 1) / kBK;
-#pragma unroll
-  for (int s = 0; s < kStages; ++s) issue(s, s * kBK);
+    for (int i = 0; i < kLoads; ++i) issue(s, s * kBK, i, inside);
+  }
   wait_loads<(kStages - 1) * kLoads>();
   __builtin_amdgcn_s_barrier();
-  fetch(s_stages, 0, 0);
-  int stage = 0;
-  for (int it = 0; it < iterations; ++it) {
-    const int next = stage + 1 == kStages ? 0 : stage + 1;
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      if (k + 1 < kSteps) {
-        fetch(s_stages + stage * kStageBytes, k + 1, (k + 1) & 1);
-        multiply(k & 1, 0, kTM);
-      } else {
-        multiply(k & 1, 0, kTM / 2);
-        // everyone's reads of this stage are done and everyone's loads of the
-        // next have landed: this buffer is free for the stage after the last
+  for (int i = 0; i < kTM + kTN; ++i) fetch(s_stages, 0, 0, i);
+  int stage = 0;
+  for (int k0 = 0; k0 < p.K; k0 += kBK) {
+    const int next = stage + 1 == kStages ? 0 : stage + 1;
+    static_for<kSteps>([&](auto step) {
+      constexpr int k = decltype(step)::value;
+      constexpr bool kLast = k + 1 == kSteps;
+      constexpr int kProducts = kTM * kTN, kReads = kTM + kTN, kNewLoads = kLast ? kLoads : 0;
+      constexpr int kOthers = kReads + kNewLoads;
+      const int8_t* from = s_stages + (kLast ? next : stage) * kStageBytes;
+      const int k_new = k0 + kStages * kBK;
+      bool inside[2] = {};
+      if constexpr (kLast) {
+        // this wavefront's loads of the next stage have landed and its reads
+        // of this one are done; beyond the barrier, everyone's are: the next
+        // stage may be read, and this one's place be filled again
         wait_loads<(kStages - 2) * kLoads>();
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
-        issue(stage, (it + kStages) * kBK);
-        fetch(s_stages + next * kStageBytes, 0, (k + 1) & 1);
-        multiply(k & 1, kTM / 2, kTM);
+        inside[0] = k_new + 16 * piece[0] < p.K;
+        inside[1] = k_new + 16 * piece[1] < p.K;
       }
-    }
+      __builtin_amdgcn_sched_barrier(0);
+      static_for<kProducts>([&](auto product) {
+        constexpr int t = decltype(product)::value;
+        // the other operations, spread evenly over all products but two, the
+        // loads evenly among the reads
+        constexpr int kSpan = kProducts > 4 ? kProducts - 2 : kProducts;
+        constexpr int kFrom = (t * kOthers + kSpan - 1) / kSpan;
+        constexpr int kTo = ((t + 1) * kOthers + kSpan - 1) / kSpan;
+        constexpr int kEnd = kTo < kOthers ? kTo : kOthers;
+        static_for<(kFrom < kEnd ? kEnd - kFrom : 0)>([&](auto other) {
+          constexpr int o = kFrom + decltype(other)::value;
+          constexpr int kBefore = o * kNewLoads / kOthers;
+          if constexpr ((o + 1) * kNewLoads / kOthers > kBefore)
+            issue(stage, k_new, kBefore, inside);
+          else
+            fetch(from, kLast ? 0 : k + 1, (k + 1) & 1, o - kBefore);
+        });
+        __builtin_amdgcn_sched_barrier(0);
+        acc[t / kTN][t % kTN] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+            fb[k & 1][t % kTN], fa[k & 1][t / kTN], acc[t / kTN][t % kTN], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    });
     stage = next;
   }
-  // loads of stages beyond K (they bring zeros) end before the buffers are
-  // used again
+  const int64_t m_wave = m0 + (wave / kWN) * kTM * 16, n_wave = n0 + (wave % kWN) * kTN * 16;
+  Out out;
+  out.load_scales(p, m_wave, n_wave);
+  // loads of stages beyond K (they bring zeros) end before LDS is used again
   wait_loads<0>();
   __syncthreads();
-  constexpr int kStripBytes = 32 * (32 * kTN + 4) * 4;
-  static_assert(kStripBytes * kWaves <= kStages * kStageBytes, "strips fit");
-  int8_t* strip = s_stages + wave * kStripBytes;
-#pragma unroll
-  for (int i = 0; i < kTM; ++i)
-    store_strip<T, kTN>(p, acc[i], reinterpret_cast<int*>(strip),
-                        m0 + ((wave / kWN) * kTM + i) * 32, n0 + (wave % kWN) * kTN * 32);
+  out.store(p, acc, s_stages + wave * Out::kBytes, m_wave, n_wave);
 }
 
 }  // namespace fn

@@ -263,22 +263,37 @@ unsigned tile_grid(fn::ProductArgs* p) {
 }
 
 template <typename T>
-int launch_product(fn::ProductArgs p, hipStream_t st) {
+int launch_product(fn::ProductArgs p, int cus, hipStream_t st) {
   // whole 16-byte pieces from 16-byte aligned rows, a tile's rows within the
   // 31-bit offsets of its buffer resource
   const bool pieces = ((uintptr_t)p.a | (uintptr_t)p.b | (uint64_t)p.a_stride |
                        (uint64_t)p.b_stride | (uint64_t)p.K) % 16 == 0 &&
                       std::max(p.a_stride, p.b_stride) <= (0x7FFFFFF0 - 131072) / 256;
   unsigned grid = 0;
-  if (pieces && p.M * (__int128)p.N >= (int64_t)256 * 256 * 200) {
-    grid = tile_grid<256, 256>(&p);
-    if (grid) fn::product_tile_kernel<T, 256, 256, 2, 2, 64, 4, 1><<<grid, 256, 0, st>>>(p);
-  } else if (pieces) {
-    grid = tile_grid<128, 128>(&p);
-    if (grid) fn::product_tile_kernel<T, 128, 128, 2, 2, 64, 4, 2><<<grid, 256, 0, st>>>(p);
-  } else {
+  // The largest tile of which there are enough for every compute unit to have
+  // two at a time, and otherwise smaller ones: large tiles move fewer bytes
+  // per product, small ones fill the device.  Measured in us, 256x256 /
+  // 128x128 / 128x64 / 64x64: 8192^3 395 / 483 / 611 / 783; 50176x1024x768
+  // 61 / 60 / 62 / 97; 2048^3 25 / 13.2 / 13.2 / 16; 512x4096x4096
+  // 40 / 22 / 13.8 / 15.8; 1999x1000x1024 16 / 8.8 / 7.3 / 7.4.
+  auto tiles = [&](int64_t bm, int64_t bn) {
+    return (__int128)((p.M + bm - 1) / bm) * ((p.N + bn - 1) / bn);
+  };
+  if (!pieces) {
     grid = tile_grid<128, 128>(&p);
     if (grid) fn::product_any_kernel<T><<<grid, 256, 0, st>>>(p);
+  } else if (tiles(256, 256) >= 2 * cus) {
+    grid = tile_grid<256, 256>(&p);
+    if (grid) fn::product_tile_kernel<T, 256, 256, 2, 4, 2, 2><<<grid, 512, 0, st>>>(p);
+  } else if (tiles(128, 128) >= 2 * cus) {
+    grid = tile_grid<128, 128>(&p);
+    if (grid) fn::product_tile_kernel<T, 128, 128, 2, 2, 2, 2><<<grid, 256, 0, st>>>(p);
+  } else if (tiles(128, 64) >= cus) {
+    grid = tile_grid<128, 64>(&p);
+    if (grid) fn::product_tile_kernel<T, 128, 64, 2, 2, 3, 2><<<grid, 256, 0, st>>>(p);
+  } else {
+    grid = tile_grid<64, 64>(&p);
+    if (grid) fn::product_tile_kernel<T, 64, 64, 2, 2, 4, 2><<<grid, 256, 0, st>>>(p);
   }
   if (grid == 0) return fail(FN_EOVERFLOW, "grid size limit exceeded");
   return launch_status("product kernel launch");
@@ -430,7 +445,9 @@ FN_EXPORT int fn_matmul_q8(const int8_t* a_dev, int64_t a_stride, const float* a
   p.N = N;
   p.K = K;
   hipStream_t st = (hipStream_t)stream;
-  if (out_dtype == FN_OUT_FP32) return launch_product<float>(p, st);
-  if (out_dtype == FN_OUT_FP16) return launch_product<_Float16>(p, st);
-  return launch_product<fn::BF16>(p, st);
+  int cus = 0;
+  FN_TRY(device_cu_count(dev, &cus));
+  if (out_dtype == FN_OUT_FP32) return launch_product<float>(p, cus, st);
+  if (out_dtype == FN_OUT_FP16) return launch_product<_Float16>(p, cus, st);
+  return launch_product<fn::BF16>(p, cus, st);
 }

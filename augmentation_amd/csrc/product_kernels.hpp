@@ -22,7 +22,6 @@
 namespace fn {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -84,160 +83,31 @@ __device__ __forceinline__ TileAt tile_at(uint32_t block, const ProductArgs& p) 
   return {band * kGroup + in % height, in / height};
 }
 
-// Sixteen codes k0 .. k0 + 15 of a row, zeros from K on.
+// Sixteen codes k0 .. k0 + 15 of a row, zeros from K on.  Near the end of a
+// row the last sixteen are read and shifted down, so that every lane makes one
+// load and none reads beyond the row.
 __device__ __forceinline__ i32x4 load16(const int8_t* row, int32_t k0, int32_t K) {
-  i32x4 v = {0, 0, 0, 0};
-  if (k0 + 16 <= K) {
-    v = *reinterpret_cast<const i32x4_any*>(row + k0);
-  } else {
+  if (K < 16) {
+    i32x4 v = {0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < 16; ++j)
       if (k0 + j < K) v[j >> 2] |= (int)((uint32_t)(uint8_t)row[k0 + j] << (8 * (j & 3)));
+    return v;
   }
-  return v;
-}
-
-// kE consecutive outputs of one row from their integer sums.
-template <typename T, int kE>
-__device__ __forceinline__ void store_outputs(const int (&acc)[kE], float sa, const float (&sb)[kE],
-                                              const float (&bias)[kE], T* p, int n) {
-  float v[8];
-#pragma unroll
-  for (int j = 0; j < kE; ++j) v[j] = (float)acc[j] * sa * sb[j] + bias[j];
-  if constexpr (sizeof(T) == 4) {
-    if (n >= 4) {
-      u32x4_any q;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) q[j] = __builtin_bit_cast(uint32_t, v[j]);
-      *reinterpret_cast<u32x4_any*>(p) = q;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j < n) p[j] = v[j];
-    }
+  const int32_t k = min(k0, K - 16);
+  const i32x4 v = *reinterpret_cast<const i32x4_any*>(row + k);
+  const int32_t bits = 8 * min(k0 - k, 16);
+  if (bits == 0) return v;
+  uint64_t lo = (uint64_t)(uint32_t)v[1] << 32 | (uint32_t)v[0];
+  uint64_t hi = (uint64_t)(uint32_t)v[3] << 32 | (uint32_t)v[2];
+  if (bits >= 64) {
+    lo = bits == 128 ? 0 : hi >> (bits - 64);
+    hi = 0;
   } else {
-    Vec8<T> q;
-    q.set(v);
-    if (n >= 8)
-      q.store(p);
-    else
-      q.store_some(p, n);
+    lo = lo >> bits | hi << (64 - bits);
+    hi >>= bits;
   }
-}
-
-// A wavefront's kTn x 32 channels by 32 tokens of sums go through its own
-// piece of LDS and leave as rows of the output.  m0, n0: first token and
-// channel.  kPitch: 32-bit words from one token's row in LDS to the next; the
-// four words beyond the row keep a quad's 16-byte writes off the same banks.
-template <typename T, int kTn>
-__device__ __forceinline__ void store_strip(const ProductArgs& p, const i32x16* acc,
-                                            int* lds, int64_t m0, int64_t n0) {
-  constexpr int kN = 32 * kTn, kPitch = kN + 4;
-  constexpr int kE = 16 / (int)sizeof(T);  // outputs per 16-byte store
-  constexpr int kLanes = kN / kE;          // lanes along a row
-  constexpr int kRowsAtOnce = 64 / kLanes;
-  const int lane = (int)(threadIdx.x & 63u);
-#pragma unroll
-  for (int t = 0; t < kTn; ++t)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const i32x4 v = {acc[t][4 * q], acc[t][4 * q + 1], acc[t][4 * q + 2], acc[t][4 * q + 3]};
-      *reinterpret_cast<i32x4*>(lds + (lane & 31) * kPitch + 32 * t + 8 * q + 4 * (lane >> 5)) = v;
-    }
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  const int64_t n = n0 + kE * (lane % kLanes);
-  const int left = (int)min(p.N - n, (int64_t)kE);
-  if (left > 0) {
-    float sb[kE], bias[kE];
-#pragma unroll
-    for (int j = 0; j < kE; ++j) {
-      sb[j] = j < left ? p.sb[n + j] : 0.0f;
-      bias[j] = j < left && p.bias != nullptr ? p.bias[n + j] : 0.0f;
-    }
-#pragma unroll
-    for (int i = 0; i < 32 / kRowsAtOnce; ++i) {
-      const int r = i * kRowsAtOnce + lane / kLanes;
-      const int64_t m = m0 + r;
-      if (m >= p.M) continue;
-      int v[kE];
-#pragma unroll
-      for (int j = 0; j < kE; j += 4) {
-        const i32x4 u = *reinterpret_cast<const i32x4*>(lds + r * kPitch + kE * (lane % kLanes) + j);
-        v[j] = u[0];
-        v[j + 1] = u[1];
-        v[j + 2] = u[2];
-        v[j + 3] = u[3];
-      }
-      store_outputs<T, kE>(v, p.sa[m], sb, bias, (T*)p.out + m * p.out_stride + n, left);
-    }
-  }
-}
-
-// Tiles of 128 tokens x 128 channels through registers: rows may start at any
-// byte and K may be anything.  Four wavefronts, each 64 x 64 as 2 x 2 tiles
-// of the 32x32x32 instruction; 64 codes of K at a time, the next 64 loaded
-// while the matrix cores work on these.
-//
-// In LDS a row of 64 codes is four 16-byte pieces; piece c of row r lies at
-// position c ^ swizzle(r), which spreads the sixteen lanes that read together
-// over all banks.
-__device__ __forceinline__ int piece_swizzle(int row) {
-  return ((row >> 2) & 1) << 1 | (((row >> 1) ^ (row >> 3)) & 1);
-}
-
-template <typename T>
-__global__ __launch_bounds__(256) void product_any_kernel(ProductArgs p) {
-  __shared__ __align__(16) int8_t s_tile[2 * 128 * 64 > 4 * 32 * 68 * 4 ? 2 * 128 * 64
-                                                                       : 4 * 32 * 68 * 4];
-  int8_t* s_a = s_tile;
-  int8_t* s_b = s_tile + 128 * 64;
-  const int lane = (int)(threadIdx.x & 63u), wave = (int)(threadIdx.x >> 6);
-  const TileAt tile = tile_at(blockIdx.x, p);
-  const int64_t m0 = (int64_t)tile.m * 128, n0 = (int64_t)tile.n * 128;
-  const int row = (int)(threadIdx.x >> 2), piece = (int)(threadIdx.x & 3u);
-  i32x4 ra[2], rb[2];
-  auto load = [&](int32_t k0) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t m = m0 + row + 64 * i, n = n0 + row + 64 * i;
-      ra[i] = m < p.M ? load16(p.a + m * p.a_stride, k0 + 16 * piece, p.K) : i32x4{0, 0, 0, 0};
-      rb[i] = n < p.N ? load16(p.b + n * p.b_stride, k0 + 16 * piece, p.K) : i32x4{0, 0, 0, 0};
-    }
-  };
-  i32x16 acc[2][2] = {};  // [token tile][channel tile]
-  load(0);
-  for (int32_t k0 = 0; k0 < p.K; k0 += 64) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = row + 64 * i, at = r * 64 + 16 * (piece ^ piece_swizzle(r));
-      *reinterpret_cast<i32x4*>(s_a + at) = ra[i];
-      *reinterpret_cast<i32x4*>(s_b + at) = rb[i];
-    }
-    __syncthreads();
-    if (k0 + 64 < p.K) load(k0 + 64);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      i32x4 fa[2], fb[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int r = 32 * t + (lane & 31);
-        const int at = 16 * ((2 * k + (lane >> 5)) ^ piece_swizzle(r));
-        fa[t] = *reinterpret_cast<const i32x4*>(s_a + (64 * (wave >> 1) + r) * 64 + at);
-        fb[t] = *reinterpret_cast<const i32x4*>(s_b + (64 * (wave & 1) + r) * 64 + at);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
-    }
-  }
-  __syncthreads();
-  int* strip = reinterpret_cast<int*>(s_tile) + wave * 32 * 68;
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    store_strip<T, 2>(p, acc[i], strip, m0 + 64 * (wave >> 1) + 32 * i, n0 + 64 * (wave & 1));
+  return i32x4{(int)(uint32_t)lo, (int)(lo >> 32), (int)(uint32_t)hi, (int)(hi >> 32)};
 }
 
 // ---------------------------------------------------------------------------
@@ -508,6 +378,267 @@ __global__ __launch_bounds__(64 * kWM * kWN, kPerSimd) void product_tile_kernel(
   wait_loads<0>();
   __syncthreads();
   out.store(p, acc, s_stages + wave * Out::kBytes, m_wave, n_wave);
+}
+
+// Tiles through registers: rows may start at any byte and K may be anything,
+// which direct loads to LDS cannot serve.  Two stages of 128 codes; the codes
+// of two more are on their way to registers meanwhile.  Work-groups of kWM x 2
+// wavefronts; the layout of a stage and of the fragments is
+// product_tile_kernel's.
+template <typename T, int kBM, int kBN, int kWM>
+__global__ __launch_bounds__(128 * kWM, 2) void product_any_kernel(ProductArgs p) {
+  constexpr int kThreads = 128 * kWM, kTM = kBM / kWM / 16, kTN = kBN / 32;
+  constexpr int kRows = kBM + kBN, kStageBytes = kRows * kBK;
+  constexpr int kLoads = kRows * 8 / kThreads;  // pieces per thread and stage
+  using Out = OutputTile<T, kTM, kTN>;
+  constexpr int kOutBytes = 2 * kWM * Out::kBytes;
+  __shared__ __align__(1024) int8_t s_stages[2 * kStageBytes > kOutBytes ? 2 * kStageBytes
+                                                                         : kOutBytes];
+  const int lane = (int)(threadIdx.x & 63u), wave = (int)(threadIdx.x >> 6);
+  const TileAt tile = tile_at(blockIdx.x, p);
+  const int64_t m0 = (int64_t)tile.m * kBM, n0 = (int64_t)tile.n * kBN;
+  // this thread's piece of every kThreads / 8-th row: the tokens' rows first,
+  // then the channels'
+  const int piece = (int)(threadIdx.x & 7u), row = (int)(threadIdx.x >> 3);
+  const int8_t* from[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int r = row + kThreads / 8 * i;
+    const int64_t m = m0 + r, n = n0 + r - kBM;
+    from[i] = r < kBM ? (m < p.M ? p.a + m * p.a_stride : nullptr)
+                      : (n < p.N ? p.b + n * p.b_stride : nullptr);
+  }
+  // the codes of the next two stages: memory takes longer than one stage's
+  // products
+  i32x4 held[2][kLoads];
+  auto load = [&](i32x4 (&to)[kLoads], int k0) {
+    if (k0 >= p.K) return;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      to[i] = from[i] != nullptr ? load16(from[i], k0 + 16 * piece, p.K) : i32x4{0, 0, 0, 0};
+  };
+  auto put = [&](const i32x4 (&codes)[kLoads], int stage) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int r = row + kThreads / 8 * i;
+      *reinterpret_cast<i32x4*>(s_stages + stage * kStageBytes + r * kBK +
+                                16 * staged_piece(r, piece)) = codes[i];
+    }
+  };
+  const int at_a = ((wave >> 1) * kTM * 16 + (lane & 15)) * kBK;
+  const int at_b = (kBM + (wave & 1) * kTN * 16 + (lane & 15)) * kBK;
+  i32x4 acc[kTM][kTN] = {};
+  auto multiply = [&](const int8_t* buf) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int at = 16 * staged_piece(lane & 15, 4 * k + (lane >> 4));
+      i32x4 fa[kTM], fb[kTN];
+#pragma unroll
+      for (int j = 0; j < kTN; ++j)
+        fb[j] = *reinterpret_cast<const i32x4*>(buf + at_b + j * 16 * kBK + at);
+#pragma unroll
+      for (int i = 0; i < kTM; ++i)
+        fa[i] = *reinterpret_cast<const i32x4*>(buf + at_a + i * 16 * kBK + at);
+#pragma unroll
+      for (int i = 0; i < kTM; ++i)
+#pragma unroll
+        for (int j = 0; j < kTN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
+    }
+  };
+  load(held[0], 0);
+  load(held[1], kBK);
+  for (int k0 = 0; k0 < p.K; k0 += 2 * kBK) {
+    // stage 0 was last read before the barrier of stage 1, and so on
+    put(held[0], 0);
+    __syncthreads();
+    load(held[0], k0 + 2 * kBK);
+    multiply(s_stages);
+    if (k0 + kBK >= p.K) break;
+    put(held[1], 1);
+    __syncthreads();
+    load(held[1], k0 + 3 * kBK);
+    multiply(s_stages + kStageBytes);
+  }
+  const int64_t m_wave = m0 + (wave >> 1) * kTM * 16, n_wave = n0 + (wave & 1) * kTN * 16;
+  Out out;
+  out.load_scales(p, m_wave, n_wave);
+  __syncthreads();
+  out.store(p, acc, s_stages + wave * Out::kBytes, m_wave, n_wave);
+}
+
+// The integer sums of kWaves wavefronts that divided K between them, joined in
+// LDS, and the outputs from them.
+template <typename T, int kMT, int kNT, int kWaves>
+__device__ __forceinline__ void join_waves(const ProductArgs& p, const i32x4 (&acc)[kMT][kNT],
+                                           int* s_sum, int64_t m0, int64_t n0) {
+  constexpr int kOutputs = kMT * kNT * 256;
+  const int lane = (int)(threadIdx.x & 63u), wave = (int)(threadIdx.x >> 6);
+#pragma unroll
+  for (int i = 0; i < kMT; ++i)
+#pragma unroll
+    for (int j = 0; j < kNT; ++j)
+      *reinterpret_cast<i32x4*>(&s_sum[wave * kOutputs + (i * kNT + j) * 256 + 4 * lane]) =
+          acc[i][j];
+  __syncthreads();
+  for (int o = (int)threadIdx.x; o < kOutputs; o += 64 * kWaves) {
+    const int channel = o % (16 * kNT), token = o / (16 * kNT);
+    const int64_t n = n0 + channel, m = m0 + token;
+    if (m >= p.M) break;
+    if (n >= p.N) continue;
+    const int at = ((token >> 4) * kNT + (channel >> 4)) * 256 +
+                   4 * ((channel >> 2 & 3) * 16 + (token & 15)) + (channel & 3);
+    int sum = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) sum += s_sum[w * kOutputs + at];
+    const float y = (float)sum * p.sa[m] * p.sb[n] + (p.bias != nullptr ? p.bias[n] : 0.0f);
+    if constexpr (sizeof(T) == 4)
+      ((float*)p.out)[m * p.out_stride + n] = y;
+    else
+      ((uint16_t*)p.out)[m * p.out_stride + n] = (uint16_t)two_halves<T>(y, 0.0f);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens, rows at multiples of 16 bytes: the time is that of reading b,
+// and what counts is how much of b is under way.  A work-group takes 16 kNT
+// channels (few, so that all compute units have some) and 16 kMT tokens; its
+// wavefronts divide K between them, wavefront w taking lines w, w + kWaves,
+// ... of 128 codes.  Each has a ring of kStages lines of its own in LDS and
+// waits for nobody until the sums are joined.
+template <typename T, int kMT, int kNT, int kStages, int kWaves>
+__global__ __launch_bounds__(64 * kWaves) void product_split_kernel(ProductArgs p) {
+  constexpr int kRows = 16 * (kMT + kNT), kLoads = kRows / 8;
+  constexpr int kRing = kStages * kRows * kBK;
+  constexpr int kSums = kMT * kNT * 1024;
+  __shared__ __align__(1024) int8_t s_ring[kWaves * (kRing > kSums ? kRing : kSums)];
+  const int lane = (int)(threadIdx.x & 63u);
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * kNT), m0 = (int64_t)blockIdx.y * (16 * kMT);
+  const i32x4 src_a =
+      tile_resource(p.a + m0 * p.a_stride, p.a_stride, min(p.M - m0, (int64_t)(16 * kMT)), p.K);
+  const i32x4 src_b =
+      tile_resource(p.b + n0 * p.b_stride, p.b_stride, min(p.N - n0, (int64_t)(16 * kNT)), p.K);
+  const int sub = lane / 8;
+  const int piece[2] = {staged_piece(sub, lane % 8), staged_piece(8 + sub, lane % 8)};
+  int off[kLoads];  // the channels' rows first, then the tokens'
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int r = 8 * i + sub, ra = r - 16 * kNT;
+    if (i < 2 * kNT)
+      off[i] = n0 + r < p.N ? r * (int)p.b_stride + 16 * piece[i & 1] : kOutside;
+    else
+      off[i] = m0 + ra < p.M ? ra * (int)p.a_stride + 16 * piece[i & 1] : kOutside;
+  }
+  int8_t* ring = s_ring + wave * kRing;
+  const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)ring;
+  auto issue = [&](int stage, int k0) {
+    const bool inside[2] = {k0 + 16 * piece[0] < p.K, k0 + 16 * piece[1] < p.K};
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      load_to_lds(i < 2 * kNT ? src_b : src_a, lds + stage * kRows * kBK + i * 1024,
+                  inside[i & 1] ? off[i] : kOutside, k0);
+  };
+  const int at[2] = {(lane & 15) * kBK + 16 * staged_piece(lane & 15, lane >> 4),
+                     (lane & 15) * kBK + 16 * staged_piece(lane & 15, 4 + (lane >> 4))};
+  i32x4 acc[kMT][kNT] = {};
+  constexpr int kStride = kWaves * kBK;  // codes from one line of a wavefront to its next
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) issue(s, wave * kBK + s * kStride);
+  int stage = 0;
+  for (int k0 = wave * kBK; k0 < p.K; k0 += kStride) {
+    wait_loads<(kStages - 1) * kLoads>();
+    const int8_t* from = ring + stage * kRows * kBK;
+    i32x4 fa[2][kMT], fb[2][kNT];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int j = 0; j < kNT; ++j)
+        fb[h][j] = *reinterpret_cast<const i32x4*>(from + 16 * j * kBK + at[h]);
+#pragma unroll
+      for (int i = 0; i < kMT; ++i)
+        fa[h][i] = *reinterpret_cast<const i32x4*>(from + 16 * (kNT + i) * kBK + at[h]);
+    }
+    // the line is in registers: its place may be filled again
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    issue(stage, k0 + kStages * kStride);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < kMT; ++i)
+#pragma unroll
+        for (int j = 0; j < kNT; ++j)
+          acc[i][j] =
+              __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[h][j], fa[h][i], acc[i][j], 0, 0, 0);
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+  }
+  wait_loads<0>();
+  __syncthreads();
+  join_waves<T, kMT, kNT, kWaves>(p, acc, reinterpret_cast<int*>(s_ring), m0, n0);
+}
+
+// Few tokens, rows that start at any byte, any K: product_split_kernel's
+// division of the work, with a line's codes read straight into the fragments'
+// registers (lane l: 16 codes of row l % 16), kLines lines of 128 at once.
+
+template <typename T, int kMT, int kNT, int kLines>
+__global__ __launch_bounds__(512) void product_few_kernel(ProductArgs p) {
+  constexpr int kWaves = 8, kTiles = kMT * kNT;
+  __shared__ __align__(16) int s_sum[kWaves * kTiles * 256];
+  const int lane = (int)(threadIdx.x & 63u);
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * kNT), m0 = (int64_t)blockIdx.y * (16 * kMT);
+  const int row = lane & 15, part = 16 * (lane >> 4);
+  const int8_t *pa[kMT], *pb[kNT];  // null: no such row
+#pragma unroll
+  for (int i = 0; i < kMT; ++i) {
+    const int64_t m = m0 + 16 * i + row;
+    pa[i] = m < p.M ? p.a + m * p.a_stride + part : nullptr;
+  }
+#pragma unroll
+  for (int j = 0; j < kNT; ++j) {
+    const int64_t n = n0 + 16 * j + row;
+    pb[j] = n < p.N ? p.b + n * p.b_stride + part : nullptr;
+  }
+  i32x4 acc[kMT][kNT] = {};
+  for (int k0 = wave * 128; k0 < p.K; k0 += kWaves * kLines * 128) {
+    i32x4 fa[kLines][2][kMT], fb[kLines][2][kNT];
+    // the same lines with and without a look at where K ends
+    auto load = [&](auto whole) {
+#pragma unroll
+      for (int l = 0; l < kLines; ++l)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k = k0 + l * (kWaves * 128) + 64 * h;
+          auto get = [&](const int8_t* row_at) {
+            if (row_at == nullptr) return i32x4{0, 0, 0, 0};
+            if constexpr (decltype(whole)::value)
+              return i32x4(*reinterpret_cast<const i32x4_any*>(row_at + k));
+            else
+              return load16(row_at - part, k + part, p.K);
+          };
+#pragma unroll
+          for (int j = 0; j < kNT; ++j) fb[l][h][j] = get(pb[j]);
+#pragma unroll
+          for (int i = 0; i < kMT; ++i) fa[l][h][i] = get(pa[i]);
+        }
+    };
+    if (k0 + ((kLines - 1) * kWaves + 1) * 128 <= p.K)
+      load(std::true_type{});
+    else
+      load(std::false_type{});
+#pragma unroll
+    for (int l = 0; l < kLines; ++l)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < kMT; ++i)
+#pragma unroll
+          for (int j = 0; j < kNT; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[l][h][j], fa[l][h][i], acc[i][j],
+                                                              0, 0, 0);
+  }
+  join_waves<T, kMT, kNT, kWaves>(p, acc, s_sum, m0, n0);
 }
 
 }  // namespace fn

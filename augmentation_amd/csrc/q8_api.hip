@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "fn.h"
 #include "fn_host.hpp"
@@ -262,6 +263,66 @@ unsigned tile_grid(fn::ProductArgs* p) {
   return (unsigned)(tm * tn);
 }
 
+// The time of a product in tiles, in relative units: n tiles on the busiest of
+// `cus` compute units at `each`, or `alone` where none has a second.
+double tile_cost(int64_t M, int64_t N, int bm, int bn, int cus, double alone, double each) {
+  const double n = std::ceil((double)((M + bm - 1) / bm) * (double)((N + bn - 1) / bn) / cus);
+  return n <= 1.0 ? alone : n * each;
+}
+
+template <typename T, int kBM, int kBN, int kWM, int kWN, int kStages>
+bool launch_tiles(fn::ProductArgs& p, hipStream_t st) {
+  const unsigned grid = tile_grid<kBM, kBN>(&p);
+  if (grid)
+    fn::product_tile_kernel<T, kBM, kBN, kWM, kWN, kStages, 2><<<grid, 64 * kWM * kWN, 0, st>>>(p);
+  return grid != 0;
+}
+
+template <typename T, int kBM, int kBN>
+bool launch_any(fn::ProductArgs& p, hipStream_t st) {
+  const unsigned grid = tile_grid<kBM, kBN>(&p);
+  if (grid) fn::product_any_kernel<T, kBM, kBN, 4><<<grid, 512, 0, st>>>(p);
+  return grid != 0;
+}
+
+// Work-groups of 16 kNT channels x 16 kMT tokens; false if there are too many.
+template <int kMT, int kNT>
+bool split_grid(const fn::ProductArgs& p, dim3* grid) {
+  const int64_t x = (p.N + 16 * kNT - 1) / (16 * kNT), y = (p.M + 16 * kMT - 1) / (16 * kMT);
+  *grid = dim3((unsigned)x, (unsigned)y);
+  return x <= 0x7FFFFFFF && y <= 65535;
+}
+
+template <typename T, int kMT, int kNT>
+bool launch_split(const fn::ProductArgs& p, bool pieces, hipStream_t st) {
+  dim3 grid;
+  if (!split_grid<kMT, kNT>(p, &grid)) return false;
+  if (pieces)
+    fn::product_split_kernel<T, kMT, kNT, 2, 8><<<grid, 512, 0, st>>>(p);
+  else
+    fn::product_few_kernel<T, kMT, kNT, 2><<<grid, 512, 0, st>>>(p);
+  return true;
+}
+
+// Which kernel.  Times in us, measured on 256 compute units.
+//
+// Few tokens: K divided between a work-group's wavefronts, for up to 16
+// tokens (1x4096x4096 5.1 against 9.7 in 64x64 tiles, 8x8192x8192 13.2
+// against 16.2), in groups of 16 channels as long as these give a compute
+// unit at most two, else of 64 (16x16384x2048 6.4 against 8.7); and beyond 16
+// tokens while 32x32 groups are no more than the compute units (64x4096x4096
+// 7.7 against 9.7, 128x2048x8192 9.3 against 15.7; but with twice as many
+// 48x8192x4096 12.8 against 9.8, 128x4096x4096 12.9 against 9.8).
+//
+// Else tiles: large ones move fewer bytes per product, small ones fill the
+// device.  The costs are the times of K = 4096 for tiles of 256x256, 128x128,
+// 128x64 and 64x64 with one (alone) or more to a compute unit: 8192^3 395 /
+// 483 / 611 / 783; 4096^3 57 / 68 / 85 / 102; 4096x2048x4096 45 / 35 / 41 /
+// 53; 256x8192x4096 42 / 25 / 14.8 / 16.6; 1024x1024x8192 74 / 42 / 23 / 17.7.
+//
+// Rows that start anywhere, tiles of 256x128, 128x64 and 64x64: 4000x4000x4001
+// 110 / 160 / 197; 1999x1000x1021 18.5 / 11.0 / 11.7; 300x1024x777 16.5 / 8.8
+// / 7.1.
 template <typename T>
 int launch_product(fn::ProductArgs p, int cus, hipStream_t st) {
   // whole 16-byte pieces from 16-byte aligned rows, a tile's rows within the
@@ -269,33 +330,35 @@ int launch_product(fn::ProductArgs p, int cus, hipStream_t st) {
   const bool pieces = ((uintptr_t)p.a | (uintptr_t)p.b | (uint64_t)p.a_stride |
                        (uint64_t)p.b_stride | (uint64_t)p.K) % 16 == 0 &&
                       std::max(p.a_stride, p.b_stride) <= (0x7FFFFFF0 - 131072) / 256;
-  unsigned grid = 0;
-  // The largest tile of which there are enough for every compute unit to have
-  // two at a time, and otherwise smaller ones: large tiles move fewer bytes
-  // per product, small ones fill the device.  Measured in us, 256x256 /
-  // 128x128 / 128x64 / 64x64: 8192^3 395 / 483 / 611 / 783; 50176x1024x768
-  // 61 / 60 / 62 / 97; 2048^3 25 / 13.2 / 13.2 / 16; 512x4096x4096
-  // 40 / 22 / 13.8 / 15.8; 1999x1000x1024 16 / 8.8 / 7.3 / 7.4.
-  auto tiles = [&](int64_t bm, int64_t bn) {
-    return (__int128)((p.M + bm - 1) / bm) * ((p.N + bn - 1) / bn);
-  };
-  if (!pieces) {
-    grid = tile_grid<128, 128>(&p);
-    if (grid) fn::product_any_kernel<T><<<grid, 256, 0, st>>>(p);
-  } else if (tiles(256, 256) >= 2 * cus) {
-    grid = tile_grid<256, 256>(&p);
-    if (grid) fn::product_tile_kernel<T, 256, 256, 2, 4, 2, 2><<<grid, 512, 0, st>>>(p);
-  } else if (tiles(128, 128) >= 2 * cus) {
-    grid = tile_grid<128, 128>(&p);
-    if (grid) fn::product_tile_kernel<T, 128, 128, 2, 2, 2, 2><<<grid, 256, 0, st>>>(p);
-  } else if (tiles(128, 64) >= cus) {
-    grid = tile_grid<128, 64>(&p);
-    if (grid) fn::product_tile_kernel<T, 128, 64, 2, 2, 3, 2><<<grid, 256, 0, st>>>(p);
+  const int64_t groups = ((p.M + 31) / 32) * std::min((p.N + 31) / 32, (int64_t)1 << 32);
+  bool launched = false;
+  if (p.M <= 16) {
+    launched = !pieces || (p.N + 15) / 16 <= 2 * cus ? launch_split<T, 1, 1>(p, pieces, st)
+                                                     : launch_split<T, 1, 4>(p, pieces, st);
+  } else if (groups <= cus) {
+    launched = launch_split<T, 2, 2>(p, pieces, st);
+  } else if (pieces) {
+    const double c[4] = {tile_cost(p.M, p.N, 256, 256, cus, 57, 57),
+                         tile_cost(p.M, p.N, 128, 128, cus, 22.7, 17.3),
+                         tile_cost(p.M, p.N, 128, 64, cus, 14.8, 10.3),
+                         tile_cost(p.M, p.N, 64, 64, cus, 8.9, 6.5)};
+    switch (std::min_element(c, c + 4) - c) {
+      case 0: launched = launch_tiles<T, 256, 256, 2, 4, 2>(p, st); break;
+      case 1: launched = launch_tiles<T, 128, 128, 2, 2, 2>(p, st); break;
+      case 2: launched = launch_tiles<T, 128, 64, 2, 2, 3>(p, st); break;
+      default: launched = launch_tiles<T, 64, 64, 2, 2, 4>(p, st);
+    }
   } else {
-    grid = tile_grid<64, 64>(&p);
-    if (grid) fn::product_tile_kernel<T, 64, 64, 2, 2, 4, 2><<<grid, 256, 0, st>>>(p);
+    const double c[3] = {tile_cost(p.M, p.N, 256, 128, cus, 60, 55),
+                         tile_cost(p.M, p.N, 128, 64, cus, 30, 20),
+                         tile_cost(p.M, p.N, 64, 64, cus, 20, 12.3)};
+    switch (std::min_element(c, c + 3) - c) {
+      case 0: launched = launch_any<T, 256, 128>(p, st); break;
+      case 1: launched = launch_any<T, 128, 64>(p, st); break;
+      default: launched = launch_any<T, 64, 64>(p, st);
+    }
   }
-  if (grid == 0) return fail(FN_EOVERFLOW, "grid size limit exceeded");
+  if (!launched) return fail(FN_EOVERFLOW, "grid size limit exceeded");
   return launch_status("product kernel launch");
 }
 

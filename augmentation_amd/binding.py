@@ -108,7 +108,9 @@ def _addr(x) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle, without the 2.6 us that building a
+        # torch.cuda.Stream object for it takes
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -290,7 +292,7 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
     one common stride (any contiguous tensor, a slice of its last dimension,
     one row expanded to many) and whose last dimension is contiguous."""
     if t.is_contiguous():
-        return t.size(-1)
+        return t.shape[-1]
     shape, st = t.shape, t.stride()
     stride = None
     if shape[-1] <= 1 or st[-1] == 1:
@@ -313,7 +315,7 @@ def _like(t, shape, dtype, ref: torch.Tensor, name: str) -> torch.Tensor:
     """`t` if it has this shape, dtype and device; a new tensor if it is None."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=ref.device)
-    if t.dtype != dtype or t.shape != torch.Size(shape) or t.device != ref.device:
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != ref.get_device():
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {ref.device}")
     return t
 

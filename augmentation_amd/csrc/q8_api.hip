@@ -22,7 +22,6 @@ using namespace fnhost;
   } while (0)
 
 constexpr int32_t kMaxWidth = 1 << 30;
-constexpr int32_t kMaxInRegisters = 32768;  // widest row that a work-group keeps in registers
 
 int type_bytes(int32_t dtype) {
   return dtype == FN_OUT_FP32 ? 4 : dtype == FN_OUT_FP16 || dtype == FN_OUT_BF16 ? 2 : 0;
@@ -111,34 +110,57 @@ int check_size(int64_t rows, int32_t width) {
 
 // ------------------------------------------------------------- row kernels
 
-template <typename T, int kMode, int kThreads, int kChunks>
+// Threads per row and chunks of eight elements per thread, by the row's width:
+// the fewest threads that keep a row in registers with all of them at work, a
+// wavefront's part for as long as that will do (no barrier).  0 threads: rows
+// that do not fit.
+struct RowShape {
+  int32_t width;  // up to
+  int threads, chunks;
+};
+
+constexpr RowShape kRowShapes[] = {{7, 1, 0},     {8, 1, 1},      {64, 8, 1},     {128, 8, 2},
+                                   {256, 32, 1},  {512, 32, 2},   {768, 32, 3},   {1024, 64, 2},
+                                   {2048, 64, 4}, {4096, 256, 2}, {8192, 256, 4}, {16384, 1024, 2},
+                                   {32768, 1024, 4}};
+
+RowShape row_shape(int32_t width, int32_t widest) {
+  for (const RowShape& s : kRowShapes)
+    if (width <= s.width && s.width <= widest) return s;
+  return {0, 0, 0};
+}
+
+constexpr int shape_key(int threads, int chunks) { return threads * 8 + chunks; }
+
+template <typename T, int kMode, int kThreads, int kChunks, bool kShort = false>
 void launch_rows_k(const fn::RowArgs& a, hipStream_t st) {
-  constexpr int kBlock = kThreads < 256 ? 256 : kThreads;
-  const int64_t groups = (a.rows + kBlock / kThreads - 1) / (kBlock / kThreads);
-  fn::rows_kernel<T, kMode, kThreads, kChunks>
+  constexpr int kBlock = fn::rows_block<kThreads>(), kRows = kBlock / kThreads;
+  const int64_t groups = (a.rows + kRows - 1) / kRows;
+  fn::rows_kernel<T, kMode, kThreads, kChunks, kShort>
       <<<(unsigned)std::min<int64_t>(groups, 1 << 20), kBlock, 0, st>>>(a);
 }
 
 template <typename T, int kMode>
 void launch_rows(const fn::RowArgs& a, hipStream_t st) {
-  const int32_t w = a.width;
-  if (w <= 512)
-    launch_rows_k<T, kMode, 64, 1>(a, st);
-  else if (w <= 1024)
-    launch_rows_k<T, kMode, 64, 2>(a, st);
-  else if (w <= 2048)
-    launch_rows_k<T, kMode, 256, 1>(a, st);
-  else if (w <= 4096)
-    launch_rows_k<T, kMode, 256, 2>(a, st);
-  else if (w <= 8192)
-    launch_rows_k<T, kMode, 256, 4>(a, st);
-  else if (w <= 16384)
-    launch_rows_k<T, kMode, 1024, 2>(a, st);
-  else if (w <= kMaxInRegisters)
-    launch_rows_k<T, kMode, 1024, 4>(a, st);
-  else
-    fn::rows_wide_kernel<T, kMode>
-        <<<(unsigned)std::min<int64_t>(a.rows, 1 << 20), 1024, 0, st>>>(a);
+  const RowShape s = row_shape(a.width, 32768);
+  switch (shape_key(s.threads, s.chunks)) {
+    case shape_key(1, 0): return launch_rows_k<T, kMode, 1, 1, true>(a, st);
+    case shape_key(1, 1): return launch_rows_k<T, kMode, 1, 1>(a, st);
+    case shape_key(8, 1): return launch_rows_k<T, kMode, 8, 1>(a, st);
+    case shape_key(8, 2): return launch_rows_k<T, kMode, 8, 2>(a, st);
+    case shape_key(32, 1): return launch_rows_k<T, kMode, 32, 1>(a, st);
+    case shape_key(32, 2): return launch_rows_k<T, kMode, 32, 2>(a, st);
+    case shape_key(32, 3): return launch_rows_k<T, kMode, 32, 3>(a, st);
+    case shape_key(64, 2): return launch_rows_k<T, kMode, 64, 2>(a, st);
+    case shape_key(64, 4): return launch_rows_k<T, kMode, 64, 4>(a, st);
+    case shape_key(256, 2): return launch_rows_k<T, kMode, 256, 2>(a, st);
+    case shape_key(256, 4): return launch_rows_k<T, kMode, 256, 4>(a, st);
+    case shape_key(1024, 2): return launch_rows_k<T, kMode, 1024, 2>(a, st);
+    case shape_key(1024, 4): return launch_rows_k<T, kMode, 1024, 4>(a, st);
+    default:
+      fn::rows_wide_kernel<T, kMode>
+          <<<(unsigned)std::min<int64_t>(a.rows, 1 << 20), 1024, 0, st>>>(a);
+  }
 }
 
 template <int kMode>
@@ -205,7 +227,7 @@ int norm(const void* x, int64_t x_stride, const void* residual, int64_t residual
 // about sixteen wavefronts per compute unit of a 256-unit device.  A function
 // of the sizes alone, so that results do not depend on the device.
 struct BackwardPlan {
-  int threads, chunks;  // of rows_backward_kernel; 0: the two-step kernels
+  RowShape shape;
   int32_t partials;
   int64_t rows_per_slice;
   int64_t bytes;
@@ -213,18 +235,13 @@ struct BackwardPlan {
 
 BackwardPlan plan_backward(int64_t rows, int32_t width) {
   BackwardPlan p{};
-  const int32_t limits[][3] = {{512, 64, 1},   {1024, 64, 2},   {2048, 256, 1},  {4096, 256, 2},
-                               {8192, 256, 4}, {16384, 1024, 2}, {32768, 1024, 4}};
-  for (const auto& l : limits) {
-    if (width <= l[0]) {
-      p.threads = l[1];
-      p.chunks = l[2];
-      const int block = std::max(256, p.threads);
-      const int64_t groups = (rows + block / p.threads - 1) / (block / p.threads);
-      p.partials = (int32_t)std::min<int64_t>(groups, 4096 / (block / 64));
-      p.bytes = (int64_t)p.partials * width * 4;
-      return p;
-    }
+  p.shape = row_shape(width, 16384);
+  if (p.shape.threads > 0) {
+    const int block = std::max(256, p.shape.threads);
+    const int64_t at_once = block / p.shape.threads, groups = (rows + at_once - 1) / at_once;
+    p.partials = (int32_t)std::min<int64_t>(groups, 4096 / (block / 64));
+    p.bytes = (int64_t)p.partials * width * 4;
+    return p;
   }
   const int64_t slices = std::min<int64_t>(rows, 64);
   p.rows_per_slice = slices ? (rows + slices - 1) / slices : 0;
@@ -233,22 +250,33 @@ BackwardPlan plan_backward(int64_t rows, int32_t width) {
   return p;
 }
 
+template <typename T, int kThreads, int kChunks, bool kShort = false>
+void launch_backward_k(const fn::BackwardArgs& a, hipStream_t st) {
+  fn::rows_backward_kernel<T, kThreads, kChunks, kShort>
+      <<<(unsigned)a.partials, fn::rows_block<kThreads>(), 0, st>>>(a);
+}
+
 template <typename T>
-void launch_backward(const fn::BackwardArgs& a, const BackwardPlan& p, hipStream_t st) {
-  const unsigned grid = (unsigned)p.partials;
-  switch (p.threads * 8 + p.chunks) {
-    case 64 * 8 + 1: fn::rows_backward_kernel<T, 64, 1><<<grid, 256, 0, st>>>(a); break;
-    case 64 * 8 + 2: fn::rows_backward_kernel<T, 64, 2><<<grid, 256, 0, st>>>(a); break;
-    case 256 * 8 + 1: fn::rows_backward_kernel<T, 256, 1><<<grid, 256, 0, st>>>(a); break;
-    case 256 * 8 + 2: fn::rows_backward_kernel<T, 256, 2><<<grid, 256, 0, st>>>(a); break;
-    case 256 * 8 + 4: fn::rows_backward_kernel<T, 256, 4><<<grid, 256, 0, st>>>(a); break;
-    case 1024 * 8 + 2: fn::rows_backward_kernel<T, 1024, 2><<<grid, 1024, 0, st>>>(a); break;
-    case 1024 * 8 + 4: fn::rows_backward_kernel<T, 1024, 4><<<grid, 1024, 0, st>>>(a); break;
+void launch_backward(const fn::BackwardArgs& a, const RowShape& s, hipStream_t st) {
+  switch (shape_key(s.threads, s.chunks)) {
+    case shape_key(1, 0): return launch_backward_k<T, 1, 1, true>(a, st);
+    case shape_key(1, 1): return launch_backward_k<T, 1, 1>(a, st);
+    case shape_key(8, 1): return launch_backward_k<T, 8, 1>(a, st);
+    case shape_key(8, 2): return launch_backward_k<T, 8, 2>(a, st);
+    case shape_key(32, 1): return launch_backward_k<T, 32, 1>(a, st);
+    case shape_key(32, 2): return launch_backward_k<T, 32, 2>(a, st);
+    case shape_key(32, 3): return launch_backward_k<T, 32, 3>(a, st);
+    case shape_key(64, 2): return launch_backward_k<T, 64, 2>(a, st);
+    case shape_key(64, 4): return launch_backward_k<T, 64, 4>(a, st);
+    case shape_key(256, 2): return launch_backward_k<T, 256, 2>(a, st);
+    case shape_key(256, 4): return launch_backward_k<T, 256, 4>(a, st);
+    case shape_key(1024, 2): return launch_backward_k<T, 1024, 2>(a, st);
     default: {
       fn::rows_backward_mean_kernel<T>
           <<<(unsigned)std::min<int64_t>(a.rows, 1 << 20), 1024, 0, st>>>(a);
       const unsigned columns = blocks_for(((int64_t)a.width + 7) / 8, 256);
-      fn::rows_backward_columns_kernel<T><<<dim3(columns, grid), 256, 0, st>>>(a);
+      fn::rows_backward_columns_kernel<T>
+          <<<dim3(columns, (unsigned)a.partials), 256, 0, st>>>(a);
     }
   }
 }
@@ -461,11 +489,11 @@ FN_EXPORT int fn_rms_norm_backward(const void* dout_dev, int64_t dout_stride, co
   hipStream_t st = (hipStream_t)stream;
   if (rows > 0) {
     if (dtype == FN_OUT_FP32)
-      launch_backward<float>(a, plan, st);
+      launch_backward<float>(a, plan.shape, st);
     else if (dtype == FN_OUT_FP16)
-      launch_backward<_Float16>(a, plan, st);
+      launch_backward<_Float16>(a, plan.shape, st);
     else
-      launch_backward<fn::BF16>(a, plan, st);
+      launch_backward<fn::BF16>(a, plan.shape, st);
     FN_TRY(launch_status("rows_backward_kernel launch"));
   }
   // no rows: no partial sums, and a gradient of zero

@@ -80,6 +80,23 @@ struct Vec8<float> {
       b[j] = j + 4 < n ? __builtin_bit_cast(uint32_t, p[j + 4]) : 0u;
     }
   }
+  // element j becomes element j + n (n = 0..8), zeros from the top
+  __device__ __forceinline__ void drop(int n) {
+    const u32x4 none = {0, 0, 0, 0};
+    if (n & 8) a = b = none;
+    if (n & 4) {
+      a = b;
+      b = none;
+    }
+    if (n & 2) {
+      a = u32x4{a[2], a[3], b[0], b[1]};
+      b = u32x4{b[2], b[3], 0, 0};
+    }
+    if (n & 1) {
+      a = u32x4{a[1], a[2], a[3], b[0]};
+      b = u32x4{b[1], b[2], b[3], 0};
+    }
+  }
   __device__ __forceinline__ float get(int j) const {
     return __builtin_bit_cast(float, j < 4 ? a[j & 3] : b[j & 3]);
   }
@@ -118,6 +135,14 @@ struct Half8 {
       a[j] = lo | hi << 16;
     }
   }
+  __device__ __forceinline__ void drop(int n) {
+    if (n & 8) a = u32x4{0, 0, 0, 0};
+    if (n & 4) a = u32x4{a[2], a[3], 0, 0};
+    if (n & 2) a = u32x4{a[1], a[2], a[3], 0};
+    if (n & 1)
+      a = u32x4{a[0] >> 16 | a[1] << 16, a[1] >> 16 | a[2] << 16, a[2] >> 16 | a[3] << 16,
+                a[3] >> 16};
+  }
   __device__ __forceinline__ uint32_t bits(int j) const { return (a[j >> 1] >> (16 * (j & 1))) & 0xFFFFu; }
   __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<u32x4_any*>(p) = a; }
   __device__ __forceinline__ void store_some(T* p, int n) const {
@@ -155,68 +180,101 @@ struct Vec8<BF16> : Half8<BF16> {
   }
 };
 
-template <typename T>
-__device__ __forceinline__ void load_chunk(Vec8<T>& v, const T* row, int32_t c, int32_t width) {
-  if (8 * c + 8 <= width)
-    v.load(row + 8 * c);
-  else if (8 * c < width)
-    v.load_some(row + 8 * c, width - 8 * c);
+// Chunk c of a row: elements 8 c .. 8 c + 7, as far as there are any.  A chunk
+// that the row's end cuts is read as the last eight elements of the row, and
+// the ones before it are dropped afterwards: every lane makes the same load
+// with no branch around it, so that a wavefront's loads go out together.  (Where
+// an output replaces an input, another thread may already have stored over
+// those dropped elements; nothing depends on them.)
+struct Chunk {
+  int32_t at;    // first element read
+  int32_t skip;  // elements to drop: 0 for a whole chunk, 8 for none at all
+  int32_t left;  // elements from 8 c to the row's end (negative beyond it)
+};
+
+__device__ __forceinline__ Chunk chunk_at(int32_t c, int32_t width) {
+  const int32_t at = min(8 * c, max(width - 8, 0));
+  return {at, min(8 * c - at, 8), width - 8 * c};
+}
+
+// kShort: rows of fewer than eight elements (chunk 0 is all there is)
+template <bool kShort, typename T>
+__device__ __forceinline__ void load_chunk(Vec8<T>& v, const T* row, const Chunk& c) {
+  if constexpr (kShort)
+    v.load_some(row, c.left);
   else
-    v.zero();
+    v.load(row + c.at);
+}
+
+template <bool kShort, typename T>
+__device__ __forceinline__ void trim_chunk(Vec8<T>& v, const Chunk& c) {
+  if constexpr (!kShort) {
+    if (c.skip != 0) v.drop(c.skip);
+  }
 }
 
 template <typename T>
-__device__ __forceinline__ void store_chunk(const Vec8<T>& v, T* row, int32_t c, int32_t width) {
-  if (8 * c + 8 <= width)
-    v.store(row + 8 * c);
-  else if (8 * c < width)
-    v.store_some(row + 8 * c, width - 8 * c);
+__device__ __forceinline__ void store_chunk(const Vec8<T>& v, T* row, const Chunk& c) {
+  if (c.left >= 8)
+    v.store(row + c.at);
+  else if (c.left > 0)
+    v.store_some(row + c.at + c.skip, c.left);
 }
 
 // --------------------------------------------------------------- reductions
-// Sum (or unsigned maximum) over the 64 lanes of a wavefront, the same value
-// in every lane, without LDS: shifts inside rows of 16 lanes, then the row
-// broadcasts.  The order is fixed, so a result never changes from run to run.
+// Sum (or unsigned maximum) over aligned groups of kLanes lanes of a
+// wavefront, the same bits in each of them, without LDS: exchanges with the
+// neighbour, the neighbouring pair, the mirror image in 8 and 16 lanes, the
+// next 16 and the other 32.  The order is fixed, so a result never changes
+// from run to run.
 
-template <int kCtrl, int kRowMask>
-__device__ __forceinline__ uint32_t dpp_or_zero(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, kRowMask, 0xF, false);
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xF, 0xF, true);
 }
 
-template <int kCtrl, int kRowMask>
-__device__ __forceinline__ float add_dpp(float v) {
-  return v + __builtin_bit_cast(float, dpp_or_zero<kCtrl, kRowMask>(__builtin_bit_cast(uint32_t, v)));
+template <int kLanes, typename F>
+__device__ __forceinline__ uint32_t group_fold(uint32_t v, F fold) {
+  if constexpr (kLanes >= 8) {
+    v = fold(v, dpp<0xB1>(v));   // quad_perm 1 0 3 2
+    v = fold(v, dpp<0x4E>(v));   // quad_perm 2 3 0 1
+    v = fold(v, dpp<0x141>(v));  // row_half_mirror
+  }
+  if constexpr (kLanes >= 32) {
+    v = fold(v, dpp<0x140>(v));  // row_mirror
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = fold(r[0], r[1]);
+  }
+  if constexpr (kLanes >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = fold(r[0], r[1]);
+  }
+  return v;
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-  v = add_dpp<0x111, 0xF>(v);  // lane - 1
-  v = add_dpp<0x112, 0xF>(v);  // lane - 2
-  v = add_dpp<0x114, 0xF>(v);
-  v = add_dpp<0x118, 0xF>(v);  // lane 15 of each row of 16 holds the row's sum
-  v = add_dpp<0x142, 0xA>(v);  // row 0 -> 1, row 2 -> 3
-  v = add_dpp<0x143, 0xC>(v);  // rows 0, 1 -> 2, 3
-  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+template <int kLanes>
+__device__ __forceinline__ float group_sum(float v) {
+  return __builtin_bit_cast(
+      float, group_fold<kLanes>(__builtin_bit_cast(uint32_t, v), [](uint32_t x, uint32_t y) {
+        return __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y));
+      }));
 }
 
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-  v = max(v, dpp_or_zero<0x111, 0xF>(v));
-  v = max(v, dpp_or_zero<0x112, 0xF>(v));
-  v = max(v, dpp_or_zero<0x114, 0xF>(v));
-  v = max(v, dpp_or_zero<0x118, 0xF>(v));
-  v = max(v, dpp_or_zero<0x142, 0xA>(v));
-  v = max(v, dpp_or_zero<0x143, 0xC>(v));
-  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+template <int kLanes>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  return group_fold<kLanes>(v, [](uint32_t x, uint32_t y) { return max(x, y); });
 }
 
-// Over the wavefronts of a work-group that share a row.  `parity` alternates
-// between calls, so that one barrier per call is enough: a wavefront reaches
-// the next call's writes of the same half only after everyone has left this
-// call's reads, one barrier later.
-template <int kWaves>
-__device__ __forceinline__ void group_reduce(float& sum, uint32_t& top, int parity) {
-  sum = wave_sum(sum);
-  top = wave_max(top);
-  if constexpr (kWaves > 1) {
+// Over the kThreads threads of a row: part of a wavefront, or several.
+// `parity` alternates between calls, so that one barrier per call is enough: a
+// wavefront reaches the next call's writes of the same half only after
+// everyone has left this call's reads, one barrier later.
+template <int kThreads>
+__device__ __forceinline__ void row_reduce(float& sum, uint32_t& top, int parity) {
+  sum = group_sum<kThreads>(sum);
+  top = group_max<kThreads>(top);
+  if constexpr (kThreads > 64) {
+    constexpr int kWaves = kThreads / 64;
     __shared__ float s_sum[2][kWaves];
     __shared__ uint32_t s_top[2][kWaves];
     const int wave = (int)(threadIdx.x >> 6);
@@ -278,14 +336,13 @@ __device__ __forceinline__ u32x2_any eight_codes(const float (&t)[8], const RowQ
   return c;
 }
 
-__device__ __forceinline__ void store_codes(u32x2_any v, int8_t* row, int32_t c, int32_t width) {
-  const int n = width - 8 * c;
-  if (n >= 8) {
-    *reinterpret_cast<u32x2_any*>(row + 8 * c) = v;
+__device__ __forceinline__ void store_codes(u32x2_any v, int8_t* row, const Chunk& c) {
+  if (c.left >= 8) {
+    *reinterpret_cast<u32x2_any*>(row + c.at) = v;
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (j < n) row[8 * c + j] = (int8_t)(v[j >> 2] >> (8 * (j & 3)));
+      if (j < c.left) row[c.at + c.skip + j] = (int8_t)(v[j >> 2] >> (8 * (j & 3)));
   }
 }
 
@@ -298,43 +355,59 @@ __device__ __forceinline__ float row_rstd(float sum_of_squares, int32_t width, f
 
 // ------------------------------------------------------------------ forward
 
-// kThreads work on one row, each on up to kChunks chunks of eight elements
-// (chunk k * kThreads + lane): width <= 8 * kThreads * kChunks.  A row of 64
-// threads is one wavefront and needs no barrier; four such rows make a
-// work-group.
-template <typename T, int kMode, int kThreads, int kChunks>
-__global__ __launch_bounds__(kThreads < 256 ? 256 : kThreads) void rows_kernel(RowArgs a) {
-  constexpr int kBlockThreads = kThreads < 256 ? 256 : kThreads;
-  constexpr int kRows = kBlockThreads / kThreads;
+// kThreads work on one row, each on up to kChunks chunks (chunk k * kThreads +
+// lane): width <= 8 kThreads kChunks.  Rows of up to 64 threads need no
+// barrier, and a work-group of 256 takes several; rows of more than 64 threads
+// have a work-group each.  kThreads = 1: rows of at most eight elements, of
+// any width up to that when kShort.
+template <int kThreads>
+constexpr int rows_block() {
+  return kThreads < 256 ? 256 : kThreads;
+}
+
+template <typename T, int kMode, int kThreads, int kChunks, bool kShort = false>
+__global__ __launch_bounds__(rows_block<kThreads>()) void rows_kernel(RowArgs a) {
+  constexpr int kRows = rows_block<kThreads>() / kThreads;
   const int lane = (int)threadIdx.x % kThreads;
   const int slot = (int)threadIdx.x / kThreads;
+  Chunk c[kChunks];
   Vec8<T> w[kChunks];
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k) {
+    c[k] = chunk_at(k * kThreads + lane, a.width);
+    if constexpr (kMode != kRowQuantize) load_chunk<kShort>(w[k], (const T*)a.weight, c[k]);
+  }
   if constexpr (kMode != kRowQuantize) {
 #pragma unroll
-    for (int k = 0; k < kChunks; ++k)
-      load_chunk(w[k], (const T*)a.weight, k * kThreads + lane, a.width);
+    for (int k = 0; k < kChunks; ++k) trim_chunk<kShort>(w[k], c[k]);
   }
+  const bool add = kMode != kRowQuantize && a.residual != nullptr;
   int parity = 0;
   for (int64_t row = (int64_t)blockIdx.x * kRows + slot; row < a.rows;
        row += (int64_t)gridDim.x * kRows, parity ^= 1) {
     const T* x = (const T*)a.x + row * a.x_stride;
     Vec8<T> h[kChunks];
 #pragma unroll
-    for (int k = 0; k < kChunks; ++k) load_chunk(h[k], x, k * kThreads + lane, a.width);
-    if (kMode != kRowQuantize && a.residual != nullptr) {
+    for (int k = 0; k < kChunks; ++k) load_chunk<kShort>(h[k], x, c[k]);
+    if (add) {
       const T* r = (const T*)a.residual + row * a.residual_stride;
       Vec8<T> v[kChunks];
 #pragma unroll
-      for (int k = 0; k < kChunks; ++k) load_chunk(v[k], r, k * kThreads + lane, a.width);
-      T* s = (T*)a.sum + row * a.sum_stride;
+      for (int k = 0; k < kChunks; ++k) load_chunk<kShort>(v[k], r, c[k]);
 #pragma unroll
       for (int k = 0; k < kChunks; ++k) {
         float t[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) t[j] = h[k].get(j) + v[k].get(j);
         h[k].set(t);
-        store_chunk(h[k], s, k * kThreads + lane, a.width);
       }
+    }
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) trim_chunk<kShort>(h[k], c[k]);
+    if (add) {
+      T* s = (T*)a.sum + row * a.sum_stride;
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) store_chunk(h[k], s, c[k]);
     }
     float sum = 0.0f;
     uint32_t top = 0;
@@ -350,7 +423,7 @@ __global__ __launch_bounds__(kThreads < 256 ? 256 : kThreads) void rows_kernel(R
         }
       }
     }
-    group_reduce<kThreads / 64>(sum, top, parity);
+    row_reduce<kThreads>(sum, top, parity);
     float rstd = 1.0f;
     if constexpr (kMode != kRowQuantize) {
       rstd = row_rstd(sum, a.width, a.eps);
@@ -365,7 +438,7 @@ __global__ __launch_bounds__(kThreads < 256 ? 256 : kThreads) void rows_kernel(R
         for (int j = 0; j < 8; ++j) t[j] = h[k].get(j) * rstd * w[k].get(j);
         Vec8<T> v;
         v.set(t);
-        store_chunk(v, o, k * kThreads + lane, a.width);
+        store_chunk(v, o, c[k]);
       }
     } else {
       const RowQuant q = row_quant(top, rstd);
@@ -376,17 +449,17 @@ __global__ __launch_bounds__(kThreads < 256 ? 256 : kThreads) void rows_kernel(R
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           t[j] = kMode == kRowQuantize ? h[k].get(j) : h[k].get(j) * w[k].get(j);
-        store_codes(eight_codes(t, q), o, k * kThreads + lane, a.width);
+        store_codes(eight_codes(t, q), o, c[k]);
       }
       if (lane == 0) a.scales[row] = q.scale;
     }
   }
 }
 
-// Rows of any width, one work-group of 1,024 threads each: the row is read a
-// second time (from the stored sum where there is one) instead of being kept.
-// A thread meets the same columns in both passes, so it may store over what
-// it reads.
+// Rows of any width from 8 on, one work-group of 1,024 threads each: the row
+// is read a second time (from the stored sum where there is one) instead of
+// being kept.  A thread meets the same columns in both passes, so it may store
+// over what it reads.
 template <typename T, int kMode>
 __global__ __launch_bounds__(1024) void rows_wide_kernel(RowArgs a) {
   constexpr int kThreads = 1024;
@@ -400,30 +473,34 @@ __global__ __launch_bounds__(1024) void rows_wide_kernel(RowArgs a) {
     T* s = add ? (T*)a.sum + row * a.sum_stride : nullptr;
     float sum = 0.0f;
     uint32_t top = 0;
-    for (int32_t c = lane; c < chunks; c += kThreads) {
-      Vec8<T> h, w;
-      load_chunk(h, x, c, a.width);
+    for (int32_t i = lane; i < chunks; i += kThreads) {
+      const Chunk c = chunk_at(i, a.width);
+      Vec8<T> h, v, w;
+      load_chunk<false>(h, x, c);
       if (add) {
-        Vec8<T> v;
-        load_chunk(v, r, c, a.width);
+        load_chunk<false>(v, r, c);
         float t[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) t[j] = h.get(j) + v.get(j);
         h.set(t);
-        store_chunk(h, s, c, a.width);
       }
-      if constexpr (kMode == kRowNormQ8) load_chunk(w, (const T*)a.weight, c, a.width);
+      trim_chunk<false>(h, c);
+      if (add) store_chunk(h, s, c);
+      if constexpr (kMode == kRowNormQ8) {
+        load_chunk<false>(w, (const T*)a.weight, c);
+        trim_chunk<false>(w, c);
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float v = h.get(j);
-        if constexpr (kMode != kRowQuantize) sum += v * v;
+        const float u = h.get(j);
+        if constexpr (kMode != kRowQuantize) sum += u * u;
         if constexpr (kMode != kRowNorm) {
-          const float t = kMode == kRowQuantize ? v : v * w.get(j);
+          const float t = kMode == kRowQuantize ? u : u * w.get(j);
           top = max(top, __builtin_bit_cast(uint32_t, t) & 0x7FFFFFFFu);
         }
       }
     }
-    group_reduce<kThreads / 64>(sum, top, parity);
+    row_reduce<kThreads>(sum, top, parity);
     float rstd = 1.0f;
     if constexpr (kMode != kRowQuantize) {
       rstd = row_rstd(sum, a.width, a.eps);
@@ -431,10 +508,13 @@ __global__ __launch_bounds__(1024) void rows_wide_kernel(RowArgs a) {
     }
     const RowQuant q = row_quant(top, rstd);
     const T* from = add ? s : x;
-    for (int32_t c = lane; c < chunks; c += kThreads) {
+    for (int32_t i = lane; i < chunks; i += kThreads) {
+      const Chunk c = chunk_at(i, a.width);
       Vec8<T> h, w;
-      load_chunk(h, from, c, a.width);
-      if constexpr (kMode != kRowQuantize) load_chunk(w, (const T*)a.weight, c, a.width);
+      load_chunk<false>(h, from, c);
+      if constexpr (kMode != kRowQuantize) load_chunk<false>(w, (const T*)a.weight, c);
+      trim_chunk<false>(h, c);
+      if constexpr (kMode != kRowQuantize) trim_chunk<false>(w, c);
       float t[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -443,9 +523,9 @@ __global__ __launch_bounds__(1024) void rows_wide_kernel(RowArgs a) {
       }
       if constexpr (kMode == kRowNorm) {
         h.set(t);
-        store_chunk(h, (T*)a.out + row * a.out_stride, c, a.width);
+        store_chunk(h, (T*)a.out + row * a.out_stride, c);
       } else {
-        store_codes(eight_codes(t, q), a.codes + row * a.codes_stride, c, a.width);
+        store_codes(eight_codes(t, q), a.codes + row * a.codes_stride, c);
       }
     }
     if (kMode != kRowNorm && lane == 0) a.scales[row] = q.scale;
@@ -466,7 +546,7 @@ struct BackwardArgs {
   const void* dsum;  // or null
   void* dx;
   float* partial;   // [partials][width] sums of dout n, one row per work-group (or slice)
-  float* row_mean;  // rows of more than 32,768 elements: m of each row
+  float* row_mean;  // rows that do not fit in registers: m of each row
   int64_t rows;
   int64_t dout_stride, h_stride, dsum_stride, dx_stride;  // in elements
   int64_t rows_per_slice;
@@ -476,14 +556,13 @@ struct BackwardArgs {
 
 template <typename T>
 __device__ __forceinline__ void backward_chunk(const Vec8<T>& d, const Vec8<T>& h,
-                                               const Vec8<T>& w, const Vec8<T>* s, float rstd,
+                                               const Vec8<T>& w, const Vec8<T>& s, float rstd,
                                                float mean, Vec8<T>& out) {
   float t[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float n = h.get(j) * rstd;
-    t[j] = rstd * (d.get(j) * w.get(j) - n * mean);
-    if (s != nullptr) t[j] += s->get(j);
+    t[j] = rstd * (d.get(j) * w.get(j) - n * mean) + s.get(j);
   }
   out.set(t);
 }
@@ -491,39 +570,50 @@ __device__ __forceinline__ void backward_chunk(const Vec8<T>& d, const Vec8<T>& 
 // Layout of threads and rows as in rows_kernel.  A work-group takes every
 // gridDim.x-th group of rows and keeps its columns' sums of dout n in
 // registers until the end: one row of partial sums per work-group.
-template <typename T, int kThreads, int kChunks>
-__global__ __launch_bounds__(kThreads < 256 ? 256 : kThreads) void rows_backward_kernel(
-    BackwardArgs a) {
-  constexpr int kBlockThreads = kThreads < 256 ? 256 : kThreads;
-  constexpr int kRows = kBlockThreads / kThreads;
+template <typename T, int kThreads, int kChunks, bool kShort = false>
+__global__ __launch_bounds__(rows_block<kThreads>()) void rows_backward_kernel(BackwardArgs a) {
+  constexpr int kRows = rows_block<kThreads>() / kThreads;
   const int lane = (int)threadIdx.x % kThreads;
   const int slot = (int)threadIdx.x / kThreads;
+  Chunk c[kChunks];
   Vec8<T> w[kChunks];
   float dw[kChunks][8];
 #pragma unroll
   for (int k = 0; k < kChunks; ++k) {
-    load_chunk(w[k], (const T*)a.weight, k * kThreads + lane, a.width);
+    c[k] = chunk_at(k * kThreads + lane, a.width);
+    load_chunk<kShort>(w[k], (const T*)a.weight, c[k]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[k][j] = 0.0f;
   }
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k) trim_chunk<kShort>(w[k], c[k]);
+  const bool add = a.dsum != nullptr;
   int parity = 0;
   for (int64_t row = (int64_t)blockIdx.x * kRows + slot; row < a.rows;
        row += (int64_t)gridDim.x * kRows, parity ^= 1) {
     const T* pd = (const T*)a.dout + row * a.dout_stride;
     const T* ph = (const T*)a.h + row * a.h_stride;
     Vec8<T> d[kChunks], h[kChunks], s[kChunks];
+    const float rstd = a.rstd[row];
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
-      load_chunk(d[k], pd, k * kThreads + lane, a.width);
-      load_chunk(h[k], ph, k * kThreads + lane, a.width);
+      load_chunk<kShort>(d[k], pd, c[k]);
+      load_chunk<kShort>(h[k], ph, c[k]);
     }
-    const bool add = a.dsum != nullptr;
     if (add) {
       const T* ps = (const T*)a.dsum + row * a.dsum_stride;
 #pragma unroll
-      for (int k = 0; k < kChunks; ++k) load_chunk(s[k], ps, k * kThreads + lane, a.width);
+      for (int k = 0; k < kChunks; ++k) load_chunk<kShort>(s[k], ps, c[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) s[k].zero();
     }
-    const float rstd = a.rstd[row];
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+      trim_chunk<kShort>(d[k], c[k]);
+      trim_chunk<kShort>(h[k], c[k]);
+      if (add) trim_chunk<kShort>(s[k], c[k]);
+    }
     float sum = 0.0f;
     uint32_t unused = 0;
 #pragma unroll
@@ -535,44 +625,49 @@ __global__ __launch_bounds__(kThreads < 256 ? 256 : kThreads) void rows_backward
         sum += dn * w[k].get(j);
       }
     }
-    group_reduce<kThreads / 64>(sum, unused, parity);
+    row_reduce<kThreads>(sum, unused, parity);
     const float mean = sum / (float)a.width;
     T* o = (T*)a.dx + row * a.dx_stride;
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
       Vec8<T> v;
-      backward_chunk(d[k], h[k], w[k], add ? &s[k] : nullptr, rstd, mean, v);
-      store_chunk(v, o, k * kThreads + lane, a.width);
+      backward_chunk(d[k], h[k], w[k], s[k], rstd, mean, v);
+      store_chunk(v, o, c[k]);
     }
   }
   if constexpr (kRows > 1) {
-    // the work-group's rows of sums, added in the order of the slots
-    __shared__ float s_dw[kRows - 1][kThreads * 8 * kChunks];
-    if (slot > 0) {
+    // the work-group's rows of sums, the upper half onto the lower until one
+    // is left
+    __shared__ float s_dw[kRows / 2][8 * kChunks][kThreads];
+#pragma unroll 1
+    for (int half = kRows / 2; half > 0; half /= 2) {
+      if (slot >= half && slot < 2 * half) {
 #pragma unroll
-      for (int k = 0; k < kChunks; ++k)
+        for (int k = 0; k < kChunks; ++k)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s_dw[slot - 1][(k * 8 + j) * kThreads + lane] = dw[k][j];
+          for (int j = 0; j < 8; ++j) s_dw[slot - half][8 * k + j][lane] = dw[k][j];
+      }
+      __syncthreads();
+      if (slot < half) {
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dw[k][j] += s_dw[slot][8 * k + j][lane];
+      }
+      __syncthreads();
     }
-    __syncthreads();
     if (slot > 0) return;
-#pragma unroll
-    for (int r = 0; r < kRows - 1; ++r)
-#pragma unroll
-      for (int k = 0; k < kChunks; ++k)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dw[k][j] += s_dw[r][(k * 8 + j) * kThreads + lane];
   }
   float* p = a.partial + (int64_t)blockIdx.x * a.width;
 #pragma unroll
   for (int k = 0; k < kChunks; ++k) {
     Vec8<float> v;
     v.set(dw[k]);
-    store_chunk(v, p, k * kThreads + lane, a.width);
+    store_chunk(v, p, c[k]);
   }
 }
 
-// Rows of any width, first step: m = mean(g n) of each row.
+// Rows of any width from 8 on, first step: m = mean(g n) of each row.
 template <typename T>
 __global__ __launch_bounds__(1024) void rows_backward_mean_kernel(BackwardArgs a) {
   const int32_t chunks = (int32_t)(((int64_t)a.width + 7) / 8);
@@ -583,15 +678,19 @@ __global__ __launch_bounds__(1024) void rows_backward_mean_kernel(BackwardArgs a
     const float rstd = a.rstd[row];
     float sum = 0.0f;
     uint32_t unused = 0;
-    for (int32_t c = (int32_t)threadIdx.x; c < chunks; c += 1024) {
+    for (int32_t i = (int32_t)threadIdx.x; i < chunks; i += 1024) {
+      const Chunk c = chunk_at(i, a.width);
       Vec8<T> d, h, w;
-      load_chunk(d, pd, c, a.width);
-      load_chunk(h, ph, c, a.width);
-      load_chunk(w, (const T*)a.weight, c, a.width);
+      load_chunk<false>(d, pd, c);
+      load_chunk<false>(h, ph, c);
+      load_chunk<false>(w, (const T*)a.weight, c);
+      trim_chunk<false>(d, c);
+      trim_chunk<false>(h, c);
+      trim_chunk<false>(w, c);
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum += d.get(j) * (h.get(j) * rstd) * w.get(j);
     }
-    group_reduce<16>(sum, unused, parity);
+    row_reduce<1024>(sum, unused, parity);
     if (threadIdx.x == 0) a.row_mean[row] = sum / (float)a.width;
   }
 }
@@ -600,28 +699,33 @@ __global__ __launch_bounds__(1024) void rows_backward_mean_kernel(BackwardArgs a
 template <typename T>
 __global__ __launch_bounds__(256) void rows_backward_columns_kernel(BackwardArgs a) {
   const int32_t chunks = (int32_t)(((int64_t)a.width + 7) / 8);
-  const int32_t c = (int32_t)(blockIdx.x * 256u + threadIdx.x);
-  if (c >= chunks) return;
+  const int32_t i = (int32_t)(blockIdx.x * 256u + threadIdx.x);
+  if (i >= chunks) return;
+  const Chunk c = chunk_at(i, a.width);
   const int64_t first = (int64_t)blockIdx.y * a.rows_per_slice;
   const int64_t end = min(first + a.rows_per_slice, a.rows);
   Vec8<T> w;
-  load_chunk(w, (const T*)a.weight, c, a.width);
+  load_chunk<false>(w, (const T*)a.weight, c);
+  trim_chunk<false>(w, c);
   float dw[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   for (int64_t row = first; row < end; ++row) {
     Vec8<T> d, h, s, v;
-    load_chunk(d, (const T*)a.dout + row * a.dout_stride, c, a.width);
-    load_chunk(h, (const T*)a.h + row * a.h_stride, c, a.width);
-    const bool add = a.dsum != nullptr;
-    if (add) load_chunk(s, (const T*)a.dsum + row * a.dsum_stride, c, a.width);
+    load_chunk<false>(d, (const T*)a.dout + row * a.dout_stride, c);
+    load_chunk<false>(h, (const T*)a.h + row * a.h_stride, c);
+    s.zero();
+    if (a.dsum != nullptr) load_chunk<false>(s, (const T*)a.dsum + row * a.dsum_stride, c);
+    trim_chunk<false>(d, c);
+    trim_chunk<false>(h, c);
+    trim_chunk<false>(s, c);
     const float rstd = a.rstd[row];
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[j] += d.get(j) * (h.get(j) * rstd);
-    backward_chunk(d, h, w, add ? &s : nullptr, rstd, a.row_mean[row], v);
-    store_chunk(v, (T*)a.dx + row * a.dx_stride, c, a.width);
+    backward_chunk(d, h, w, s, rstd, a.row_mean[row], v);
+    store_chunk(v, (T*)a.dx + row * a.dx_stride, c);
   }
   Vec8<float> v;
   v.set(dw);
-  store_chunk(v, a.partial + (int64_t)blockIdx.y * a.width, c, a.width);
+  store_chunk(v, a.partial + (int64_t)blockIdx.y * a.width, c);
 }
 
 // dweight = the sum of the rows of partial sums: 16 columns per work-group,

@@ -23,7 +23,6 @@ namespace fn {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4_any __attribute__((ext_vector_type(4), aligned(1)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 // Two numbers rounded to a 16-bit type, in one register.

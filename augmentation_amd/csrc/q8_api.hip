@@ -121,8 +121,8 @@ struct RowShape {
 
 constexpr RowShape kRowShapes[] = {{7, 1, 0},     {8, 1, 1},      {64, 8, 1},     {128, 8, 2},
                                    {256, 32, 1},  {512, 32, 2},   {768, 32, 3},   {1024, 64, 2},
-                                   {2048, 64, 4}, {4096, 256, 2}, {8192, 256, 4}, {16384, 1024, 2},
-                                   {32768, 1024, 4}};
+                                   {2048, 64, 4}, {4096, 256, 2}, {6144, 256, 3}, {8192, 512, 2},
+                                   {16384, 1024, 2}, {32768, 1024, 4}};
 
 RowShape row_shape(int32_t width, int32_t widest) {
   for (const RowShape& s : kRowShapes)
@@ -154,7 +154,8 @@ void launch_rows(const fn::RowArgs& a, hipStream_t st) {
     case shape_key(64, 2): return launch_rows_k<T, kMode, 64, 2>(a, st);
     case shape_key(64, 4): return launch_rows_k<T, kMode, 64, 4>(a, st);
     case shape_key(256, 2): return launch_rows_k<T, kMode, 256, 2>(a, st);
-    case shape_key(256, 4): return launch_rows_k<T, kMode, 256, 4>(a, st);
+    case shape_key(256, 3): return launch_rows_k<T, kMode, 256, 3>(a, st);
+    case shape_key(512, 2): return launch_rows_k<T, kMode, 512, 2>(a, st);
     case shape_key(1024, 2): return launch_rows_k<T, kMode, 1024, 2>(a, st);
     case shape_key(1024, 4): return launch_rows_k<T, kMode, 1024, 4>(a, st);
     default:
@@ -223,12 +224,15 @@ int norm(const void* x, int64_t x_stride, const void* residual, int64_t residual
   return launch_rows_type<kMode>(a, dtype, stream);
 }
 
-// Work-groups of the backward kernels, each with one row of partial sums:
-// about sixteen wavefronts per compute unit of a 256-unit device.  A function
-// of the sizes alone, so that results do not depend on the device.
+// Work-groups of the backward kernels, each with one row of partial sums: two
+// for each unit of a 256-unit device where they take several rows at a time,
+// one where a row takes all of it (measured for 256 / 512 / 1,024 partial rows,
+// with their sum, in us: 50176x768 - / 59 / 61, 8192x4096 50 / 53 / 62,
+// 16384x8192 176 / 180 / -, 4099x5003 47 / 48 / 57).  A function of the sizes
+// alone, so that results do not depend on the device.
 struct BackwardPlan {
   RowShape shape;
-  int32_t partials;
+  int32_t partials, pitch;
   int64_t rows_per_slice;
   int64_t bytes;
 };
@@ -236,17 +240,17 @@ struct BackwardPlan {
 BackwardPlan plan_backward(int64_t rows, int32_t width) {
   BackwardPlan p{};
   p.shape = row_shape(width, 16384);
+  p.pitch = (width + 3) / 4 * 4;
   if (p.shape.threads > 0) {
-    const int block = std::max(256, p.shape.threads);
-    const int64_t at_once = block / p.shape.threads, groups = (rows + at_once - 1) / at_once;
-    p.partials = (int32_t)std::min<int64_t>(groups, 4096 / (block / 64));
-    p.bytes = (int64_t)p.partials * width * 4;
+    const int64_t at_once = p.shape.threads < 256 ? 256 / p.shape.threads : 1;
+    p.partials = (int32_t)std::min<int64_t>((rows + at_once - 1) / at_once, at_once > 1 ? 512 : 256);
+    p.bytes = (int64_t)p.partials * p.pitch * 4;
     return p;
   }
   const int64_t slices = std::min<int64_t>(rows, 64);
   p.rows_per_slice = slices ? (rows + slices - 1) / slices : 0;
   p.partials = slices ? (int32_t)((rows + p.rows_per_slice - 1) / p.rows_per_slice) : 0;
-  p.bytes = (int64_t)p.partials * width * 4 + rows * 4;
+  p.bytes = ((int64_t)p.partials * p.pitch * 4 + rows * 4 + 15) / 16 * 16;
   return p;
 }
 
@@ -269,7 +273,8 @@ void launch_backward(const fn::BackwardArgs& a, const RowShape& s, hipStream_t s
     case shape_key(64, 2): return launch_backward_k<T, 64, 2>(a, st);
     case shape_key(64, 4): return launch_backward_k<T, 64, 4>(a, st);
     case shape_key(256, 2): return launch_backward_k<T, 256, 2>(a, st);
-    case shape_key(256, 4): return launch_backward_k<T, 256, 4>(a, st);
+    case shape_key(256, 3): return launch_backward_k<T, 256, 3>(a, st);
+    case shape_key(512, 2): return launch_backward_k<T, 512, 2>(a, st);
     case shape_key(1024, 2): return launch_backward_k<T, 1024, 2>(a, st);
     default: {
       fn::rows_backward_mean_kernel<T>
@@ -465,7 +470,7 @@ FN_EXPORT int fn_rms_norm_backward(const void* dout_dev, int64_t dout_stride, co
       {"rstd_dev", rstd_dev, rows ? 1 : 0, rows, 0, 4, false},
       {"dx_dev", dx_dev, rows, width, dx_stride, e, true, 7u},
       {"dweight_dev", dweight_dev, 1, width, 0, 4, true},
-      {"workspace_dev", workspace_dev, plan.bytes ? 1 : 0, plan.bytes / 4, 0, 4, true},
+      {"workspace_dev", workspace_dev, plan.bytes ? 1 : 0, plan.bytes / 16, 0, 16, true},
   };
   int dev = -1;
   FN_TRY(check_buffers(buffers, &dev));
@@ -477,7 +482,7 @@ FN_EXPORT int fn_rms_norm_backward(const void* dout_dev, int64_t dout_stride, co
   a.dsum = dsum_dev;
   a.dx = dx_dev;
   a.partial = (float*)workspace_dev;
-  a.row_mean = (float*)workspace_dev + (int64_t)plan.partials * width;
+  a.row_mean = (float*)workspace_dev + (int64_t)plan.partials * plan.pitch;
   a.rows = rows;
   a.dout_stride = dout_stride;
   a.h_stride = h_stride;
@@ -486,6 +491,7 @@ FN_EXPORT int fn_rms_norm_backward(const void* dout_dev, int64_t dout_stride, co
   a.rows_per_slice = plan.rows_per_slice;
   a.width = width;
   a.partials = plan.partials;
+  a.pitch = plan.pitch;
   hipStream_t st = (hipStream_t)stream;
   if (rows > 0) {
     if (dtype == FN_OUT_FP32)
@@ -497,8 +503,8 @@ FN_EXPORT int fn_rms_norm_backward(const void* dout_dev, int64_t dout_stride, co
     FN_TRY(launch_status("rows_backward_kernel launch"));
   }
   // no rows: no partial sums, and a gradient of zero
-  fn::column_sum_kernel<<<blocks_for(width, 16), 1024, 0, st>>>(a.partial, a.partials, width,
-                                                                dweight_dev);
+  fn::column_sum_kernel<<<blocks_for(width, 64), 1024, 0, st>>>(a.partial, a.partials, a.pitch,
+                                                                width, dweight_dev);
   return launch_status("column_sum_kernel launch");
 }
 

@@ -46,11 +46,14 @@ struct RowArgs {
 
 // ------------------------------------------------------------- vector access
 // Eight consecutive elements, at any alignment of the element's size: the
-// hardware's global loads and stores take unaligned addresses.
+// hardware's global loads and stores take unaligned addresses.  Rows are met
+// once, so both are non-temporal (16384x8192 bf16: norm 182 -> 173 us, to
+// codes 159 -> 149 us, backward 191 -> 179 us).
 
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ float bf16_to_float(uint32_t bits) {
   return __builtin_bit_cast(float, bits << 16);
@@ -70,8 +73,8 @@ struct Vec8<float> {
   u32x4 a, b;
   __device__ __forceinline__ void zero() { a = b = u32x4{0, 0, 0, 0}; }
   __device__ __forceinline__ void load(const float* p) {
-    a = *reinterpret_cast<const u32x4_any*>(p);
-    b = *reinterpret_cast<const u32x4_any*>(p + 4);
+    a = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
+    b = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p + 4));
   }
   __device__ __forceinline__ void load_some(const float* p, int n) {
 #pragma unroll
@@ -108,8 +111,8 @@ struct Vec8<float> {
     }
   }
   __device__ __forceinline__ void store(float* p) const {
-    *reinterpret_cast<u32x4_any*>(p) = a;
-    *reinterpret_cast<u32x4_any*>(p + 4) = b;
+    __builtin_nontemporal_store(a, reinterpret_cast<u32x4_any*>(p));
+    __builtin_nontemporal_store(b, reinterpret_cast<u32x4_any*>(p + 4));
   }
   __device__ __forceinline__ void store_some(float* p, int n) const {
 #pragma unroll
@@ -124,7 +127,7 @@ struct Half8 {
   u32x4 a;
   __device__ __forceinline__ void zero() { a = u32x4{0, 0, 0, 0}; }
   __device__ __forceinline__ void load(const T* p) {
-    a = *reinterpret_cast<const u32x4_any*>(p);
+    a = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
   }
   __device__ __forceinline__ void load_some(const T* p, int n) {
     const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
@@ -144,7 +147,9 @@ struct Half8 {
                 a[3] >> 16};
   }
   __device__ __forceinline__ uint32_t bits(int j) const { return (a[j >> 1] >> (16 * (j & 1))) & 0xFFFFu; }
-  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<u32x4_any*>(p) = a; }
+  __device__ __forceinline__ void store(T* p) const {
+    __builtin_nontemporal_store(a, reinterpret_cast<u32x4_any*>(p));
+  }
   __device__ __forceinline__ void store_some(T* p, int n) const {
     uint16_t* q = reinterpret_cast<uint16_t*>(p);
 #pragma unroll
@@ -240,8 +245,8 @@ __device__ __forceinline__ uint32_t group_fold(uint32_t v, F fold) {
     v = fold(v, dpp<0x4E>(v));   // quad_perm 2 3 0 1
     v = fold(v, dpp<0x141>(v));  // row_half_mirror
   }
+  if constexpr (kLanes >= 16) v = fold(v, dpp<0x140>(v));  // row_mirror
   if constexpr (kLanes >= 32) {
-    v = fold(v, dpp<0x140>(v));  // row_mirror
     const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
     v = fold(r[0], r[1]);
   }
@@ -338,7 +343,7 @@ __device__ __forceinline__ u32x2_any eight_codes(const float (&t)[8], const RowQ
 
 __device__ __forceinline__ void store_codes(u32x2_any v, int8_t* row, const Chunk& c) {
   if (c.left >= 8) {
-    *reinterpret_cast<u32x2_any*>(row + c.at) = v;
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x2_any*>(row + c.at));
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -545,13 +550,14 @@ struct BackwardArgs {
   const float* rstd;
   const void* dsum;  // or null
   void* dx;
-  float* partial;   // [partials][width] sums of dout n, one row per work-group (or slice)
+  float* partial;   // [partials][pitch] sums of dout n, one row per work-group (or slice)
   float* row_mean;  // rows that do not fit in registers: m of each row
   int64_t rows;
   int64_t dout_stride, h_stride, dsum_stride, dx_stride;  // in elements
   int64_t rows_per_slice;
   int32_t width;
   int32_t partials;
+  int32_t pitch;  // width rounded up to whole vectors of four
 };
 
 template <typename T>
@@ -588,26 +594,37 @@ __global__ __launch_bounds__(rows_block<kThreads>()) void rows_backward_kernel(B
 #pragma unroll
   for (int k = 0; k < kChunks; ++k) trim_chunk<kShort>(w[k], c[k]);
   const bool add = a.dsum != nullptr;
-  int parity = 0;
-  for (int64_t row = (int64_t)blockIdx.x * kRows + slot; row < a.rows;
-       row += (int64_t)gridDim.x * kRows, parity ^= 1) {
+  // the next row is on its way while this one is worked on
+  struct Row {
+    Vec8<T> d[kChunks], h[kChunks], s[kChunks];
+    float rstd;
+  };
+  auto load = [&](Row& r, int64_t row) {
     const T* pd = (const T*)a.dout + row * a.dout_stride;
     const T* ph = (const T*)a.h + row * a.h_stride;
-    Vec8<T> d[kChunks], h[kChunks], s[kChunks];
-    const float rstd = a.rstd[row];
+    r.rstd = a.rstd[row];
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
-      load_chunk<kShort>(d[k], pd, c[k]);
-      load_chunk<kShort>(h[k], ph, c[k]);
+      load_chunk<kShort>(r.d[k], pd, c[k]);
+      load_chunk<kShort>(r.h[k], ph, c[k]);
     }
     if (add) {
       const T* ps = (const T*)a.dsum + row * a.dsum_stride;
 #pragma unroll
-      for (int k = 0; k < kChunks; ++k) load_chunk<kShort>(s[k], ps, c[k]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < kChunks; ++k) s[k].zero();
+      for (int k = 0; k < kChunks; ++k) load_chunk<kShort>(r.s[k], ps, c[k]);
     }
+  };
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t row = (int64_t)blockIdx.x * kRows + slot;
+  Row next;
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k) next.s[k].zero();
+  if (row < a.rows) load(next, row);
+  for (int parity = 0; row < a.rows; row += step, parity ^= 1) {
+    Row now = next;
+    if (row + step < a.rows) load(next, row + step);
+    auto &d = now.d, &h = now.h, &s = now.s;
+    const float rstd = now.rstd;
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
       trim_chunk<kShort>(d[k], c[k]);
@@ -658,7 +675,7 @@ __global__ __launch_bounds__(rows_block<kThreads>()) void rows_backward_kernel(B
     }
     if (slot > 0) return;
   }
-  float* p = a.partial + (int64_t)blockIdx.x * a.width;
+  float* p = a.partial + (int64_t)blockIdx.x * a.pitch;
 #pragma unroll
   for (int k = 0; k < kChunks; ++k) {
     Vec8<float> v;
@@ -725,28 +742,37 @@ __global__ __launch_bounds__(256) void rows_backward_columns_kernel(BackwardArgs
   }
   Vec8<float> v;
   v.set(dw);
-  store_chunk(v, a.partial + (int64_t)blockIdx.y * a.width, c);
+  store_chunk(v, a.partial + (int64_t)blockIdx.y * a.pitch, c);
 }
 
-// dweight = the sum of the rows of partial sums: 16 columns per work-group,
-// 64 threads to a column, joined in a fixed order.
+// dweight = the sum of the rows of partial sums: 64 columns per work-group,
+// four to a thread, 64 threads to a column, joined in a fixed order.
 __global__ __launch_bounds__(1024) void column_sum_kernel(const float* partial, int32_t partials,
-                                                          int32_t width, float* dweight) {
-  __shared__ float s_sum[64][17];
-  const int col = (int)(threadIdx.x & 15u), part = (int)(threadIdx.x >> 4);
-  const int64_t c = (int64_t)blockIdx.x * 16 + col;
-  float sum = 0.0f;
-  if (c < width) {
+                                                          int32_t pitch, int32_t width,
+                                                          float* dweight) {
+  __shared__ float s_sum[64][64 + 4];
+  const int col = 4 * (int)(threadIdx.x & 15u), part = (int)(threadIdx.x >> 4);
+  const int64_t c = (int64_t)blockIdx.x * 64 + col;
+  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (c < pitch) {
 #pragma unroll 8
-    for (int32_t p = part; p < partials; p += 64) sum += partial[(int64_t)p * width + c];
+    for (int32_t p = part; p < partials; p += 64) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(partial + (int64_t)p * pitch + c);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum[j] += v[j];
+    }
   }
-  s_sum[part][col] = sum;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) s_sum[part][col + j] = sum[j];
   __syncthreads();
-  if (part == 0 && c < width) {
-#pragma unroll 8
-    for (int p = 1; p < 64; ++p) sum += s_sum[p][col];
-    dweight[c] = sum;
-  }
+  // sixteen threads to a column, then their neighbours' sums
+  const int column = (int)(threadIdx.x >> 4), first = (int)(threadIdx.x & 15u);
+  float all = 0.0f;
+#pragma unroll
+  for (int p = 0; p < 4; ++p) all += s_sum[first + 16 * p][column];
+  all = group_sum<16>(all);
+  const int64_t out = (int64_t)blockIdx.x * 64 + column;
+  if (first == 0 && out < width) dweight[out] = all;
 }
 
 }  // namespace fn

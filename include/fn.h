@@ -270,7 +270,7 @@ int fn_quantize_rows(const void* x_dev, int64_t x_stride, int64_t rows, int32_t 
  *             order that the sizes alone fix (no atomics).  rows = 0 writes
  *             zeros.
  * dx_dev may be exactly dout_dev, h_dev or dsum_dev.  workspace_dev: at least
- * fn_rms_norm_backward_workspace(rows, width) bytes, 4-byte aligned, that no
+ * fn_rms_norm_backward_workspace(rows, width) bytes, 16-byte aligned, that no
  * other call in flight uses.  For a norm whose output was quantised, dout is
  * the gradient of code * scale, passed straight through the rounding.
  */

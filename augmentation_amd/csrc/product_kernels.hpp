@@ -158,7 +158,7 @@ __device__ __forceinline__ int staged_piece(int row, int piece) {
 // and rounded where they are, 64 tokens at a time go through the wavefront's
 // own piece of LDS (rows of kPitch bytes; the 16 bytes beyond a row's
 // channels keep rows off the same banks) and leave as 16-byte stores along
-// rows.
+// rows, non-temporal (50176x1024x768 to fp16: 78 -> 65 us, 8192^3 409 -> 404).
 template <typename T, int kTM, int kTN>
 struct OutputTile {
   static constexpr int kTokens = kTM < 4 ? 16 * kTM : 64;  // tokens that leave together
@@ -220,7 +220,7 @@ struct OutputTile {
         const u32x4 v = *reinterpret_cast<const u32x4*>(lds + r * kPitch + 16 * (lane % kLanes));
         T* to = (T*)p.out + m * p.out_stride + n;
         if (m < p.M && left == kE) {
-          *reinterpret_cast<u32x4_any*>(to) = v;
+          __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any*>(to));
         } else if (m < p.M && left > 0) {
           store_part(v, to, left);
         }

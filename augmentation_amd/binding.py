@@ -10,6 +10,7 @@ the library has not been built (there is no CPU fallback).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -276,14 +277,18 @@ def params_to_numpy(t: torch.Tensor) -> np.ndarray:
 
 
 # ------------------------------------- tensor helpers: the 8-bit linear layer
+#
+# These are called once per layer and token, so they keep to the fewest
+# attribute reads that check an argument.
 
 _TYPE_CODES = {torch.float32: FN_OUT_FP32, torch.float16: FN_OUT_FP16, torch.bfloat16: FN_OUT_BF16}
+_CODE_TYPES = {code: t for t, code in _TYPE_CODES.items()}
 
 
-def _type_code(t: torch.Tensor) -> int:
-    code = _TYPE_CODES.get(t.dtype)
+def _type_code(dtype) -> int:
+    code = _TYPE_CODES.get(dtype)
     if code is None:
-        raise ValueError(f"dtype {t.dtype}: float32, float16 or bfloat16 is needed")
+        raise ValueError(f"dtype {dtype}: float32, float16 or bfloat16 is needed")
     return code
 
 
@@ -311,52 +316,68 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
                      "(use .contiguous())")
 
 
-def _like(t, shape, dtype, ref: torch.Tensor, name: str) -> torch.Tensor:
-    """`t` if it has this shape, dtype and device; a new tensor if it is None."""
+def _want(t, shape, dtype, dev: int, name: str, flat: bool = False) -> torch.Tensor:
+    """`t` if it has this shape, dtype and device (and is contiguous, if
+    `flat`); a new tensor if it is None."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=ref.device)
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != ref.get_device():
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {ref.device}")
-    return t
-
-
-def _flat(t, shape, dtype, ref: torch.Tensor, name: str) -> torch.Tensor:
-    t = _like(t, shape, dtype, ref, name)
-    if not t.is_contiguous():
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on cuda:{dev}")
+    if flat and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t
 
 
-def _rows_of(x: torch.Tensor) -> tuple[int, int]:
-    if x.dim() < 1 or not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor of at least one dimension")
-    width = x.size(-1)
-    return (x.numel() // width if width else 0), width
+def _rows_of(x: torch.Tensor):
+    """(shape, rows, width, device index) of a (..., D) CUDA tensor."""
+    shape, dev = x.shape, x.get_device()
+    if dev < 0 or len(shape) < 1:
+        raise ValueError("a CUDA tensor of at least one dimension is needed")
+    width = shape[-1]
+    return shape, (x.numel() // width if width else 0), width, dev
 
 
-def _norm_inputs(x, weight, residual, sum_out):
-    rows, width = _rows_of(x)
-    weight = _flat(weight, (width,), x.dtype, x, "weight")
-    if residual is None:
-        if sum_out is not None:
-            raise ValueError("sum_out without a residual")
-        return rows, width, weight, 0, None, 0
-    residual = _like(residual, x.shape, x.dtype, x, "residual")
-    sum_out = _like(sum_out, x.shape, x.dtype, x, "sum_out")
-    return (rows, width, weight, _row_stride(residual, "residual"), sum_out,
-            _row_stride(sum_out, "sum_out"))
+def _norm(x, weight, eps, residual, sum_out, stream, out_args, q8):
+    """What both norms pass before and after their own outputs."""
+    shape, rows, width, dev = _rows_of(x)
+    dtype = x.dtype
+    code = _type_code(dtype)
+    _want(weight, (width,), dtype, dev, "weight", True)
+    res_at = sum_at = None
+    res_stride = sum_stride = 0
+    if residual is not None:
+        _want(residual, shape, dtype, dev, "residual")
+        sum_out = _want(sum_out, shape, dtype, dev, "sum_out")
+        res_at, res_stride = residual.data_ptr(), _row_stride(residual, "residual")
+        sum_at, sum_stride = sum_out.data_ptr(), _row_stride(sum_out, "sum_out")
+    elif sum_out is not None:
+        raise ValueError("sum_out without a residual")
+    if q8:
+        codes, scales, rstd = out_args
+        codes = _want(codes, shape, torch.int8, dev, "codes")
+        scales = _want(scales, shape[:-1], torch.float32, dev, "scales", True)
+        if rstd is not None:
+            _want(rstd, shape[:-1], torch.float32, dev, "rstd", True)
+        _check(_lib.fn_rms_norm_q8(
+            x.data_ptr(), _row_stride(x, "x"), res_at, res_stride, weight.data_ptr(), rows, width,
+            eps, code, sum_at, sum_stride, codes.data_ptr(), _row_stride(codes, "codes"),
+            scales.data_ptr(), None if rstd is None else rstd.data_ptr(), _stream(stream)))
+        return codes, scales, x if residual is None else sum_out
+    out, rstd = out_args
+    out = _want(out, shape, dtype, dev, "out")
+    rstd = _want(rstd, shape[:-1], torch.float32, dev, "rstd", True)
+    _check(_lib.fn_rms_norm(
+        x.data_ptr(), _row_stride(x, "x"), res_at, res_stride, weight.data_ptr(), rows, width, eps,
+        code, sum_at, sum_stride, out.data_ptr(), _row_stride(out, "out"), rstd.data_ptr(),
+        _stream(stream)))
+    return out, rstd, x if residual is None else sum_out
 
 
 def rms_norm(x, weight, eps=1e-6, residual=None, out=None, sum_out=None, rstd=None, stream=None):
     """fn_rms_norm on (..., D) CUDA tensors of one dtype.  Returns (out, rstd,
     h): the norm of h = x + residual, each row's 1/rms (fp32), and h itself
     (x when there is no residual).  out and sum_out may be x or residual."""
-    rows, width, weight, r_stride, sum_out, s_stride = _norm_inputs(x, weight, residual, sum_out)
-    out = _like(out, x.shape, x.dtype, x, "out")
-    rstd = _flat(rstd, x.shape[:-1], torch.float32, x, "rstd")
-    fn_rms_norm(x, _row_stride(x, "x"), residual, r_stride, weight, rows, width, eps,
-                _type_code(x), sum_out, s_stride, out, _row_stride(out, "out"), rstd, stream)
-    return out, rstd, x if sum_out is None else sum_out
+    return _norm(x, weight, eps, residual, sum_out, stream, (out, rstd), False)
 
 
 def rms_norm_q8(x, weight, eps=1e-6, residual=None, codes=None, scales=None, sum_out=None,
@@ -365,32 +386,27 @@ def rms_norm_q8(x, weight, eps=1e-6, residual=None, codes=None, scales=None, sum
     scales, h): int8 codes of the shape of x, an fp32 scale per row, and h = x
     + residual (x when there is no residual).  sum_out may be x or residual;
     rstd, if given, receives each row's 1/rms."""
-    rows, width, weight, r_stride, sum_out, s_stride = _norm_inputs(x, weight, residual, sum_out)
-    codes = _like(codes, x.shape, torch.int8, x, "codes")
-    scales = _flat(scales, x.shape[:-1], torch.float32, x, "scales")
-    if rstd is not None:
-        rstd = _flat(rstd, x.shape[:-1], torch.float32, x, "rstd")
-    fn_rms_norm_q8(x, _row_stride(x, "x"), residual, r_stride, weight, rows, width, eps,
-                   _type_code(x), sum_out, s_stride, codes, _row_stride(codes, "codes"), scales,
-                   rstd, stream)
-    return codes, scales, x if sum_out is None else sum_out
+    return _norm(x, weight, eps, residual, sum_out, stream, (codes, scales, rstd), True)
 
 
 def quantize_rows(x, codes=None, scales=None, stream=None):
     """fn_quantize_rows on a (..., D) CUDA tensor: (int8 codes of its shape,
     an fp32 scale per row)."""
-    rows, width = _rows_of(x)
-    codes = _like(codes, x.shape, torch.int8, x, "codes")
-    scales = _flat(scales, x.shape[:-1], torch.float32, x, "scales")
-    fn_quantize_rows(x, _row_stride(x, "x"), rows, width, _type_code(x), codes,
-                     _row_stride(codes, "codes"), scales, stream)
+    shape, rows, width, dev = _rows_of(x)
+    codes = _want(codes, shape, torch.int8, dev, "codes")
+    scales = _want(scales, shape[:-1], torch.float32, dev, "scales", True)
+    _check(_lib.fn_quantize_rows(
+        x.data_ptr(), _row_stride(x, "x"), rows, width, _type_code(x.dtype), codes.data_ptr(),
+        _row_stride(codes, "codes"), scales.data_ptr(), _stream(stream)))
     return codes, scales
+
+
+_workspace_bytes = functools.lru_cache(maxsize=256)(fn_rms_norm_backward_workspace)  # of the sizes
 
 
 def rms_norm_backward_workspace(rows, width, device="cuda") -> torch.Tensor:
     """A workspace for rms_norm_backward on rows of this size."""
-    return torch.empty(fn_rms_norm_backward_workspace(rows, width) // 4, dtype=torch.float32,
-                       device=device)
+    return torch.empty(_workspace_bytes(rows, width), dtype=torch.uint8, device=device)
 
 
 def rms_norm_backward(dout, h, weight, rstd, dsum=None, dx=None, dweight=None, workspace=None,
@@ -401,21 +417,29 @@ def rms_norm_backward(dout, h, weight, rstd, dsum=None, dx=None, dweight=None, w
     or dsum.  Without a workspace one is allocated for the call; with
     `stream` other than the current one, pass a workspace that lives until
     the stream has finished."""
-    rows, width = _rows_of(h)
-    weight = _flat(weight, (width,), h.dtype, h, "weight")
-    dout = _like(dout, h.shape, h.dtype, h, "dout")
-    rstd = _flat(rstd, h.shape[:-1], torch.float32, h, "rstd")
-    d_stride = 0
+    shape, rows, width, dev = _rows_of(h)
+    dtype = h.dtype
+    code = _type_code(dtype)
+    _want(weight, (width,), dtype, dev, "weight", True)
+    _want(dout, shape, dtype, dev, "dout")
+    _want(rstd, shape[:-1], torch.float32, dev, "rstd", True)
+    dsum_at, dsum_stride = None, 0
     if dsum is not None:
-        dsum = _like(dsum, h.shape, h.dtype, h, "dsum")
-        d_stride = _row_stride(dsum, "dsum")
-    dx = _like(dx, h.shape, h.dtype, h, "dx")
-    dweight = _flat(dweight, (width,), torch.float32, h, "dweight")
+        _want(dsum, shape, dtype, dev, "dsum")
+        dsum_at, dsum_stride = dsum.data_ptr(), _row_stride(dsum, "dsum")
+    dx = _want(dx, shape, dtype, dev, "dx")
+    dweight = _want(dweight, (width,), torch.float32, dev, "dweight", True)
     if workspace is None:
-        workspace = rms_norm_backward_workspace(rows, width, h.device)
-    fn_rms_norm_backward(dout, _row_stride(dout, "dout"), h, _row_stride(h, "h"), weight, rstd,
-                         dsum, d_stride, rows, width, _type_code(h), dx, _row_stride(dx, "dx"),
-                         dweight, workspace, workspace.numel() * workspace.element_size(), stream)
+        size = _workspace_bytes(rows, width)
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        at = workspace.data_ptr() if size else None
+    else:
+        at, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(_lib.fn_rms_norm_backward(
+        dout.data_ptr(), _row_stride(dout, "dout"), h.data_ptr(), _row_stride(h, "h"),
+        weight.data_ptr(), rstd.data_ptr(), dsum_at, dsum_stride, rows, width, code, dx.data_ptr(),
+        _row_stride(dx, "dx"), dweight.data_ptr(), at, size, _stream(stream)))
     return dx, dweight
 
 
@@ -423,23 +447,27 @@ def matmul_q8(a, a_scales, b, b_scales, bias=None, out_dtype=FN_OUT_BF16, out=No
     """fn_matmul_q8: the (..., N) product of int8 codes a (..., K) with a scale
     per row and b (N, K) with a scale per row, plus an fp32 bias (N,).  Given
     `out`, its dtype counts and not out_dtype."""
-    if a.dtype != torch.int8 or b.dtype != torch.int8 or a.dim() < 1 or b.dim() != 2 \
-            or not a.is_cuda or b.device != a.device or a.size(-1) != b.size(1):
+    shape, b_shape, dev = a.shape, b.shape, a.get_device()
+    if a.dtype is not torch.int8 or b.dtype is not torch.int8 or len(shape) < 1 \
+            or len(b_shape) != 2 or dev < 0 or b.get_device() != dev or shape[-1] != b_shape[1]:
         raise ValueError("a must be an int8 (..., K) CUDA tensor and b an int8 (N, K) one beside it")
-    N, K = b.shape
-    lead = a.shape[:-1]
+    N, K = b_shape
+    lead = shape[:-1]
     M = lead.numel()
     if out is None:
-        tdt = {code: t for t, code in _TYPE_CODES.items()}.get(out_dtype)
-        if tdt is None:
+        if out_dtype not in _CODE_TYPES:
             raise ValueError(f"unknown out_dtype {out_dtype}")
+        out = torch.empty((*lead, N), dtype=_CODE_TYPES[out_dtype], device=dev)
     else:
-        tdt = out.dtype
-    out = _like(out, (*lead, N), tdt, a, "out")
-    a_scales = _flat(a_scales, lead, torch.float32, a, "a_scales")
-    b_scales = _flat(b_scales, (N,), torch.float32, a, "b_scales")
+        out_dtype = _type_code(out.dtype)
+        _want(out, (*lead, N), out.dtype, dev, "out")
+    _want(a_scales, lead, torch.float32, dev, "a_scales", True)
+    _want(b_scales, (N,), torch.float32, dev, "b_scales", True)
     if bias is not None:
-        bias = _flat(bias, (N,), torch.float32, a, "bias")
-    fn_matmul_q8(a, _row_stride(a, "a") if K else 0, a_scales, b, _row_stride(b, "b") if K else 0,
-                 b_scales, bias, M, N, K, _type_code(out), out, _row_stride(out, "out"), stream)
+        _want(bias, (N,), torch.float32, dev, "bias", True)
+    _check(_lib.fn_matmul_q8(
+        a.data_ptr(), _row_stride(a, "a") if K else 0, a_scales.data_ptr(), b.data_ptr(),
+        _row_stride(b, "b") if K else 0, b_scales.data_ptr(),
+        None if bias is None else bias.data_ptr(), M, N, K, out_dtype, out.data_ptr(),
+        _row_stride(out, "out"), _stream(stream)))
     return out

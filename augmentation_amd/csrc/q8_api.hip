@@ -122,7 +122,7 @@ struct RowShape {
 constexpr RowShape kRowShapes[] = {{7, 1, 0},     {8, 1, 1},      {64, 8, 1},     {128, 8, 2},
                                    {256, 32, 1},  {512, 32, 2},   {768, 32, 3},   {1024, 64, 2},
                                    {2048, 64, 4}, {4096, 256, 2}, {6144, 256, 3}, {8192, 512, 2},
-                                   {16384, 1024, 2}, {32768, 1024, 4}};
+                                   {16384, 512, 4}, {32768, 1024, 4}};
 
 RowShape row_shape(int32_t width, int32_t widest) {
   for (const RowShape& s : kRowShapes)
@@ -156,7 +156,7 @@ void launch_rows(const fn::RowArgs& a, hipStream_t st) {
     case shape_key(256, 2): return launch_rows_k<T, kMode, 256, 2>(a, st);
     case shape_key(256, 3): return launch_rows_k<T, kMode, 256, 3>(a, st);
     case shape_key(512, 2): return launch_rows_k<T, kMode, 512, 2>(a, st);
-    case shape_key(1024, 2): return launch_rows_k<T, kMode, 1024, 2>(a, st);
+    case shape_key(512, 4): return launch_rows_k<T, kMode, 512, 4>(a, st);
     case shape_key(1024, 4): return launch_rows_k<T, kMode, 1024, 4>(a, st);
     default:
       fn::rows_wide_kernel<T, kMode>
@@ -235,6 +235,7 @@ struct BackwardPlan {
   int32_t partials, pitch;
   int64_t rows_per_slice;
   int64_t bytes;
+  bool direct;
 };
 
 BackwardPlan plan_backward(int64_t rows, int32_t width) {
@@ -243,8 +244,13 @@ BackwardPlan plan_backward(int64_t rows, int32_t width) {
   p.pitch = (width + 3) / 4 * 4;
   if (p.shape.threads > 0) {
     const int64_t at_once = p.shape.threads < 256 ? 256 / p.shape.threads : 1;
-    p.partials = (int32_t)std::min<int64_t>((rows + at_once - 1) / at_once, at_once > 1 ? 512 : 256);
-    p.bytes = (int64_t)p.partials * p.pitch * 4;
+    const int64_t groups = (rows + at_once - 1) / at_once;
+    p.partials = (int32_t)std::min<int64_t>(groups, at_once > 1 ? 512 : 256);
+    // so few rows that one work-group's sums are the gradient: it does two
+    // groups of rows in less time than the second launch takes
+    p.direct = groups == 1 || groups == 2;
+    if (p.direct) p.partials = 1;
+    p.bytes = p.direct ? 0 : (int64_t)p.partials * p.pitch * 4;
     return p;
   }
   const int64_t slices = std::min<int64_t>(rows, 64);
@@ -275,7 +281,7 @@ void launch_backward(const fn::BackwardArgs& a, const RowShape& s, hipStream_t s
     case shape_key(256, 2): return launch_backward_k<T, 256, 2>(a, st);
     case shape_key(256, 3): return launch_backward_k<T, 256, 3>(a, st);
     case shape_key(512, 2): return launch_backward_k<T, 512, 2>(a, st);
-    case shape_key(1024, 2): return launch_backward_k<T, 1024, 2>(a, st);
+    case shape_key(512, 4): return launch_backward_k<T, 512, 4>(a, st);
     default: {
       fn::rows_backward_mean_kernel<T>
           <<<(unsigned)std::min<int64_t>(a.rows, 1 << 20), 1024, 0, st>>>(a);
@@ -481,7 +487,7 @@ FN_EXPORT int fn_rms_norm_backward(const void* dout_dev, int64_t dout_stride, co
   a.rstd = rstd_dev;
   a.dsum = dsum_dev;
   a.dx = dx_dev;
-  a.partial = (float*)workspace_dev;
+  a.partial = plan.direct ? dweight_dev : (float*)workspace_dev;
   a.row_mean = (float*)workspace_dev + (int64_t)plan.partials * plan.pitch;
   a.rows = rows;
   a.dout_stride = dout_stride;
@@ -501,6 +507,7 @@ FN_EXPORT int fn_rms_norm_backward(const void* dout_dev, int64_t dout_stride, co
     else
       launch_backward<fn::BF16>(a, plan.shape, st);
     FN_TRY(launch_status("rows_backward_kernel launch"));
+    if (plan.direct) return ok();
   }
   // no rows: no partial sums, and a gradient of zero
   fn::column_sum_kernel<<<blocks_for(width, 64), 1024, 0, st>>>(a.partial, a.partials, a.pitch,

@@ -594,7 +594,9 @@ __global__ __launch_bounds__(rows_block<kThreads>()) void rows_backward_kernel(B
 #pragma unroll
   for (int k = 0; k < kChunks; ++k) trim_chunk<kShort>(w[k], c[k]);
   const bool add = a.dsum != nullptr;
-  // the next row is on its way while this one is worked on
+  // the next row is on its way while this one is worked on, where there are
+  // registers for both
+  constexpr bool kAhead = kChunks * sizeof(T) <= 12;
   struct Row {
     Vec8<T> d[kChunks], h[kChunks], s[kChunks];
     float rstd;
@@ -619,10 +621,11 @@ __global__ __launch_bounds__(rows_block<kThreads>()) void rows_backward_kernel(B
   Row next;
 #pragma unroll
   for (int k = 0; k < kChunks; ++k) next.s[k].zero();
-  if (row < a.rows) load(next, row);
+  if (kAhead && row < a.rows) load(next, row);
   for (int parity = 0; row < a.rows; row += step, parity ^= 1) {
+    if (!kAhead) load(next, row);
     Row now = next;
-    if (row + step < a.rows) load(next, row + step);
+    if (kAhead && row + step < a.rows) load(next, row + step);
     auto &d = now.d, &h = now.h, &s = now.s;
     const float rstd = now.rstd;
 #pragma unroll

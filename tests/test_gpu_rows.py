@@ -466,7 +466,8 @@ def test_refusals_on_device_buffers(fn):
     refused("overlap", fn.rms_norm_backward, buf[:10], x, w, torch.ones(10, device="cuda"),
             dx=buf[5:15])
     small = torch.zeros(2, dtype=torch.float32, device="cuda")
-    refused("workspace", fn.rms_norm_backward, x, x, w, torch.ones(10, device="cuda"),
+    many = torch.zeros(3000, 64, dtype=t, device="cuda")
+    refused("workspace", fn.rms_norm_backward, many, many, w, torch.ones(3000, device="cuda"),
             workspace=small)
     refused("x_dev", fn.fn_rms_norm, torch.zeros(10, 64, dtype=t), 64, None, 0, w, 10, 64, 1e-6, 1,
             None, 0, buf, 64, None)

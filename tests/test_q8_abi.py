@@ -79,7 +79,7 @@ BACK = dict(dout=None, dout_stride=64, h=None, h_stride=64, weight=None, rstd=No
 
 @pytest.mark.parametrize("kw,code,word", [
     (dict(rows=-1), -1, "rows"), (dict(width=0), -1, "width"), (dict(dtype=7), -1, "dtype"),
-    (dict(workspace_bytes=0), -1, "workspace"), (dict(h_stride=-2), -1, "negative"),
+    (dict(rows=4000, workspace_bytes=0), -1, "workspace"), (dict(h_stride=-2), -1, "negative"),
     (dict(dx_stride=1), -1, "shorter"), (dict(dsum=4096, dsum_stride=-1), -1, "negative"),
     (dict(), -1, "dout_dev is NULL"), (dict(rows=0), -1, "dweight_dev is NULL"),
 ])
@@ -98,8 +98,10 @@ def test_backward_workspace_sizes(b):
     last = 0
     for rows in (1, 5, 100, 10_000, 10_000_000):
         size = b.fn_rms_norm_backward_workspace(rows, 768)
-        # whole rows of partial sums, more of them for more rows, up to a limit
-        assert size >= last and size % (768 * 4) == 0 and 768 * 4 <= size <= 4096 * 768 * 4
+        # whole rows of partial sums, more of them for more rows, up to a
+        # limit; none where one work-group's sums are the gradient
+        assert size >= last and size % (768 * 4) == 0 and size <= 4096 * 768 * 4
+        assert (size == 0) == (rows <= 5)
         last = size
     # wide rows add one fp32 number for each row
     wide = b.fn_rms_norm_backward_workspace(1000, 50_000)

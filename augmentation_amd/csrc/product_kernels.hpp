@@ -576,68 +576,75 @@ __global__ __launch_bounds__(64 * kWaves) void product_split_kernel(ProductArgs 
   join_waves<T, kMT, kNT, kWaves>(p, acc, reinterpret_cast<int*>(s_ring), m0, n0);
 }
 
-// Few tokens, rows that start at any byte, any K: product_split_kernel's
-// division of the work, with a line's codes read straight into the fragments'
-// registers (lane l: 16 codes of row l % 16), kLines lines of 128 at once.
-
-template <typename T, int kMT, int kNT, int kLines>
-__global__ __launch_bounds__(512) void product_few_kernel(ProductArgs p) {
-  constexpr int kWaves = 8, kTiles = kMT * kNT;
-  __shared__ __align__(16) int s_sum[kWaves * kTiles * 256];
+// Few tokens, rows that start at any byte, any K: product_split_kernel with the
+// lines through registers, two of them under way.  Eight lanes read a row's
+// 128 codes, which costs unaligned loads little (fragments read straight from
+// memory, 64 bytes of a row at a time, took 128x794x2502 16.8 us against 7.7,
+// 1x4096x4095 10.2 against 5.6).  A wavefront writes a line to its own piece of
+// LDS and reads it back as fragments; its LDS operations take effect in their
+// order, and nobody else's matter.
+template <typename T, int kMT, int kNT, int kWaves>
+__global__ __launch_bounds__(64 * kWaves) void product_split_any_kernel(ProductArgs p) {
+  constexpr int kRows = 16 * (kMT + kNT), kLoads = kRows / 8;
+  constexpr int kLine = kRows * kBK, kSums = kMT * kNT * 1024;
+  __shared__ __align__(1024) int8_t s_lines[kWaves * (kLine > kSums ? kLine : kSums)];
   const int lane = (int)(threadIdx.x & 63u);
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int64_t n0 = (int64_t)blockIdx.x * (16 * kNT), m0 = (int64_t)blockIdx.y * (16 * kMT);
-  const int row = lane & 15, part = 16 * (lane >> 4);
-  const int8_t *pa[kMT], *pb[kNT];  // null: no such row
+  const int8_t* from[kLoads];  // the channels' rows first, then the tokens'; null: no such row
 #pragma unroll
-  for (int i = 0; i < kMT; ++i) {
-    const int64_t m = m0 + 16 * i + row;
-    pa[i] = m < p.M ? p.a + m * p.a_stride + part : nullptr;
+  for (int i = 0; i < kLoads; ++i) {
+    const int r = 8 * i + lane / 8;
+    const int64_t n = n0 + r, m = m0 + r - 16 * kNT;
+    from[i] = i < 2 * kNT ? (n < p.N ? p.b + n * p.b_stride : nullptr)
+                          : (m < p.M ? p.a + m * p.a_stride : nullptr);
   }
-#pragma unroll
-  for (int j = 0; j < kNT; ++j) {
-    const int64_t n = n0 + 16 * j + row;
-    pb[j] = n < p.N ? p.b + n * p.b_stride + part : nullptr;
-  }
+  int8_t* line = s_lines + wave * kLine;
+  const int at[2] = {(lane & 15) * kBK + 16 * staged_piece(lane & 15, lane >> 4),
+                     (lane & 15) * kBK + 16 * staged_piece(lane & 15, 4 + (lane >> 4))};
   i32x4 acc[kMT][kNT] = {};
-  for (int k0 = wave * 128; k0 < p.K; k0 += kWaves * kLines * 128) {
-    i32x4 fa[kLines][2][kMT], fb[kLines][2][kNT];
-    // the same lines with and without a look at where K ends
-    auto load = [&](auto whole) {
+  i32x4 held[2][kLoads];
+  auto load = [&](i32x4 (&to)[kLoads], int k0) {
+    if (k0 >= p.K) return;
 #pragma unroll
-      for (int l = 0; l < kLines; ++l)
+    for (int i = 0; i < kLoads; ++i)
+      to[i] = from[i] != nullptr ? load16(from[i], k0 + 16 * (lane % 8), p.K) : i32x4{0, 0, 0, 0};
+  };
+  auto multiply = [&](const i32x4 (&codes)[kLoads]) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int k = k0 + l * (kWaves * 128) + 64 * h;
-          auto get = [&](const int8_t* row_at) {
-            if (row_at == nullptr) return i32x4{0, 0, 0, 0};
-            if constexpr (decltype(whole)::value)
-              return i32x4(*reinterpret_cast<const i32x4_any*>(row_at + k));
-            else
-              return load16(row_at - part, k + part, p.K);
-          };
+    for (int i = 0; i < kLoads; ++i) {
+      const int r = 8 * i + lane / 8;
+      *reinterpret_cast<i32x4*>(line + r * kBK + 16 * staged_piece(r, lane % 8)) = codes[i];
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
 #pragma unroll
-          for (int j = 0; j < kNT; ++j) fb[l][h][j] = get(pb[j]);
+    for (int h = 0; h < 2; ++h) {
+      i32x4 fa[kMT], fb[kNT];
 #pragma unroll
-          for (int i = 0; i < kMT; ++i) fa[l][h][i] = get(pa[i]);
-        }
-    };
-    if (k0 + ((kLines - 1) * kWaves + 1) * 128 <= p.K)
-      load(std::true_type{});
-    else
-      load(std::false_type{});
+      for (int j = 0; j < kNT; ++j)
+        fb[j] = *reinterpret_cast<const i32x4*>(line + 16 * j * kBK + at[h]);
 #pragma unroll
-    for (int l = 0; l < kLines; ++l)
+      for (int i = 0; i < kMT; ++i)
+        fa[i] = *reinterpret_cast<const i32x4*>(line + 16 * (kNT + i) * kBK + at[h]);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int i = 0; i < kMT; ++i)
 #pragma unroll
-        for (int i = 0; i < kMT; ++i)
-#pragma unroll
-          for (int j = 0; j < kNT; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[l][h][j], fa[l][h][i], acc[i][j],
-                                                              0, 0, 0);
+        for (int j = 0; j < kNT; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  };
+  constexpr int kStride = kWaves * kBK;
+  load(held[0], wave * kBK);
+  load(held[1], wave * kBK + kStride);
+  for (int k0 = wave * kBK; k0 < p.K; k0 += 2 * kStride) {
+    multiply(held[0]);
+    load(held[0], k0 + 2 * kStride);
+    if (k0 + kStride < p.K) multiply(held[1]);
+    load(held[1], k0 + 3 * kStride);
   }
-  join_waves<T, kMT, kNT, kWaves>(p, acc, s_sum, m0, n0);
+  __syncthreads();
+  join_waves<T, kMT, kNT, kWaves>(p, acc, reinterpret_cast<int*>(s_lines), m0, n0);
 }
 
 }  // namespace fn

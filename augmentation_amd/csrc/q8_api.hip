@@ -302,11 +302,13 @@ unsigned tile_grid(fn::ProductArgs* p) {
   return (unsigned)(tm * tn);
 }
 
-// The time of a product in tiles, in relative units: n tiles on the busiest of
-// `cus` compute units at `each`, or `alone` where none has a second.
-double tile_cost(int64_t M, int64_t N, int bm, int bn, int cus, double alone, double each) {
+// The time of a product in tiles, in relative units: `first` and `each` for
+// every tile on the busiest of `cus` compute units, or `alone` where none has
+// a second.
+double tile_cost(int64_t M, int64_t N, int bm, int bn, int cus, double alone, double first,
+                 double each) {
   const double n = std::ceil((double)((M + bm - 1) / bm) * (double)((N + bn - 1) / bn) / cus);
-  return n <= 1.0 ? alone : n * each;
+  return n <= 1.0 ? alone : first + n * each;
 }
 
 template <typename T, int kBM, int kBN, int kWM, int kWN, int kStages>
@@ -332,14 +334,14 @@ bool split_grid(const fn::ProductArgs& p, dim3* grid) {
   return x <= 0x7FFFFFFF && y <= 65535;
 }
 
-template <typename T, int kMT, int kNT>
-bool launch_split(const fn::ProductArgs& p, bool pieces, hipStream_t st) {
+template <typename T, int kMT, int kNT, bool kPieces>
+bool launch_split(const fn::ProductArgs& p, hipStream_t st) {
   dim3 grid;
   if (!split_grid<kMT, kNT>(p, &grid)) return false;
-  if (pieces)
+  if constexpr (kPieces)
     fn::product_split_kernel<T, kMT, kNT, 2, 8><<<grid, 512, 0, st>>>(p);
   else
-    fn::product_few_kernel<T, kMT, kNT, 2><<<grid, 512, 0, st>>>(p);
+    fn::product_split_any_kernel<T, kMT, kNT, 8><<<grid, 512, 0, st>>>(p);
   return true;
 }
 
@@ -359,9 +361,10 @@ bool launch_split(const fn::ProductArgs& p, bool pieces, hipStream_t st) {
 // 483 / 611 / 783; 4096^3 57 / 68 / 85 / 102; 4096x2048x4096 45 / 35 / 41 /
 // 53; 256x8192x4096 42 / 25 / 14.8 / 16.6; 1024x1024x8192 74 / 42 / 23 / 17.7.
 //
-// Rows that start anywhere, tiles of 256x128, 128x64 and 64x64: 4000x4000x4001
-// 110 / 160 / 197; 1999x1000x1021 18.5 / 11.0 / 11.7; 300x1024x777 16.5 / 8.8
-// / 7.1.
+// Rows that start anywhere: groups of 32x16 take the place of 32x32
+// (128x794x2502 6.1 against 7.7, 32x4096x4095 8.8 against 11.5); tiles of
+// 256x128, 128x64 and 64x64: 4000x4000x4001 110 / 160 / 197; 1999x1000x1021
+// 18.5 / 11.0 / 11.7; 300x1024x777 16.5 / 8.8 / 7.1.
 template <typename T>
 int launch_product(fn::ProductArgs p, int cus, hipStream_t st) {
   // whole 16-byte pieces from 16-byte aligned rows, a tile's rows within the
@@ -371,16 +374,18 @@ int launch_product(fn::ProductArgs p, int cus, hipStream_t st) {
                       std::max(p.a_stride, p.b_stride) <= (0x7FFFFFF0 - 131072) / 256;
   const int64_t groups = ((p.M + 31) / 32) * std::min((p.N + 31) / 32, (int64_t)1 << 32);
   bool launched = false;
-  if (p.M <= 16) {
-    launched = !pieces || (p.N + 15) / 16 <= 2 * cus ? launch_split<T, 1, 1>(p, pieces, st)
-                                                     : launch_split<T, 1, 4>(p, pieces, st);
+  if (p.M <= 16 && !pieces) {
+    launched = launch_split<T, 1, 1, false>(p, st);
+  } else if (p.M <= 16) {
+    launched = (p.N + 15) / 16 <= 2 * cus ? launch_split<T, 1, 1, true>(p, st)
+                                          : launch_split<T, 1, 4, true>(p, st);
   } else if (groups <= cus) {
-    launched = launch_split<T, 2, 2>(p, pieces, st);
+    launched = pieces ? launch_split<T, 2, 2, true>(p, st) : launch_split<T, 2, 1, false>(p, st);
   } else if (pieces) {
-    const double c[4] = {tile_cost(p.M, p.N, 256, 256, cus, 57, 57),
-                         tile_cost(p.M, p.N, 128, 128, cus, 22.7, 17.3),
-                         tile_cost(p.M, p.N, 128, 64, cus, 14.8, 10.3),
-                         tile_cost(p.M, p.N, 64, 64, cus, 8.9, 6.5)};
+    const double c[4] = {tile_cost(p.M, p.N, 256, 256, cus, 57, 0, 57),
+                         tile_cost(p.M, p.N, 128, 128, cus, 22.7, 0, 17.3),
+                         tile_cost(p.M, p.N, 128, 64, cus, 14.8, 0, 10.3),
+                         tile_cost(p.M, p.N, 64, 64, cus, 8.9, 3.5, 6.3)};
     switch (std::min_element(c, c + 4) - c) {
       case 0: launched = launch_tiles<T, 256, 256, 2, 4, 2>(p, st); break;
       case 1: launched = launch_tiles<T, 128, 128, 2, 2, 2>(p, st); break;
@@ -388,9 +393,9 @@ int launch_product(fn::ProductArgs p, int cus, hipStream_t st) {
       default: launched = launch_tiles<T, 64, 64, 2, 2, 4>(p, st);
     }
   } else {
-    const double c[3] = {tile_cost(p.M, p.N, 256, 128, cus, 60, 55),
-                         tile_cost(p.M, p.N, 128, 64, cus, 30, 20),
-                         tile_cost(p.M, p.N, 64, 64, cus, 20, 12.3)};
+    const double c[3] = {tile_cost(p.M, p.N, 256, 128, cus, 60, 0, 55),
+                         tile_cost(p.M, p.N, 128, 64, cus, 30, 0, 20),
+                         tile_cost(p.M, p.N, 64, 64, cus, 20, 0, 12.3)};
     switch (std::min_element(c, c + 3) - c) {
       case 0: launched = launch_any<T, 256, 128>(p, st); break;
       case 1: launched = launch_any<T, 128, 64>(p, st); break;

@@ -319,6 +319,53 @@ bool launch_tiles(fn::ProductArgs& p, hipStream_t st) {
   return grid != 0;
 }
 
+// The cheapest of the four tiles for M tokens, and its cost.
+int best_tile(int64_t M, int64_t N, int cus, double* cost) {
+  const double c[4] = {tile_cost(M, N, 256, 256, cus, 57, 0, 57),
+                       tile_cost(M, N, 128, 128, cus, 22.7, 0, 17.3),
+                       tile_cost(M, N, 128, 64, cus, 14.8, 0, 10.3),
+                       tile_cost(M, N, 64, 64, cus, 8.9, 3.5, 6.3)};
+  const int best = (int)(std::min_element(c, c + 4) - c);
+  *cost = c[best];
+  return best;
+}
+
+template <typename T>
+bool launch_tiles_of(int tile, fn::ProductArgs& p, hipStream_t st) {
+  switch (tile) {
+    case 0: return launch_tiles<T, 256, 256, 2, 4, 2>(p, st);
+    case 1: return launch_tiles<T, 128, 128, 2, 2, 2>(p, st);
+    case 2: return launch_tiles<T, 128, 64, 2, 2, 3>(p, st);
+    default: return launch_tiles<T, 64, 64, 2, 2, 4>(p, st);
+  }
+}
+
+// One launch, or two: the tokens that give every compute unit the same number
+// of 256x256 tiles, and the rest in whatever tiles suit them, where that costs
+// less than a last round of tiles on a few compute units (a launch is 4 us;
+// costs are for K = 4096).
+template <typename T>
+bool launch_tiles_best(fn::ProductArgs& p, int cus, hipStream_t st) {
+  double cost = 0.0, rest_cost = 0.0;
+  int tile = best_tile(p.M, p.N, cus, &cost);
+  const int64_t tiles_n = (p.N + 255) / 256, rounds = p.M / 256 * tiles_n / cus;
+  const int64_t head = tiles_n <= cus ? rounds * cus / tiles_n * 256 : 0;
+  if (head > 0 && head < p.M) {
+    const int rest = best_tile(p.M - head, p.N, cus, &rest_cost);
+    if (rounds * 57 + rest_cost + 4.0 * 4096 / std::max(p.K, 64) < cost) {
+      fn::ProductArgs first = p;
+      first.M = head;
+      if (!launch_tiles_of<T>(0, first, st)) return false;
+      p.a += head * p.a_stride;
+      p.sa += head;
+      p.out = (T*)p.out + head * p.out_stride;
+      p.M -= head;
+      tile = rest;
+    }
+  }
+  return launch_tiles_of<T>(tile, p, st);
+}
+
 template <typename T, int kBM, int kBN>
 bool launch_any(fn::ProductArgs& p, hipStream_t st) {
   const unsigned grid = tile_grid<kBM, kBN>(&p);
@@ -372,7 +419,7 @@ int launch_product(fn::ProductArgs p, int cus, hipStream_t st) {
   const bool pieces = ((uintptr_t)p.a | (uintptr_t)p.b | (uint64_t)p.a_stride |
                        (uint64_t)p.b_stride | (uint64_t)p.K) % 16 == 0 &&
                       std::max(p.a_stride, p.b_stride) <= (0x7FFFFFF0 - 131072) / 256;
-  const int64_t groups = ((p.M + 31) / 32) * std::min((p.N + 31) / 32, (int64_t)1 << 32);
+  const double groups = std::ceil(p.M / 32.0) * std::ceil(p.N / 32.0);
   bool launched = false;
   if (p.M <= 16 && !pieces) {
     launched = launch_split<T, 1, 1, false>(p, st);
@@ -382,16 +429,7 @@ int launch_product(fn::ProductArgs p, int cus, hipStream_t st) {
   } else if (groups <= cus) {
     launched = pieces ? launch_split<T, 2, 2, true>(p, st) : launch_split<T, 2, 1, false>(p, st);
   } else if (pieces) {
-    const double c[4] = {tile_cost(p.M, p.N, 256, 256, cus, 57, 0, 57),
-                         tile_cost(p.M, p.N, 128, 128, cus, 22.7, 0, 17.3),
-                         tile_cost(p.M, p.N, 128, 64, cus, 14.8, 0, 10.3),
-                         tile_cost(p.M, p.N, 64, 64, cus, 8.9, 3.5, 6.3)};
-    switch (std::min_element(c, c + 4) - c) {
-      case 0: launched = launch_tiles<T, 256, 256, 2, 4, 2>(p, st); break;
-      case 1: launched = launch_tiles<T, 128, 128, 2, 2, 2>(p, st); break;
-      case 2: launched = launch_tiles<T, 128, 64, 2, 2, 3>(p, st); break;
-      default: launched = launch_tiles<T, 64, 64, 2, 2, 4>(p, st);
-    }
+    launched = launch_tiles_best<T>(p, cus, st);
   } else {
     const double c[3] = {tile_cost(p.M, p.N, 256, 128, cus, 60, 0, 55),
                          tile_cost(p.M, p.N, 128, 64, cus, 30, 0, 20),

@@ -17,12 +17,15 @@ ROUTES = {
     "few tokens, groups of 64 channels": (9, 8501, 272),
     "few tokens, groups of 64 channels, whole": (16, 16384, 256),
     "32 x 32 groups": (61, 4001, 1040),
-    "64 x 64 tiles": (150, 6001, 400),
+    "128 x 64 tiles, the second row in part": (150, 6001, 400),
+    "64 x 64 tiles": (100, 4001, 400),
     "128 x 64 tiles": (500, 4090, 272),
     "128 x 128 tiles": (4090, 2040, 400),
     "256 x 256 tiles": (4090, 4070, 400),
     "256 x 256 tiles, whole": (4096, 4096, 128),
     "256 x 256 tiles, one stage in part": (4095, 4095, 48),
+    "whole rounds of 256 x 256 tiles, and the rest": (16677, 1024, 1296),
+    "whole rounds of 256 x 256 tiles, and a few tokens": (8195, 2047, 2048),
     "any row, few tokens": (11, 5001, 1033),
     "any row, 32 x 16 groups": (100, 1001, 2049),
     "any row, 64 x 64 tiles": (700, 1001, 333),

@@ -315,7 +315,7 @@ template <typename T, int kBM, int kBN, int kWM, int kWN, int kStages>
 bool launch_tiles(fn::ProductArgs& p, hipStream_t st) {
   const unsigned grid = tile_grid<kBM, kBN>(&p);
   if (grid)
-    fn::product_tile_kernel<T, kBM, kBN, kWM, kWN, kStages, 2><<<grid, 64 * kWM * kWN, 0, st>>>(p);
+    fn::product_tile_kernel<T, kBM, kBN, kWM, kWN, kStages><<<grid, 64 * kWM * kWN, 0, st>>>(p);
   return grid != 0;
 }
 

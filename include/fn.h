@@ -16,7 +16,9 @@
  *   - section 12: the rectangle sampler (gate, up to 10 attempts of area
  *     fraction and log aspect ratio, rounding, acceptance, corner).
  * The page runs this per image on CPU threads; here one call processes a
- * whole batch on one GPU.
+ * whole batch on one GPU.  The operators of a model's 8-bit linear layer
+ * follow at the end: a norm that quantises, row quantisation, the product of
+ * the codes and the norm's gradients.
  *
  * Conventions for every entry point:
  *   - Pointers named *_dev are device memory (hipMalloc or a PyTorch CUDA

@@ -598,7 +598,7 @@ __global__ __launch_bounds__(rows_block<kThreads>()) void rows_backward_kernel(B
   const bool add = a.dsum != nullptr;
   // the next row is on its way while this one is worked on, where there are
   // registers for both
-  constexpr bool kAhead = kChunks * sizeof(T) <= 12;
+  constexpr bool kAhead = kChunks <= 3;
   struct Row {
     Vec8<T> d[kChunks], h[kChunks], s[kChunks];
     float rstd;
@@ -616,18 +616,23 @@ __global__ __launch_bounds__(rows_block<kThreads>()) void rows_backward_kernel(B
       const T* ps = (const T*)a.dsum + row * a.dsum_stride;
 #pragma unroll
       for (int k = 0; k < kChunks; ++k) load_chunk<kShort>(r.s[k], ps, c[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) r.s[k].zero();
     }
   };
   const int64_t step = (int64_t)gridDim.x * kRows;
   int64_t row = (int64_t)blockIdx.x * kRows + slot;
   Row next;
-#pragma unroll
-  for (int k = 0; k < kChunks; ++k) next.s[k].zero();
   if (kAhead && row < a.rows) load(next, row);
   for (int parity = 0; row < a.rows; row += step, parity ^= 1) {
-    if (!kAhead) load(next, row);
-    Row now = next;
-    if (kAhead && row + step < a.rows) load(next, row + step);
+    Row now;
+    if constexpr (kAhead) {
+      now = next;
+      if (row + step < a.rows) load(next, row + step);
+    } else {
+      load(now, row);
+    }
     auto &d = now.d, &h = now.h, &s = now.s;
     const float rstd = now.rstd;
 #pragma unroll

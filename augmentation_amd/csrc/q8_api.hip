@@ -112,17 +112,21 @@ int check_size(int64_t rows, int32_t width) {
 
 // Threads per row and chunks of eight elements per thread, by the row's width:
 // the fewest threads that keep a row in registers with all of them at work, a
-// wavefront's part for as long as that will do (no barrier).  0 threads: rows
-// that do not fit.
+// wavefront's part for as long as that will do (no barrier).  Measured, norm to
+// codes with a residual, us: 1000000x12 with 2 / 4 / 8 threads 26 / 36 / 62;
+// 100000x100 with 8 / 16 / 32 24 / 21 / 32; 30000x1500 with 64x3 / 256x1 60 /
+// 74; 30000x2040 backward with 64x4 / 128x2 / 256x1 92 / 99 / 101.
+// 0 threads: rows that do not fit.
 struct RowShape {
   int32_t width;  // up to
   int threads, chunks;
 };
 
-constexpr RowShape kRowShapes[] = {{7, 1, 0},     {8, 1, 1},      {64, 8, 1},     {128, 8, 2},
-                                   {256, 32, 1},  {512, 32, 2},   {768, 32, 3},   {1024, 64, 2},
-                                   {2048, 64, 4}, {4096, 256, 2}, {6144, 256, 3}, {8192, 512, 2},
-                                   {16384, 512, 4}, {32768, 1024, 4}};
+constexpr RowShape kRowShapes[] = {{7, 1, 0},      {8, 1, 1},      {16, 2, 1},     {32, 4, 1},
+                                   {64, 8, 1},     {128, 16, 1},   {256, 16, 2},   {512, 32, 2},
+                                   {768, 32, 3},   {1024, 64, 2},  {1536, 64, 3},  {2048, 64, 4},
+                                   {4096, 256, 2}, {6144, 256, 3}, {8192, 512, 2}, {16384, 512, 4},
+                                   {32768, 1024, 4}};
 
 RowShape row_shape(int32_t width, int32_t widest) {
   for (const RowShape& s : kRowShapes)
@@ -130,7 +134,7 @@ RowShape row_shape(int32_t width, int32_t widest) {
   return {0, 0, 0};
 }
 
-constexpr int shape_key(int threads, int chunks) { return threads * 8 + chunks; }
+constexpr int shape_key(int threads, int chunks) { return threads * 16 + chunks; }
 
 template <typename T, int kMode, int kThreads, int kChunks, bool kShort = false>
 void launch_rows_k(const fn::RowArgs& a, hipStream_t st) {
@@ -146,17 +150,26 @@ void launch_rows(const fn::RowArgs& a, hipStream_t st) {
   switch (shape_key(s.threads, s.chunks)) {
     case shape_key(1, 0): return launch_rows_k<T, kMode, 1, 1, true>(a, st);
     case shape_key(1, 1): return launch_rows_k<T, kMode, 1, 1>(a, st);
+    case shape_key(2, 1): return launch_rows_k<T, kMode, 2, 1>(a, st);
+    case shape_key(4, 1): return launch_rows_k<T, kMode, 4, 1>(a, st);
     case shape_key(8, 1): return launch_rows_k<T, kMode, 8, 1>(a, st);
-    case shape_key(8, 2): return launch_rows_k<T, kMode, 8, 2>(a, st);
-    case shape_key(32, 1): return launch_rows_k<T, kMode, 32, 1>(a, st);
+    case shape_key(16, 1): return launch_rows_k<T, kMode, 16, 1>(a, st);
+    case shape_key(16, 2): return launch_rows_k<T, kMode, 16, 2>(a, st);
     case shape_key(32, 2): return launch_rows_k<T, kMode, 32, 2>(a, st);
     case shape_key(32, 3): return launch_rows_k<T, kMode, 32, 3>(a, st);
     case shape_key(64, 2): return launch_rows_k<T, kMode, 64, 2>(a, st);
+    case shape_key(64, 3): return launch_rows_k<T, kMode, 64, 3>(a, st);
     case shape_key(64, 4): return launch_rows_k<T, kMode, 64, 4>(a, st);
     case shape_key(256, 2): return launch_rows_k<T, kMode, 256, 2>(a, st);
     case shape_key(256, 3): return launch_rows_k<T, kMode, 256, 3>(a, st);
     case shape_key(512, 2): return launch_rows_k<T, kMode, 512, 2>(a, st);
-    case shape_key(512, 4): return launch_rows_k<T, kMode, 512, 4>(a, st);
+    case shape_key(512, 4):
+      // rows of 16 bits have registers for half the threads (12000x12344 to
+      // codes: 214 us against 260)
+      if constexpr (sizeof(T) == 2)
+        return launch_rows_k<T, kMode, 256, 8>(a, st);
+      else
+        return launch_rows_k<T, kMode, 512, 4>(a, st);
     case shape_key(1024, 4): return launch_rows_k<T, kMode, 1024, 4>(a, st);
     default:
       fn::rows_wide_kernel<T, kMode>
@@ -225,9 +238,9 @@ int norm(const void* x, int64_t x_stride, const void* residual, int64_t residual
 }
 
 // Work-groups of the backward kernels, each with one row of partial sums: two
-// for each unit of a 256-unit device where they take several rows at a time,
-// one where a row takes all of it (measured for 256 / 512 / 1,024 partial rows,
-// with their sum, in us: 50176x768 - / 59 / 61, 8192x4096 50 / 53 / 62,
+// for each unit of a 256-unit device for rows of up to 1,024 elements, one for
+// wider ones (measured for 256 / 512 / 1,024 partial rows, with their sum, in
+// us: 50176x768 - / 59 / 61, 30000x1500 68 / 72 / 77, 8192x4096 50 / 53 / 62,
 // 16384x8192 176 / 180 / -, 4099x5003 47 / 48 / 57).  A function of the sizes
 // alone, so that results do not depend on the device.
 struct BackwardPlan {
@@ -243,9 +256,9 @@ BackwardPlan plan_backward(int64_t rows, int32_t width) {
   p.shape = row_shape(width, 16384);
   p.pitch = (width + 3) / 4 * 4;
   if (p.shape.threads > 0) {
-    const int64_t at_once = p.shape.threads < 256 ? 256 / p.shape.threads : 1;
+    const int64_t at_once = p.shape.threads <= 64 ? 256 / p.shape.threads : 1;
     const int64_t groups = (rows + at_once - 1) / at_once;
-    p.partials = (int32_t)std::min<int64_t>(groups, at_once > 1 ? 512 : 256);
+    p.partials = (int32_t)std::min<int64_t>(groups, width <= 1024 ? 512 : 256);
     // so few rows that one work-group's sums are the gradient: it does two
     // groups of rows in less time than the second launch takes
     p.direct = groups == 1 || groups == 2;
@@ -271,12 +284,15 @@ void launch_backward(const fn::BackwardArgs& a, const RowShape& s, hipStream_t s
   switch (shape_key(s.threads, s.chunks)) {
     case shape_key(1, 0): return launch_backward_k<T, 1, 1, true>(a, st);
     case shape_key(1, 1): return launch_backward_k<T, 1, 1>(a, st);
+    case shape_key(2, 1): return launch_backward_k<T, 2, 1>(a, st);
+    case shape_key(4, 1): return launch_backward_k<T, 4, 1>(a, st);
     case shape_key(8, 1): return launch_backward_k<T, 8, 1>(a, st);
-    case shape_key(8, 2): return launch_backward_k<T, 8, 2>(a, st);
-    case shape_key(32, 1): return launch_backward_k<T, 32, 1>(a, st);
+    case shape_key(16, 1): return launch_backward_k<T, 16, 1>(a, st);
+    case shape_key(16, 2): return launch_backward_k<T, 16, 2>(a, st);
     case shape_key(32, 2): return launch_backward_k<T, 32, 2>(a, st);
     case shape_key(32, 3): return launch_backward_k<T, 32, 3>(a, st);
     case shape_key(64, 2): return launch_backward_k<T, 64, 2>(a, st);
+    case shape_key(64, 3): return launch_backward_k<T, 64, 3>(a, st);
     case shape_key(64, 4): return launch_backward_k<T, 64, 4>(a, st);
     case shape_key(256, 2): return launch_backward_k<T, 256, 2>(a, st);
     case shape_key(256, 3): return launch_backward_k<T, 256, 3>(a, st);

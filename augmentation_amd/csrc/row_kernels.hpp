@@ -230,9 +230,9 @@ __device__ __forceinline__ void store_chunk(const Vec8<T>& v, T* row, const Chun
 
 // --------------------------------------------------------------- reductions
 // Sum (or unsigned maximum) over aligned groups of kLanes lanes of a
-// wavefront, the same bits in each of them, without LDS: exchanges with the
-// neighbour, the neighbouring pair, the mirror image in 8 and 16 lanes, the
-// next 16 and the other 32.  The order is fixed, so a result never changes
+// wavefront (1 to 64, a power of two), the same bits in each of them, without
+// LDS: exchanges with the neighbour, the neighbouring pair, the mirror image in
+// 8 and 16 lanes, the next 16 and the other 32.  The order is fixed, so a result never changes
 // from run to run.
 
 template <int kCtrl>
@@ -242,11 +242,9 @@ __device__ __forceinline__ uint32_t dpp(uint32_t v) {
 
 template <int kLanes, typename F>
 __device__ __forceinline__ uint32_t group_fold(uint32_t v, F fold) {
-  if constexpr (kLanes >= 8) {
-    v = fold(v, dpp<0xB1>(v));   // quad_perm 1 0 3 2
-    v = fold(v, dpp<0x4E>(v));   // quad_perm 2 3 0 1
-    v = fold(v, dpp<0x141>(v));  // row_half_mirror
-  }
+  if constexpr (kLanes >= 2) v = fold(v, dpp<0xB1>(v));    // quad_perm 1 0 3 2
+  if constexpr (kLanes >= 4) v = fold(v, dpp<0x4E>(v));    // quad_perm 2 3 0 1
+  if constexpr (kLanes >= 8) v = fold(v, dpp<0x141>(v));   // row_half_mirror
   if constexpr (kLanes >= 16) v = fold(v, dpp<0x140>(v));  // row_mirror
   if constexpr (kLanes >= 32) {
     const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
@@ -281,6 +279,7 @@ __device__ __forceinline__ void row_reduce(float& sum, uint32_t& top, int parity
   sum = group_sum<kThreads>(sum);
   top = group_max<kThreads>(top);
   if constexpr (kThreads > 64) {
+    // the row is the work-group's only one (rows_block)
     constexpr int kWaves = kThreads / 64;
     __shared__ float s_sum[2][kWaves];
     __shared__ uint32_t s_top[2][kWaves];
@@ -369,7 +368,7 @@ __device__ __forceinline__ float row_rstd(float sum_of_squares, int32_t width, f
 // any width up to that when kShort.
 template <int kThreads>
 constexpr int rows_block() {
-  return kThreads < 256 ? 256 : kThreads;
+  return kThreads <= 64 ? 256 : kThreads;
 }
 
 template <typename T, int kMode, int kThreads, int kChunks, bool kShort = false>

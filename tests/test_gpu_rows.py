@@ -482,3 +482,35 @@ def test_refusals_on_device_buffers(fn):
         with pytest.raises(ValueError):
             bad()
     assert not buf.any()
+
+
+MORE_WIDTHS = [3, 4, 5, 6, 10, 12, 16, 17, 24, 28, 31, 32, 33, 100, 127, 128, 129, 200, 255, 256,
+               600, 769, 900, 1500, 1536, 1537, 3000, 6143, 6144, 6145, 10001, 12344, 12345, 20001]
+
+
+@pytest.mark.parametrize("t", TYPES, ids=str)
+@pytest.mark.parametrize("width", MORE_WIDTHS)
+def test_rows_of_every_shape_of_threads(fn, width, t):
+    """The widths at which the threads per row change, and between: more rows
+    than a work-group takes, an odd number of them."""
+    n = 259 if width < 4000 else 21
+    x, r, w = rows(width, n, width, t), rows(width + 1, n, width, t), weights(width, width, t)
+    h, rstd, y = reference(x, r, w)
+    rel = (depth(width) / 2 + 6) * U
+    out, got_rstd, got_h = fn.rms_norm(x, w, EPS, residual=r)
+    assert torch.equal(got_h, h)
+    check_close(got_rstd, rstd, rstd * rel, "rstd")
+    check_close(out, y, y.abs() * (half(t) + rel + 2 * U) + tiny(t), "out")
+    codes, scales, _ = fn.rms_norm_q8(x, w, EPS, residual=r)
+    want, top = codes_of(h.float() * w.float())
+    assert torch.equal(codes.cpu(), want)
+    check_close(scales, top * rstd.cpu() / 127, top * rstd.cpu() / 127 * (rel + 3 * U), "scales")
+    codes, scales = fn.quantize_rows(x)
+    want, top = codes_of(x.float())
+    assert torch.equal(codes.cpu(), want)
+    check_close(scales, top / 127, top / 127 * U + tiny(torch.float32), "scales")
+    dout = rows(width + 2, n, width, t, spread=0.2)
+    dx, dweight = fn.rms_norm_backward(dout, h, w, rstd.float(), dsum=x)
+    want, size, dw, dw_size = backward_reference(dout, h, w, rstd.float(), x)
+    check_close(dx, want, want.abs() * half(t) + size + tiny(t), "dx")
+    check_close(dweight, dw, dw_size * (n + 3 + 32 + 64 + 3) * U + tiny(torch.float32), "dweight")

@@ -115,7 +115,9 @@ int check_size(int64_t rows, int32_t width) {
 // wavefront's part for as long as that will do (no barrier).  Measured, norm to
 // codes with a residual, us: 1000000x12 with 2 / 4 / 8 threads 26 / 36 / 62;
 // 100000x100 with 8 / 16 / 32 24 / 21 / 32; 30000x1500 with 64x3 / 256x1 60 /
-// 74; 30000x2040 backward with 64x4 / 128x2 / 256x1 92 / 99 / 101.
+// 74; 30000x2040 backward with 64x4 / 128x2 / 256x1 92 / 99 / 101; 13000x2560
+// with 64x5 / 256x2 45 / 46, backward 53 / 64, but 300x2560 5.7 / 4.6, which a
+// caller's next launch mostly covers.
 // 0 threads: rows that do not fit.
 struct RowShape {
   int32_t width;  // up to
@@ -125,8 +127,8 @@ struct RowShape {
 constexpr RowShape kRowShapes[] = {{7, 1, 0},      {8, 1, 1},      {16, 2, 1},     {32, 4, 1},
                                    {64, 8, 1},     {128, 16, 1},   {256, 16, 2},   {512, 32, 2},
                                    {768, 32, 3},   {1024, 64, 2},  {1536, 64, 3},  {2048, 64, 4},
-                                   {4096, 256, 2}, {6144, 256, 3}, {8192, 512, 2}, {16384, 512, 4},
-                                   {32768, 1024, 4}};
+                                   {2560, 64, 5},  {4096, 256, 2}, {6144, 256, 3}, {8192, 512, 2},
+                                   {16384, 512, 4}, {32768, 1024, 4}};
 
 RowShape row_shape(int32_t width, int32_t widest) {
   for (const RowShape& s : kRowShapes)
@@ -160,6 +162,7 @@ void launch_rows(const fn::RowArgs& a, hipStream_t st) {
     case shape_key(64, 2): return launch_rows_k<T, kMode, 64, 2>(a, st);
     case shape_key(64, 3): return launch_rows_k<T, kMode, 64, 3>(a, st);
     case shape_key(64, 4): return launch_rows_k<T, kMode, 64, 4>(a, st);
+    case shape_key(64, 5): return launch_rows_k<T, kMode, 64, 5>(a, st);
     case shape_key(256, 2): return launch_rows_k<T, kMode, 256, 2>(a, st);
     case shape_key(256, 3): return launch_rows_k<T, kMode, 256, 3>(a, st);
     case shape_key(512, 2): return launch_rows_k<T, kMode, 512, 2>(a, st);
@@ -294,6 +297,7 @@ void launch_backward(const fn::BackwardArgs& a, const RowShape& s, hipStream_t s
     case shape_key(64, 2): return launch_backward_k<T, 64, 2>(a, st);
     case shape_key(64, 3): return launch_backward_k<T, 64, 3>(a, st);
     case shape_key(64, 4): return launch_backward_k<T, 64, 4>(a, st);
+    case shape_key(64, 5): return launch_backward_k<T, 64, 5>(a, st);
     case shape_key(256, 2): return launch_backward_k<T, 256, 2>(a, st);
     case shape_key(256, 3): return launch_backward_k<T, 256, 3>(a, st);
     case shape_key(512, 2): return launch_backward_k<T, 512, 2>(a, st);

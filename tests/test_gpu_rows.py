@@ -85,7 +85,7 @@ def reference(x, residual, weight):
 
 
 WIDTHS = [1, 2, 7, 8, 9, 15, 63, 64, 65, 257, 511, 512, 513, 768, 1000, 1023, 1024, 1025, 2047,
-          2048, 2049, 4095, 4096, 4097, 5003, 8191, 8192, 8193, 16383, 16384, 16385, 32767, 32768,
+          2048, 2049, 2560, 2561, 4095, 4096, 4097, 5003, 8191, 8192, 8193, 16383, 16384, 16385, 32767, 32768,
           32769, 40001, 65544]
 
 
@@ -195,7 +195,7 @@ def padded(x, left, right, fill):
 
 
 @pytest.mark.parametrize("t", TYPES, ids=str)
-@pytest.mark.parametrize("width", [1, 8, 100, 768, 1021, 2048, 5003, 20000, 33001])
+@pytest.mark.parametrize("width", [1, 8, 100, 768, 1021, 2048, 2243, 2560, 5003, 20000, 33001])
 def test_strided_rows_and_guard_columns(fn, width, t):
     """Inputs and outputs as column ranges at odd offsets: the same results,
     and nothing beside them is written."""

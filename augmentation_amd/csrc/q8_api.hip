@@ -261,7 +261,12 @@ BackwardPlan plan_backward(int64_t rows, int32_t width) {
   if (p.shape.threads > 0) {
     const int64_t at_once = p.shape.threads <= 64 ? 256 / p.shape.threads : 1;
     const int64_t groups = (rows + at_once - 1) / at_once;
-    p.partials = (int32_t)std::min<int64_t>(groups, width <= 1024 ? 512 : 256);
+    // one work-group per compute unit, or two where registers hold both and
+    // one alone leaves lanes idle (us with 256 / 512 work-groups: 10000x2816 52 /
+    // 47, 40000x3328 187 / 175, 10000x3840 57 / 57, 40000x4096 206 / 221) and rows
+    // are enough to pay for the longer sum of partial rows (3000x3328 22.7 / 23.2)
+    const bool idle = width > 2560 && width <= 3584 && rows >= 6000;
+    p.partials = (int32_t)std::min<int64_t>(groups, width <= 1024 || idle ? 512 : 256);
     // so few rows that one work-group's sums are the gradient: it does two
     // groups of rows in less time than the second launch takes
     p.direct = groups == 1 || groups == 2;

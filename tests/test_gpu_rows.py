@@ -514,3 +514,18 @@ def test_rows_of_every_shape_of_threads(fn, width, t):
     want, size, dw, dw_size = backward_reference(dout, h, w, rstd.float(), x)
     check_close(dx, want, want.abs() * half(t) + size + tiny(t), "dx")
     check_close(dweight, dw, dw_size * (n + 3 + 32 + 64 + 3) * U + tiny(torch.float32), "dweight")
+
+
+@pytest.mark.parametrize("t", TYPES, ids=str)
+@pytest.mark.parametrize("n,width", [(6100, 2811), (5999, 2811), (6000, 3585)])
+def test_gradients_of_rows_for_many_work_groups(fn, n, width, t):
+    """Where the number of work-groups changes with the rows and the width."""
+    h, w = rows(1, n, width, t), weights(2, width, t)
+    dout = rows(3, n, width, t, spread=0.2)
+    rstd = (1 / torch.sqrt(h.double().square().mean(1) + EPS)).float()
+    dx, dweight = fn.rms_norm_backward(dout, h, w, rstd)
+    want, size, dw, dw_size = backward_reference(dout, h, w, rstd, None)
+    check_close(dx, want, want.abs() * half(t) + size + tiny(t), "dx")
+    # the rows of one thread, then 512 partial sums
+    chain = n // 256 + 1 + 512 + 3
+    check_close(dweight, dw, dw_size * chain * U + tiny(torch.float32), "dweight")

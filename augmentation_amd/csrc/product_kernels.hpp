@@ -263,7 +263,17 @@ struct OutputTile {
 // at 1.85 GHz: power bounds it, for the same products alone hold 2.36 GHz and
 // take 290 us.  Short sums are bound by what no product covers, the first loads
 // and the outputs: 50176x1024x768 50 us, 38 at the rate of a large product.
-template <typename T, int kBM, int kBN, int kWM, int kWN, int kStages>
+//
+// kLines: every row starts at a cache line.  Else a stage still brings whole
+// lines: of row r it has the codes from 128 s - d to 128 s + 127 - d, d the
+// distance of the row's start from its line's.  Piece j of the 128 codes from
+// 128 s on then stands at its usual place, in stage s if j + d / 16 < 8 and
+// otherwise in the next one; rows eight apart have the same d, so a lane has
+// one for all its rows.  Read as they are, rows off the lines take two for
+// each load (2048x2048x4112 in 128x64 tiles 31 us, so 25, with rows on the lines
+// 23), but the next stage has to have landed, too, which 256x256 tiles have no
+// room for.
+template <typename T, int kBM, int kBN, int kWM, int kWN, int kStages, bool kLines>
 __global__ __launch_bounds__(64 * kWM * kWN, 2) void product_tile_kernel(ProductArgs p) {
   constexpr int kWaves = kWM * kWN, kTM = kBM / kWM / 16, kTN = kBN / kWN / 16;
   constexpr int kStageBytes = (kBM + kBN) * kBK;
@@ -300,84 +310,115 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void product_tile_kernel(Product
         load_words_to_lds(c < kA ? sa : c < kA + kB ? sb : bias, to + 256 * c,
                           256 * (c < kA ? c : c < kA + kB ? c - kA : c - kA - kB) + 4 * lane);
   }
-  const i32x4 src_a =
-      tile_resource(p.a + m0 * p.a_stride, p.a_stride, min(p.M - m0, (int64_t)kBM), p.K);
-  const i32x4 src_b =
-      tile_resource(p.b + n0 * p.b_stride, p.b_stride, min(p.N - n0, (int64_t)kBN), p.K);
+  const int8_t *a = p.a + m0 * p.a_stride, *b = p.b + n0 * p.b_stride;
+  // pieces from the line's start to the first row's and, for each row, more
+  const int first_a = kLines ? 0 : (int)((uintptr_t)a >> 4) & 7;
+  const int first_b = kLines ? 0 : (int)((uintptr_t)b >> 4) & 7;
+  const int more_a = kLines ? 0 : (int)(p.a_stride >> 4), more_b = kLines ? 0 : (int)(p.b_stride >> 4);
+  const i32x4 src_a = tile_resource(a - 16 * first_a, p.a_stride, min(p.M - m0, (int64_t)kBM),
+                                    p.K + 16 * first_a);
+  const i32x4 src_b = tile_resource(b - 16 * first_b, p.b_stride, min(p.N - n0, (int64_t)kBN),
+                                    p.K + 16 * first_b);
   // load i of a wavefront brings eight rows; every other one has this lane's
   // piece at the same place
   static_assert(kLoadsA % 2 == 0 && kLoadsB % 2 == 0, "rows per wavefront: a multiple of 16");
   const int sub = lane / 8;
   const int piece[2] = {staged_piece(sub, lane % 8), staged_piece(8 + sub, lane % 8)};
+  // this lane's first code in stage 0: before the row, if its piece of the
+  // line is
+  const int d_a = (first_a + sub * more_a) & 7, d_b = (first_b + sub * more_b) & 7;
+  const int code_a[2] = {16 * (((piece[0] + d_a) & 7) - d_a), 16 * (((piece[1] + d_a) & 7) - d_a)};
+  const int code_b[2] = {16 * (((piece[0] + d_b) & 7) - d_b), 16 * (((piece[1] + d_b) & 7) - d_b)};
   int off_a[kLoadsA], off_b[kLoadsB];
 #pragma unroll
   for (int i = 0; i < kLoadsA; ++i) {
     const int r = (wave * kLoadsA + i) * 8 + sub;
-    off_a[i] = m0 + r < p.M ? r * (int)p.a_stride + 16 * piece[i & 1] : kOutside;
+    off_a[i] = m0 + r < p.M ? 16 * first_a + r * (int)p.a_stride + code_a[i & 1] : kOutside;
   }
 #pragma unroll
   for (int i = 0; i < kLoadsB; ++i) {
     const int r = (wave * kLoadsB + i) * 8 + sub;
-    off_b[i] = n0 + r < p.N ? r * (int)p.b_stride + 16 * piece[i & 1] : kOutside;
+    off_b[i] = n0 + r < p.N ? 16 * first_b + r * (int)p.b_stride + code_b[i & 1] : kOutside;
   }
   const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)s_stages;
-  // load i of the stage that begins at code k0; pieces from K on (K is whole
-  // pieces) bring zeros
-  auto issue = [&](int stage, int k0, int i, const bool (&inside)[2]) {
+  // load i of the stage that begins at code k0; pieces before the row and from
+  // K on (K is whole pieces) bring zeros
+  struct Inside {
+    bool a[2], b[2];
+  };
+  auto inside_of = [&](int k0) {
+    const uint32_t K = (uint32_t)p.K;
+    return Inside{{(uint32_t)(k0 + code_a[0]) < K, (uint32_t)(k0 + code_a[1]) < K},
+                  {(uint32_t)(k0 + code_b[0]) < K, (uint32_t)(k0 + code_b[1]) < K}};
+  };
+  auto issue = [&](int stage, int k0, int i, const Inside& inside) {
     const uint32_t to = lds + stage * kStageBytes;
     if (i < kLoadsA)
-      load_to_lds(src_a, to + (wave * kLoadsA + i) * 1024, inside[i & 1] ? off_a[i] : kOutside, k0);
+      load_to_lds(src_a, to + (wave * kLoadsA + i) * 1024, inside.a[i & 1] ? off_a[i] : kOutside,
+                  k0);
     else
       load_to_lds(src_b, to + kBM * kBK + (wave * kLoadsB + i - kLoadsA) * 1024,
-                  inside[i & 1] ? off_b[i - kLoadsA] : kOutside, k0);
+                  inside.b[i & 1] ? off_b[i - kLoadsA] : kOutside, k0);
   };
 
   // fragments: lane l holds codes 16 (l / 16) .. + 15 of row l % 16
   const int at_a = ((wave / kWN) * kTM * 16 + (lane & 15)) * kBK;
   const int at_b = kBM * kBK + ((wave % kWN) * kTN * 16 + (lane & 15)) * kBK;
   int at_piece[kSteps];
+  bool later_a[kSteps], later_b[kSteps];  // does the piece stand in the next stage
 #pragma unroll
-  for (int k = 0; k < kSteps; ++k) at_piece[k] = 16 * staged_piece(lane & 15, 4 * k + (lane >> 4));
+  for (int k = 0; k < kSteps; ++k) {
+    const int j = 4 * k + (lane >> 4);
+    at_piece[k] = 16 * staged_piece(lane & 15, j);
+    later_a[k] = j + ((first_a + (lane & 7) * more_a) & 7) >= 8;
+    later_b[k] = j + ((first_b + (lane & 7) * more_b) & 7) >= 8;
+  }
   i32x4 fa[2][kTM], fb[2][kTN];
-  auto fetch = [&](const int8_t* buf, int k, int slot, int i) {
+  auto fetch = [&](const int8_t* buf, const int8_t* later, int k, int slot, int i) {
+    const int8_t* from_a = !kLines && later_a[k] ? later : buf;
+    const int8_t* from_b = !kLines && later_b[k] ? later : buf;
     if (i < kTN)
-      fb[slot][i] = *reinterpret_cast<const i32x4*>(buf + at_b + i * 16 * kBK + at_piece[k]);
+      fb[slot][i] = *reinterpret_cast<const i32x4*>(from_b + at_b + i * 16 * kBK + at_piece[k]);
     else
       fa[slot][i - kTN] =
-          *reinterpret_cast<const i32x4*>(buf + at_a + (i - kTN) * 16 * kBK + at_piece[k]);
+          *reinterpret_cast<const i32x4*>(from_a + at_a + (i - kTN) * 16 * kBK + at_piece[k]);
   };
   i32x4 acc[kTM][kTN] = {};
 
+  // the stages that must have landed beyond the one that is worked on
+  constexpr int kAhead = kLines ? 0 : 1;
+  static_assert(kStages >= 2 + kAhead, "a stage is read while the next one lands");
 #pragma unroll
   for (int s = 0; s < kStages; ++s) {
-    const bool inside[2] = {s * kBK + 16 * piece[0] < p.K, s * kBK + 16 * piece[1] < p.K};
+    const Inside inside = inside_of(s * kBK);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) issue(s, s * kBK, i, inside);
   }
-  wait_loads<(kStages - 1) * kLoads>();
+  wait_loads<(kStages - 1 - kAhead) * kLoads>();
   __builtin_amdgcn_s_barrier();
 #pragma unroll
-  for (int i = 0; i < kTM + kTN; ++i) fetch(s_stages, 0, 0, i);
+  for (int i = 0; i < kTM + kTN; ++i) fetch(s_stages, s_stages + kStageBytes, 0, 0, i);
   int stage = 0;
   for (int k0 = 0; k0 < p.K; k0 += kBK) {
     const int next = stage + 1 == kStages ? 0 : stage + 1;
+    const int after = next + 1 == kStages ? 0 : next + 1;
     static_for<kSteps>([&](auto step) {
       constexpr int k = decltype(step)::value;
       constexpr bool kLast = k + 1 == kSteps;
       constexpr int kProducts = kTM * kTN, kReads = kTM + kTN, kNewLoads = kLast ? kLoads : 0;
       constexpr int kOthers = kReads + kNewLoads;
       const int8_t* from = s_stages + (kLast ? next : stage) * kStageBytes;
+      const int8_t* later = s_stages + (kLast ? after : next) * kStageBytes;
       const int k_new = k0 + kStages * kBK;
-      bool inside[2] = {};
+      Inside inside = {};
       if constexpr (kLast) {
         // this wavefront's loads of the next stage have landed and its reads
         // of this one are done; beyond the barrier, everyone's are: the next
         // stage may be read, and this one's place be filled again
-        wait_loads<(kStages - 2) * kLoads>();
+        wait_loads<(kStages - 2 - kAhead) * kLoads>();
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
-        inside[0] = k_new + 16 * piece[0] < p.K;
-        inside[1] = k_new + 16 * piece[1] < p.K;
+        inside = inside_of(k_new);
       }
       __builtin_amdgcn_sched_barrier(0);
       static_for<kProducts>([&](auto product) {
@@ -394,7 +435,7 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void product_tile_kernel(Product
           if constexpr ((o + 1) * kNewLoads / kOthers > kBefore)
             issue(stage, k_new, kBefore, inside);
           else
-            fetch(from, kLast ? 0 : k + 1, (k + 1) & 1, o - kBefore);
+            fetch(from, later, kLast ? 0 : k + 1, (k + 1) & 1, o - kBefore);
         });
         __builtin_amdgcn_sched_barrier(0);
         acc[t / kTN][t % kTN] = __builtin_amdgcn_mfma_i32_16x16x64_i8(

@@ -336,11 +336,12 @@ double tile_cost(int64_t M, int64_t N, int bm, int bn, int cus, double alone, do
   return n <= 1.0 ? alone : first + n * each;
 }
 
-template <typename T, int kBM, int kBN, int kWM, int kWN, int kStages>
+template <typename T, int kBM, int kBN, int kWM, int kWN, int kStages, bool kLines = true>
 bool launch_tiles(fn::ProductArgs& p, hipStream_t st) {
   const unsigned grid = tile_grid<kBM, kBN>(&p);
   if (grid)
-    fn::product_tile_kernel<T, kBM, kBN, kWM, kWN, kStages><<<grid, 64 * kWM * kWN, 0, st>>>(p);
+    fn::product_tile_kernel<T, kBM, kBN, kWM, kWN, kStages, kLines>
+        <<<grid, 64 * kWM * kWN, 0, st>>>(p);
   return grid != 0;
 }
 
@@ -357,11 +358,22 @@ int best_tile(int64_t M, int64_t N, int cus, double* cost) {
 
 template <typename T>
 bool launch_tiles_of(int tile, fn::ProductArgs& p, hipStream_t st) {
+  // Rows off the cache lines, in us as they are / by whole lines: 128x64 tiles,
+  // 2048x2048x4112 31 / 25, 1536x1536x1600 12.5 / 11.8; 64x64, 1024x1024x8208
+  // 21.4 / 19.7, 1999x1000x1008 8.2 / 7.8.  128x128 would need three stages,
+  // and so a compute unit each: 4096x2048x4112 45 / 42, but 4090x2040x1040
+  // 18.6 / 19.7.
+  const bool lines = ((uintptr_t)p.a | (uintptr_t)p.b | (uint64_t)p.a_stride |
+                      (uint64_t)p.b_stride) % fn::kBK == 0;
   switch (tile) {
     case 0: return launch_tiles<T, 256, 256, 2, 4, 2>(p, st);
     case 1: return launch_tiles<T, 128, 128, 2, 2, 2>(p, st);
-    case 2: return launch_tiles<T, 128, 64, 2, 2, 3>(p, st);
-    default: return launch_tiles<T, 64, 64, 2, 2, 4>(p, st);
+    case 2:
+      return lines ? launch_tiles<T, 128, 64, 2, 2, 3>(p, st)
+                   : launch_tiles<T, 128, 64, 2, 2, 3, false>(p, st);
+    default:
+      return lines ? launch_tiles<T, 64, 64, 2, 2, 4>(p, st)
+                   : launch_tiles<T, 64, 64, 2, 2, 4, false>(p, st);
   }
 }
 

@@ -100,3 +100,26 @@ def test_outputs_beyond_4_gib(fn, m, n, k):
     for r in some.split(4):
         y = sums(a[r], b).float() * sa[r][:, None] * sb[None, :]
         assert torch.equal(out[r], y.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("m,n", [(1000, 600), (1500, 1700), (2100, 2000), (4090, 2040)])
+@pytest.mark.parametrize("k,a_stride,a_from,b_stride,b_from",
+                         [(16, 16, 0, 16, 0), (112, 144, 16, 112, 0), (128, 128, 112, 256, 16),
+                          (144, 144, 0, 400, 128), (400, 464, 48, 400, 0), (1040, 1040, 0, 1040, 0),
+                          (1152, 1168, 0, 1152, 64), (1264, 1280, 0, 1264, 32)])
+def test_rows_off_the_cache_lines(fn, m, n, k, a_stride, a_from, b_stride, b_from):
+    """Rows of whole 16-byte pieces that start at other places than multiples
+    of 128 bytes, each operand at its own."""
+    a, sa, b, sb, bias = operands(m + n + k, m, n, k)
+
+    def placed(v, stride, start):
+        # nothing but the operand's own codes may reach the sums
+        flat = torch.full((start + v.size(0) * stride,), 77, dtype=torch.int8, device="cuda")
+        at = flat[start:].view(v.size(0), stride)[:, :k]
+        at.copy_(v)
+        return at
+
+    out = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+    fn.matmul_q8(placed(a, a_stride, a_from), sa, placed(b, b_stride, b_from), sb, bias=bias,
+                 out=out)
+    check(out, sums(a, b), sa, sb, bias, torch.bfloat16)

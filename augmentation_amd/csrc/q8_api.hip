@@ -360,9 +360,9 @@ template <typename T>
 bool launch_tiles_of(int tile, fn::ProductArgs& p, hipStream_t st) {
   // Rows off the cache lines, in us as they are / by whole lines: 128x64 tiles,
   // 2048x2048x4112 31 / 25, 1536x1536x1600 12.5 / 11.8; 64x64, 1024x1024x8208
-  // 21.4 / 19.7, 1999x1000x1008 8.2 / 7.8.  128x128 would need three stages,
-  // and so a compute unit each: 4096x2048x4112 45 / 42, but 4090x2040x1040
-  // 18.6 / 19.7.
+  // 21.4 / 19.7, 1999x1000x1008 8.2 / 7.8.  128x128 would need more
+  // stages, and so a compute unit each: with four, 4096x2048x4112 45 / 42, but
+  // 4090x2040x1040 18.6 / 19.7.
   const bool lines = ((uintptr_t)p.a | (uintptr_t)p.b | (uint64_t)p.a_stride |
                       (uint64_t)p.b_stride) % fn::kBK == 0;
   switch (tile) {

@@ -148,8 +148,8 @@ struct Half8 {
       a = u32x4{a[0] >> 16 | a[1] << 16, a[1] >> 16 | a[2] << 16, a[2] >> 16 | a[3] << 16,
                 a[3] >> 16};
   }
-  __device__ __forceinline__ void drop_last() {
-    a[3] &= 0xFFFFu;
+  __device__ __forceinline__ void drop_last(bool yes) {
+    a[3] &= yes ? 0xFFFFu : ~0u;
   }
   __device__ __forceinline__ uint32_t bits(int j) const { return (a[j >> 1] >> (16 * (j & 1))) & 0xFFFFu; }
   __device__ __forceinline__ void store(T* p) const {
@@ -219,16 +219,23 @@ __device__ __forceinline__ void load_chunk(Vec8<T>& v, const T* row, const Chunk
     v.load(row + c.at);
 }
 
-template <bool kShort, bool kShift = false, typename T>
+template <bool kShort, typename T>
 __device__ __forceinline__ void trim_chunk(Vec8<T>& v, const Chunk& c) {
-  if constexpr (kShift) {
-    if (c.skip < 0)
-      v.drop_last();
-    else if (c.skip != 0)
-      v.drop(c.skip);
-  } else if constexpr (!kShort) {
+  if constexpr (!kShort) {
     if (c.skip != 0) v.drop(c.skip);
   }
+}
+
+// Chunk k of a thread in rows that may be shifted and go beyond every thread's
+// chunk 0: only that one may begin late, and only the others end early.
+template <bool kShort, bool kShift, typename T>
+__device__ __forceinline__ void trim_chunk(Vec8<T>& v, const Chunk& c, int k) {
+  if constexpr (!kShift)
+    trim_chunk<kShort>(v, c);
+  else if (k > 0)
+    trim_chunk<kShort>(v, c);
+  else
+    v.drop_last(c.skip < 0);
 }
 
 template <typename T>
@@ -427,7 +434,7 @@ __global__ __launch_bounds__(rows_block<kThreads>()) void rows_kernel(RowArgs a)
       }
     }
 #pragma unroll
-    for (int k = 0; k < kChunks; ++k) trim_chunk<kShort, kShift>(h[k], c[k]);
+    for (int k = 0; k < kChunks; ++k) trim_chunk<kShort, kShift>(h[k], c[k], k);
     if (add) {
       T* s = (T*)a.sum + row * a.sum_stride;
 #pragma unroll
@@ -607,7 +614,7 @@ __global__ __launch_bounds__(rows_block<kThreads>()) void rows_backward_kernel(B
   // every other row where an odd number of 16-bit elements follow each other.
   // A work-group of the odd rows has its chunks shifted by one element (rows
   // and width decide, not addresses, which would change a row's sums with them;
-  // 10000x4095 fp16 83 -> 68 us, 4099x5003 bf16 47 -> 44).
+  // 10000x4095 83 -> 66 us, 4099x5003 47 -> 40, without dsum 68 -> 53 and 39 -> 37).
   constexpr bool kShift = sizeof(T) == 2 && kRows == 1;
   int32_t shift = 0;
   if constexpr (kShift) shift = a.width & (int)(blockIdx.x & 1u);
@@ -619,7 +626,7 @@ __global__ __launch_bounds__(rows_block<kThreads>()) void rows_backward_kernel(B
     for (int j = 0; j < 8; ++j) dw[k][j] = 0.0f;
   }
 #pragma unroll
-  for (int k = 0; k < kChunks; ++k) trim_chunk<kShort, kShift>(w[k], c[k]);
+  for (int k = 0; k < kChunks; ++k) trim_chunk<kShort, kShift>(w[k], c[k], k);
   const bool add = a.dsum != nullptr;
   // the next row is on its way while this one is worked on, where there are
   // registers for both
@@ -662,9 +669,9 @@ __global__ __launch_bounds__(rows_block<kThreads>()) void rows_backward_kernel(B
     const float rstd = now.rstd;
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
-      trim_chunk<kShort, kShift>(d[k], c[k]);
-      trim_chunk<kShort, kShift>(h[k], c[k]);
-      if (add) trim_chunk<kShort, kShift>(s[k], c[k]);
+      trim_chunk<kShort, kShift>(d[k], c[k], k);
+      trim_chunk<kShort, kShift>(h[k], c[k], k);
+      if (add) trim_chunk<kShort, kShift>(s[k], c[k], k);
     }
     float sum = 0.0f;
     uint32_t unused = 0;

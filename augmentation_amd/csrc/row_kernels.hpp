@@ -400,7 +400,7 @@ __global__ __launch_bounds__(rows_block<kThreads>()) void rows_kernel(RowArgs a)
   // 25.5 -> 22.7 us; with several 300000x101 28 -> 30).
   constexpr bool kShift = sizeof(T) == 2 && kMode == kRowQuantize && kRows == 1;
   int32_t shift = 0;
-  if constexpr (kShift) shift = a.width & (int)(blockIdx.x & 1u);
+  if constexpr (kShift) shift = a.width & (int)a.x_stride & (int)(blockIdx.x & 1u);
   Chunk c[kChunks];
   Vec8<T> w[kChunks];
 #pragma unroll
@@ -612,12 +612,13 @@ __global__ __launch_bounds__(rows_block<kThreads>()) void rows_backward_kernel(B
   float dw[kChunks][8];
   // Loads that begin within a dword take a quarter more time, as do those of
   // every other row where an odd number of 16-bit elements follow each other.
-  // A work-group of the odd rows has its chunks shifted by one element (rows
-  // and width decide, not addresses, which would change a row's sums with them;
-  // 10000x4095 83 -> 66 us, 4099x5003 47 -> 40, without dsum 68 -> 53 and 39 -> 37).
+  // A work-group of the odd rows has its chunks shifted by one element (row,
+  // width and stride decide, not addresses, which would change a row's sums with
+  // them; 10000x4095 83 -> 66 us, 4099x5003 47 -> 40, without dsum 68 -> 53 and
+  // 39 -> 37; but rows of 4095 at a stride of 4096 54 -> 67, so not these).
   constexpr bool kShift = sizeof(T) == 2 && kRows == 1;
   int32_t shift = 0;
-  if constexpr (kShift) shift = a.width & (int)(blockIdx.x & 1u);
+  if constexpr (kShift) shift = a.width & (int)a.dout_stride & (int)(blockIdx.x & 1u);
 #pragma unroll
   for (int k = 0; k < kChunks; ++k) {
     c[k] = chunk_at(k * kThreads + lane, a.width, shift);

@@ -22,6 +22,7 @@ using namespace fnhost;
   } while (0)
 
 constexpr int32_t kMaxWidth = 1 << 30;
+constexpr int32_t kColumnsPerLaunch = 1 << 26;  // of the sum of partial rows
 
 int type_bytes(int32_t dtype) {
   return dtype == FN_OUT_FP32 ? 4 : dtype == FN_OUT_FP16 || dtype == FN_OUT_BF16 ? 2 : 0;
@@ -589,10 +590,15 @@ FN_EXPORT int fn_rms_norm_backward(const void* dout_dev, int64_t dout_stride, co
     FN_TRY(launch_status("rows_backward_kernel launch"));
     if (plan.direct) return ok();
   }
-  // no rows: no partial sums, and a gradient of zero
-  fn::column_sum_kernel<<<blocks_for(width, 64), 1024, 0, st>>>(a.partial, a.partials, a.pitch,
-                                                                width, dweight_dev);
-  return launch_status("column_sum_kernel launch");
+  // no rows: no partial sums, and a gradient of zero.  2^26 columns, 2^30
+  // threads, to a launch: HIP takes fewer than 2^32 of them
+  for (int32_t c = 0; c < width; c += kColumnsPerLaunch) {
+    const int32_t columns = std::min(width - c, kColumnsPerLaunch);
+    fn::column_sum_kernel<<<blocks_for(columns, 64), 1024, 0, st>>>(
+        rows > 0 ? a.partial + c : nullptr, a.partials, a.pitch, columns, dweight_dev + c);
+    FN_TRY(launch_status("column_sum_kernel launch"));
+  }
+  return ok();
 }
 
 FN_EXPORT int fn_matmul_q8(const int8_t* a_dev, int64_t a_stride, const float* a_scales_dev,

@@ -789,7 +789,9 @@ __global__ __launch_bounds__(256) void rows_backward_columns_kernel(BackwardArgs
 }
 
 // dweight = the sum of the rows of partial sums: 64 columns per work-group,
-// four to a thread, 64 threads to a column, joined in a fixed order.
+// four to a thread, 64 threads to a column, joined in a fixed order.  `width`
+// columns from a multiple of four on; a row's last vector of four may be
+// partly beyond them, but not beyond the pitch.
 __global__ __launch_bounds__(1024) void column_sum_kernel(const float* partial, int32_t partials,
                                                           int32_t pitch, int32_t width,
                                                           float* dweight) {
@@ -797,7 +799,7 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* partial, 
   const int col = 4 * (int)(threadIdx.x & 15u), part = (int)(threadIdx.x >> 4);
   const int64_t c = (int64_t)blockIdx.x * 64 + col;
   float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (c < pitch) {
+  if (c < width) {
 #pragma unroll 8
     for (int32_t p = part; p < partials; p += 64) {
       const f32x4 v = *reinterpret_cast<const f32x4*>(partial + (int64_t)p * pitch + c);

@@ -318,11 +318,10 @@ void launch_backward(const fn::BackwardArgs& a, const RowShape& s, hipStream_t s
   }
 }
 
-// Tiles of kBM tokens x kBN channels: the grid, or 0 if it has too many.
+// Tiles of kBM tokens x kBN channels: the grid.
 template <int kBM, int kBN>
 unsigned tile_grid(fn::ProductArgs* p) {
   const int64_t tm = (p->M + kBM - 1) / kBM, tn = (p->N + kBN - 1) / kBN;
-  if ((__int128)tm * tn > 0x7FFFFFFF) return 0;
   p->tiles_m = (uint32_t)tm;
   p->tiles_n = (uint32_t)tn;
   return (unsigned)(tm * tn);
@@ -338,12 +337,10 @@ double tile_cost(int64_t M, int64_t N, int bm, int bn, int cus, double alone, do
 }
 
 template <typename T, int kBM, int kBN, int kWM, int kWN, int kStages, bool kLines = true>
-bool launch_tiles(fn::ProductArgs& p, hipStream_t st) {
+void launch_tiles(fn::ProductArgs& p, hipStream_t st) {
   const unsigned grid = tile_grid<kBM, kBN>(&p);
-  if (grid)
-    fn::product_tile_kernel<T, kBM, kBN, kWM, kWN, kStages, kLines>
-        <<<grid, 64 * kWM * kWN, 0, st>>>(p);
-  return grid != 0;
+  fn::product_tile_kernel<T, kBM, kBN, kWM, kWN, kStages, kLines>
+      <<<grid, 64 * kWM * kWN, 0, st>>>(p);
 }
 
 // The cheapest of the four tiles for M tokens, and its cost.
@@ -358,7 +355,7 @@ int best_tile(int64_t M, int64_t N, int cus, double* cost) {
 }
 
 template <typename T>
-bool launch_tiles_of(int tile, fn::ProductArgs& p, hipStream_t st) {
+void launch_tiles_of(int tile, fn::ProductArgs& p, hipStream_t st) {
   // Rows off the cache lines, in us as they are / by whole lines: 128x64 tiles,
   // 2048x2048x4112 31 / 25, 1536x1536x1600 12.5 / 11.8; 64x64, 1024x1024x8208
   // 21.4 / 19.7, 1999x1000x1008 8.2 / 7.8.  128x128 would need more
@@ -383,7 +380,7 @@ bool launch_tiles_of(int tile, fn::ProductArgs& p, hipStream_t st) {
 // less than a last round of tiles on a few compute units (a launch is 4 us;
 // costs are for K = 4096).
 template <typename T>
-bool launch_tiles_best(fn::ProductArgs& p, int cus, hipStream_t st) {
+void launch_tiles_best(fn::ProductArgs& p, int cus, hipStream_t st) {
   double cost = 0.0, rest_cost = 0.0;
   int tile = best_tile(p.M, p.N, cus, &cost);
   const int64_t tiles_n = (p.N + 255) / 256, rounds = p.M / 256 * tiles_n / cus;
@@ -393,7 +390,7 @@ bool launch_tiles_best(fn::ProductArgs& p, int cus, hipStream_t st) {
     if (rounds * 57 + rest_cost + 4.0 * 4096 / std::max(p.K, 64) < cost) {
       fn::ProductArgs first = p;
       first.M = head;
-      if (!launch_tiles_of<T>(0, first, st)) return false;
+      launch_tiles_of<T>(0, first, st);
       p.a += head * p.a_stride;
       p.sa += head;
       p.out = (T*)p.out + head * p.out_stride;
@@ -401,33 +398,23 @@ bool launch_tiles_best(fn::ProductArgs& p, int cus, hipStream_t st) {
       tile = rest;
     }
   }
-  return launch_tiles_of<T>(tile, p, st);
+  launch_tiles_of<T>(tile, p, st);
 }
 
 template <typename T, int kBM, int kBN>
-bool launch_any(fn::ProductArgs& p, hipStream_t st) {
+void launch_any(fn::ProductArgs& p, hipStream_t st) {
   const unsigned grid = tile_grid<kBM, kBN>(&p);
-  if (grid) fn::product_any_kernel<T, kBM, kBN, 4><<<grid, 512, 0, st>>>(p);
-  return grid != 0;
+  fn::product_any_kernel<T, kBM, kBN, 4><<<grid, 512, 0, st>>>(p);
 }
 
-// Work-groups of 16 kNT channels x 16 kMT tokens; false if there are too many.
-template <int kMT, int kNT>
-bool split_grid(const fn::ProductArgs& p, dim3* grid) {
-  const int64_t x = (p.N + 16 * kNT - 1) / (16 * kNT), y = (p.M + 16 * kMT - 1) / (16 * kMT);
-  *grid = dim3((unsigned)x, (unsigned)y);
-  return x <= 0x7FFFFFFF && y <= 65535;
-}
-
+// Work-groups of 16 kNT channels x 16 kMT tokens.
 template <typename T, int kMT, int kNT, bool kPieces>
-bool launch_split(const fn::ProductArgs& p, hipStream_t st) {
-  dim3 grid;
-  if (!split_grid<kMT, kNT>(p, &grid)) return false;
+void launch_split(const fn::ProductArgs& p, hipStream_t st) {
+  const dim3 grid(blocks_for(p.N, 16 * kNT), blocks_for(p.M, 16 * kMT));
   if constexpr (kPieces)
     fn::product_split_kernel<T, kMT, kNT, 2, 8><<<grid, 512, 0, st>>>(p);
   else
     fn::product_split_any_kernel<T, kMT, kNT, 8><<<grid, 512, 0, st>>>(p);
-  return true;
 }
 
 // Which kernel.  Times in us, measured on 256 compute units.
@@ -451,35 +438,59 @@ bool launch_split(const fn::ProductArgs& p, hipStream_t st) {
 // 256x128, 128x64 and 64x64: 4000x4000x4001 110 / 160 / 197; 1999x1000x1021
 // 18.5 / 11.0 / 11.7; 300x1024x777 16.5 / 8.8 / 7.1.
 template <typename T>
-int launch_product(fn::ProductArgs p, int cus, hipStream_t st) {
+void launch_part(fn::ProductArgs p, int cus, hipStream_t st) {
   // whole 16-byte pieces from 16-byte aligned rows, a tile's rows within the
   // 31-bit offsets of its buffer resource
   const bool pieces = ((uintptr_t)p.a | (uintptr_t)p.b | (uint64_t)p.a_stride |
                        (uint64_t)p.b_stride | (uint64_t)p.K) % 16 == 0 &&
                       std::max(p.a_stride, p.b_stride) <= (0x7FFFFFF0 - 131072) / 256;
   const double groups = std::ceil(p.M / 32.0) * std::ceil(p.N / 32.0);
-  bool launched = false;
   if (p.M <= 16 && !pieces) {
-    launched = launch_split<T, 1, 1, false>(p, st);
+    launch_split<T, 1, 1, false>(p, st);
+  } else if (p.M <= 16 && (p.N + 15) / 16 <= 2 * cus) {
+    launch_split<T, 1, 1, true>(p, st);
   } else if (p.M <= 16) {
-    launched = (p.N + 15) / 16 <= 2 * cus ? launch_split<T, 1, 1, true>(p, st)
-                                          : launch_split<T, 1, 4, true>(p, st);
+    launch_split<T, 1, 4, true>(p, st);
+  } else if (groups <= cus && pieces) {
+    launch_split<T, 2, 2, true>(p, st);
   } else if (groups <= cus) {
-    launched = pieces ? launch_split<T, 2, 2, true>(p, st) : launch_split<T, 2, 1, false>(p, st);
+    launch_split<T, 2, 1, false>(p, st);
   } else if (pieces) {
-    launched = launch_tiles_best<T>(p, cus, st);
+    launch_tiles_best<T>(p, cus, st);
   } else {
     const double c[3] = {tile_cost(p.M, p.N, 256, 128, cus, 60, 0, 55),
                          tile_cost(p.M, p.N, 128, 64, cus, 30, 0, 20),
                          tile_cost(p.M, p.N, 64, 64, cus, 20, 0, 12.3)};
     switch (std::min_element(c, c + 3) - c) {
-      case 0: launched = launch_any<T, 256, 128>(p, st); break;
-      case 1: launched = launch_any<T, 128, 64>(p, st); break;
-      default: launched = launch_any<T, 64, 64>(p, st);
+      case 0: launch_any<T, 256, 128>(p, st); break;
+      case 1: launch_any<T, 128, 64>(p, st); break;
+      default: launch_any<T, 64, 64>(p, st);
     }
   }
-  if (!launched) return fail(FN_EOVERFLOW, "grid size limit exceeded");
-  return launch_status("product kernel launch");
+}
+
+// The whole product, in parts of fewer than 2^32 threads, which is what HIP
+// takes in a launch: at most 2^26 channels (32 threads each in groups of 16
+// channels x 16 tokens) and 2^22 tiles of 64x64 (512 threads each).
+template <typename T>
+int launch_product(const fn::ProductArgs& p, int cus, hipStream_t st) {
+  const int64_t channels = std::min<int64_t>(p.N, (int64_t)1 << 26);
+  const int64_t tokens = ((int64_t)1 << 22) / ((channels + 63) / 64) / 4 * 256;
+  for (int64_t n = 0; n < p.N; n += channels)
+    for (int64_t m = 0; m < p.M; m += tokens) {
+      fn::ProductArgs part = p;
+      part.a += m * p.a_stride;
+      part.sa += m;
+      part.b += n * p.b_stride;
+      part.sb += n;
+      if (p.bias != nullptr) part.bias += n;
+      part.out = (T*)p.out + m * p.out_stride + n;
+      part.M = std::min(tokens, p.M - m);
+      part.N = std::min(channels, p.N - n);
+      launch_part<T>(part, cus, st);
+      FN_TRY(launch_status("product kernel launch"));
+    }
+  return ok();
 }
 
 }  // namespace

@@ -15,6 +15,7 @@ import os
 
 import numpy as np
 import torch  # loads the HIP runtime the library binds to
+from torch.autograd import forward_ad
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfn.so")
@@ -280,9 +281,24 @@ def params_to_numpy(t: torch.Tensor) -> np.ndarray:
 #
 # These are called once per layer and token, so they keep to the fewest
 # attribute reads that check an argument.
+#
+# They compute and do not differentiate: no result has a gradient function.  A
+# tensor that requires a gradient while gradients are recorded, or that carries
+# a forward-mode tangent, is refused, for its derivative would be lost without
+# a word.  In training they stand inside a torch.autograd.Function (rms_norm in
+# its forward, rms_norm_backward in its backward), where torch records none.
 
 _TYPE_CODES = {torch.float32: FN_OUT_FP32, torch.float16: FN_OUT_FP16, torch.bfloat16: FN_OUT_BF16}
 _CODE_TYPES = {code: t for t, code in _TYPE_CODES.items()}
+
+
+def _refuse_gradients(*tensors) -> None:
+    if torch._C._any_requires_grad(*tensors) and torch.is_grad_enabled():
+        raise ValueError("an argument requires a gradient, which this call does not record: call it "
+                         "under torch.no_grad() or within a torch.autograd.Function")
+    if forward_ad._current_level >= 0 and any(
+            t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise ValueError("an argument carries a forward-mode tangent, which this call does not carry on")
 
 
 def _type_code(dtype) -> int:
@@ -292,12 +308,13 @@ def _type_code(dtype) -> int:
     return code
 
 
-def _row_stride(t: torch.Tensor, name: str) -> int:
+def _row_stride(t: torch.Tensor, name: str, width: int | None = None) -> int:
     """The row stride of a (..., D) tensor whose leading dimensions step by
     one common stride (any contiguous tensor, a slice of its last dimension,
-    one row expanded to many) and whose last dimension is contiguous."""
+    one row expanded to many) and whose last dimension is contiguous.
+    `width`: D, where the caller knows it."""
     if t.is_contiguous():
-        return t.shape[-1]
+        return t.shape[-1] if width is None else width
     shape, st = t.shape, t.stride()
     stride = None
     if shape[-1] <= 1 or st[-1] == 1:
@@ -339,6 +356,7 @@ def _rows_of(x: torch.Tensor):
 
 def _norm(x, weight, eps, residual, sum_out, stream, out_args, q8):
     """What both norms pass before and after their own outputs."""
+    _refuse_gradients(x, weight, residual, sum_out, *out_args)
     shape, rows, width, dev = _rows_of(x)
     dtype = x.dtype
     code = _type_code(dtype)
@@ -348,8 +366,8 @@ def _norm(x, weight, eps, residual, sum_out, stream, out_args, q8):
     if residual is not None:
         _want(residual, shape, dtype, dev, "residual")
         sum_out = _want(sum_out, shape, dtype, dev, "sum_out")
-        res_at, res_stride = residual.data_ptr(), _row_stride(residual, "residual")
-        sum_at, sum_stride = sum_out.data_ptr(), _row_stride(sum_out, "sum_out")
+        res_at, res_stride = residual.data_ptr(), _row_stride(residual, "residual", width)
+        sum_at, sum_stride = sum_out.data_ptr(), _row_stride(sum_out, "sum_out", width)
     elif sum_out is not None:
         raise ValueError("sum_out without a residual")
     if q8:
@@ -359,16 +377,16 @@ def _norm(x, weight, eps, residual, sum_out, stream, out_args, q8):
         if rstd is not None:
             _want(rstd, shape[:-1], torch.float32, dev, "rstd", True)
         _check(_lib.fn_rms_norm_q8(
-            x.data_ptr(), _row_stride(x, "x"), res_at, res_stride, weight.data_ptr(), rows, width,
-            eps, code, sum_at, sum_stride, codes.data_ptr(), _row_stride(codes, "codes"),
+            x.data_ptr(), _row_stride(x, "x", width), res_at, res_stride, weight.data_ptr(), rows, width,
+            eps, code, sum_at, sum_stride, codes.data_ptr(), _row_stride(codes, "codes", width),
             scales.data_ptr(), None if rstd is None else rstd.data_ptr(), _stream(stream)))
         return codes, scales, x if residual is None else sum_out
     out, rstd = out_args
     out = _want(out, shape, dtype, dev, "out")
     rstd = _want(rstd, shape[:-1], torch.float32, dev, "rstd", True)
     _check(_lib.fn_rms_norm(
-        x.data_ptr(), _row_stride(x, "x"), res_at, res_stride, weight.data_ptr(), rows, width, eps,
-        code, sum_at, sum_stride, out.data_ptr(), _row_stride(out, "out"), rstd.data_ptr(),
+        x.data_ptr(), _row_stride(x, "x", width), res_at, res_stride, weight.data_ptr(), rows, width, eps,
+        code, sum_at, sum_stride, out.data_ptr(), _row_stride(out, "out", width), rstd.data_ptr(),
         _stream(stream)))
     return out, rstd, x if residual is None else sum_out
 
@@ -392,12 +410,13 @@ def rms_norm_q8(x, weight, eps=1e-6, residual=None, codes=None, scales=None, sum
 def quantize_rows(x, codes=None, scales=None, stream=None):
     """fn_quantize_rows on a (..., D) CUDA tensor: (int8 codes of its shape,
     an fp32 scale per row)."""
+    _refuse_gradients(x, scales)
     shape, rows, width, dev = _rows_of(x)
     codes = _want(codes, shape, torch.int8, dev, "codes")
     scales = _want(scales, shape[:-1], torch.float32, dev, "scales", True)
     _check(_lib.fn_quantize_rows(
-        x.data_ptr(), _row_stride(x, "x"), rows, width, _type_code(x.dtype), codes.data_ptr(),
-        _row_stride(codes, "codes"), scales.data_ptr(), _stream(stream)))
+        x.data_ptr(), _row_stride(x, "x", width), rows, width, _type_code(x.dtype), codes.data_ptr(),
+        _row_stride(codes, "codes", width), scales.data_ptr(), _stream(stream)))
     return codes, scales
 
 
@@ -417,6 +436,7 @@ def rms_norm_backward(dout, h, weight, rstd, dsum=None, dx=None, dweight=None, w
     or dsum.  Without a workspace one is allocated for the call; with
     `stream` other than the current one, pass a workspace that lives until
     the stream has finished."""
+    _refuse_gradients(dout, h, weight, rstd, dsum, dx, dweight)
     shape, rows, width, dev = _rows_of(h)
     dtype = h.dtype
     code = _type_code(dtype)
@@ -426,7 +446,7 @@ def rms_norm_backward(dout, h, weight, rstd, dsum=None, dx=None, dweight=None, w
     dsum_at, dsum_stride = None, 0
     if dsum is not None:
         _want(dsum, shape, dtype, dev, "dsum")
-        dsum_at, dsum_stride = dsum.data_ptr(), _row_stride(dsum, "dsum")
+        dsum_at, dsum_stride = dsum.data_ptr(), _row_stride(dsum, "dsum", width)
     dx = _want(dx, shape, dtype, dev, "dx")
     dweight = _want(dweight, (width,), torch.float32, dev, "dweight", True)
     if workspace is None:
@@ -437,9 +457,9 @@ def rms_norm_backward(dout, h, weight, rstd, dsum=None, dx=None, dweight=None, w
     else:
         at, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _check(_lib.fn_rms_norm_backward(
-        dout.data_ptr(), _row_stride(dout, "dout"), h.data_ptr(), _row_stride(h, "h"),
+        dout.data_ptr(), _row_stride(dout, "dout", width), h.data_ptr(), _row_stride(h, "h", width),
         weight.data_ptr(), rstd.data_ptr(), dsum_at, dsum_stride, rows, width, code, dx.data_ptr(),
-        _row_stride(dx, "dx"), dweight.data_ptr(), at, size, _stream(stream)))
+        _row_stride(dx, "dx", width), dweight.data_ptr(), at, size, _stream(stream)))
     return dx, dweight
 
 
@@ -447,6 +467,7 @@ def matmul_q8(a, a_scales, b, b_scales, bias=None, out_dtype=FN_OUT_BF16, out=No
     """fn_matmul_q8: the (..., N) product of int8 codes a (..., K) with a scale
     per row and b (N, K) with a scale per row, plus an fp32 bias (N,).  Given
     `out`, its dtype counts and not out_dtype."""
+    _refuse_gradients(a_scales, b_scales, bias, out)
     shape, b_shape, dev = a.shape, b.shape, a.get_device()
     if a.dtype is not torch.int8 or b.dtype is not torch.int8 or len(shape) < 1 \
             or len(b_shape) != 2 or dev < 0 or b.get_device() != dev or shape[-1] != b_shape[1]:
@@ -466,8 +487,8 @@ def matmul_q8(a, a_scales, b, b_scales, bias=None, out_dtype=FN_OUT_BF16, out=No
     if bias is not None:
         _want(bias, (N,), torch.float32, dev, "bias", True)
     _check(_lib.fn_matmul_q8(
-        a.data_ptr(), _row_stride(a, "a") if K else 0, a_scales.data_ptr(), b.data_ptr(),
-        _row_stride(b, "b") if K else 0, b_scales.data_ptr(),
+        a.data_ptr(), _row_stride(a, "a", K) if K else 0, a_scales.data_ptr(), b.data_ptr(),
+        _row_stride(b, "b", K) if K else 0, b_scales.data_ptr(),
         None if bias is None else bias.data_ptr(), M, N, K, out_dtype, out.data_ptr(),
-        _row_stride(out, "out"), _stream(stream)))
+        _row_stride(out, "out", N), _stream(stream)))
     return out

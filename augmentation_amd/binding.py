@@ -26,6 +26,10 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
+# what every call asks torch for, without the attribute reads on the way
+_current_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+_any_requires_grad, _increment_version = torch._C._any_requires_grad, torch._C._increment_version
+
 FN_OK, FN_EINVAL, FN_EOVERFLOW, FN_EHIP = 0, -1, -2, -3
 FN_OUT_FP32, FN_OUT_FP16, FN_OUT_FP16_PAD4, FN_OUT_BF16 = 0, 1, 2, 3
 
@@ -112,7 +116,7 @@ def _stream(stream) -> int | None:
     if stream is None:
         # the current stream's handle, without the 2.6 us that building a
         # torch.cuda.Stream object for it takes
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _current_stream(_current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -287,18 +291,22 @@ def params_to_numpy(t: torch.Tensor) -> np.ndarray:
 # a forward-mode tangent, is refused, for its derivative would be lost without
 # a word.  In training they stand inside a torch.autograd.Function (rms_norm in
 # its forward, rms_norm_backward in its backward), where torch records none.
+# What a call writes counts a version, as with torch's in-place operations: a
+# backward pass that saved such a tensor raises instead of using what has taken
+# its place.
 
 _TYPE_CODES = {torch.float32: FN_OUT_FP32, torch.float16: FN_OUT_FP16, torch.bfloat16: FN_OUT_BF16}
 _CODE_TYPES = {code: t for t, code in _TYPE_CODES.items()}
 
 
 def _refuse_gradients(*tensors) -> None:
-    if torch._C._any_requires_grad(*tensors) and torch.is_grad_enabled():
-        raise ValueError("an argument requires a gradient, which this call does not record: call it "
-                         "under torch.no_grad() or within a torch.autograd.Function")
+    if _any_requires_grad(*tensors) and torch.is_grad_enabled():
+        raise ValueError("an argument requires a gradient, which this call does not record: call "
+                         "it under torch.no_grad() or within a torch.autograd.Function")
     if forward_ad._current_level >= 0 and any(
             t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
-        raise ValueError("an argument carries a forward-mode tangent, which this call does not carry on")
+        raise ValueError("an argument carries a forward-mode tangent, which this call does not "
+                         "carry on")
 
 
 def _type_code(dtype) -> int:
@@ -308,13 +316,12 @@ def _type_code(dtype) -> int:
     return code
 
 
-def _row_stride(t: torch.Tensor, name: str, width: int | None = None) -> int:
+def _row_stride(t: torch.Tensor, name: str) -> int:
     """The row stride of a (..., D) tensor whose leading dimensions step by
     one common stride (any contiguous tensor, a slice of its last dimension,
-    one row expanded to many) and whose last dimension is contiguous.
-    `width`: D, where the caller knows it."""
+    one row expanded to many) and whose last dimension is contiguous."""
     if t.is_contiguous():
-        return t.shape[-1] if width is None else width
+        return t.shape[-1]
     shape, st = t.shape, t.stride()
     stride = None
     if shape[-1] <= 1 or st[-1] == 1:
@@ -366,10 +373,12 @@ def _norm(x, weight, eps, residual, sum_out, stream, out_args, q8):
     if residual is not None:
         _want(residual, shape, dtype, dev, "residual")
         sum_out = _want(sum_out, shape, dtype, dev, "sum_out")
-        res_at, res_stride = residual.data_ptr(), _row_stride(residual, "residual", width)
-        sum_at, sum_stride = sum_out.data_ptr(), _row_stride(sum_out, "sum_out", width)
+        res_at, sum_at = residual.data_ptr(), sum_out.data_ptr()
+        res_stride = width if residual.is_contiguous() else _row_stride(residual, "residual")
+        sum_stride = width if sum_out.is_contiguous() else _row_stride(sum_out, "sum_out")
     elif sum_out is not None:
         raise ValueError("sum_out without a residual")
+    x_stride = width if x.is_contiguous() else _row_stride(x, "x")
     if q8:
         codes, scales, rstd = out_args
         codes = _want(codes, shape, torch.int8, dev, "codes")
@@ -377,17 +386,20 @@ def _norm(x, weight, eps, residual, sum_out, stream, out_args, q8):
         if rstd is not None:
             _want(rstd, shape[:-1], torch.float32, dev, "rstd", True)
         _check(_lib.fn_rms_norm_q8(
-            x.data_ptr(), _row_stride(x, "x", width), res_at, res_stride, weight.data_ptr(), rows, width,
-            eps, code, sum_at, sum_stride, codes.data_ptr(), _row_stride(codes, "codes", width),
-            scales.data_ptr(), None if rstd is None else rstd.data_ptr(), _stream(stream)))
+            x.data_ptr(), x_stride, res_at, res_stride, weight.data_ptr(), rows, width, eps, code,
+            sum_at, sum_stride, codes.data_ptr(),
+            width if codes.is_contiguous() else _row_stride(codes, "codes"), scales.data_ptr(),
+            None if rstd is None else rstd.data_ptr(), _stream(stream)))
+        _increment_version([t for t in (codes, scales, sum_out, rstd) if t is not None])
         return codes, scales, x if residual is None else sum_out
     out, rstd = out_args
     out = _want(out, shape, dtype, dev, "out")
     rstd = _want(rstd, shape[:-1], torch.float32, dev, "rstd", True)
     _check(_lib.fn_rms_norm(
-        x.data_ptr(), _row_stride(x, "x", width), res_at, res_stride, weight.data_ptr(), rows, width, eps,
-        code, sum_at, sum_stride, out.data_ptr(), _row_stride(out, "out", width), rstd.data_ptr(),
-        _stream(stream)))
+        x.data_ptr(), x_stride, res_at, res_stride, weight.data_ptr(), rows, width, eps, code,
+        sum_at, sum_stride, out.data_ptr(), width if out.is_contiguous() else _row_stride(out, "out"),
+        rstd.data_ptr(), _stream(stream)))
+    _increment_version((out, rstd) if residual is None else (out, rstd, sum_out))
     return out, rstd, x if residual is None else sum_out
 
 
@@ -415,8 +427,11 @@ def quantize_rows(x, codes=None, scales=None, stream=None):
     codes = _want(codes, shape, torch.int8, dev, "codes")
     scales = _want(scales, shape[:-1], torch.float32, dev, "scales", True)
     _check(_lib.fn_quantize_rows(
-        x.data_ptr(), _row_stride(x, "x", width), rows, width, _type_code(x.dtype), codes.data_ptr(),
-        _row_stride(codes, "codes", width), scales.data_ptr(), _stream(stream)))
+        x.data_ptr(), width if x.is_contiguous() else _row_stride(x, "x"), rows, width,
+        _type_code(x.dtype), codes.data_ptr(),
+        width if codes.is_contiguous() else _row_stride(codes, "codes"), scales.data_ptr(),
+        _stream(stream)))
+    _increment_version((codes, scales))
     return codes, scales
 
 
@@ -446,7 +461,8 @@ def rms_norm_backward(dout, h, weight, rstd, dsum=None, dx=None, dweight=None, w
     dsum_at, dsum_stride = None, 0
     if dsum is not None:
         _want(dsum, shape, dtype, dev, "dsum")
-        dsum_at, dsum_stride = dsum.data_ptr(), _row_stride(dsum, "dsum", width)
+        dsum_at = dsum.data_ptr()
+        dsum_stride = width if dsum.is_contiguous() else _row_stride(dsum, "dsum")
     dx = _want(dx, shape, dtype, dev, "dx")
     dweight = _want(dweight, (width,), torch.float32, dev, "dweight", True)
     if workspace is None:
@@ -457,9 +473,12 @@ def rms_norm_backward(dout, h, weight, rstd, dsum=None, dx=None, dweight=None, w
     else:
         at, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _check(_lib.fn_rms_norm_backward(
-        dout.data_ptr(), _row_stride(dout, "dout", width), h.data_ptr(), _row_stride(h, "h", width),
-        weight.data_ptr(), rstd.data_ptr(), dsum_at, dsum_stride, rows, width, code, dx.data_ptr(),
-        _row_stride(dx, "dx", width), dweight.data_ptr(), at, size, _stream(stream)))
+        dout.data_ptr(), width if dout.is_contiguous() else _row_stride(dout, "dout"),
+        h.data_ptr(), width if h.is_contiguous() else _row_stride(h, "h"), weight.data_ptr(),
+        rstd.data_ptr(), dsum_at, dsum_stride, rows, width, code, dx.data_ptr(),
+        width if dx.is_contiguous() else _row_stride(dx, "dx"), dweight.data_ptr(), at, size,
+        _stream(stream)))
+    _increment_version((dx, dweight) if workspace is None else (dx, dweight, workspace))
     return dx, dweight
 
 
@@ -487,8 +506,9 @@ def matmul_q8(a, a_scales, b, b_scales, bias=None, out_dtype=FN_OUT_BF16, out=No
     if bias is not None:
         _want(bias, (N,), torch.float32, dev, "bias", True)
     _check(_lib.fn_matmul_q8(
-        a.data_ptr(), _row_stride(a, "a", K) if K else 0, a_scales.data_ptr(), b.data_ptr(),
-        _row_stride(b, "b", K) if K else 0, b_scales.data_ptr(),
+        a.data_ptr(), K if a.is_contiguous() else _row_stride(a, "a"), a_scales.data_ptr(),
+        b.data_ptr(), K if b.is_contiguous() else _row_stride(b, "b"), b_scales.data_ptr(),
         None if bias is None else bias.data_ptr(), M, N, K, out_dtype, out.data_ptr(),
-        _row_stride(out, "out", N), _stream(stream)))
+        N if out.is_contiguous() else _row_stride(out, "out"), _stream(stream)))
+    _increment_version((out,))
     return out

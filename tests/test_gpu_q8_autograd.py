@@ -66,3 +66,42 @@ def test_lost_gradients_are_refused_on_the_device(fn):
     with torch.no_grad():
         out, _, _ = fn.rms_norm(x, w)
     assert not out.requires_grad and torch.equal(out, fn.rms_norm(x, w.detach())[0])
+
+
+def test_written_tensors_count_a_version(fn):
+    """Every tensor that a call writes, and no other: a backward pass that saved
+    one of them before raises rather than use what has taken its place."""
+    def made(*shape, t=torch.float32):
+        return torch.ones(*shape, dtype=t, device="cuda")
+
+    x, r, w, out, h, dsum = (made(700, 64) if k != 2 else made(64) for k in range(6))
+    rstd, scales, codes, dw = made(700), made(700), made(700, 64, t=torch.int8), made(64)
+    ws = fn.rms_norm_backward_workspace(700, 64)
+    product = made(700, 700)
+    everything = [x, r, w, out, h, dsum, rstd, scales, codes, dw, ws, product]
+
+    def writes(call, *written):
+        before = [v._version for v in everything]
+        call()
+        for v, old in zip(everything, before):
+            assert v._version == old + any(v is o for o in written)
+
+    writes(lambda: fn.rms_norm(x, w, residual=r, sum_out=h, out=out, rstd=rstd), h, out, rstd)
+    writes(lambda: fn.rms_norm(x, w, residual=r, sum_out=r, out=x), r, x)
+    writes(lambda: fn.rms_norm(x, w, out=x), x)
+    writes(lambda: fn.rms_norm(x, w))
+    writes(lambda: fn.rms_norm_q8(x, w, residual=r, sum_out=h, codes=codes, scales=scales, rstd=rstd),
+           h, codes, scales, rstd)
+    writes(lambda: fn.quantize_rows(x, codes=codes, scales=scales), codes, scales)
+    writes(lambda: fn.rms_norm_backward(out, h, w, rstd, dsum=dsum, dx=dsum, dweight=dw, workspace=ws),
+           dsum, dw, ws)
+    writes(lambda: fn.matmul_q8(codes, scales, codes, scales, out=product), product)
+    with torch.inference_mode():
+        assert fn.quantize_rows(made(3, 8))[0].shape == (3, 8)
+
+    leaf = made(700, 64).requires_grad_()
+    y = leaf * h  # saves h
+    with torch.no_grad():
+        fn.rms_norm(x, w, residual=h, sum_out=h)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()

@@ -122,6 +122,18 @@ def _stream(stream) -> int | None:
     return int(stream)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A new tensor that belongs to the call's stream: its memory was last used
+    there.  One of the current stream's could still be in use by that, and be
+    written from both."""
+    if stream is None or _stream(stream) == _stream(None):
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _check(rc: int) -> int:
     if rc != FN_OK:
         raise FnError(rc, fn_last_error())
@@ -247,6 +259,12 @@ def fn_test_timeline(stamps, tiles) -> int:
 
 
 # ------------------------------------------------------------ tensor helpers
+#
+# `stream`: a torch.cuda.Stream or a handle; the current stream if None.  What a
+# helper allocates belongs to that stream, as with torch.cuda.stream(stream).
+# As for torch's own work on several streams, the caller sees to it that the
+# arguments are ready for the stream and live until it has finished, and waits
+# for it before results are used elsewhere.
 
 def fused_normalize(x: torch.Tensor, mean, std, flip_p=0.5, erase_p=0.0, scale=(0.02, 0.33),
                     ratio=(0.3, 3.3), seed=0, out_dtype=FN_OUT_FP32, out=None,
@@ -260,7 +278,7 @@ def fused_normalize(x: torch.Tensor, mean, std, flip_p=0.5, erase_p=0.0, scale=(
     tdt = torch.float32 if out_dtype == FN_OUT_FP32 else torch.float16
     shape = (N, H, W, 4 if out_dtype == FN_OUT_FP16_PAD4 else C)
     if out is None:
-        out = torch.empty(shape, dtype=tdt, device=x.device)
+        out = _empty(shape, tdt, x.device, stream)
     elif out.dtype != tdt or tuple(out.shape) != shape or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor of shape %s and out_dtype" % (shape,))
     fn_fused_normalize(x, N, H, W, C, mean, std, flip_p, erase_p, scale[0], scale[1], ratio[0],
@@ -271,7 +289,7 @@ def fused_normalize(x: torch.Tensor, mean, std, flip_p=0.5, erase_p=0.0, scale=(
 def sample_params(N, H, W, flip_p=0.5, erase_p=0.0, scale=(0.02, 0.33), ratio=(0.3, 3.3), seed=0,
                   device="cuda", stream=None) -> torch.Tensor:
     """fn_params into a new (N, 8) int32 CUDA tensor (fields in PARAMS_DTYPE order)."""
-    out = torch.empty((max(N, 0), 8), dtype=torch.int32, device=device)
+    out = _empty((max(N, 0), 8), torch.int32, device, stream)
     fn_params(seed, N, H, W, flip_p, erase_p, scale[0], scale[1], ratio[0], ratio[1], out, stream)
     return out
 
@@ -340,11 +358,11 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
                      "(use .contiguous())")
 
 
-def _want(t, shape, dtype, dev: int, name: str, flat: bool = False) -> torch.Tensor:
+def _want(t, shape, dtype, dev: int, name: str, flat: bool = False, stream=None) -> torch.Tensor:
     """`t` if it has this shape, dtype and device (and is contiguous, if
-    `flat`); a new tensor if it is None."""
+    `flat`); a new tensor of the stream's if it is None."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return _empty(shape, dtype, dev, stream)
     if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on cuda:{dev}")
     if flat and not t.is_contiguous():
@@ -372,7 +390,7 @@ def _norm(x, weight, eps, residual, sum_out, stream, out_args, q8):
     res_stride = sum_stride = 0
     if residual is not None:
         _want(residual, shape, dtype, dev, "residual")
-        sum_out = _want(sum_out, shape, dtype, dev, "sum_out")
+        sum_out = _want(sum_out, shape, dtype, dev, "sum_out", False, stream)
         res_at, sum_at = residual.data_ptr(), sum_out.data_ptr()
         res_stride = width if residual.is_contiguous() else _row_stride(residual, "residual")
         sum_stride = width if sum_out.is_contiguous() else _row_stride(sum_out, "sum_out")
@@ -381,8 +399,8 @@ def _norm(x, weight, eps, residual, sum_out, stream, out_args, q8):
     x_stride = width if x.is_contiguous() else _row_stride(x, "x")
     if q8:
         codes, scales, rstd = out_args
-        codes = _want(codes, shape, torch.int8, dev, "codes")
-        scales = _want(scales, shape[:-1], torch.float32, dev, "scales", True)
+        codes = _want(codes, shape, torch.int8, dev, "codes", False, stream)
+        scales = _want(scales, shape[:-1], torch.float32, dev, "scales", True, stream)
         if rstd is not None:
             _want(rstd, shape[:-1], torch.float32, dev, "rstd", True)
         _check(_lib.fn_rms_norm_q8(
@@ -393,8 +411,8 @@ def _norm(x, weight, eps, residual, sum_out, stream, out_args, q8):
         _increment_version([t for t in (codes, scales, sum_out, rstd) if t is not None])
         return codes, scales, x if residual is None else sum_out
     out, rstd = out_args
-    out = _want(out, shape, dtype, dev, "out")
-    rstd = _want(rstd, shape[:-1], torch.float32, dev, "rstd", True)
+    out = _want(out, shape, dtype, dev, "out", False, stream)
+    rstd = _want(rstd, shape[:-1], torch.float32, dev, "rstd", True, stream)
     _check(_lib.fn_rms_norm(
         x.data_ptr(), x_stride, res_at, res_stride, weight.data_ptr(), rows, width, eps, code,
         sum_at, sum_stride, out.data_ptr(), width if out.is_contiguous() else _row_stride(out, "out"),
@@ -424,8 +442,8 @@ def quantize_rows(x, codes=None, scales=None, stream=None):
     an fp32 scale per row)."""
     _refuse_gradients(x, scales)
     shape, rows, width, dev = _rows_of(x)
-    codes = _want(codes, shape, torch.int8, dev, "codes")
-    scales = _want(scales, shape[:-1], torch.float32, dev, "scales", True)
+    codes = _want(codes, shape, torch.int8, dev, "codes", False, stream)
+    scales = _want(scales, shape[:-1], torch.float32, dev, "scales", True, stream)
     _check(_lib.fn_quantize_rows(
         x.data_ptr(), width if x.is_contiguous() else _row_stride(x, "x"), rows, width,
         _type_code(x.dtype), codes.data_ptr(),
@@ -448,9 +466,7 @@ def rms_norm_backward(dout, h, weight, rstd, dsum=None, dx=None, dweight=None, w
     """fn_rms_norm_backward on (..., D) CUDA tensors of one dtype; rstd and h
     as rms_norm returned them.  Returns (dx, dweight): the gradient of x (and
     of the residual) and the fp32 gradient of the weight.  dx may be dout, h
-    or dsum.  Without a workspace one is allocated for the call; with
-    `stream` other than the current one, pass a workspace that lives until
-    the stream has finished."""
+    or dsum.  Without a workspace one is allocated for the call."""
     _refuse_gradients(dout, h, weight, rstd, dsum, dx, dweight)
     shape, rows, width, dev = _rows_of(h)
     dtype = h.dtype
@@ -463,12 +479,12 @@ def rms_norm_backward(dout, h, weight, rstd, dsum=None, dx=None, dweight=None, w
         _want(dsum, shape, dtype, dev, "dsum")
         dsum_at = dsum.data_ptr()
         dsum_stride = width if dsum.is_contiguous() else _row_stride(dsum, "dsum")
-    dx = _want(dx, shape, dtype, dev, "dx")
-    dweight = _want(dweight, (width,), torch.float32, dev, "dweight", True)
+    dx = _want(dx, shape, dtype, dev, "dx", False, stream)
+    dweight = _want(dweight, (width,), torch.float32, dev, "dweight", True, stream)
     if workspace is None:
         size = _workspace_bytes(rows, width)
         if size:
-            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+            workspace = _empty((size,), torch.uint8, dev, stream)
         at = workspace.data_ptr() if size else None
     else:
         at, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -497,7 +513,7 @@ def matmul_q8(a, a_scales, b, b_scales, bias=None, out_dtype=FN_OUT_BF16, out=No
     if out is None:
         if out_dtype not in _CODE_TYPES:
             raise ValueError(f"unknown out_dtype {out_dtype}")
-        out = torch.empty((*lead, N), dtype=_CODE_TYPES[out_dtype], device=dev)
+        out = _empty((*lead, N), _CODE_TYPES[out_dtype], dev, stream)
     else:
         out_dtype = _type_code(out.dtype)
         _want(out, (*lead, N), out.dtype, dev, "out")

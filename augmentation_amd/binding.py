@@ -487,6 +487,8 @@ def rms_norm_backward(dout, h, weight, rstd, dsum=None, dx=None, dweight=None, w
             workspace = _empty((size,), torch.uint8, dev, stream)
         at = workspace.data_ptr() if size else None
     else:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
         at, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _check(_lib.fn_rms_norm_backward(
         dout.data_ptr(), width if dout.is_contiguous() else _row_stride(dout, "dout"),

@@ -466,7 +466,9 @@ def rms_norm_backward(dout, h, weight, rstd, dsum=None, dx=None, dweight=None, w
     """fn_rms_norm_backward on (..., D) CUDA tensors of one dtype; rstd and h
     as rms_norm returned them.  Returns (dx, dweight): the gradient of x (and
     of the residual) and the fp32 gradient of the weight.  dx may be dout, h
-    or dsum.  Without a workspace one is allocated for the call."""
+    or dsum.  Without a workspace one is allocated for the call.  The last bit
+    of dx in 16-bit rows of odd width beyond 2,560 may depend on whether the
+    row's number and dout's row stride are odd."""
     _refuse_gradients(dout, h, weight, rstd, dsum, dx, dweight)
     shape, rows, width, dev = _rows_of(h)
     dtype = h.dtype

@@ -612,10 +612,11 @@ __global__ __launch_bounds__(rows_block<kThreads>()) void rows_backward_kernel(B
   float dw[kChunks][8];
   // Loads that begin within a dword take a quarter more time, as do those of
   // every other row where an odd number of 16-bit elements follow each other.
-  // A work-group of the odd rows has its chunks shifted by one element (row,
-  // width and stride decide, not addresses, which would change a row's sums with
-  // them; 10000x4095 83 -> 66 us, 4099x5003 47 -> 40, without dsum 68 -> 53 and
-  // 39 -> 37; but rows of 4095 at a stride of 4096 54 -> 67, so not these).
+  // A work-group of the odd rows has its chunks shifted by one element, which
+  // changes the order of its rows' means, though not of dweight (row, width and
+  // stride decide, not addresses, which would change a row's sums with them;
+  // 10000x4095 83 -> 66 us, 4099x5003 47 -> 40, without dsum 68 -> 53 and 39 ->
+  // 37; but rows of 4095 at a stride of 4096 54 -> 67, so not these).
   constexpr bool kShift = sizeof(T) == 2 && kRows == 1;
   int32_t shift = 0;
   if constexpr (kShift) shift = a.width & (int)a.dout_stride & (int)(blockIdx.x & 1u);

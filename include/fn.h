@@ -271,6 +271,11 @@ int fn_quantize_rows(const void* x_dev, int64_t x_stride, int64_t rows, int32_t 
  *   dweight = sum over the rows of dout * n, fp32, overwritten, joined in an
  *             order that the sizes alone fix (no atomics).  rows = 0 writes
  *             zeros.
+ * A row's mean is summed in an order that the width, the type and rows and
+ * dout_stride fix, but not the same for every row: 16-bit rows of odd width
+ * from 2561 to 16384 at an odd dout_stride are added up from another first
+ * element if their number is odd.  There dx of equal rows may differ by the
+ * rounding of that sum; dweight does not depend on it.
  * dx_dev may be exactly dout_dev, h_dev or dsum_dev.  workspace_dev: at least
  * fn_rms_norm_backward_workspace(rows, width) bytes, 16-byte aligned, that no
  * other call in flight uses.  For a norm whose output was quantised, dout is

@@ -11,7 +11,9 @@
 // rstd is a common factor of the row, so it cancels in code_j: the codes need
 // the maximum alone, which no order of evaluation changes, and h_j w_j is
 // exact in fp32 for 16-bit types.  The sum of squares and the maximum are
-// taken in the same pass, so one reduction serves both.
+// taken in the same pass, so one reduction serves both.  One reciprocal for a
+// row, instead of a division for each element, costs a code that may fall to
+// either side where 127 t_j / A is within 127 * 3 * 2^-24 of half way.
 //
 // Every element is read once and written once: a row stays in registers
 // between the reduction and the output (rows of more than 32,768 elements

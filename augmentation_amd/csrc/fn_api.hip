@@ -340,7 +340,6 @@ int plan_tiles(fn::FusedArgs* a, int64_t N, int32_t H, int64_t row, int64_t elem
   const int64_t tile_rows = a->images_per_tile == 1 ? a->rows_per_tile : a->images_per_tile * H;
   const int64_t lds = row_slot > 0 ? tile_rows * row_slot + 16 : (tile_bytes + 32 + 15) / 16 * 16;
   if (lds > lds_limit) return fail(FN_EOVERFLOW, "tile exceeds the LDS budget");
-  if (a->total_tiles > 0x7FFFFFFF) return fail(FN_EOVERFLOW, "grid size limit exceeded");
   a->lds_buffer_bytes = (int32_t)lds;
   return FN_OK;
 }
@@ -369,17 +368,24 @@ FN_EXPORT int fn_params_ex(uint64_t seed, int64_t first_sample_id, int64_t N, in
                           &a);
   if (rc) return rc;
   if (first_sample_id < 0) return fail(FN_EINVAL, "first_sample_id must be >= 0");
-  a.first_sample = (uint64_t)first_sample_id;
   if (N < 0) return fail(FN_EINVAL, "N must be >= 0");
   if (N > ((int64_t)1 << 36)) return fail(FN_EOVERFLOW, "N too large");
   if (N == 0) return ok();
   int dev = -1;
   rc = check_device_range(params_dev, (size_t)N * sizeof(fn_sample_params), "params_dev", &dev);
   if (rc) return rc;
+  // sixteen threads a sample: 2^26 samples to a launch keep it below 2^32
+  constexpr int64_t kSamplesPerLaunch = (int64_t)1 << 26;
   const int64_t samples_per_block = fn::kBlock / 16;
-  fn::params_kernel<<<blocks_for(N, samples_per_block), fn::kBlock, 0, (hipStream_t)stream>>>(
-      a, N, reinterpret_cast<fn::SampleParams*>(params_dev));
-  return launch_status("params_kernel launch");
+  for (int64_t n = 0; n < N; n += kSamplesPerLaunch) {
+    const int64_t part = std::min(N - n, kSamplesPerLaunch);
+    a.first_sample = (uint64_t)first_sample_id + (uint64_t)n;
+    fn::params_kernel<<<blocks_for(part, samples_per_block), fn::kBlock, 0, (hipStream_t)stream>>>(
+        a, part, reinterpret_cast<fn::SampleParams*>(params_dev) + n);
+    rc = launch_status("params_kernel launch");
+    if (rc) return rc;
+  }
+  return ok();
 }
 
 FN_EXPORT int fn_params(uint64_t seed, int64_t N, int32_t H, int32_t W, float flip_p,
@@ -469,6 +475,22 @@ int fused_normalize_impl(const uint8_t* in_u8_dev, const int64_t* strides, int64
   const uintptr_t o0 = (uintptr_t)out_dev, o1 = o0 + (uintptr_t)out_elems * out_bytes;
   if (i0 < o1 && o0 < i1) return fail(FN_EINVAL, "input and output overlap");
 
+  // a batch that would take 2^32 threads, which HIP does not start in one
+  // launch: its halves (whole sixteens of images, so that both outputs are
+  // aligned alike)
+  auto in_halves = [&]() {
+    const int64_t half = (N / 2 + 15) / 16 * 16;
+    if (half >= N) return fail(FN_EOVERFLOW, "grid size limit exceeded");
+    const int half_rc = fused_normalize_impl(in_u8_dev, strides, half, H, W, C, mean, std, flip_p,
+                                             erase_p, scale_min, scale_max, ratio_min, ratio_max,
+                                             seed, first_sample_id, out_dtype, out_dev, stream);
+    if (half_rc) return half_rc;
+    return fused_normalize_impl(in_u8_dev + half * image_stride, strides, N - half, H, W, C, mean,
+                                std, flip_p, erase_p, scale_min, scale_max, ratio_min, ratio_max,
+                                seed, first_sample_id + half, out_dtype,
+                                (char*)out_dev + half * H * W * oc * out_bytes, stream);
+  };
+
   a.in = in_u8_dev;
   a.out = out_dev;
   a.N = N;
@@ -510,6 +532,9 @@ int fused_normalize_impl(const uint8_t* in_u8_dev, const int64_t* strides, int64
     if (rc) return rc;
     rc = plan_tiles(&a, N, H, row, elems, cus, row_slot, lds_all);
     if (rc) return rc;
+    const int32_t threads = out_dtype == FN_OUT_FP32 ? fn::tiles_threads<float>()
+                                                     : fn::tiles_threads<_Float16>();
+    if (a.total_tiles > kMaxThreads / threads) return in_halves();
     a.row_slot = (int32_t)row_slot;
     a.div_gps = make_fast_div((uint32_t)std::max<int64_t>(row_slot / 16, 1));
     a.div_row = make_fast_div((uint32_t)row);
@@ -518,8 +543,6 @@ int fused_normalize_impl(const uint8_t* in_u8_dev, const int64_t* strides, int64
     a.div_tpi = make_fast_div((uint32_t)a.tiles_per_image);
     {
       const int32_t chunk = out_dtype == FN_OUT_FP32 ? 4 : 8;  // outputs per 16-byte store
-      const int32_t threads = out_dtype == FN_OUT_FP32 ? fn::tiles_threads<float>()
-                                                       : fn::tiles_threads<_Float16>();
       // chunks per row: 0 for rows shorter than one vector, which only the
       // flat kernel takes
       const int32_t cpr = (int32_t)(row_out / chunk);
@@ -572,11 +595,12 @@ int fused_normalize_impl(const uint8_t* in_u8_dev, const int64_t* strides, int64
       a.iter = iter;
       const int64_t per_block = (int64_t)fn::kBlock * iter;
       const int64_t grid = (a.total_groups + per_block - 1) / per_block;
-      if (grid > 0x7FFFFFFF) return fail(FN_EOVERFLOW, "grid size limit exceeded");
+      if (grid > kMaxThreads / fn::kBlock) return in_halves();
       launch_grouped(a, C, px, out_dtype, (unsigned)grid, st);
       return launch_status("fused_grouped_kernel launch");
     }
   }
+  if (N * a.tiles_per_image > kMaxThreads / fn::kBlock) return in_halves();
   const unsigned grid = (unsigned)(N * a.tiles_per_image);
   if (out_dtype == FN_OUT_FP32)
     fn::fused_generic_kernel<float><<<grid, fn::kBlock, 0, st>>>(a);
@@ -619,7 +643,7 @@ FN_EXPORT int fn_test_erase_dims(const uint32_t* w_scale_dev, const uint32_t* w_
   int rc = make_draw_args(0, H, W, 0.0f, 1.0f, scale_min, scale_max, ratio_min, ratio_max, &a);
   if (rc) return rc;
   if (count < 0) return fail(FN_EINVAL, "count must be >= 0");
-  if (count > ((int64_t)1 << 36)) return fail(FN_EOVERFLOW, "count too large");
+  if (count > kMaxThreads / fn::kBlock * fn::kBlock) return fail(FN_EOVERFLOW, "count too large");
   if (count == 0) return ok();
   int dev = -1;
   if ((rc = check_device_range(w_scale_dev, count * 4, "w_scale_dev", &dev)) ||
@@ -637,7 +661,7 @@ FN_EXPORT int fn_test_cr_ops(int32_t op, const float* a_dev, const float* b_dev,
                              float* out_dev, void* stream) {
   if (op < 0 || op > 2) return fail(FN_EINVAL, "op must be 0 (exp), 1 (sqrt) or 2 (div)");
   if (count < 0) return fail(FN_EINVAL, "count must be >= 0");
-  if (count > ((int64_t)1 << 36)) return fail(FN_EOVERFLOW, "count too large");
+  if (count > kMaxThreads / fn::kBlock * fn::kBlock) return fail(FN_EOVERFLOW, "count too large");
   if (count == 0) return ok();
   int rc;
   int dev = -1;
@@ -677,7 +701,9 @@ FN_EXPORT int fn_test_stream(const void* src_dev, void* dst_dev, int64_t in_byte
   if (in_bytes < 0 || in_bytes % 16 != 0) return fail(FN_EINVAL, "in_bytes must be a multiple of 16");
   if ((((uintptr_t)src_dev | (uintptr_t)dst_dev) & 15u) != 0)
     return fail(FN_EINVAL, "src_dev and dst_dev must be 16-byte aligned");
-  if (in_bytes > ((int64_t)1 << 40)) return fail(FN_EOVERFLOW, "in_bytes too large");
+  const int64_t lanes = in_bytes / (widen == 2 ? 8 : 16);
+  if (lanes > kMaxThreads / fn::kBlock * fn::kBlock)
+    return fail(FN_EOVERFLOW, "in_bytes too large");
   if (in_bytes == 0) return ok();
   int rc;
   int dev = -1;
@@ -687,7 +713,6 @@ FN_EXPORT int fn_test_stream(const void* src_dev, void* dst_dev, int64_t in_byte
   const uintptr_t s0 = (uintptr_t)src_dev, d0 = (uintptr_t)dst_dev;
   if (s0 < d0 + (uintptr_t)(in_bytes * widen) && d0 < s0 + (uintptr_t)in_bytes)
     return fail(FN_EINVAL, "source and destination overlap");
-  const int64_t lanes = in_bytes / (widen == 2 ? 8 : 16);
   const unsigned grid = blocks_for(lanes, fn::kBlock);
   const uint8_t* src = reinterpret_cast<const uint8_t*>(src_dev);
   fn::u32x4* dst = reinterpret_cast<fn::u32x4*>(dst_dev);

@@ -84,6 +84,10 @@ inline int launch_status(const char* what) {
   return ok();
 }
 
+// HIP starts fewer than 2^32 threads along a dimension of a launch.  More are
+// refused, or silently taken modulo 2^32.
+constexpr int64_t kMaxThreads = 0xFFFFFFFF;
+
 inline unsigned blocks_for(int64_t items, int64_t per_block) {
   return (unsigned)((items + per_block - 1) / per_block);
 }

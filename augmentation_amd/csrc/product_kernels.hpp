@@ -253,16 +253,18 @@ struct OutputTile {
 // One tile of kBM tokens x kBN channels per work-group of kWM x kWN
 // wavefronts, each with kTM x kTN tiles of the 16x16x64 instruction (measured
 // against 32x32x32 on 8192^3: 2.54 against 2.42 POP/s; the smaller one moves
-// fewer accumulator registers per operation, and the power limit, not the
-// count of cycles, is what such a product meets first).
+// fewer accumulator registers per operation, and the clock that falls under
+// load costs such a product more than the count of cycles).
 //
 // A wavefront's products of one step (64 codes of K) are its time for
 // everything else: between them it reads the next step's fragments from LDS
 // and, in a stage's last step, issues its share of a later stage's loads.
 // 8192^3 takes 395 to 440 us (2.5 to 2.8 POP/s) with the matrix cores 64% busy
-// at 1.85 GHz: power bounds it, for the same products alone hold 2.36 GHz and
-// take 290 us.  Short sums are bound by what no product covers, the first loads
-// and the outputs: 50176x1024x768 50 us, 38 at the rate of a large product.
+// at 1.85 GHz.  The same products alone hold 2.36 GHz and take 290 us, so the
+// clock under load is most of the difference; why they are a quarter idle
+// even then is not known.  Short sums are bound by what no product covers, the
+// first loads and the outputs: 50176x1024x768 50 to 52 us, 28 to 32 at the rate
+// of 8192^3.
 //
 // kLines: every row starts at a cache line.  Else a stage still brings whole
 // lines: of row r it has the codes from 128 s - d to 128 s + 127 - d, d the

@@ -117,9 +117,9 @@ int check_size(int64_t rows, int32_t width) {
 // codes with a residual, us: 1000000x12 with 2 / 4 / 8 threads 26 / 36 / 62;
 // 100000x100 with 8 / 16 / 32 24 / 21 / 32; 30000x1500 with 64x3 / 256x1 60 /
 // 74; 30000x2040 backward with 64x4 / 128x2 / 256x1 92 / 99 / 101; 13000x2560
-// with 64x5 / 256x2 45 / 46, backward 53 / 64, but 300x2560 5.7 / 4.6, which a
-// caller's next launch mostly covers.
-// 0 threads: rows that do not fit.
+// with 64x5 / 256x2 45 / 46, backward 53 / 64, but 300x2560 5.7 / 4.6: the
+// choice is by the width alone, so that a row's sums do not depend on how many
+// rows there are.  0 threads: rows that do not fit.
 struct RowShape {
   int32_t width;  // up to
   int threads, chunks;
@@ -174,6 +174,7 @@ void launch_rows(const fn::RowArgs& a, hipStream_t st) {
         return launch_rows_k<T, kMode, 256, 8>(a, st);
       else
         return launch_rows_k<T, kMode, 512, 4>(a, st);
+    // 128 registers a thread: fp32 rows to codes spill 8 of them
     case shape_key(1024, 4): return launch_rows_k<T, kMode, 1024, 4>(a, st);
     default:
       fn::rows_wide_kernel<T, kMode>
@@ -404,6 +405,7 @@ void launch_tiles_best(fn::ProductArgs& p, int cus, hipStream_t st) {
 template <typename T, int kBM, int kBN>
 void launch_any(fn::ProductArgs& p, hipStream_t st) {
   const unsigned grid = tile_grid<kBM, kBN>(&p);
+  // with fp32 outputs the 256x128 tiles spill 2 of their 256 registers
   fn::product_any_kernel<T, kBM, kBN, 4><<<grid, 512, 0, st>>>(p);
 }
 

@@ -56,6 +56,12 @@ _SIGS = {
                              _P, _i64, _P],
     "fn_rms_norm_backward_workspace": [_i64, _i32, _P],
     "fn_matmul_q8": [_P, _i64, _P, _P, _i64, _P, _P, _i64, _i64, _i32, _i32, _P, _i64, _P],
+    "fn_dropout": [_P, _i64, _P, _i64, _i64, _i32, _f32, _u64, _i64, _i32, _P, _i64, _P],
+    "fn_layer_norm": [_P, _i64, _P, _i64, _P, _P, _i64, _i32, _f32, _f32, _u64, _i64, _i32, _P, _i64,
+                      _P, _i64, _P, _P, _P],
+    "fn_layer_norm_backward": [_P, _i64, _P, _i64, _P, _P, _P, _P, _i64, _i64, _i32, _f32, _u64,
+                               _i64, _i32, _P, _i64, _P, _i64, _P, _P, _P, _i64, _P],
+    "fn_layer_norm_backward_workspace": [_i64, _i32, _P],
     "fn_test_erase_dims": [_P, _P, _i64, _i32, _i32, _f32, _f32, _f32, _f32, _P, _P, _P, _P],
     "fn_test_cr_ops": [_i32, _P, _P, _i64, _P, _P],
     "fn_test_stream": [_P, _P, _i64, _i32, _P],
@@ -75,7 +81,8 @@ _declare(_lib)
 
 EXPORTED = ("fn_fused_normalize", "fn_fused_normalize_ex", "fn_params", "fn_params_ex",
             "fn_rms_norm", "fn_rms_norm_q8", "fn_quantize_rows", "fn_rms_norm_backward",
-            "fn_rms_norm_backward_workspace", "fn_matmul_q8",
+            "fn_rms_norm_backward_workspace", "fn_matmul_q8", "fn_dropout", "fn_layer_norm",
+            "fn_layer_norm_backward", "fn_layer_norm_backward_workspace",
             "fn_last_error", "fn_test_erase_dims", "fn_test_cr_ops", "fn_test_stream",
             "fn_test_timeline")
 
@@ -236,6 +243,40 @@ def fn_matmul_q8(a, a_stride, a_scales, b, b_stride, b_scales, bias, M, N, K, ou
     return _check(_lib.fn_matmul_q8(_addr(a), a_stride, _addr(a_scales), _addr(b), b_stride,
                                     _addr(b_scales), _addr(bias), M, N, K, out_dtype, _addr(out),
                                     out_stride, _stream(stream)))
+
+
+def fn_dropout(x, x_stride, residual, residual_stride, rows, width, dropout_p, seed, first_row,
+               dtype, out, out_stride, stream=None) -> int:
+    return _check(_lib.fn_dropout(_addr(x), x_stride, _addr(residual), residual_stride, rows, width,
+                                  dropout_p, seed & 0xFFFFFFFFFFFFFFFF, first_row, dtype,
+                                  _addr(out), out_stride, _stream(stream)))
+
+
+def fn_layer_norm(x, x_stride, residual, residual_stride, weight, bias, rows, width, eps, dropout_p,
+                  seed, first_row, dtype, sum_out, sum_stride, out, out_stride, mean, rstd,
+                  stream=None) -> int:
+    return _check(_lib.fn_layer_norm(
+        _addr(x), x_stride, _addr(residual), residual_stride, _addr(weight), _addr(bias), rows,
+        width, eps, dropout_p, seed & 0xFFFFFFFFFFFFFFFF, first_row, dtype, _addr(sum_out),
+        sum_stride, _addr(out), out_stride, _addr(mean), _addr(rstd), _stream(stream)))
+
+
+def fn_layer_norm_backward(dout, dout_stride, h, h_stride, weight, mean, rstd, dsum, dsum_stride,
+                           rows, width, dropout_p, seed, first_row, dtype, dh, dh_stride, dx,
+                           dx_stride, dweight, dbias, workspace, workspace_bytes,
+                           stream=None) -> int:
+    return _check(_lib.fn_layer_norm_backward(
+        _addr(dout), dout_stride, _addr(h), h_stride, _addr(weight), _addr(mean), _addr(rstd),
+        _addr(dsum), dsum_stride, rows, width, dropout_p, seed & 0xFFFFFFFFFFFFFFFF, first_row,
+        dtype, _addr(dh), dh_stride, _addr(dx), dx_stride, _addr(dweight), _addr(dbias),
+        _addr(workspace), workspace_bytes, _stream(stream)))
+
+
+def fn_layer_norm_backward_workspace(rows, width) -> int:
+    """The workspace's size in bytes."""
+    n = _i64()
+    _check(_lib.fn_layer_norm_backward_workspace(rows, width, ctypes.byref(n)))
+    return n.value
 
 
 def fn_test_erase_dims(w_scale, w_ratio, count, H, W, scale_min, scale_max, ratio_min, ratio_max,
@@ -532,3 +573,132 @@ def matmul_q8(a, a_scales, b, b_scales, bias=None, out_dtype=FN_OUT_BF16, out=No
         N if out.is_contiguous() else _row_stride(out, "out"), _stream(stream)))
     _increment_version((out,))
     return out
+
+
+# ------------------------- tensor helpers: dropout and layer norm, in training
+#
+# As the helpers of the 8-bit linear layer: they differentiate nothing, refuse
+# arguments whose gradients would be lost, and count a version for what they
+# write.
+
+def _stride_of(t, width, name) -> int:
+    return width if t.is_contiguous() else _row_stride(t, name)
+
+
+def _rows_in(t, shape, dtype, dev, width, name):
+    """(address, row stride) of an optional input of these rows."""
+    if t is None:
+        return None, 0
+    _want(t, shape, dtype, dev, name)
+    return t.data_ptr(), _stride_of(t, width, name)
+
+
+def _affine(t, width, dtype, dev, name):
+    return None if t is None else _want(t, (width,), dtype, dev, name, True).data_ptr()
+
+
+def dropout(x, p, seed, first_row=0, residual=None, out=None, stream=None):
+    """fn_dropout on (..., D) CUDA tensors of one dtype: the tensor residual +
+    dropout(x).  Row r of x (counted over its leading dimensions) draws from
+    stream (seed, first_row + r); the gradient is the same call on out's.  out
+    may be x or residual."""
+    _refuse_gradients(x, residual, out)
+    shape, rows, width, dev = _rows_of(x)
+    dtype = x.dtype
+    code = _type_code(dtype)
+    res_at, res_stride = _rows_in(residual, shape, dtype, dev, width, "residual")
+    out = _want(out, shape, dtype, dev, "out", False, stream)
+    _check(_lib.fn_dropout(x.data_ptr(), _stride_of(x, width, "x"), res_at, res_stride, rows, width,
+                           p, seed & 0xFFFFFFFFFFFFFFFF, first_row, code, out.data_ptr(),
+                           _stride_of(out, width, "out"), _stream(stream)))
+    _increment_version((out,))
+    return out
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None, p=0.0, seed=0, first_row=0,
+               out=None, sum_out=None, mean=None, rstd=None, stream=None):
+    """fn_layer_norm on (..., D) CUDA tensors of one dtype.  Returns (out, mean,
+    rstd, h): the norm of h = residual + dropout(x), each row's mean and
+    1/deviation (fp32), and h itself (x where there is no residual and p = 0).
+    out and sum_out may be x or residual."""
+    _refuse_gradients(x, weight, bias, residual, out, sum_out, mean, rstd)
+    shape, rows, width, dev = _rows_of(x)
+    dtype = x.dtype
+    code = _type_code(dtype)
+    res_at, res_stride = _rows_in(residual, shape, dtype, dev, width, "residual")
+    sum_at, sum_stride = None, 0
+    summed = residual is not None or p > 0
+    if summed:
+        sum_out = _want(sum_out, shape, dtype, dev, "sum_out", False, stream)
+        sum_at, sum_stride = sum_out.data_ptr(), _stride_of(sum_out, width, "sum_out")
+    elif sum_out is not None:
+        raise ValueError("sum_out without a residual and dropout")
+    out = _want(out, shape, dtype, dev, "out", False, stream)
+    mean = _want(mean, shape[:-1], torch.float32, dev, "mean", True, stream)
+    rstd = _want(rstd, shape[:-1], torch.float32, dev, "rstd", True, stream)
+    _check(_lib.fn_layer_norm(
+        x.data_ptr(), _stride_of(x, width, "x"), res_at, res_stride,
+        _affine(weight, width, dtype, dev, "weight"), _affine(bias, width, dtype, dev, "bias"), rows,
+        width, eps, p, seed & 0xFFFFFFFFFFFFFFFF, first_row, code, sum_at, sum_stride,
+        out.data_ptr(), _stride_of(out, width, "out"), mean.data_ptr(), rstd.data_ptr(),
+        _stream(stream)))
+    _increment_version((out, mean, rstd, sum_out) if summed else (out, mean, rstd))
+    return out, mean, rstd, sum_out if summed else x
+
+
+_layer_workspace_bytes = functools.lru_cache(maxsize=256)(fn_layer_norm_backward_workspace)
+
+
+def layer_norm_backward_workspace(rows, width, device="cuda") -> torch.Tensor:
+    """A workspace for layer_norm_backward on rows of this size."""
+    return torch.empty(_layer_workspace_bytes(rows, width), dtype=torch.uint8, device=device)
+
+
+def _workspace(workspace, size, dev, stream):
+    """(tensor or None, address, bytes) of a call's workspace of `size` bytes."""
+    if workspace is None:
+        if not size:
+            return None, None, 0
+        workspace = _empty((size,), torch.uint8, dev, stream)
+        return workspace, workspace.data_ptr(), size
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def layer_norm_backward(dout, h, weight, mean, rstd, dsum=None, p=0.0, seed=0, first_row=0, dh=None,
+                        dx=None, dweight=None, dbias=None, workspace=None, stream=None):
+    """fn_layer_norm_backward on (..., D) CUDA tensors of one dtype; mean, rstd
+    and h as layer_norm returned them, weight None for a norm without one, p,
+    seed and first_row as there.  Returns (dh, dx, dweight, dbias): the gradient
+    of h and of the residual, the gradient of x behind the dropout (dh itself
+    for p = 0), and the fp32 gradients of weight and bias.  dh and dx may be
+    dout, h or dsum.  Without a workspace one is allocated for the call."""
+    _refuse_gradients(dout, h, weight, mean, rstd, dsum, dh, dx, dweight, dbias)
+    shape, rows, width, dev = _rows_of(h)
+    dtype = h.dtype
+    code = _type_code(dtype)
+    _want(dout, shape, dtype, dev, "dout")
+    _want(mean, shape[:-1], torch.float32, dev, "mean", True)
+    _want(rstd, shape[:-1], torch.float32, dev, "rstd", True)
+    dsum_at, dsum_stride = _rows_in(dsum, shape, dtype, dev, width, "dsum")
+    dh = _want(dh, shape, dtype, dev, "dh", False, stream)
+    dx_at, dx_stride = None, 0
+    if p > 0:
+        dx = _want(dx, shape, dtype, dev, "dx", False, stream)
+        dx_at, dx_stride = dx.data_ptr(), _stride_of(dx, width, "dx")
+    elif dx is not None:
+        raise ValueError("dx without dropout: dh is the gradient of x")
+    dweight = _want(dweight, (width,), torch.float32, dev, "dweight", True, stream)
+    dbias = _want(dbias, (width,), torch.float32, dev, "dbias", True, stream)
+    given = workspace is not None
+    workspace, at, size = _workspace(workspace, _layer_workspace_bytes(rows, width), dev, stream)
+    _check(_lib.fn_layer_norm_backward(
+        dout.data_ptr(), _stride_of(dout, width, "dout"), h.data_ptr(), _stride_of(h, width, "h"),
+        _affine(weight, width, dtype, dev, "weight"), mean.data_ptr(), rstd.data_ptr(), dsum_at,
+        dsum_stride, rows, width, p, seed & 0xFFFFFFFFFFFFFFFF, first_row, code, dh.data_ptr(),
+        _stride_of(dh, width, "dh"), dx_at, dx_stride, dweight.data_ptr(), dbias.data_ptr(), at,
+        size, _stream(stream)))
+    _increment_version([t for t in (dh, dx, dweight, dbias, workspace if given else None)
+                        if t is not None])
+    return dh, dh if dx is None else dx, dweight, dbias

@@ -795,9 +795,8 @@ __global__ __launch_bounds__(256) void rows_backward_columns_kernel(BackwardArgs
 // four to a thread, 64 threads to a column, joined in a fixed order.  `width`
 // columns from a multiple of four on; a row's last vector of four may be
 // partly beyond them, but not beyond the pitch.
-__global__ __launch_bounds__(1024) void column_sum_kernel(const float* partial, int32_t partials,
-                                                          int32_t pitch, int32_t width,
-                                                          float* dweight) {
+__device__ __forceinline__ void column_sum(const float* partial, int32_t partials, int32_t pitch,
+                                           int32_t width, float* dweight) {
   __shared__ float s_sum[64][64 + 4];
   const int col = 4 * (int)(threadIdx.x & 15u), part = (int)(threadIdx.x >> 4);
   const int64_t c = (int64_t)blockIdx.x * 64 + col;
@@ -821,6 +820,11 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* partial, 
   all = group_sum<16>(all);
   const int64_t out = (int64_t)blockIdx.x * 64 + column;
   if (first == 0 && out < width) dweight[out] = all;
+}
+
+[[maybe_unused]] static __global__ __launch_bounds__(1024) void column_sum_kernel(
+    const float* partial, int32_t partials, int32_t pitch, int32_t width, float* dweight) {
+  column_sum(partial, partials, pitch, width, dweight);
 }
 
 }  // namespace fn

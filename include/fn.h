@@ -309,6 +309,88 @@ int fn_matmul_q8(const int8_t* a_dev, int64_t a_stride, const float* a_scales_de
                  const float* bias_dev, int64_t M, int64_t N, int32_t K, int32_t out_dtype,
                  void* out_dev, int64_t out_stride, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* Dropout and layer norm, with their gradients: what stands between the     */
+/* linear layers of a network in training.  Matrices, strides, types,         */
+/* overlaps and errors as for the 8-bit linear layer.                         */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * fn_dropout -- out = residual + dropout(x), or dropout(x) if residual_dev is
+ * NULL, in fp32 with one rounding to dtype at the end.  The mask is never
+ * stored: it is a function of (seed, first_row + row, column), so the gradient
+ * of x is the same call on the gradient of out (without a residual, or with
+ * another gradient of x to add), and a batch split into calls with matching
+ * first_row gives the bits of the whole one.
+ *   dropout_p   the probability of an element's loss, in [0, 1]; it counts in
+ *               steps of 1/65536: D = rint(65536 dropout_p) in 65536 are lost,
+ *               and the others multiplied by 65536 / (65536 - D), rounded to
+ *               fp32, so that the expectation is exact.
+ *   first_row   >= 0; row r draws from stream (seed, first_row + r).  Give
+ *               every use of a step rows, or a seed, of its own.
+ * Column j of a row has 16 bits of block j / 8 of the row's stream: half j % 2
+ * (the low one first) of output (j % 8) / 2 of Philox4x32-10 with counter
+ * (j / 8, 2^31, row low, row high) and key (seed low, seed high).  It is lost
+ * if they are below D.  fn_params' words have counters below these, so the
+ * streams have none in common.  A lost element is +0 (plus the residual)
+ * whatever x holds there, NaN included.
+ * out_dev may be exactly x_dev or residual_dev (same stride).
+ * Errors: also FN_EINVAL for dropout_p outside [0, 1] or first_row < 0,
+ * FN_EOVERFLOW for first_row + rows beyond 2^63 - 1.
+ */
+int fn_dropout(const void* x_dev, int64_t x_stride, const void* residual_dev,
+               int64_t residual_stride, int64_t rows, int32_t width, float dropout_p, uint64_t seed,
+               int64_t first_row, int32_t dtype, void* out_dev, int64_t out_stride, void* stream);
+
+/*
+ * fn_layer_norm -- h = residual + dropout(x) and its layer norm, per row:
+ *   h    = fn_dropout's result (x + residual for dropout_p = 0), rounded to
+ *          dtype and stored in sum_dev; h = x and sum_dev = NULL without a
+ *          residual and dropout;
+ *   mean = sum(h) / width,  rstd = 1 / sqrt(sum((h - mean)^2) / width + eps),
+ *          stored if mean_dev and rstd_dev are not NULL (the backward pass
+ *          takes both);
+ *   out  = (h - mean) * rstd * weight + bias, rounded to dtype.
+ * weight_dev and bias_dev: `width` elements of dtype, or NULL for ones and
+ * zeros.  eps > 0.  sum_dev and out_dev may each be exactly x_dev or
+ * residual_dev, not each other.  A row that holds a NaN or an infinity, or
+ * whose sum or squares overflow fp32, is NaN throughout, with rstd = NaN.
+ */
+int fn_layer_norm(const void* x_dev, int64_t x_stride, const void* residual_dev,
+                  int64_t residual_stride, const void* weight_dev, const void* bias_dev,
+                  int64_t rows, int32_t width, float eps, float dropout_p, uint64_t seed,
+                  int64_t first_row, int32_t dtype, void* sum_dev, int64_t sum_stride,
+                  void* out_dev, int64_t out_stride, float* mean_dev, float* rstd_dev,
+                  void* stream);
+
+/*
+ * fn_layer_norm_backward -- the gradients of fn_layer_norm.  dout is the
+ * gradient of out; dsum (or NULL) the gradient that reaches h by another way;
+ * h the sum (x if there was none), mean and rstd what the forward pass stored.
+ * With n = (h - mean) * rstd and g = dout * weight:
+ *   dh      = rstd * (g - mean(g) - n * mean(g * n)) + dsum: the gradient of h
+ *             and of the residual, rounded to dtype;
+ *   dx      = dropout(dh) with the forward pass's mask, from dh in fp32 and
+ *             rounded once.  dx_dev is NULL for dropout_p = 0, where dh is the
+ *             gradient of x too;
+ *   dweight = sum over the rows of dout * n,  dbias = sum over the rows of
+ *             dout: fp32, overwritten, joined in an order that the sizes alone
+ *             fix (no atomics); either may be NULL.  rows = 0 writes zeros.
+ * dh_dev and dx_dev may each be exactly dout_dev, h_dev or dsum_dev, not each
+ * other.  workspace_dev: at least fn_layer_norm_backward_workspace(rows, width)
+ * bytes, 16-byte aligned, that no other call in flight uses.
+ */
+int fn_layer_norm_backward(const void* dout_dev, int64_t dout_stride, const void* h_dev,
+                           int64_t h_stride, const void* weight_dev, const float* mean_dev,
+                           const float* rstd_dev, const void* dsum_dev, int64_t dsum_stride,
+                           int64_t rows, int32_t width, float dropout_p, uint64_t seed,
+                           int64_t first_row, int32_t dtype, void* dh_dev, int64_t dh_stride,
+                           void* dx_dev, int64_t dx_stride, float* dweight_dev, float* dbias_dev,
+                           void* workspace_dev, int64_t workspace_bytes, void* stream);
+
+/* Writes to *bytes (host) the workspace that fn_layer_norm_backward needs. */
+int fn_layer_norm_backward_workspace(int64_t rows, int32_t width, int64_t* bytes);
+
 /* The message of the last nonzero return on the calling thread ("" if none).
  * The pointer stays valid until the next call on the same thread. */
 const char* fn_last_error(void);

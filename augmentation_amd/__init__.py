@@ -23,6 +23,9 @@ _BINDING_NAMES = (
     "fn_rms_norm_backward_workspace", "fn_matmul_q8", "FN_OUT_BF16", "rms_norm", "rms_norm_q8",
     "quantize_rows", "rms_norm_backward", "rms_norm_backward_workspace", "matmul_q8",
     "fn_dropout", "fn_layer_norm", "fn_layer_norm_backward", "fn_layer_norm_backward_workspace",
+    "fn_linear_cross_entropy", "fn_linear_cross_entropy_backward",
+    "fn_linear_cross_entropy_workspace", "linear_cross_entropy", "linear_cross_entropy_backward",
+    "linear_cross_entropy_workspace",
     "dropout", "layer_norm", "layer_norm_backward", "layer_norm_backward_workspace",
 )
 

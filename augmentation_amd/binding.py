@@ -62,6 +62,11 @@ _SIGS = {
     "fn_layer_norm_backward": [_P, _i64, _P, _i64, _P, _P, _P, _P, _i64, _i64, _i32, _f32, _u64,
                                _i64, _i32, _P, _i64, _P, _i64, _P, _P, _P, _i64, _P],
     "fn_layer_norm_backward_workspace": [_i64, _i32, _P],
+    "fn_linear_cross_entropy": [_P, _i64, _P, _i64, _P, _P, _i64, _i64, _i32, _f32, _i32, _P, _P, _P,
+                                _i64, _P],
+    "fn_linear_cross_entropy_backward": [_P, _i64, _P, _i64, _P, _i64, _P, _P, _P, _i64, _i64, _i32,
+                                         _f32, _i32, _P, _i64, _P, _i64, _P, _P, _i64, _P],
+    "fn_linear_cross_entropy_workspace": [_i64, _i64, _i32, _i32, _i32, _i32, _i32, _P],
     "fn_test_erase_dims": [_P, _P, _i64, _i32, _i32, _f32, _f32, _f32, _f32, _P, _P, _P, _P],
     "fn_test_cr_ops": [_i32, _P, _P, _i64, _P, _P],
     "fn_test_stream": [_P, _P, _i64, _i32, _P],
@@ -83,6 +88,8 @@ EXPORTED = ("fn_fused_normalize", "fn_fused_normalize_ex", "fn_params", "fn_para
             "fn_rms_norm", "fn_rms_norm_q8", "fn_quantize_rows", "fn_rms_norm_backward",
             "fn_rms_norm_backward_workspace", "fn_matmul_q8", "fn_dropout", "fn_layer_norm",
             "fn_layer_norm_backward", "fn_layer_norm_backward_workspace",
+            "fn_linear_cross_entropy", "fn_linear_cross_entropy_backward",
+            "fn_linear_cross_entropy_workspace",
             "fn_last_error", "fn_test_erase_dims", "fn_test_cr_ops", "fn_test_stream",
             "fn_test_timeline")
 
@@ -276,6 +283,35 @@ def fn_layer_norm_backward_workspace(rows, width) -> int:
     """The workspace's size in bytes."""
     n = _i64()
     _check(_lib.fn_layer_norm_backward_workspace(rows, width, ctypes.byref(n)))
+    return n.value
+
+
+def fn_linear_cross_entropy(x, x_stride, weight, weight_stride, bias, targets, rows, classes, width,
+                            smoothing, dtype, losses, lse, workspace, workspace_bytes,
+                            stream=None) -> int:
+    return _check(_lib.fn_linear_cross_entropy(
+        _addr(x), x_stride, _addr(weight), weight_stride, _addr(bias), _addr(targets), rows, classes,
+        width, smoothing, dtype, _addr(losses), _addr(lse), _addr(workspace), workspace_bytes,
+        _stream(stream)))
+
+
+def fn_linear_cross_entropy_backward(dlosses, dlosses_stride, x, x_stride, weight, weight_stride,
+                                     bias, targets, lse, rows, classes, width, smoothing, dtype, dx,
+                                     dx_stride, dweight, dweight_stride, dbias, workspace,
+                                     workspace_bytes, stream=None) -> int:
+    return _check(_lib.fn_linear_cross_entropy_backward(
+        _addr(dlosses), dlosses_stride, _addr(x), x_stride, _addr(weight), weight_stride,
+        _addr(bias), _addr(targets), _addr(lse), rows, classes, width, smoothing, dtype, _addr(dx),
+        dx_stride, _addr(dweight), dweight_stride, _addr(dbias), _addr(workspace), workspace_bytes,
+        _stream(stream)))
+
+
+def fn_linear_cross_entropy_workspace(rows, classes, width, dtype, in_place_x, in_place_weight,
+                                      backward_pass) -> int:
+    """The workspace's size in bytes."""
+    n = _i64()
+    _check(_lib.fn_linear_cross_entropy_workspace(rows, classes, width, dtype, in_place_x,
+                                                  in_place_weight, backward_pass, ctypes.byref(n)))
     return n.value
 
 
@@ -702,3 +738,108 @@ def layer_norm_backward(dout, h, weight, mean, rstd, dsum=None, p=0.0, seed=0, f
     _increment_version([t for t in (dh, dx, dweight, dbias, workspace if given else None)
                         if t is not None])
     return dh, dh if dx is None else dx, dweight, dbias
+
+
+# --------------------- tensor helpers: the linear head's softmax cross entropy
+
+_head_workspace_bytes = functools.lru_cache(maxsize=256)(fn_linear_cross_entropy_workspace)
+
+
+def _head(x, weight, targets, bias):
+    """What both passes check and pass of their inputs."""
+    shape, rows, width, dev = _rows_of(x)
+    dtype = x.dtype
+    code = _type_code(dtype)
+    if weight.dim() != 2 or weight.shape[0] < 1:
+        raise ValueError("weight must be a (classes, width) tensor")
+    classes = weight.shape[0]
+    _want(weight, (classes, width), dtype, dev, "weight")
+    _want(targets, shape[:-1], torch.int64, dev, "targets", True)
+    if bias is not None:
+        _want(bias, (classes,), torch.float32, dev, "bias", True)
+    return (shape, rows, classes, width, dev, code, _stride_of(x, width, "x"),
+            _stride_of(weight, width, "weight"))
+
+
+def _in_place(t, stride, width) -> bool:
+    """Whether the library reads these rows where they are."""
+    e = t.element_size()
+    return ((t.data_ptr() | stride * e | width * e) % 16 == 0 and stride >= width
+            and stride * e < 2**23)
+
+
+def linear_cross_entropy_workspace(x, weight, backward=False) -> torch.Tensor:
+    """A workspace for linear_cross_entropy on operands of these sizes and
+    places, or for its backward pass."""
+    _, rows, width, dev = _rows_of(x)
+    return torch.empty(_head_workspace_bytes(
+        rows, weight.shape[0], width, _type_code(x.dtype), _in_place(x, _stride_of(x, width, "x"), width),
+        _in_place(weight, _stride_of(weight, width, "weight"), width), backward), dtype=torch.uint8,
+        device=x.device)
+
+
+def linear_cross_entropy(x, weight, targets, bias=None, smoothing=0.0, losses=None, lse=None,
+                         workspace=None, stream=None):
+    """fn_linear_cross_entropy: the softmax cross entropy of the logits
+    x weight^T + bias, which are not kept.  x is (..., D), weight (classes, D)
+    of the same dtype, bias fp32, targets int64 of x's leading shape (outside
+    0..classes-1: ignored).  Returns (losses, lse), fp32 of that shape.  Without
+    a workspace one is allocated for the call."""
+    _refuse_gradients(x, weight, bias, losses, lse)
+    shape, rows, classes, width, dev, code, x_stride, w_stride = _head(x, weight, targets, bias)
+    losses = _want(losses, shape[:-1], torch.float32, dev, "losses", True, stream)
+    lse = _want(lse, shape[:-1], torch.float32, dev, "lse", True, stream)
+    given = workspace is not None
+    workspace, at, size = _workspace(workspace, _head_workspace_bytes(
+        rows, classes, width, code, _in_place(x, x_stride, width), _in_place(weight, w_stride, width),
+        False), dev, stream)
+    _check(_lib.fn_linear_cross_entropy(
+        x.data_ptr(), x_stride, weight.data_ptr(), w_stride,
+        None if bias is None else bias.data_ptr(), targets.data_ptr(), rows, classes, width,
+        smoothing, code, losses.data_ptr(), lse.data_ptr(), at, size, _stream(stream)))
+    _increment_version((losses, lse, workspace) if given else (losses, lse))
+    return losses, lse
+
+
+def linear_cross_entropy_backward(dlosses, x, weight, targets, lse, bias=None, smoothing=0.0,
+                                  dx=None, dweight=None, dbias=None, want_dx=True,
+                                  want_dweight=True, workspace=None, stream=None):
+    """fn_linear_cross_entropy_backward: (dx, dweight, dbias) for the gradients
+    dlosses of linear_cross_entropy's losses (fp32 of their shape, one number
+    expanded included) and the lse that it returned.  dx and dweight are of the
+    operands' dtype (None if not wanted), dbias is fp32 (None without a bias).
+    Without a workspace one is allocated for the call."""
+    _refuse_gradients(dlosses, x, weight, lse, bias, dx, dweight, dbias)
+    shape, rows, classes, width, dev, code, x_stride, w_stride = _head(x, weight, targets, bias)
+    dtype, lead = x.dtype, shape[:-1]
+    _want(dlosses, lead, torch.float32, dev, "dlosses")
+    _want(lse, lead, torch.float32, dev, "lse", True)
+    dloss_stride = 1 if dlosses.is_contiguous() else _row_stride(dlosses.unsqueeze(-1), "dlosses")
+    dx_at = dw_at = None
+    dx_stride = dw_stride = 0
+    if want_dx:
+        dx = _want(dx, shape, dtype, dev, "dx", False, stream)
+        dx_at, dx_stride = dx.data_ptr(), _stride_of(dx, width, "dx")
+    elif dx is not None:
+        raise ValueError("dx is given and not wanted")
+    if want_dweight:
+        dweight = _want(dweight, (classes, width), dtype, dev, "dweight", False, stream)
+        dw_at, dw_stride = dweight.data_ptr(), _stride_of(dweight, width, "dweight")
+    elif dweight is not None:
+        raise ValueError("dweight is given and not wanted")
+    if bias is not None:
+        dbias = _want(dbias, (classes,), torch.float32, dev, "dbias", True, stream)
+    elif dbias is not None:
+        raise ValueError("dbias without a bias")
+    given = workspace is not None
+    workspace, at, size = _workspace(workspace, _head_workspace_bytes(
+        rows, classes, width, code, _in_place(x, x_stride, width), _in_place(weight, w_stride, width),
+        True), dev, stream)
+    _check(_lib.fn_linear_cross_entropy_backward(
+        dlosses.data_ptr(), dloss_stride, x.data_ptr(), x_stride, weight.data_ptr(), w_stride,
+        None if bias is None else bias.data_ptr(), targets.data_ptr(), lse.data_ptr(), rows, classes,
+        width, smoothing, code, dx_at, dx_stride, dw_at, dw_stride,
+        None if dbias is None else dbias.data_ptr(), at, size, _stream(stream)))
+    _increment_version([t for t in (dx, dweight, dbias, workspace if given else None)
+                        if t is not None])
+    return dx, dweight, dbias

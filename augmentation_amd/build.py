@@ -21,11 +21,15 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
-SOURCES = [os.path.join(HERE, "csrc", f) for f in ("fn_api.hip", "q8_api.hip", "layer_api.hip")]
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("fn_api.hip", "q8_api.hip", "layer_api.hip",
+                                                   "loss_api.hip", "loss_fp32.hip",
+                                                   "loss_fp16.hip", "loss_bf16.hip")]
 HEADERS = [os.path.join(HERE, "csrc", h) for h in ("fn_host.hpp", "fn_device.hpp",
                                                    "fn_kernels.hpp", "fn_rows_host.hpp",
                                                    "row_kernels.hpp", "product_kernels.hpp",
-                                                   "layer_kernels.hpp", "exp2_table.inc")] + [
+                                                   "layer_kernels.hpp", "loss_kernels.hpp",
+                                                   "loss_small_kernels.hpp", "loss_launch.hpp",
+                                                   "exp2_table.inc")] + [
     os.path.join(ROOT, "include", "fn.h")]
 LIB_PATH = os.path.join(HERE, "libfn.so")
 # the instrumented build: the tiles kernel records per-tile clock stamps

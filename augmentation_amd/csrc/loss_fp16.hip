@@ -1,0 +1,11 @@
+// loss_fp16.hip -- the linear cross entropy's large kernels for fp16 operands.
+#include "loss_launch.hpp"
+
+namespace fn {
+
+template <>
+void launch_head<_Float16>(int output, bool across_a, HeadLaunch l, hipStream_t st) {
+  launch_head_any<_Float16>(output, across_a, l, st);
+}
+
+}  // namespace fn

@@ -1,0 +1,11 @@
+// loss_fp32.hip -- the linear cross entropy's large kernels for fp32 operands.
+#include "loss_launch.hpp"
+
+namespace fn {
+
+template <>
+void launch_head<float>(int output, bool across_a, HeadLaunch l, hipStream_t st) {
+  launch_head_any<float>(output, across_a, l, st);
+}
+
+}  // namespace fn

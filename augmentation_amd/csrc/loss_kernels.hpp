@@ -1,0 +1,587 @@
+// loss_kernels.hpp -- softmax cross entropy of a linear head, whose logits are
+// never kept, and its gradients.
+//
+//   z[t, v] = sum_k x[t, k] w[v, k] + bias[v]                     (fp32)
+//   lse[t]  = log sum_v exp z[t, v]
+//   loss[t] = lse[t] - (1 - s) z[t, y_t] - s mean_v z[t, v]
+//   g[t, v] = dloss[t] (exp(z[t, v] - lse[t]) - (1 - s) [v = y_t] - s / V)
+//   dx = g w,  dw = g^T x,  dbias[v] = sum_t g[t, v]
+//
+// Forward: a product whose epilogue reduces every tile of logits to a maximum
+// and a sum of exponentials per row, and a second kernel that joins a row's
+// tiles.  Backward: the logits again, in pieces of the classes, turned into g
+// where they are (rounded once to the operands' type, as the matrix
+// instructions take them), then the two products with it.  What is computed a
+// second time is a third of the backward pass; what is not kept is T x V
+// logits.
+//
+// One kernel serves the three products.  They differ in how their operands lie:
+// "along" the contraction (x and w in the logits, g in dx: a row of memory is
+// a row of the operand) or "across" it (w in dx, g and x in dw: a row of memory
+// is one element of the contraction for all rows of the operand).
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "product_kernels.hpp"
+#include "row_kernels.hpp"
+
+namespace fn {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// exp(v) for v <= 0: exp2 of v log2(e), whose rounding error is made good to
+// first order (for v near -20 it alone would be 10^-6 of the result).
+__device__ __forceinline__ float exp_below(float v) {
+  constexpr float kLog2e = 0x1.715476p+0f, kRest = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
+  const float t = v * kLog2e;
+  const float r = __builtin_fmaf(v, kRest, __builtin_fmaf(v, kLog2e, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  // -infinity gives 0, where r is NaN
+  return v < -200.0f ? 0.0f : __builtin_fmaf(e, r * kLn2, e);
+}
+
+// A fragment is 16 bytes of a lane: eight 16-bit numbers or four fp32 ones of
+// one row, of the contraction's 32 or 16 that a step takes.
+template <typename T>
+__device__ __forceinline__ f32x4 multiply_add(i32x4 a, i32x4 b, f32x4 c) {
+  if constexpr (std::is_same_v<T, BF16>) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  } else if constexpr (std::is_same_v<T, _Float16>) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  } else {
+    const f32x4 u = __builtin_bit_cast(f32x4, a), v = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(u[j], v[j], c, 0, 0, 0);
+    return c;
+  }
+}
+
+// An operand of a product: `rows` rows of memory of `length` bytes each, `stride`
+// bytes apart, all multiples of 16.  Along the contraction a row of memory is a
+// row of the operand, across it an element of the contraction.
+struct Operand {
+  const char* p;
+  int64_t stride, rows;
+  int64_t length;
+};
+
+enum HeadOutput {
+  kHeadStatistics = 0,  // of the logits: maximum, sum of exponentials, target
+  kHeadGradient = 1,    // the logits' gradient, rounded
+  kHeadRounded = 2,     // the product in the operands' type
+  kHeadSums = 3,        // the product in fp32, stored or added
+};
+
+struct HeadArgs {
+  Operand a, b;
+  int64_t M, N;     // rows of a and b as operands: rows and columns of the output
+  int64_t K;        // elements of the contraction, of which a work-group takes
+  int64_t K_split;  // so many (a multiple of a stage's), the blockIdx.y-th
+  uint32_t tiles_m, tiles_n;
+  // kHeadStatistics and kHeadGradient
+  const float* bias;  // of the N classes, or null
+  const int64_t* targets;
+  int64_t first_class, classes;  // of these N; of the whole head
+  float smoothing;
+  // kHeadStatistics: [M][stat_tiles] maxima and sums, from tile first_tile on
+  f32x2* stats;
+  float* sums;     // [M][stat_tiles] sums of logits, or null
+  float* target_z; // [M]
+  int64_t stat_tiles, first_tile;
+  // kHeadGradient
+  const float* lse;
+  const float* dlosses;
+  int64_t dloss_stride;
+  float* bias_sums;  // [rows of wavefronts][out_stride] sums of g, or null
+  // kHeadGradient multiplies by scale[0], kHeadRounded by scale[1]; null: 1
+  const float* scale;
+  void* out;
+  int64_t out_stride;   // in elements
+  int64_t split_stride; // kHeadSums: elements between the splits' outputs
+  bool add;             // kHeadSums: to what is there
+};
+
+// Bytes of a stage for each row of an operand: eight pieces of 16.  Along the
+// contraction it is a line of memory; across it, a stage is as many elements of
+// the contraction, each a row of all the tile's rows.
+constexpr int kStageRow = 128;
+
+// Brings one operand's share of a stage to LDS, kRows of its rows, and reads
+// fragments from there.
+//
+// Along: LDS holds kRows rows of eight pieces, permuted as staged_piece says.
+// Across: kStageRow / sizeof(T) rows, of the contraction, each of kRows
+// elements; piece c of row r lies at c ^ swizzle(r).  Sixteen-bit fragments are
+// read transposed (two reads of four elements of the contraction each: lanes
+// 4 j .. 4 j + 3 of sixteen point to sixteen elements of row j, and lane i
+// receives element i of the four rows); fp32 ones are four single reads.
+template <typename T, bool kAcross, int kRows, int kWaves, int kTiles>
+struct Stager {
+  static constexpr int kE = (int)sizeof(T);
+  static constexpr int kLoads = kRows / 8 / kWaves;  // of 1,024 bytes, per wavefront and stage
+  static constexpr int kStageK = kStageRow / kE;     // elements of the contraction
+  static constexpr int kRowBytes = kAcross ? kRows * kE : kStageRow;
+  static_assert(kLoads % 2 == 0, "rows per wavefront: a multiple of 16");
+
+  int off[kLoads];
+  int piece_byte[2];  // along: where in a row this lane's pieces are
+  int at[kAcross ? kTiles : 1], at_step[2];
+  const char* p;
+  int64_t stride, rows, length;
+  i32x4 resource;
+
+  static __device__ __forceinline__ int swizzle(int r) {
+    if constexpr (kE == 4) return 4 * ((r >> 2) & 3);
+    // the eight rows that 32 lanes read together, over all banks
+    if constexpr (kRowBytes >= 256) return 2 * ((r & 3) | ((r >> 3) & 1) << 2);
+    return 2 * (((r >> 1) & 1) | ((r >> 3) & 1) << 1);
+  }
+
+  static __device__ __forceinline__ i32x4 make_resource(const char* at, int64_t bytes) {
+    const uint64_t a = (uint64_t)(uintptr_t)at;
+    const int64_t n = bytes < 0 ? 0 : bytes < 0x7FFFFFF0 ? bytes : 0x7FFFFFF0;
+    return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+                 __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)),
+                 __builtin_amdgcn_readfirstlane((int)n), 0x00027000};
+  }
+
+  // row0: the tile's first row as an operand; tile0: the wavefront's
+  __device__ __forceinline__ void start(const Operand& o, int64_t row0, int wave, int tile0) {
+    const int lane = (int)(threadIdx.x & 63u);
+    stride = o.stride;
+    rows = o.rows;
+    if constexpr (kAcross) {
+      p = o.p + row0 * kE;
+      length = o.length - row0 * kE;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int byte = (wave * kLoads + i) * 1024 + 16 * lane;
+        const int r = byte / kRowBytes, c = ((byte % kRowBytes) >> 4) ^ swizzle(r);
+        off[i] = 16 * c < length ? r * (int)stride + 16 * c : kOutside;
+      }
+      const int i = lane & 15, g = lane >> 4;
+      if constexpr (kE == 4) {
+        const int r = 4 * g;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+          at[t] = r * kRowBytes + 16 * ((4 * (tile0 + t) + (i >> 2)) ^ swizzle(r)) + 4 * (i & 3);
+      } else {
+        const int r = 8 * g + (i >> 2);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+          at[t] = r * kRowBytes + 16 * ((2 * (tile0 + t) + ((i & 3) >> 1)) ^ swizzle(r)) +
+                  8 * (i & 1);
+      }
+    } else {
+      p = o.p + row0 * stride;
+      length = o.length;
+      const int64_t here = min(rows - row0, (int64_t)kRows);
+      resource = make_resource(p, here > 0 ? (here - 1) * stride + length : 0);
+      const int sub = lane / 8;
+      piece_byte[0] = 16 * staged_piece(sub, lane % 8);
+      piece_byte[1] = 16 * staged_piece(8 + sub, lane % 8);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = (wave * kLoads + i) * 8 + sub;
+        off[i] = r < here ? r * (int)stride + piece_byte[i & 1] : kOutside;
+      }
+      at[0] = (tile0 * 16 + (lane & 15)) * kStageRow;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) at_step[k] = 16 * staged_piece(lane & 15, 4 * k + (lane >> 4));
+    }
+  }
+
+  // What the loads of the stage from element k0 of the contraction on need,
+  // which ends before k_end: elements from there on are zeros.
+  struct Stage {
+    i32x4 resource;
+    int k_byte;
+    bool inside[2];
+  };
+
+  __device__ __forceinline__ Stage stage(int64_t k0, int64_t k_end) const {
+    Stage s;
+    if constexpr (kAcross) {
+      // rows beyond the last one lie beyond the resource
+      const int64_t left = min(k_end - k0, (int64_t)kStageK);
+      s.resource = make_resource(p + k0 * stride, left > 0 ? (left - 1) * stride + length : 0);
+      s.k_byte = 0;
+      s.inside[0] = s.inside[1] = true;
+    } else {
+      s.resource = resource;
+      s.k_byte = (int)(k0 * kE);
+      const int64_t left = (k_end - k0) * kE;
+      s.inside[0] = piece_byte[0] < left;
+      s.inside[1] = piece_byte[1] < left;
+    }
+    return s;
+  }
+
+  __device__ __forceinline__ void load(const Stage& s, uint32_t lds, int wave, int i) const {
+    load_to_lds(s.resource, lds + (wave * kLoads + i) * 1024, s.inside[i & 1] ? off[i] : kOutside,
+                s.k_byte);
+  }
+
+  // Tile t's fragment of step k (of two).
+  __device__ __forceinline__ i32x4 fragment(const int8_t* buf, int k, int t) const {
+    if constexpr (!kAcross) {
+      return *reinterpret_cast<const i32x4*>(buf + at[0] + t * 16 * kStageRow + at_step[k]);
+    } else if constexpr (kE == 4) {
+      i32x4 v;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] = *reinterpret_cast<const int*>(buf + at[t] + (16 * k + j) * kRowBytes);
+      return v;
+    } else {
+      typedef __attribute__((address_space(3))) i16x4 Lds;
+      const auto* q = (const __attribute__((address_space(3))) int8_t*)buf + at[t] + 32 * k * kRowBytes;
+      const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds*)q));
+      const u32x2 hi = __builtin_bit_cast(
+          u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds*)(q + 4 * kRowBytes)));
+      return i32x4{(int)lo[0], (int)lo[1], (int)hi[0], (int)hi[1]};
+    }
+  }
+};
+
+// Values of a wavefront's tiles, in the accumulators' layout, to rows of out:
+// through the wavefront's piece of LDS, 64 rows at a time, and out as 16-byte
+// stores along rows, as OutputTile does.  value(i, j, c): of row 16 i + lane %
+// 16, column 16 j + 4 (lane / 16) + c.
+template <typename T, int kTM, int kTN>
+struct ValueTile {
+  static constexpr int kTokens = kTM < 4 ? 16 * kTM : 64;
+  static constexpr int kPitch = 16 * kTN * (int)sizeof(T) + 16;
+  static constexpr int kBytes = kTokens * kPitch;
+
+  template <typename F>
+  static __device__ __forceinline__ void store(F&& value, int8_t* lds, T* out, int64_t out_stride,
+                                               int64_t m0, int64_t n0, int64_t M, int64_t N) {
+    constexpr int kE = 16 / (int)sizeof(T);  // outputs per 16-byte store
+    constexpr int kLanes = 16 * kTN / kE;    // lanes along a row
+    constexpr int kRowsAtOnce = 64 / kLanes;
+    constexpr int kTiles = kTokens / 16;
+    const int lane = (int)(threadIdx.x & 63u);
+    const int64_t n = n0 + kE * (lane % kLanes);
+    const int left = (int)min(max(N - n, (int64_t)0), (int64_t)kE);
+#pragma unroll
+    for (int i0 = 0; i0 < kTM; i0 += kTiles) {
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int j = 0; j < kTN; ++j) {
+          float v[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) v[c] = value(i0 + i, j, c);
+          int8_t* at = lds + (16 * i + (lane & 15)) * kPitch +
+                       (16 * j + 4 * (lane >> 4)) * (int)sizeof(T);
+          if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<f32x4*>(at) = f32x4{v[0], v[1], v[2], v[3]};
+          else
+            *reinterpret_cast<u32x2*>(at) =
+                u32x2{two_halves<T>(v[0], v[1]), two_halves<T>(v[2], v[3])};
+        }
+      // one wavefront's LDS operations take effect in their order
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+#pragma unroll
+      for (int i = 0; i < kTokens / kRowsAtOnce; ++i) {
+        const int r = i * kRowsAtOnce + lane / kLanes;
+        const int64_t m = m0 + 16 * i0 + r;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(lds + r * kPitch + 16 * (lane % kLanes));
+        T* to = out + m * out_stride + n;
+        if (m < M && left == kE)
+          *reinterpret_cast<u32x4_any*>(to) = v;
+        else if (m < M && left > 0)
+          OutputTile<T, kTM, kTN>::store_part(v, to, left);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    }
+  }
+};
+
+// Sum or maximum over the four lanes that hold columns of the same row.
+template <typename F>
+__device__ __forceinline__ float fold_row(float v, F fold) {
+  auto bits = [](float x) { return __builtin_bit_cast(uint32_t, x); };
+  auto number = [](uint32_t x) { return __builtin_bit_cast(float, x); };
+  const auto r = __builtin_amdgcn_permlane16_swap(bits(v), bits(v), false, false);
+  v = fold(number(r[0]), number(r[1]));
+  const auto q = __builtin_amdgcn_permlane32_swap(bits(v), bits(v), false, false);
+  return fold(number(q[0]), number(q[1]));
+}
+
+__device__ __forceinline__ TileAt head_tile_at(uint32_t block, const HeadArgs& p) {
+  ProductArgs q{};
+  q.tiles_m = p.tiles_m;
+  q.tiles_n = p.tiles_n;
+  return tile_at(block, q);
+}
+
+constexpr float kMinusInfinity = -__builtin_inff();
+
+// A tile of kBM x kBN outputs per work-group of kWM x kWN wavefronts, kStages
+// stages of 128 bytes of the contraction on their way, as in
+// product_tile_kernel: between the products of a step stand, one at a time, the
+// reads of the next step's fragments and the loads of a later stage.
+template <typename T, int kOutput, bool kAcrossA, bool kAcrossB, int kBM, int kBN, int kWM, int kWN,
+          int kStages>
+__global__ __launch_bounds__(64 * kWM * kWN, 2) void head_kernel(HeadArgs p) {
+  constexpr int kWaves = kWM * kWN, kTM = kBM / kWM / 16, kTN = kBN / kWN / 16;
+  constexpr int kStageBytes = (kBM + kBN) * kStageRow;
+  using StagerA = Stager<T, kAcrossA, kBM, kWaves, kTM>;
+  using StagerB = Stager<T, kAcrossB, kBN, kWaves, kTN>;
+  using Tile = ValueTile<T, kTM, kTN>;
+  constexpr int kLoadsA = StagerA::kLoads, kLoads = kLoadsA + StagerB::kLoads;
+  constexpr int kStageK = StagerA::kStageK, kSteps = 2;
+  constexpr int kOutBytes = kWaves * Tile::kBytes;
+  constexpr int kLds = kStages * kStageBytes > kOutBytes ? kStages * kStageBytes : kOutBytes;
+  __shared__ __align__(1024) int8_t s_stages[kLds];
+  const int lane = (int)(threadIdx.x & 63u);
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+
+  const TileAt tile = head_tile_at(blockIdx.x, p);
+  const int64_t m0 = (int64_t)tile.m * kBM, n0 = (int64_t)tile.n * kBN;
+  const int64_t k_begin = (int64_t)blockIdx.y * p.K_split;
+  const int64_t k_end = min(k_begin + p.K_split, p.K);
+  StagerA sa;
+  StagerB sb;
+  sa.start(p.a, m0, wave, (wave / kWN) * kTM);
+  sb.start(p.b, n0, wave, (wave % kWN) * kTN);
+  const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)s_stages;
+  struct Next {
+    typename StagerA::Stage a;
+    typename StagerB::Stage b;
+  };
+  auto next_of = [&](int64_t k0) { return Next{sa.stage(k0, k_end), sb.stage(k0, k_end)}; };
+  auto issue = [&](int stage, int i, const Next& next) {
+    const uint32_t to = lds + stage * kStageBytes;
+    if (i < kLoadsA)
+      sa.load(next.a, to, wave, i);
+    else
+      sb.load(next.b, to + kBM * kStageRow, wave, i - kLoadsA);
+  };
+  i32x4 fa[2][kTM], fb[2][kTN];
+  auto fetch = [&](const int8_t* buf, int k, int slot, int i) {
+    if (i < kTN)
+      fb[slot][i] = sb.fragment(buf + kBM * kStageRow, k, i);
+    else
+      fa[slot][i - kTN] = sa.fragment(buf, k, i - kTN);
+  };
+  f32x4 acc[kTM][kTN] = {};
+
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) {
+    const Next next = next_of(k_begin + s * kStageK);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) issue(s, i, next);
+  }
+  wait_loads<(kStages - 1) * kLoads>();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < kTM + kTN; ++i) fetch(s_stages, 0, 0, i);
+  int stage = 0;
+  for (int64_t k0 = k_begin; k0 < k_end; k0 += kStageK) {
+    const int after = stage + 1 == kStages ? 0 : stage + 1;
+    static_for<kSteps>([&](auto step) {
+      constexpr int k = decltype(step)::value;
+      constexpr bool kLast = k + 1 == kSteps;
+      constexpr int kProducts = kTM * kTN, kReads = kTM + kTN, kNewLoads = kLast ? kLoads : 0;
+      constexpr int kOthers = kReads + kNewLoads;
+      const int8_t* from = s_stages + (kLast ? after : stage) * kStageBytes;
+      Next next;
+      if constexpr (kLast) {
+        // this wavefront's loads of the next stage have landed and its reads
+        // of this one are done; beyond the barrier, everyone's are: the next
+        // stage may be read, and this one's place be filled again
+        wait_loads<(kStages - 2) * kLoads>();
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        next = next_of(k0 + kStages * kStageK);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      static_for<kProducts>([&](auto product) {
+        constexpr int t = decltype(product)::value;
+        // the other operations, spread evenly over all products but two, the
+        // loads evenly among the reads
+        constexpr int kSpan = kProducts > 4 ? kProducts - 2 : kProducts;
+        constexpr int kFrom = (t * kOthers + kSpan - 1) / kSpan;
+        constexpr int kTo = ((t + 1) * kOthers + kSpan - 1) / kSpan;
+        constexpr int kEnd = kTo < kOthers ? kTo : kOthers;
+        static_for<(kFrom < kEnd ? kEnd - kFrom : 0)>([&](auto other) {
+          constexpr int o = kFrom + decltype(other)::value;
+          constexpr int kBefore = o * kNewLoads / kOthers;
+          if constexpr ((o + 1) * kNewLoads / kOthers > kBefore)
+            issue(stage, kBefore, next);
+          else
+            fetch(from, kLast ? 0 : k + 1, (k + 1) & 1, o - kBefore);
+        });
+        __builtin_amdgcn_sched_barrier(0);
+        acc[t / kTN][t % kTN] =
+            multiply_add<T>(fb[k & 1][t % kTN], fa[k & 1][t / kTN], acc[t / kTN][t % kTN]);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    });
+    stage = after;
+  }
+  // loads of stages beyond the end (they bring zeros) end before LDS is used
+  // again
+  wait_loads<0>();
+  __syncthreads();
+
+  const int m_wave = (wave / kWN) * kTM * 16, n_wave = (wave % kWN) * kTN * 16;
+  const int64_t m_lane = m0 + m_wave + (lane & 15), n_lane = n0 + n_wave + 4 * (lane >> 4);
+  int8_t* const own = s_stages + wave * Tile::kBytes;
+  // this lane's columns that exist: 16 j + c < columns
+  const int columns = (int)min(max(p.N - n_lane, (int64_t)0), (int64_t)kBN);
+  // the number of a row's target among them, -1 if it is elsewhere
+  auto target_of = [&](int64_t y) {
+    const int64_t t = y - p.first_class - n_lane;
+    return t >= 0 && t < columns ? (int)t : -1;
+  };
+
+  if constexpr (kOutput == kHeadSums) {
+    float* out = (float*)p.out + (int64_t)blockIdx.y * p.split_stride;
+#pragma unroll
+    for (int i = 0; i < kTM; ++i)
+#pragma unroll
+      for (int j = 0; j < kTN; ++j) {
+        const int64_t m = m_lane + 16 * i, n = n_lane + 16 * j;
+        // rows have room for whole vectors of four
+        if (m < p.M && n < p.N) {
+          f32x4* to = reinterpret_cast<f32x4*>(out + m * p.out_stride + n);
+          *to = p.add ? *to + acc[i][j] : acc[i][j];
+        }
+      }
+  } else if constexpr (kOutput == kHeadRounded) {
+    const float scale = p.scale != nullptr ? p.scale[1] : 1.0f;
+    Tile::store([&](int i, int j, int c) { return acc[i][j][c] * scale; }, own, (T*)p.out,
+                p.out_stride, m0 + m_wave, n0 + n_wave, p.M, p.N);
+  } else {
+    // the logits
+#pragma unroll
+    for (int j = 0; j < kTN; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float bias =
+            p.bias != nullptr && 16 * j + c < columns ? p.bias[n_lane + 16 * j + c] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < kTM; ++i) acc[i][j][c] += bias;
+      }
+    if constexpr (kOutput == kHeadStatistics) {
+      // of the work-group's rows in each column of wavefronts
+      float* s_top = reinterpret_cast<float*>(s_stages);
+      float* s_sum = s_top + kWN * kBM;
+      float* s_all = s_sum + kWN * kBM;
+#pragma unroll
+      for (int i = 0; i < kTM; ++i) {
+        const int64_t m = m_lane + 16 * i;
+        float top = kMinusInfinity, all = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kTN; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (16 * j + c < columns) {
+              top = fmaxf(top, acc[i][j][c]);
+              all += acc[i][j][c];
+            }
+        top = fold_row(top, [](float x, float y) { return fmaxf(x, y); });
+        // a row of which nothing is left has no exponentials
+        const float base = top == kMinusInfinity ? 0.0f : top;
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kTN; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            sum += 16 * j + c < columns ? exp_below(acc[i][j][c] - base) : 0.0f;
+        sum = fold_row(sum, [](float x, float y) { return x + y; });
+        if (p.sums != nullptr) all = fold_row(all, [](float x, float y) { return x + y; });
+        if ((lane >> 4) == 0) {
+          const int at = (wave % kWN) * kBM + m_wave + 16 * i + (lane & 15);
+          s_top[at] = top;
+          s_sum[at] = sum;
+          s_all[at] = all;
+        }
+        if (m < p.M) {
+          const int target = target_of(p.targets[m]);
+#pragma unroll
+          for (int j = 0; j < kTN; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (target == 16 * j + c) p.target_z[m] = acc[i][j][c];
+        }
+      }
+      __syncthreads();
+      for (int r = (int)threadIdx.x; r < kBM; r += 64 * kWaves) {
+        const int64_t m = m0 + r;
+        if (m >= p.M) break;
+        float top = s_top[r];
+#pragma unroll
+        for (int w = 1; w < kWN; ++w) top = fmaxf(top, s_top[w * kBM + r]);
+        float sum = 0.0f, all = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWN; ++w) {
+          const float t = s_top[w * kBM + r];
+          sum += t == kMinusInfinity ? s_sum[w * kBM + r] : s_sum[w * kBM + r] * exp_below(t - top);
+          all += s_all[w * kBM + r];
+        }
+        const int64_t at = m * p.stat_tiles + p.first_tile + tile.n;
+        p.stats[at] = f32x2{top, sum};
+        if (p.sums != nullptr) p.sums[at] = all;
+      }
+    } else {
+      const float scale = p.scale != nullptr ? p.scale[0] : 1.0f;
+      const float even = p.smoothing / (float)p.classes;
+#pragma unroll
+      for (int i = 0; i < kTM; ++i) {
+        const int64_t m = m_lane + 16 * i;
+        int64_t y = -1;
+        float lse = 0.0f, dloss = 0.0f;
+        if (m < p.M) {
+          y = p.targets[m];
+          lse = p.lse[m];
+          dloss = p.dlosses[m * p.dloss_stride] * scale;
+        }
+        const bool counts = y >= 0 && y < p.classes;
+        const int target = target_of(y);
+#pragma unroll
+        for (int j = 0; j < kTN; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float g = exp_below(acc[i][j][c] - lse) - even;
+            if (target == 16 * j + c) g -= 1.0f - p.smoothing;
+            acc[i][j][c] = counts && 16 * j + c < columns ? g * dloss : 0.0f;
+          }
+      }
+      if (p.bias_sums != nullptr) {
+        // a wavefront's rows, then the sixteen lanes that hold a column
+        const float unscale = p.scale != nullptr ? p.scale[1] : 1.0f;
+        float* to = p.bias_sums + ((int64_t)tile.m * kWM + wave / kWN) * p.out_stride;
+#pragma unroll
+        for (int j = 0; j < kTN; ++j) {
+          f32x4 sum = acc[0][j];
+#pragma unroll
+          for (int i = 1; i < kTM; ++i) sum += acc[i][j];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sum[c] = group_sum<16>(sum[c]) * unscale;
+          if ((lane & 15) == 0 && n_lane + 16 * j < p.out_stride)
+            *reinterpret_cast<f32x4*>(to + n_lane + 16 * j) = sum;
+        }
+      }
+      // to the end of the row of memory: what lies beyond the classes is zero,
+      // and takes part in the next product
+      Tile::store([&](int i, int j, int c) { return acc[i][j][c]; }, own, (T*)p.out, p.out_stride,
+                  m0 + m_wave, n0 + n_wave, p.M, p.out_stride);
+    }
+  }
+}
+
+}  // namespace fn

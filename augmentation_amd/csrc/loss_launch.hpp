@@ -1,0 +1,62 @@
+// loss_launch.hpp -- the launches of the linear cross entropy's large kernels.
+// They are instantiated in a source file for each type, which compile side by
+// side.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include "loss_kernels.hpp"
+
+namespace fn {
+
+// Tiles of 256x256, 128x128 and 64x64 outputs.
+constexpr int kHeadTileSizes[3] = {256, 128, 64};
+// rows of wavefronts in a tile, each with a row of bias_sums
+constexpr int kHeadTileRows = 2;
+
+struct HeadLaunch {
+  HeadArgs args;
+  int tile;    // which of the sizes
+  int splits;  // of the contraction
+};
+
+template <typename T, int kOutput, bool kAcrossA, bool kAcrossB>
+void launch_head_tiles(HeadLaunch& l, hipStream_t st) {
+  HeadArgs& p = l.args;
+  const int64_t size = kHeadTileSizes[l.tile];
+  p.tiles_m = (uint32_t)((p.M + size - 1) / size);
+  p.tiles_n = (uint32_t)((p.N + size - 1) / size);
+  const dim3 grid(p.tiles_m * p.tiles_n, (unsigned)l.splits);
+  switch (l.tile) {
+    case 0:
+      head_kernel<T, kOutput, kAcrossA, kAcrossB, 256, 256, 2, 4, 2><<<grid, 512, 0, st>>>(p);
+      break;
+    case 1:
+      head_kernel<T, kOutput, kAcrossA, kAcrossB, 128, 128, 2, 2, 2><<<grid, 256, 0, st>>>(p);
+      break;
+    default:
+      head_kernel<T, kOutput, kAcrossA, kAcrossB, 64, 64, 2, 2, 4><<<grid, 256, 0, st>>>(p);
+  }
+}
+
+// `across_a`: how a lies in the products with g (dw: across, dx: along); b lies
+// across in both, and both along in the logits.
+template <typename T>
+void launch_head(int output, bool across_a, HeadLaunch l, hipStream_t st);
+
+template <typename T>
+void launch_head_any(int output, bool across_a, HeadLaunch& l, hipStream_t st) {
+  if (output == kHeadStatistics)
+    launch_head_tiles<T, kHeadStatistics, false, false>(l, st);
+  else if (output == kHeadGradient)
+    launch_head_tiles<T, kHeadGradient, false, false>(l, st);
+  else if (output == kHeadRounded && !across_a)
+    launch_head_tiles<T, kHeadRounded, false, true>(l, st);
+  else if (output == kHeadRounded)
+    launch_head_tiles<T, kHeadRounded, true, true>(l, st);
+  else if (!across_a)
+    launch_head_tiles<T, kHeadSums, false, true>(l, st);
+  else
+    launch_head_tiles<T, kHeadSums, true, true>(l, st);
+}
+
+}  // namespace fn

@@ -1,0 +1,130 @@
+// loss_small_kernels.hpp -- what the linear cross entropy does around its
+// products: joining a row's statistics, the scale of fp16 gradients, the
+// rounding of sums and the copies of operands that lie off 16 bytes.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include "loss_kernels.hpp"
+
+namespace fn {
+
+struct JoinArgs {
+  const f32x2* stats;
+  const float* sums;  // or null
+  const float* target_z;
+  const int64_t* targets;
+  float* losses;
+  float* lse;
+  int64_t rows, classes;
+  int64_t tiles;
+  float smoothing;
+};
+
+// A row's tiles joined: a wavefront per row.
+__global__ __launch_bounds__(256) void loss_join_kernel(JoinArgs p) {
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = (int)(threadIdx.x & 63u);
+  if (row >= p.rows) return;
+  const f32x2* from = p.stats + row * p.tiles;
+  float top = kMinusInfinity, all = 0.0f;
+  for (int64_t i = lane; i < p.tiles; i += 64) top = fmaxf(top, from[i][0]);
+  auto bits = [](float x) { return __builtin_bit_cast(uint32_t, x); };
+  top = __builtin_bit_cast(
+      float, group_fold<64>(bits(top), [&](uint32_t x, uint32_t y) {
+        return bits(fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y)));
+      }));
+  float sum = 0.0f;
+  for (int64_t i = lane; i < p.tiles; i += 64) {
+    const f32x2 v = from[i];
+    sum += v[0] == kMinusInfinity ? v[1] : v[1] * exp_below(v[0] - top);
+    if (p.sums != nullptr) all += p.sums[row * p.tiles + i];
+  }
+  sum = group_sum<64>(sum);
+  all = group_sum<64>(all);
+  if (lane != 0) return;
+  const float lse = top + logf(sum);
+  p.lse[row] = lse;
+  const int64_t y = p.targets[row];
+  float loss = 0.0f;
+  if (y >= 0 && y < p.classes) {
+    loss = lse - (1.0f - p.smoothing) * p.target_z[row];
+    if (p.sums != nullptr) loss -= p.smoothing * (all / (float)p.classes);
+  }
+  p.losses[row] = loss;
+}
+
+// The power of two that brings the largest |dloss| to 2^14 at most, and its
+// inverse: fp16 holds gradients of classes of small probability only then.
+__global__ __launch_bounds__(1024) void loss_scale_kernel(const float* dlosses, int64_t stride,
+                                                          int64_t rows, float* scale) {
+  __shared__ float s_top[16];
+  float top = 0.0f;
+  for (int64_t i = threadIdx.x; i < rows; i += 1024) top = fmaxf(top, fabsf(dlosses[i * stride]));
+  const uint32_t all = group_max<64>(__builtin_bit_cast(uint32_t, top));
+  if ((threadIdx.x & 63u) == 0) s_top[threadIdx.x >> 6] = __builtin_bit_cast(float, all);
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int w = 0; w < 16; ++w) top = fmaxf(top, s_top[w]);
+  // |dloss| < 2^exponent; both powers within fp32's normal numbers
+  const int exponent = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 126;
+  const int up = min(max(14 - exponent, -120), 120);
+  scale[0] = __builtin_bit_cast(float, (uint32_t)(127 + up) << 23);
+  scale[1] = __builtin_bit_cast(float, (uint32_t)(127 - up) << 23);
+}
+
+// out = RN_T(scale[1] * the sum of `splits` products in fp32): a thread takes
+// four elements of a row.
+template <typename T>
+__global__ __launch_bounds__(256) void loss_round_kernel(const float* sums, int64_t pitch,
+                                                         int64_t split_stride, int splits,
+                                                         int64_t rows, int64_t width,
+                                                         const float* scale, T* out,
+                                                         int64_t out_stride) {
+  const int64_t n = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (n >= width) return;
+  const float by = scale != nullptr ? scale[1] : 1.0f;
+  for (int64_t m = blockIdx.y; m < rows; m += gridDim.y) {
+    const float* from = sums + m * pitch + n;
+    f32x4 v = *reinterpret_cast<const f32x4*>(from);
+    for (int s = 1; s < splits; ++s)
+      v += *reinterpret_cast<const f32x4*>(from + s * split_stride);
+    T* to = out + m * out_stride + n;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (n + c < width) {
+        if constexpr (sizeof(T) == 4)
+          to[c] = v[c] * by;
+        else
+          reinterpret_cast<uint16_t*>(to)[c] = (uint16_t)two_halves<T>(v[c] * by, 0.0f);
+      }
+  }
+}
+
+// Rows of any alignment to rows of whole 16-byte pieces, zeros at their ends: a
+// thread takes a piece.
+template <typename T>
+__global__ __launch_bounds__(256) void loss_pack_kernel(const T* from, int64_t stride, int64_t rows,
+                                                        int32_t width, T* to, int32_t pitch) {
+  constexpr int kE = 16 / (int)sizeof(T);
+  const int32_t c = (int32_t)(blockIdx.x * 256 + threadIdx.x) * kE;
+  if (c >= pitch) return;
+  for (int64_t m = blockIdx.y; m < rows; m += gridDim.y) {
+    const T* row = from + m * stride;
+    u32x4 v = {0, 0, 0, 0};
+    if (c + kE <= width) {
+      v = *reinterpret_cast<const u32x4_any*>(row + c);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kE; ++j)
+        if (c + j < width) {
+          if constexpr (sizeof(T) == 4)
+            v[j] = __builtin_bit_cast(uint32_t, row[c + j]);
+          else
+            v[j >> 1] |= (uint32_t)__builtin_bit_cast(uint16_t, row[c + j]) << (16 * (j & 1));
+        }
+    }
+    *reinterpret_cast<u32x4*>(to + m * pitch + c) = v;
+  }
+}
+
+}  // namespace fn

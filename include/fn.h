@@ -391,6 +391,75 @@ int fn_layer_norm_backward(const void* dout_dev, int64_t dout_stride, const void
 /* Writes to *bytes (host) the workspace that fn_layer_norm_backward needs. */
 int fn_layer_norm_backward_workspace(int64_t rows, int32_t width, int64_t* bytes);
 
+/* ------------------------------------------------------------------------ */
+/* The softmax cross entropy of a linear head over many classes, whose logits */
+/* are never kept, and its gradients.                                         */
+/*                                                                            */
+/* x is rows x width (features), weight classes x width, both of dtype with   */
+/* any row stride; bias `classes` fp32 numbers or NULL.  With                 */
+/*   z[t, v] = sum_k x[t, k] weight[v, k] + bias[v]                           */
+/* in fp32:                                                                   */
+/*   lse[t]  = log(sum_v exp(z[t, v])),                                       */
+/*   loss[t] = lse[t] - (1 - smoothing) z[t, y_t] - smoothing mean_v z[t, v]. */
+/* targets are 64-bit; a row whose target y_t lies outside 0..classes-1 (-100, */
+/* say) is ignored: its loss and its gradients are zero.  smoothing lies in    */
+/* [0, 1].  A class of bias -infinity is left out: probability 0, and a loss   */
+/* of +infinity for rows that want it.  A row with a NaN or +infinity among    */
+/* its logits, or all classes left out, has a NaN loss.                        */
+/*                                                                            */
+/* Speed only: operands are read in place if in_place(x), which is that the    */
+/* base, the stride and the width are multiples of 16 bytes and the stride is  */
+/* at least the width and below 2^23 bytes; others are copied to the          */
+/* workspace first.                                                           */
+/*                                                                            */
+/* Errors: FN_EINVAL as for the other matrices, for classes or width < 1,      */
+/* smoothing outside [0, 1] or a workspace that is too short; FN_EOVERFLOW     */
+/* for rows or classes > 2^28, width > 2^20, or a product of two of the three  */
+/* > 2^36.                                                                     */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * fn_linear_cross_entropy -- the losses and lse (which the backward pass takes),
+ * `rows` fp32 numbers each.  Sums are fp32, in an order that the sizes alone
+ * fix.  workspace_dev: at least fn_linear_cross_entropy_workspace(...) bytes,
+ * 16-byte aligned, that no other call in flight uses.
+ */
+int fn_linear_cross_entropy(const void* x_dev, int64_t x_stride, const void* weight_dev,
+                            int64_t weight_stride, const float* bias_dev,
+                            const int64_t* targets_dev, int64_t rows, int64_t classes,
+                            int32_t width, float smoothing, int32_t dtype, float* losses_dev,
+                            float* lse_dev, void* workspace_dev, int64_t workspace_bytes,
+                            void* stream);
+
+/*
+ * fn_linear_cross_entropy_backward -- the gradients.  dlosses are the gradients
+ * of the losses, a stride apart (0: one number for all rows).  With
+ *   g[t, v] = dloss[t] (exp(z[t, v] - lse[t]) - (1 - smoothing) [v = y_t]
+ *                       - smoothing / classes)     (0 in an ignored row):
+ *   dx = g weight, dweight = g^T x, rounded to dtype; dbias[v] = sum_t g[t, v]
+ * in fp32.  All are overwritten; each may be NULL.  The logits are computed
+ * again, a piece of the classes at a time, and g is rounded to dtype before its
+ * products, as the matrix instructions take it (dbias comes before that); the
+ * sums are fp32, in an order that the sizes alone fix (no atomics).  In fp16 g
+ * is scaled by a power of two that brings the largest |dloss| to 2^14, and its
+ * products back: probabilities down to 2^-28 keep all their digits in rows of
+ * that dloss.  rows = 0 writes zeros.
+ */
+int fn_linear_cross_entropy_backward(
+    const float* dlosses_dev, int64_t dlosses_stride, const void* x_dev, int64_t x_stride,
+    const void* weight_dev, int64_t weight_stride, const float* bias_dev,
+    const int64_t* targets_dev, const float* lse_dev, int64_t rows, int64_t classes, int32_t width,
+    float smoothing, int32_t dtype, void* dx_dev, int64_t dx_stride, void* dweight_dev,
+    int64_t dweight_stride, float* dbias_dev, void* workspace_dev, int64_t workspace_bytes,
+    void* stream);
+
+/* Writes to *bytes (host) the workspace that fn_linear_cross_entropy
+ * (backward_pass 0) or its gradients (1) need.  in_place_x, in_place_weight:
+ * nonzero if the operand can be read in place, as above; 0 is always enough. */
+int fn_linear_cross_entropy_workspace(int64_t rows, int64_t classes, int32_t width, int32_t dtype,
+                                      int32_t in_place_x, int32_t in_place_weight,
+                                      int32_t backward_pass, int64_t* bytes);
+
 /* The message of the last nonzero return on the calling thread ("" if none).
  * The pointer stays valid until the next call on the same thread. */
 const char* fn_last_error(void);

@@ -280,9 +280,10 @@ int backward(const Call& c, const Plan& p, const Gradients& g) {
   const fn::Operand x = operand<T>(c.x, c.x_stride, c.rows, c.width, p.width_packed,
                                    p.pack_x ? ws + p.x : nullptr, c.st);
   const float* scale = nullptr;
-  if constexpr (std::is_same_v<T, _Float16>) {
-    fn::loss_scale_kernel<<<1, 1024, 0, c.st>>>(g.dlosses, g.dloss_stride, c.rows,
-                                                (float*)(ws + p.scale));
+  if constexpr (sizeof(T) == 2) {
+    fn::loss_scale_kernel<<<1, 1024, 0, c.st>>>(
+        g.dlosses, g.dloss_stride, c.rows, std::is_same_v<T, _Float16> ? 16384.0f : 1.0f,
+        (float*)(ws + p.scale));
     FN_TRY(launch_status("loss_scale_kernel launch"));
     scale = (const float*)(ws + p.scale);
   }

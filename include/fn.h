@@ -440,10 +440,10 @@ int fn_linear_cross_entropy(const void* x_dev, int64_t x_stride, const void* wei
  * in fp32.  All are overwritten; each may be NULL.  The logits are computed
  * again, a piece of the classes at a time, and g is rounded to dtype before its
  * products, as the matrix instructions take it (dbias comes before that); the
- * sums are fp32, in an order that the sizes alone fix (no atomics).  In fp16 g
- * is scaled by a power of two that brings the largest |dloss| to 2^14, and its
- * products back: probabilities down to 2^-28 keep all their digits in rows of
- * that dloss.  rows = 0 writes zeros.
+ * sums are fp32, in an order that the sizes alone fix (no atomics).  In 16-bit
+ * types g is scaled so that the largest finite |dloss| is 1 (bf16) or 2^14
+ * (fp16, where probabilities down to 2^-28 then keep all their digits in rows of
+ * that dloss), and its products back.  rows = 0 writes zeros.
  */
 int fn_linear_cross_entropy_backward(
     const float* dlosses_dev, int64_t dlosses_stride, const void* x_dev, int64_t x_stride,

@@ -814,7 +814,11 @@ def linear_cross_entropy_backward(dlosses, x, weight, targets, lse, bias=None, s
     dtype, lead = x.dtype, shape[:-1]
     _want(dlosses, lead, torch.float32, dev, "dlosses")
     _want(lse, lead, torch.float32, dev, "lse", True)
-    dloss_stride = 1 if dlosses.is_contiguous() else _row_stride(dlosses.unsqueeze(-1), "dlosses")
+    dloss_stride = 1
+    if not dlosses.is_contiguous():
+        if any(dlosses.stride()):
+            raise ValueError("dlosses must be contiguous or one number expanded")
+        dloss_stride = 0
     dx_at = dw_at = None
     dx_stride = dw_stride = 0
     if want_dx:

@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "fn.h"
 #include "fn_host.hpp"
@@ -24,6 +25,7 @@ constexpr int64_t kUnits = 256;
 // for every product to fill the device, few enough to stay in the memory-side
 // cache until both products have read it.
 constexpr int64_t kPieceBytes = (int64_t)1 << 27;
+constexpr int64_t kFewRows = 8192;
 constexpr int32_t kMaxFeatures = 1 << 20;
 constexpr int64_t kMaxClasses = (int64_t)1 << 28;
 // a stage's rows times the stride within the 31-bit offsets of a resource
@@ -32,38 +34,48 @@ constexpr int64_t kMaxStrideBytes = ((int64_t)1 << 31) / 256 - 1;
 struct Choice {
   int tile = 0, splits = 1;
   int64_t K_split = 0;
+  double cost = 0.0;  // us
 };
 
-// The tile and the splits of the contraction for M x N outputs and K elements
-// of it, by the time they would take (us; of a tile of 256, 128 or 64 rows, for
-// 4,096 bytes of the contraction).
-Choice choose(int64_t M, int64_t N, int64_t K, int64_t e, bool splittable) {
-  const double each[3] = {e == 2 ? 57.0 : 220.0, e == 2 ? 17.3 : 56.0, e == 2 ? 6.3 : 14.5};
-  const int64_t stage = fn::kStageRow / e;
-  Choice best;
-  double least = 1e300;
-  for (int tile = 0; tile < 3; ++tile) {
-    const int64_t size = fn::kHeadTileSizes[tile];
-    const int64_t tiles = ((M + size - 1) / size) * ((N + size - 1) / size);
-    if (tiles >= (int64_t)1 << 22) continue;  // 2^32 threads to a launch
-    for (int splits = 1; splits <= 64; splits *= 2) {
-      if (splits > 1 && (!splittable || K < 8 * stage * splits || tiles * splits > 4 * kUnits)) break;
-      const int64_t K_split = ((K + splits - 1) / splits + stage - 1) / stage * stage;
-      const double rounds = std::ceil((double)tiles * splits / kUnits);
-      double cost = rounds * (each[tile] * K_split * e / 4096.0 + 1.5);
-      // partial products are written and read again, in a launch of their own
-      if (splits > 1) cost += 3.0 + (double)M * N * 8.0 * splits / 4e6;
-      if (cost < least) {
-        least = cost;
-        best = {tile, splits, K_split};
-      }
-    }
-  }
-  best.K_split = std::max<int64_t>(best.K_split, stage);
-  return best;
+// The time of a tile of 256, 128 and 64 rows and columns for 4,096 bytes of the
+// contraction, us.
+double tile_time(int tile, int64_t e) {
+  constexpr double kTimes[2][3] = {{57.0, 17.3, 6.3}, {220.0, 56.0, 14.5}};
+  return kTimes[e == 4][tile];
+}
+
+int64_t tiles_of(int tile, int64_t M, int64_t N) {
+  const int64_t size = fn::kHeadTileSizes[tile];
+  return ((M + size - 1) / size) * ((N + size - 1) / size);
+}
+
+// `tiles` on the device, each with `bytes` of the contraction.
+double rounds_time(int tile, int64_t e, int64_t tiles, int64_t bytes) {
+  return std::ceil((double)tiles / kUnits) * (tile_time(tile, e) * bytes / 4096.0 + 1.5);
 }
 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// The tile and the splits of the contraction for M x N outputs and K elements
+// of it, by the time they would take.
+Choice choose(int64_t M, int64_t N, int64_t K, int64_t e, bool splittable) {
+  const int64_t stage = fn::kStageRow / e;
+  Choice best;
+  best.cost = 1e300;
+  for (int tile = 0; tile < 3; ++tile) {
+    const int64_t tiles = tiles_of(tile, M, N);
+    if (tiles >= (int64_t)1 << 22) continue;  // 2^32 threads to a launch
+    for (int splits = 1; splits <= 64; splits *= 2) {
+      if (splits > 1 && (!splittable || K < 8 * stage * splits || tiles * splits > 4 * kUnits)) break;
+      const int64_t K_split = std::max(round_up((K + splits - 1) / splits, stage), stage);
+      double cost = 3.0 + rounds_time(tile, e, tiles * splits, K_split * e);
+      // partial products are written and read again, in a launch of their own
+      if (splits > 1) cost += 3.0 + (double)M * N * 8.0 * splits / 4e6;
+      if (cost < best.cost) best = {tile, splits, K_split, cost};
+    }
+  }
+  return best;
+}
 
 // Parts of a workspace, one behind the other.
 struct Parts {
@@ -75,67 +87,108 @@ struct Parts {
   }
 };
 
+// A call goes through its classes in pieces of the same size, but for the last.
 struct Plan {
   bool pack_x, pack_w;
   int64_t width_packed;  // elements
   int64_t piece;         // classes
   int64_t pieces;
-  Choice logits, dx, dw;
-  bool sum_dx, sum_dw;  // in fp32 first
-  int64_t pitch;        // of g's rows, elements
-  int64_t sum_pitch;    // of fp32 products' rows
-  int64_t stat_tiles, bias_rows;
+  Choice logits[2], dx[2], dw[2];  // [1]: of a shorter last piece
+  int pair_tile;                   // of dx and dw in one launch, or -1
+  bool sum_dx;                     // in fp32 first
+  int64_t pitch;                   // of g's rows, elements
+  int64_t sum_pitch;               // of fp32 products' rows
+  int64_t stat_tiles;
   // places in the workspace
   int64_t scale, x, w, stats, sums, target_z, g, dx_sums, dw_sums, bias_sums;
   int64_t bytes;
+
+  int64_t last(int64_t classes) const { return classes - (pieces - 1) * piece; }
+  int which(int64_t count) const { return count == piece ? 0 : 1; }
 };
 
-// `bytes` of a plan without some optional output is at most that of one with
-// it.
+int64_t head_tiles(const Choice& c, int64_t n) {
+  const int64_t size = fn::kHeadTileSizes[c.tile];
+  return (n + size - 1) / size;
+}
+
+// Classes of a piece, at most `most` of them: as many as give every compute unit
+// the same number of 256x256 tiles (4096x50000x4096 bf16, gradients, with pieces of
+// 12544 / 16384: 4.50 / 3.80 ms).
+int64_t piece_of(int64_t rows, int64_t most) {
+  const int64_t m = (rows + 255) / 256, rounds = m * (most / 256) / kUnits;
+  return rounds > 0 ? std::max<int64_t>(rounds * kUnits / m, 1) * 256 : most;
+}
+
 Plan plan_of(int64_t rows, int64_t classes, int32_t width, int64_t e, bool pack_x, bool pack_w,
              bool backward) {
   Plan p{};
   p.pack_x = pack_x;
   p.pack_w = pack_w;
   p.width_packed = round_up(width, 16 / e);
-  const int64_t per_class = std::max<int64_t>(rows, 1) * e;
-  // what a piece of the classes has in the workspace: their gradients, or a
-  // copy of their weights
-  const int64_t piece_bytes =
-      backward ? std::max(classes * per_class, pack_w ? classes * p.width_packed * e : 0)
-               : (pack_w ? classes * p.width_packed * e : 0);
-  p.pieces = std::max<int64_t>((piece_bytes + kPieceBytes - 1) / kPieceBytes, 1);
-  p.piece = round_up((classes + p.pieces - 1) / p.pieces, 256);
-  p.piece = std::min({classes, p.piece, kMaxStrideBytes / e / 256 * 256});
-  p.pieces = (classes + p.piece - 1) / p.piece;
   const int64_t K = pack_x || pack_w ? p.width_packed : width;
-  p.logits = choose(rows, p.piece, K, e, false);
+  // what a class of a piece has in the workspace: its gradients, a copy of its
+  // weights
+  const int64_t per_class =
+      std::max(backward ? std::max<int64_t>(rows, 1) * e : 0, pack_w ? p.width_packed * e : 0);
+  int64_t most = round_up(classes, 256);
+  if (per_class > 0) most = std::min(most, std::max<int64_t>(kPieceBytes / per_class / 256, 1) * 256);
+  if (backward) most = std::min(most, kMaxStrideBytes / e / 256 * 256);
+  p.piece = classes;
+  if (most < classes) {
+    p.piece = piece_of(rows, most);
+  } else if (!backward) {
+    // whole rounds of tiles first and the rest in smaller ones, if that is less
+    const int64_t piece = piece_of(rows, classes / 256 * 256);
+    if (piece > 0 && piece < classes &&
+        choose(rows, piece, K, e, false).cost + choose(rows, classes - piece, K, e, false).cost <
+            choose(rows, classes, K, e, false).cost)
+      p.piece = piece;
+  }
+  p.pieces = (classes + p.piece - 1) / p.piece;
+  const int64_t counts[2] = {p.piece, p.last(classes)};
   Parts parts;
   p.scale = parts.take(8);
   if (pack_x) p.x = parts.take(rows * p.width_packed * e);
   if (pack_w) p.w = parts.take(p.piece * p.width_packed * e);
+  for (int k = 0; k < 2; ++k) p.logits[k] = choose(rows, counts[k], K, e, false);
   if (!backward) {
-    const int64_t size = fn::kHeadTileSizes[p.logits.tile];
-    // pieces are whole tiles, but for the last
-    p.stat_tiles = (p.pieces - 1) * ((p.piece + size - 1) / size) +
-                   (classes - (p.pieces - 1) * p.piece + size - 1) / size;
+    p.stat_tiles = (p.pieces - 1) * head_tiles(p.logits[0], p.piece) +
+                   head_tiles(p.logits[p.which(counts[1])], counts[1]);
     p.stats = parts.take(rows * p.stat_tiles * 8);
     p.sums = parts.take(rows * p.stat_tiles * 4);
     p.target_z = parts.take(rows * 4);
-  } else {
-    const int64_t size = fn::kHeadTileSizes[p.logits.tile];
-    p.pitch = round_up(p.piece, 64);
-    p.sum_pitch = round_up(width, 4);
-    p.dx = choose(rows, width, p.piece, e, true);
-    p.dw = choose(p.piece, width, rows, e, true);
-    p.sum_dx = p.pieces > 1 || p.dx.splits > 1;
-    p.sum_dw = p.dw.splits > 1;
-    p.bias_rows = (rows + size - 1) / size * fn::kHeadTileRows;
-    p.g = parts.take(rows * p.pitch * e);
-    if (p.sum_dx) p.dx_sums = parts.take(p.dx.splits * rows * p.sum_pitch * 4);
-    if (p.sum_dw) p.dw_sums = parts.take(p.dw.splits * p.piece * p.sum_pitch * 4);
-    p.bias_sums = parts.take(p.bias_rows * p.pitch * 4);
+    p.bytes = parts.bytes;
+    return p;
   }
+  p.pitch = round_up(p.piece, 64);
+  p.sum_pitch = round_up(width, 4);
+  p.pair_tile = -1;
+  int64_t bias_rows = 0, dw_rows = 0;
+  for (int k = 0; k < 2; ++k) {
+    // dx's sums of the first piece fill every split's place, a later one may
+    // use fewer
+    p.dx[k] = choose(rows, width, counts[k], e, k == 0);
+    p.dw[k] = choose(counts[k], width, rows, e, true);
+    bias_rows = std::max(bias_rows, head_tiles(p.logits[k], rows) * fn::kHeadTileRows);
+    if (p.dw[k].splits > 1) dw_rows = std::max(dw_rows, p.dw[k].splits * counts[k]);
+  }
+  p.sum_dx = p.pieces > 1 || p.dx[0].splits > 1;
+  if (p.pieces == 1 && rows > 0) {
+    double least = p.dx[0].cost + p.dw[0].cost;
+    for (int tile = 1; tile < 3; ++tile) {
+      const int64_t tiles = tiles_of(tile, rows, width) + tiles_of(tile, classes, width);
+      const double cost = 3.0 + rounds_time(tile, e, tiles, std::max(rows, classes) * e);
+      if (tiles < (int64_t)1 << 22 && cost < least) {
+        least = cost;
+        p.pair_tile = tile;
+      }
+    }
+  }
+  p.g = parts.take(rows * p.pitch * e);
+  if (p.sum_dx) p.dx_sums = parts.take(p.dx[0].splits * rows * p.sum_pitch * 4);
+  if (dw_rows > 0) p.dw_sums = parts.take(dw_rows * p.sum_pitch * 4);
+  p.bias_sums = parts.take(bias_rows * p.pitch * 4);
   p.bytes = parts.bytes;
   return p;
 }
@@ -196,7 +249,7 @@ fn::HeadArgs head_args(const Call& c, const Plan& p, const fn::Operand& x, const
   a.M = c.rows;
   a.N = count;
   a.K = p.pack_x || p.pack_w ? p.width_packed : c.width;
-  a.K_split = p.logits.K_split;
+  a.K_split = p.logits[p.which(count)].K_split;
   a.bias = c.bias != nullptr ? c.bias + first : nullptr;
   a.targets = c.targets;
   a.first_class = first;
@@ -210,7 +263,6 @@ int forward(const Call& c, const Plan& p, float* losses, float* lse) {
   char* const ws = c.workspace;
   const fn::Operand x = operand<T>(c.x, c.x_stride, c.rows, c.width, p.width_packed,
                                    p.pack_x ? ws + p.x : nullptr, c.st);
-  const int64_t size = fn::kHeadTileSizes[p.logits.tile];
   for (int64_t first = 0, tile = 0; first < c.classes; first += p.piece) {
     const int64_t count = std::min(p.piece, c.classes - first);
     const fn::Operand w = operand<T>((const T*)c.w + first * c.w_stride, c.w_stride, count, c.width,
@@ -221,9 +273,10 @@ int forward(const Call& c, const Plan& p, float* losses, float* lse) {
     a.target_z = (float*)(ws + p.target_z);
     a.stat_tiles = p.stat_tiles;
     a.first_tile = tile;
-    fn::launch_head<T>(fn::kHeadStatistics, false, {a, p.logits.tile, 1}, c.st);
+    const Choice& choice = p.logits[p.which(count)];
+    fn::launch_head<T>(fn::kHeadStatistics, false, {a, choice.tile, 1}, c.st);
     FN_TRY(launch_status("head_kernel launch"));
-    tile += (count + size - 1) / size;
+    tile += head_tiles(choice, count);
   }
   fn::JoinArgs j{};
   j.stats = (const fn::f32x2*)(ws + p.stats);
@@ -279,16 +332,26 @@ int backward(const Call& c, const Plan& p, const Gradients& g) {
   char* const ws = c.workspace;
   const fn::Operand x = operand<T>(c.x, c.x_stride, c.rows, c.width, p.width_packed,
                                    p.pack_x ? ws + p.x : nullptr, c.st);
-  const float* scale = nullptr;
+  float* scale = nullptr;
+  float scale_to = 0.0f;
   if constexpr (sizeof(T) == 2) {
-    fn::loss_scale_kernel<<<1, 1024, 0, c.st>>>(
-        g.dlosses, g.dloss_stride, c.rows, std::is_same_v<T, _Float16> ? 16384.0f : 1.0f,
-        (float*)(ws + p.scale));
-    FN_TRY(launch_status("loss_scale_kernel launch"));
-    scale = (const float*)(ws + p.scale);
+    scale = (float*)(ws + p.scale);
+    scale_to = std::is_same_v<T, _Float16> ? 16384.0f : 1.0f;
+    // few rows: each work-group of the first kernel looks for the largest
+    // dloss, for less than a launch takes
+    if (c.rows > kFewRows || c.rows == 0) {
+      fn::loss_scale_kernel<<<1, 1024, 0, c.st>>>(g.dlosses, g.dloss_stride, c.rows, scale_to,
+                                                  scale);
+      FN_TRY(launch_status("loss_scale_kernel launch"));
+      scale_to = 0.0f;
+    }
   }
+  const bool pair = p.pair_tile > 0 && g.dx != nullptr && g.dw != nullptr;
   for (int64_t first = 0; first < c.classes; first += p.piece) {
     const int64_t count = std::min(p.piece, c.classes - first);
+    const int k = p.which(count);
+    const int32_t bias_rows = (int32_t)(head_tiles(p.logits[k], c.rows) * fn::kHeadTileRows);
+    float* const bias_sums = (float*)(ws + p.bias_sums);
     const fn::Operand w = operand<T>((const T*)c.w + first * c.w_stride, c.w_stride, count, c.width,
                                      p.width_packed, p.pack_w ? ws + p.w : nullptr, c.st);
     if (c.rows > 0) {
@@ -296,61 +359,78 @@ int backward(const Call& c, const Plan& p, const Gradients& g) {
       a.lse = g.lse;
       a.dlosses = g.dlosses;
       a.dloss_stride = g.dloss_stride;
-      a.bias_sums = g.dbias != nullptr ? (float*)(ws + p.bias_sums) : nullptr;
+      a.bias_sums = g.dbias != nullptr ? bias_sums : nullptr;
       a.scale = scale;
+      a.scale_to = scale_to;
       a.out = ws + p.g;
       a.out_stride = p.pitch;
-      fn::launch_head<T>(fn::kHeadGradient, false, {a, p.logits.tile, 1}, c.st);
+      fn::launch_head<T>(fn::kHeadGradient, false, {a, p.logits[k].tile, 1}, c.st);
       FN_TRY(launch_status("head_kernel launch"));
+    }
+    const fn::Operand gradient = {ws + p.g, p.pitch * e, c.rows, p.pitch * e};
+    fn::HeadArgs dx{}, dw{};
+    dx.a = dw.a = gradient;
+    dx.b = w;
+    dw.b = x;
+    dx.M = dw.K = c.rows;
+    dx.K = dw.M = count;
+    dx.N = dw.N = c.width;
+    dx.scale = dw.scale = scale;
+    dx.out = g.dx;
+    dx.out_stride = g.dx_stride;
+    T* const dw_out = (T*)g.dw + first * g.dw_stride;
+    dw.out = dw_out;
+    dw.out_stride = g.dw_stride;
+    if (pair) {
+      fn::HeadPairArgs both{};
+      dx.K_split = round_up(count, fn::kStageRow / e);
+      dw.K_split = round_up(c.rows, fn::kStageRow / e);
+      both.dx = dx;
+      both.dw = dw;
+      both.bias_sums = bias_sums;
+      both.pitch = p.pitch;
+      both.bias_rows = bias_rows;
+      both.dbias = g.dbias;
+      fn::launch_head_pair<T>(both, p.pair_tile, c.st);
+      return launch_status("head_pair_kernel launch");
     }
     if (g.dbias != nullptr) {
       fn::column_sum_kernel<<<blocks_for(count, 64), 1024, 0, c.st>>>(
-          (const float*)(ws + p.bias_sums), c.rows > 0 ? (int32_t)p.bias_rows : 0,
-          (int32_t)p.pitch, (int32_t)count, g.dbias + first);
+          bias_sums, c.rows > 0 ? bias_rows : 0, (int32_t)p.pitch, (int32_t)count,
+          g.dbias + first);
       FN_TRY(launch_status("column_sum_kernel launch"));
     }
-    const fn::Operand gradient = {ws + p.g, p.pitch * e, c.rows, p.pitch * e};
     if (g.dx != nullptr && c.rows > 0) {
-      fn::HeadArgs a{};
-      a.a = gradient;
-      a.b = w;
-      a.M = c.rows;
-      a.N = c.width;
-      a.K = count;
-      a.K_split = p.dx.K_split;
-      a.scale = scale;
-      a.out = p.sum_dx ? (void*)(ws + p.dx_sums) : g.dx;
-      a.out_stride = p.sum_dx ? p.sum_pitch : g.dx_stride;
-      a.split_stride = c.rows * p.sum_pitch;
-      a.add = first > 0;
+      dx.K_split = p.dx[k].K_split;
+      if (p.sum_dx) {
+        dx.out = ws + p.dx_sums;
+        dx.out_stride = p.sum_pitch;
+        dx.split_stride = c.rows * p.sum_pitch;
+        dx.add = first > 0;
+      }
       fn::launch_head<T>(p.sum_dx ? fn::kHeadSums : fn::kHeadRounded, false,
-                         {a, p.dx.tile, p.dx.splits}, c.st);
+                         {dx, p.dx[k].tile, p.dx[k].splits}, c.st);
       FN_TRY(launch_status("head_kernel launch"));
     }
     if (g.dw != nullptr) {
-      fn::HeadArgs a{};
-      a.a = gradient;
-      a.b = x;
-      a.M = count;
-      a.N = c.width;
-      a.K = c.rows;
-      a.K_split = p.dw.K_split;
-      a.scale = scale;
-      T* const out = (T*)g.dw + first * g.dw_stride;
-      a.out = p.sum_dw ? (void*)(ws + p.dw_sums) : out;
-      a.out_stride = p.sum_dw ? p.sum_pitch : g.dw_stride;
-      a.split_stride = p.piece * p.sum_pitch;
-      fn::launch_head<T>(p.sum_dw ? fn::kHeadSums : fn::kHeadRounded, true,
-                         {a, p.dw.tile, p.dw.splits}, c.st);
+      const int splits = p.dw[k].splits;
+      dw.K_split = p.dw[k].K_split;
+      if (splits > 1) {
+        dw.out = ws + p.dw_sums;
+        dw.out_stride = p.sum_pitch;
+        dw.split_stride = count * p.sum_pitch;
+      }
+      fn::launch_head<T>(splits > 1 ? fn::kHeadSums : fn::kHeadRounded, true,
+                         {dw, p.dw[k].tile, splits}, c.st);
       FN_TRY(launch_status("head_kernel launch"));
-      if (p.sum_dw)
-        FN_TRY(round_sums<T>((const float*)(ws + p.dw_sums), p, a.split_stride, p.dw.splits, count,
-                             c.width, scale, out, g.dw_stride, c.st));
+      if (splits > 1)
+        FN_TRY(round_sums<T>((const float*)(ws + p.dw_sums), p, dw.split_stride, splits, count,
+                             c.width, scale, dw_out, g.dw_stride, c.st));
     }
   }
   if (g.dx != nullptr && p.sum_dx)
-    FN_TRY(round_sums<T>((const float*)(ws + p.dx_sums), p, c.rows * p.sum_pitch, p.dx.splits,
-                         c.rows, c.width, scale, (T*)g.dx, g.dx_stride, c.st));
+    FN_TRY(round_sums<T>((const float*)(ws + p.dx_sums), p, c.rows * p.sum_pitch,
+                         p.dx[0].splits, c.rows, c.width, scale, (T*)g.dx, g.dx_stride, c.st));
   return ok();
 }
 
@@ -415,6 +495,8 @@ FN_EXPORT int fn_linear_cross_entropy_backward(
     void* stream) {
   FN_TRY(check_head(rows, classes, width, dtype));
   if (!in_unit(smoothing)) return fail(FN_EINVAL, "smoothing must lie in [0, 1]");
+  if (dlosses_stride != 0 && dlosses_stride != 1)
+    return fail(FN_EINVAL, "dlosses_stride must be 0 or 1");
   const int64_t e = type_bytes(dtype), one = rows ? 1 : 0;
   const Plan plan = plan_of(rows, classes, width, e, !in_place(x_dev, x_stride, width, e),
                             !in_place(weight_dev, weight_stride, width, e), true);

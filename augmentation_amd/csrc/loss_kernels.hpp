@@ -99,10 +99,13 @@ struct HeadArgs {
   // kHeadGradient
   const float* lse;
   const float* dlosses;
-  int64_t dloss_stride;
+  int64_t dloss_stride;  // 0 or 1
   float* bias_sums;  // [rows of wavefronts][out_stride] sums of g, or null
-  // kHeadGradient multiplies by scale[0], kHeadRounded by scale[1]; null: 1
-  const float* scale;
+  // kHeadGradient multiplies by scale[0] and kHeadRounded by scale[1]; null: by
+  // 1.  With scale_to > 0 kHeadGradient finds them itself, as loss_scale_kernel
+  // does, and leaves them there.
+  float* scale;
+  float scale_to;
   void* out;
   int64_t out_stride;   // in elements
   int64_t split_stride; // kHeadSums: elements between the splits' outputs
@@ -326,260 +329,375 @@ __device__ __forceinline__ TileAt head_tile_at(uint32_t block, const HeadArgs& p
 
 constexpr float kMinusInfinity = -__builtin_inff();
 
+// What brings the largest finite |dloss| to `to`, and back.  Rounded to 16 bits
+// as they are, the gradients of a mean loss would all be off by the rounding of
+// 1 / rows, the same way (4096 rows of bf16: 3.0e-3 of dx against 1.7e-3, dx's
+// own rounding); and fp16 holds those of classes of small probability only if
+// they are large.
+struct Scale {
+  float up, down;
+};
+
+// By all threads of the work-group; s_top: a word for each wavefront.
+template <int kThreads>
+__device__ __forceinline__ Scale find_scale(const float* dlosses, int64_t stride, int64_t rows,
+                                            float to, uint32_t* s_top) {
+  uint32_t top = 0;
+  for (int64_t i = threadIdx.x; i < rows; i += kThreads) {
+    const uint32_t v = __builtin_bit_cast(uint32_t, dlosses[i * stride]) & 0x7FFFFFFFu;
+    if (v < 0x7F800000u) top = max(top, v);
+  }
+  top = group_max<64>(top);
+  if ((threadIdx.x & 63u) == 0) s_top[threadIdx.x >> 6] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kThreads / 64; ++w) top = max(top, s_top[w]);
+  // numbers so small that the inverse would overflow are scaled by less
+  const float largest = fmaxf(__builtin_bit_cast(float, top), 0x1p-100f);
+  return {to / largest, largest / to};
+}
+
 // A tile of kBM x kBN outputs per work-group of kWM x kWN wavefronts, kStages
 // stages of 128 bytes of the contraction on their way, as in
 // product_tile_kernel: between the products of a step stand, one at a time, the
 // reads of the next step's fragments and the loads of a later stage.
 template <typename T, int kOutput, bool kAcrossA, bool kAcrossB, int kBM, int kBN, int kWM, int kWN,
           int kStages>
-__global__ __launch_bounds__(64 * kWM * kWN, 2) void head_kernel(HeadArgs p) {
-  constexpr int kWaves = kWM * kWN, kTM = kBM / kWM / 16, kTN = kBN / kWN / 16;
-  constexpr int kStageBytes = (kBM + kBN) * kStageRow;
+struct HeadTile {
+  static constexpr int kWaves = kWM * kWN, kTM = kBM / kWM / 16, kTN = kBN / kWN / 16;
+  static constexpr int kStageBytes = (kBM + kBN) * kStageRow;
   using StagerA = Stager<T, kAcrossA, kBM, kWaves, kTM>;
   using StagerB = Stager<T, kAcrossB, kBN, kWaves, kTN>;
   using Tile = ValueTile<T, kTM, kTN>;
-  constexpr int kLoadsA = StagerA::kLoads, kLoads = kLoadsA + StagerB::kLoads;
-  constexpr int kStageK = StagerA::kStageK, kSteps = 2;
-  constexpr int kOutBytes = kWaves * Tile::kBytes;
-  constexpr int kLds = kStages * kStageBytes > kOutBytes ? kStages * kStageBytes : kOutBytes;
-  __shared__ __align__(1024) int8_t s_stages[kLds];
-  const int lane = (int)(threadIdx.x & 63u);
-  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  static constexpr int kLoadsA = StagerA::kLoads, kLoads = kLoadsA + StagerB::kLoads;
+  static constexpr int kStageK = StagerA::kStageK, kSteps = 2;
+  static constexpr int kOutBytes = kWaves * Tile::kBytes;
+  static constexpr int kMainBytes =
+      kStages * kStageBytes > kOutBytes ? kStages * kStageBytes : kOutBytes;
+  // what the logits need beside: bias, lse, dlosses, targets, a word for each
+  // wavefront
+  static constexpr bool kSides = kOutput == kHeadStatistics || kOutput == kHeadGradient;
+  static constexpr int kSideBytes = kSides ? 4 * (kBN + 4 * kBM + 64) : 0;
+  static constexpr int kLds = kMainBytes + kSideBytes;
 
-  const TileAt tile = head_tile_at(blockIdx.x, p);
-  const int64_t m0 = (int64_t)tile.m * kBM, n0 = (int64_t)tile.n * kBN;
-  const int64_t k_begin = (int64_t)blockIdx.y * p.K_split;
-  const int64_t k_end = min(k_begin + p.K_split, p.K);
-  StagerA sa;
-  StagerB sb;
-  sa.start(p.a, m0, wave, (wave / kWN) * kTM);
-  sb.start(p.b, n0, wave, (wave % kWN) * kTN);
-  const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)s_stages;
-  struct Next {
-    typename StagerA::Stage a;
-    typename StagerB::Stage b;
-  };
-  auto next_of = [&](int64_t k0) { return Next{sa.stage(k0, k_end), sb.stage(k0, k_end)}; };
-  auto issue = [&](int stage, int i, const Next& next) {
-    const uint32_t to = lds + stage * kStageBytes;
-    if (i < kLoadsA)
-      sa.load(next.a, to, wave, i);
-    else
-      sb.load(next.b, to + kBM * kStageRow, wave, i - kLoadsA);
-  };
-  i32x4 fa[2][kTM], fb[2][kTN];
-  auto fetch = [&](const int8_t* buf, int k, int slot, int i) {
-    if (i < kTN)
-      fb[slot][i] = sb.fragment(buf + kBM * kStageRow, k, i);
-    else
-      fa[slot][i - kTN] = sa.fragment(buf, k, i - kTN);
-  };
-  f32x4 acc[kTM][kTN] = {};
+  // The block-th tile, the split-th part of the contraction.
+  static __device__ __forceinline__ void run(const HeadArgs& p, uint32_t block, uint32_t split,
+                                             int8_t* s_stages) {
+    const int lane = (int)(threadIdx.x & 63u);
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
 
-#pragma unroll
-  for (int s = 0; s < kStages; ++s) {
-    const Next next = next_of(k_begin + s * kStageK);
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) issue(s, i, next);
-  }
-  wait_loads<(kStages - 1) * kLoads>();
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < kTM + kTN; ++i) fetch(s_stages, 0, 0, i);
-  int stage = 0;
-  for (int64_t k0 = k_begin; k0 < k_end; k0 += kStageK) {
-    const int after = stage + 1 == kStages ? 0 : stage + 1;
-    static_for<kSteps>([&](auto step) {
-      constexpr int k = decltype(step)::value;
-      constexpr bool kLast = k + 1 == kSteps;
-      constexpr int kProducts = kTM * kTN, kReads = kTM + kTN, kNewLoads = kLast ? kLoads : 0;
-      constexpr int kOthers = kReads + kNewLoads;
-      const int8_t* from = s_stages + (kLast ? after : stage) * kStageBytes;
-      Next next;
-      if constexpr (kLast) {
-        // this wavefront's loads of the next stage have landed and its reads
-        // of this one are done; beyond the barrier, everyone's are: the next
-        // stage may be read, and this one's place be filled again
-        wait_loads<(kStages - 2) * kLoads>();
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        next = next_of(k0 + kStages * kStageK);
+    const TileAt tile = head_tile_at(block, p);
+    const int64_t m0 = (int64_t)tile.m * kBM, n0 = (int64_t)tile.n * kBN;
+    const int64_t k_begin = (int64_t)split * p.K_split;
+    const int64_t k_end = min(k_begin + p.K_split, p.K);
+    StagerA sa;
+    StagerB sb;
+    sa.start(p.a, m0, wave, (wave / kWN) * kTM);
+    sb.start(p.b, n0, wave, (wave % kWN) * kTN);
+    const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)s_stages;
+    struct Next {
+      typename StagerA::Stage a;
+      typename StagerB::Stage b;
+    };
+    auto next_of = [&](int64_t k0) { return Next{sa.stage(k0, k_end), sb.stage(k0, k_end)}; };
+    auto issue = [&](int stage, int i, const Next& next) {
+      const uint32_t to = lds + stage * kStageBytes;
+      if (i < kLoadsA)
+        sa.load(next.a, to, wave, i);
+      else
+        sb.load(next.b, to + kBM * kStageRow, wave, i - kLoadsA);
+    };
+    i32x4 fa[2][kTM], fb[2][kTN];
+    auto fetch = [&](const int8_t* buf, int k, int slot, int i) {
+      if (i < kTN)
+        fb[slot][i] = sb.fragment(buf + kBM * kStageRow, k, i);
+      else
+        fa[slot][i - kTN] = sa.fragment(buf, k, i - kTN);
+    };
+    f32x4 acc[kTM][kTN] = {};
+
+    // They go first and have landed with the first stage: fetched after the last
+    // product they would keep the output waiting for memory once more.
+    const float* const s_bias = reinterpret_cast<const float*>(s_stages + kMainBytes);
+    const float *const s_lse = s_bias + kBN, *const s_dloss = s_lse + kBM;
+    const int64_t* const s_target = reinterpret_cast<const int64_t*>(s_dloss + kBM);
+    if constexpr (kSides) {
+      auto words = [&](const void* from, int64_t first, int64_t count, int64_t size, int to) {
+        // `count` words of `size` from the first one on, zeros behind them
+        const int64_t here = from != nullptr ? max(count - first, (int64_t)0) : 0;
+        const i32x4 r = tile_resource((const int8_t*)from + 4 * first, 0, here > 0 ? 1 : 0,
+                                      (int32_t)(4 * min(here, size)));
+        for (int c = wave; c < (int)size / 64; c += kWaves)
+          load_words_to_lds(r, lds + kMainBytes + 4 * to + 256 * c, 256 * c + 4 * lane);
+      };
+      words(p.bias, n0, p.N, kBN, 0);
+      if constexpr (kOutput == kHeadGradient) {
+        words(p.lse, m0, p.M, kBM, kBN);
+        if (p.dloss_stride != 0) words(p.dlosses, m0, p.M, kBM, kBN + kBM);
       }
-      __builtin_amdgcn_sched_barrier(0);
-      static_for<kProducts>([&](auto product) {
-        constexpr int t = decltype(product)::value;
-        // the other operations, spread evenly over all products but two, the
-        // loads evenly among the reads
-        constexpr int kSpan = kProducts > 4 ? kProducts - 2 : kProducts;
-        constexpr int kFrom = (t * kOthers + kSpan - 1) / kSpan;
-        constexpr int kTo = ((t + 1) * kOthers + kSpan - 1) / kSpan;
-        constexpr int kEnd = kTo < kOthers ? kTo : kOthers;
-        static_for<(kFrom < kEnd ? kEnd - kFrom : 0)>([&](auto other) {
-          constexpr int o = kFrom + decltype(other)::value;
-          constexpr int kBefore = o * kNewLoads / kOthers;
-          if constexpr ((o + 1) * kNewLoads / kOthers > kBefore)
-            issue(stage, kBefore, next);
-          else
-            fetch(from, kLast ? 0 : k + 1, (k + 1) & 1, o - kBefore);
+      words(p.targets, 2 * m0, 2 * p.M, 2 * kBM, kBN + 2 * kBM);
+    }
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) {
+      const Next next = next_of(k_begin + s * kStageK);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) issue(s, i, next);
+    }
+    Scale scale = {1.0f, 1.0f};
+    if constexpr (kOutput == kHeadGradient) {
+      if (p.scale_to > 0.0f) {
+        scale = find_scale<64 * kWaves>(
+            p.dlosses, p.dloss_stride, p.M, p.scale_to,
+            reinterpret_cast<uint32_t*>(s_stages + kMainBytes) + kBN + 4 * kBM);
+        if (block == 0 && threadIdx.x == 0) {
+          p.scale[0] = scale.up;
+          p.scale[1] = scale.down;
+        }
+      } else if (p.scale != nullptr) {
+        scale = {p.scale[0], p.scale[1]};
+      }
+    }
+    wait_loads<(kStages - 1) * kLoads>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < kTM + kTN; ++i) fetch(s_stages, 0, 0, i);
+    int stage = 0;
+    for (int64_t k0 = k_begin; k0 < k_end; k0 += kStageK) {
+      const int after = stage + 1 == kStages ? 0 : stage + 1;
+      static_for<kSteps>([&](auto step) {
+        constexpr int k = decltype(step)::value;
+        constexpr bool kLast = k + 1 == kSteps;
+        constexpr int kProducts = kTM * kTN, kReads = kTM + kTN, kNewLoads = kLast ? kLoads : 0;
+        constexpr int kOthers = kReads + kNewLoads;
+        const int8_t* from = s_stages + (kLast ? after : stage) * kStageBytes;
+        Next next;
+        if constexpr (kLast) {
+          // this wavefront's loads of the next stage have landed and its reads
+          // of this one are done; beyond the barrier, everyone's are: the next
+          // stage may be read, and this one's place be filled again
+          wait_loads<(kStages - 2) * kLoads>();
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+          next = next_of(k0 + kStages * kStageK);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        static_for<kProducts>([&](auto product) {
+          constexpr int t = decltype(product)::value;
+          // the other operations, spread evenly over all products but two, the
+          // loads evenly among the reads
+          constexpr int kSpan = kProducts > 4 ? kProducts - 2 : kProducts;
+          constexpr int kFrom = (t * kOthers + kSpan - 1) / kSpan;
+          constexpr int kTo = ((t + 1) * kOthers + kSpan - 1) / kSpan;
+          constexpr int kEnd = kTo < kOthers ? kTo : kOthers;
+          static_for<(kFrom < kEnd ? kEnd - kFrom : 0)>([&](auto other) {
+            constexpr int o = kFrom + decltype(other)::value;
+            constexpr int kBefore = o * kNewLoads / kOthers;
+            if constexpr ((o + 1) * kNewLoads / kOthers > kBefore)
+              issue(stage, kBefore, next);
+            else
+              fetch(from, kLast ? 0 : k + 1, (k + 1) & 1, o - kBefore);
+          });
+          __builtin_amdgcn_sched_barrier(0);
+          acc[t / kTN][t % kTN] =
+              multiply_add<T>(fb[k & 1][t % kTN], fa[k & 1][t / kTN], acc[t / kTN][t % kTN]);
+          __builtin_amdgcn_sched_barrier(0);
         });
-        __builtin_amdgcn_sched_barrier(0);
-        acc[t / kTN][t % kTN] =
-            multiply_add<T>(fb[k & 1][t % kTN], fa[k & 1][t / kTN], acc[t / kTN][t % kTN]);
-        __builtin_amdgcn_sched_barrier(0);
       });
-    });
-    stage = after;
-  }
-  // loads of stages beyond the end (they bring zeros) end before LDS is used
-  // again
-  wait_loads<0>();
-  __syncthreads();
+      stage = after;
+    }
+    // loads of stages beyond the end (they bring zeros) end before LDS is used
+    // again
+    wait_loads<0>();
+    __syncthreads();
 
-  const int m_wave = (wave / kWN) * kTM * 16, n_wave = (wave % kWN) * kTN * 16;
-  const int64_t m_lane = m0 + m_wave + (lane & 15), n_lane = n0 + n_wave + 4 * (lane >> 4);
-  int8_t* const own = s_stages + wave * Tile::kBytes;
-  // this lane's columns that exist: 16 j + c < columns
-  const int columns = (int)min(max(p.N - n_lane, (int64_t)0), (int64_t)kBN);
-  // the number of a row's target among them, -1 if it is elsewhere
-  auto target_of = [&](int64_t y) {
-    const int64_t t = y - p.first_class - n_lane;
-    return t >= 0 && t < columns ? (int)t : -1;
-  };
+    const int m_wave = (wave / kWN) * kTM * 16, n_wave = (wave % kWN) * kTN * 16;
+    const int64_t m_lane = m0 + m_wave + (lane & 15), n_lane = n0 + n_wave + 4 * (lane >> 4);
+    int8_t* const own = s_stages + wave * Tile::kBytes;
+    // this lane's columns that exist: 16 j + c < columns
+    const int columns = (int)min(max(p.N - n_lane, (int64_t)0), (int64_t)kBN);
+    // the number of a row's target among them, -1 if it is elsewhere
+    auto target_of = [&](int64_t y) {
+      const int64_t t = y - p.first_class - n_lane;
+      return t >= 0 && t < columns ? (int)t : -1;
+    };
 
-  if constexpr (kOutput == kHeadSums) {
-    float* out = (float*)p.out + (int64_t)blockIdx.y * p.split_stride;
+    if constexpr (kOutput == kHeadSums) {
+      float* out = (float*)p.out + (int64_t)split * p.split_stride;
 #pragma unroll
-    for (int i = 0; i < kTM; ++i)
+      for (int i = 0; i < kTM; ++i)
 #pragma unroll
-      for (int j = 0; j < kTN; ++j) {
-        const int64_t m = m_lane + 16 * i, n = n_lane + 16 * j;
-        // rows have room for whole vectors of four
-        if (m < p.M && n < p.N) {
-          f32x4* to = reinterpret_cast<f32x4*>(out + m * p.out_stride + n);
-          *to = p.add ? *to + acc[i][j] : acc[i][j];
+        for (int j = 0; j < kTN; ++j) {
+          const int64_t m = m_lane + 16 * i, n = n_lane + 16 * j;
+          // rows have room for whole vectors of four
+          if (m < p.M && n < p.N) {
+            f32x4* to = reinterpret_cast<f32x4*>(out + m * p.out_stride + n);
+            *to = p.add ? *to + acc[i][j] : acc[i][j];
+          }
         }
-      }
-  } else if constexpr (kOutput == kHeadRounded) {
-    const float scale = p.scale != nullptr ? p.scale[1] : 1.0f;
-    Tile::store([&](int i, int j, int c) { return acc[i][j][c] * scale; }, own, (T*)p.out,
-                p.out_stride, m0 + m_wave, n0 + n_wave, p.M, p.N);
-  } else {
-    // the logits
+    } else if constexpr (kOutput == kHeadRounded) {
+      const float scale = p.scale != nullptr ? p.scale[1] : 1.0f;
+      Tile::store([&](int i, int j, int c) { return acc[i][j][c] * scale; }, own, (T*)p.out,
+                  p.out_stride, m0 + m_wave, n0 + n_wave, p.M, p.N);
+    } else {
+      // the logits
 #pragma unroll
-    for (int j = 0; j < kTN; ++j)
+      for (int j = 0; j < kTN; ++j)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float bias =
-            p.bias != nullptr && 16 * j + c < columns ? p.bias[n_lane + 16 * j + c] : 0.0f;
+        for (int c = 0; c < 4; ++c) {
+          const float bias = s_bias[n_wave + 4 * (lane >> 4) + 16 * j + c];
 #pragma unroll
-        for (int i = 0; i < kTM; ++i) acc[i][j][c] += bias;
-      }
-    if constexpr (kOutput == kHeadStatistics) {
-      // of the work-group's rows in each column of wavefronts
-      float* s_top = reinterpret_cast<float*>(s_stages);
-      float* s_sum = s_top + kWN * kBM;
-      float* s_all = s_sum + kWN * kBM;
-#pragma unroll
-      for (int i = 0; i < kTM; ++i) {
-        const int64_t m = m_lane + 16 * i;
-        float top = kMinusInfinity, all = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kTN; ++j)
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (16 * j + c < columns) {
-              top = fmaxf(top, acc[i][j][c]);
-              all += acc[i][j][c];
-            }
-        top = fold_row(top, [](float x, float y) { return fmaxf(x, y); });
-        // a row of which nothing is left has no exponentials
-        const float base = top == kMinusInfinity ? 0.0f : top;
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kTN; ++j)
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            sum += 16 * j + c < columns ? exp_below(acc[i][j][c] - base) : 0.0f;
-        sum = fold_row(sum, [](float x, float y) { return x + y; });
-        if (p.sums != nullptr) all = fold_row(all, [](float x, float y) { return x + y; });
-        if ((lane >> 4) == 0) {
-          const int at = (wave % kWN) * kBM + m_wave + 16 * i + (lane & 15);
-          s_top[at] = top;
-          s_sum[at] = sum;
-          s_all[at] = all;
+          for (int i = 0; i < kTM; ++i) acc[i][j][c] += bias;
         }
-        if (m < p.M) {
-          const int target = target_of(p.targets[m]);
+      if constexpr (kOutput == kHeadStatistics) {
+        // of the work-group's rows in each column of wavefronts
+        float* s_top = reinterpret_cast<float*>(s_stages);
+        float* s_sum = s_top + kWN * kBM;
+        float* s_all = s_sum + kWN * kBM;
+#pragma unroll
+        for (int i = 0; i < kTM; ++i) {
+          const int64_t m = m_lane + 16 * i;
+          float top = kMinusInfinity, all = 0.0f;
 #pragma unroll
           for (int j = 0; j < kTN; ++j)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              if (target == 16 * j + c) p.target_z[m] = acc[i][j][c];
-        }
-      }
-      __syncthreads();
-      for (int r = (int)threadIdx.x; r < kBM; r += 64 * kWaves) {
-        const int64_t m = m0 + r;
-        if (m >= p.M) break;
-        float top = s_top[r];
+              if (16 * j + c < columns) {
+                top = fmaxf(top, acc[i][j][c]);
+                all += acc[i][j][c];
+              }
+          top = fold_row(top, [](float x, float y) { return fmaxf(x, y); });
+          // a row of which nothing is left has no exponentials
+          const float base = top == kMinusInfinity ? 0.0f : top;
+          float sum = 0.0f;
 #pragma unroll
-        for (int w = 1; w < kWN; ++w) top = fmaxf(top, s_top[w * kBM + r]);
-        float sum = 0.0f, all = 0.0f;
+          for (int j = 0; j < kTN; ++j)
 #pragma unroll
-        for (int w = 0; w < kWN; ++w) {
-          const float t = s_top[w * kBM + r];
-          sum += t == kMinusInfinity ? s_sum[w * kBM + r] : s_sum[w * kBM + r] * exp_below(t - top);
-          all += s_all[w * kBM + r];
-        }
-        const int64_t at = m * p.stat_tiles + p.first_tile + tile.n;
-        p.stats[at] = f32x2{top, sum};
-        if (p.sums != nullptr) p.sums[at] = all;
-      }
-    } else {
-      const float scale = p.scale != nullptr ? p.scale[0] : 1.0f;
-      const float even = p.smoothing / (float)p.classes;
-#pragma unroll
-      for (int i = 0; i < kTM; ++i) {
-        const int64_t m = m_lane + 16 * i;
-        int64_t y = -1;
-        float lse = 0.0f, dloss = 0.0f;
-        if (m < p.M) {
-          y = p.targets[m];
-          lse = p.lse[m];
-          dloss = p.dlosses[m * p.dloss_stride] * scale;
-        }
-        const bool counts = y >= 0 && y < p.classes;
-        const int target = target_of(y);
-#pragma unroll
-        for (int j = 0; j < kTN; ++j)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float g = exp_below(acc[i][j][c] - lse) - even;
-            if (target == 16 * j + c) g -= 1.0f - p.smoothing;
-            acc[i][j][c] = counts && 16 * j + c < columns ? g * dloss : 0.0f;
+            for (int c = 0; c < 4; ++c)
+              sum += 16 * j + c < columns ? exp_below(acc[i][j][c] - base) : 0.0f;
+          sum = fold_row(sum, [](float x, float y) { return x + y; });
+          if (p.sums != nullptr) all = fold_row(all, [](float x, float y) { return x + y; });
+          if ((lane >> 4) == 0) {
+            const int at = (wave % kWN) * kBM + m_wave + 16 * i + (lane & 15);
+            s_top[at] = top;
+            s_sum[at] = sum;
+            s_all[at] = all;
           }
-      }
-      if (p.bias_sums != nullptr) {
-        // a wavefront's rows, then the sixteen lanes that hold a column
-        const float unscale = p.scale != nullptr ? p.scale[1] : 1.0f;
-        float* to = p.bias_sums + ((int64_t)tile.m * kWM + wave / kWN) * p.out_stride;
+          if (m < p.M) {
+            const int target = target_of(s_target[m_wave + 16 * i + (lane & 15)]);
 #pragma unroll
-        for (int j = 0; j < kTN; ++j) {
-          f32x4 sum = acc[0][j];
+            for (int j = 0; j < kTN; ++j)
 #pragma unroll
-          for (int i = 1; i < kTM; ++i) sum += acc[i][j];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) sum[c] = group_sum<16>(sum[c]) * unscale;
-          if ((lane & 15) == 0 && n_lane + 16 * j < p.out_stride)
-            *reinterpret_cast<f32x4*>(to + n_lane + 16 * j) = sum;
+              for (int c = 0; c < 4; ++c)
+                if (target == 16 * j + c) p.target_z[m] = acc[i][j][c];
+          }
         }
+        __syncthreads();
+        for (int r = (int)threadIdx.x; r < kBM; r += 64 * kWaves) {
+          const int64_t m = m0 + r;
+          if (m >= p.M) break;
+          float top = s_top[r];
+#pragma unroll
+          for (int w = 1; w < kWN; ++w) top = fmaxf(top, s_top[w * kBM + r]);
+          float sum = 0.0f, all = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kWN; ++w) {
+            const float t = s_top[w * kBM + r];
+            sum += t == kMinusInfinity ? s_sum[w * kBM + r] : s_sum[w * kBM + r] * exp_below(t - top);
+            all += s_all[w * kBM + r];
+          }
+          const int64_t at = m * p.stat_tiles + p.first_tile + tile.n;
+          p.stats[at] = f32x2{top, sum};
+          if (p.sums != nullptr) p.sums[at] = all;
+        }
+      } else {
+        const float even = p.smoothing / (float)p.classes;
+#pragma unroll
+        for (int i = 0; i < kTM; ++i) {
+          const int64_t m = m_lane + 16 * i;
+          const int at = m_wave + 16 * i + (lane & 15);
+          const int64_t y = s_target[at];
+          const float lse = s_lse[at];
+          const float dloss = (p.dloss_stride != 0 ? s_dloss[at] : p.dlosses[0]) * scale.up;
+          const bool counts = m < p.M && y >= 0 && y < p.classes;
+          const int target = target_of(y);
+#pragma unroll
+          for (int j = 0; j < kTN; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float g = exp_below(acc[i][j][c] - lse) - even;
+              if (target == 16 * j + c) g -= 1.0f - p.smoothing;
+              acc[i][j][c] = counts && 16 * j + c < columns ? g * dloss : 0.0f;
+            }
+        }
+        if (p.bias_sums != nullptr) {
+          // a wavefront's rows, then the sixteen lanes that hold a column
+          float* to = p.bias_sums + ((int64_t)tile.m * kWM + wave / kWN) * p.out_stride;
+#pragma unroll
+          for (int j = 0; j < kTN; ++j) {
+            f32x4 sum = acc[0][j];
+#pragma unroll
+            for (int i = 1; i < kTM; ++i) sum += acc[i][j];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) sum[c] = group_sum<16>(sum[c]) * scale.down;
+            if ((lane & 15) == 0 && n_lane + 16 * j < p.out_stride)
+              *reinterpret_cast<f32x4*>(to + n_lane + 16 * j) = sum;
+          }
+        }
+        // to the end of the row of memory: what lies beyond the classes is zero,
+        // and takes part in the next product
+        Tile::store([&](int i, int j, int c) { return acc[i][j][c]; }, own, (T*)p.out, p.out_stride,
+                    m0 + m_wave, n0 + n_wave, p.M, p.out_stride);
       }
-      // to the end of the row of memory: what lies beyond the classes is zero,
-      // and takes part in the next product
-      Tile::store([&](int i, int j, int c) { return acc[i][j][c]; }, own, (T*)p.out, p.out_stride,
-                  m0 + m_wave, n0 + n_wave, p.M, p.out_stride);
+    }
+  }
+};
+
+template <typename T, int kOutput, bool kAcrossA, bool kAcrossB, int kBM, int kBN, int kWM, int kWN,
+          int kStages>
+__global__ __launch_bounds__(64 * kWM * kWN, 2) void head_kernel(HeadArgs p) {
+  using Head = HeadTile<T, kOutput, kAcrossA, kAcrossB, kBM, kBN, kWM, kWN, kStages>;
+  __shared__ __align__(1024) int8_t s_stages[Head::kLds];
+  Head::run(p, blockIdx.x, blockIdx.y, s_stages);
+}
+
+// Both products with g in one launch, for sizes where one alone leaves compute
+// units idle, and the sums of dbias: work-groups 0 .. dx_blocks - 1 have tiles of
+// dx, the next dw_blocks of dw, the others 64 classes each.
+struct HeadPairArgs {
+  HeadArgs dx, dw;
+  uint32_t dx_blocks, dw_blocks;
+  const float* bias_sums;  // [bias_rows][pitch]
+  int64_t pitch;
+  int32_t bias_rows;
+  float* dbias;
+};
+
+template <typename T, int kBM, int kBN, int kWM, int kWN, int kStages>
+__global__ __launch_bounds__(64 * kWM * kWN, 2) void head_pair_kernel(HeadPairArgs p) {
+  using Dx = HeadTile<T, kHeadRounded, false, true, kBM, kBN, kWM, kWN, kStages>;
+  using Dw = HeadTile<T, kHeadRounded, true, true, kBM, kBN, kWM, kWN, kStages>;
+  __shared__ __align__(1024) int8_t s_stages[Dx::kLds > Dw::kLds ? Dx::kLds : Dw::kLds];
+  if (blockIdx.x < p.dx_blocks) {
+    Dx::run(p.dx, blockIdx.x, 0, s_stages);
+  } else if (blockIdx.x < p.dx_blocks + p.dw_blocks) {
+    Dw::run(p.dw, blockIdx.x - p.dx_blocks, 0, s_stages);
+  } else {
+    // 64 classes: a wavefront takes every kWaves-th row of partial sums
+    constexpr int kWaves = kWM * kWN;
+    float* s_sum = reinterpret_cast<float*>(s_stages);
+    const int lane = (int)(threadIdx.x & 63u), wave = (int)(threadIdx.x >> 6);
+    const int64_t n = (int64_t)(blockIdx.x - p.dx_blocks - p.dw_blocks) * 64 + lane;
+    float sum = 0.0f;
+    if (n < p.dw.M)
+      for (int32_t r = wave; r < p.bias_rows; r += kWaves) sum += p.bias_sums[r * p.pitch + n];
+    s_sum[wave * 64 + lane] = sum;
+    __syncthreads();
+    if (wave == 0 && n < p.dw.M) {
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) sum += s_sum[w * 64 + lane];
+      p.dbias[n] = sum;
     }
   }
 }

@@ -43,6 +43,27 @@ void launch_head_tiles(HeadLaunch& l, hipStream_t st) {
 template <typename T>
 void launch_head(int output, bool across_a, HeadLaunch l, hipStream_t st);
 
+// dx and dw, and dbias, in one launch of tiles of 128x128 or 64x64.
+template <typename T>
+void launch_head_pair(HeadPairArgs p, int tile, hipStream_t st);
+
+template <typename T>
+void launch_head_pair_any(HeadPairArgs& p, int tile, hipStream_t st) {
+  const int64_t size = kHeadTileSizes[tile];
+  for (HeadArgs* a : {&p.dx, &p.dw}) {
+    a->tiles_m = (uint32_t)((a->M + size - 1) / size);
+    a->tiles_n = (uint32_t)((a->N + size - 1) / size);
+  }
+  p.dx_blocks = p.dx.tiles_m * p.dx.tiles_n;
+  p.dw_blocks = p.dw.tiles_m * p.dw.tiles_n;
+  const unsigned grid = p.dx_blocks + p.dw_blocks +
+                        (p.dbias != nullptr ? (unsigned)((p.dw.M + 63) / 64) : 0u);
+  if (tile == 1)
+    head_pair_kernel<T, 128, 128, 2, 2, 2><<<grid, 256, 0, st>>>(p);
+  else
+    head_pair_kernel<T, 64, 64, 2, 2, 4><<<grid, 256, 0, st>>>(p);
+}
+
 template <typename T>
 void launch_head_any(int output, bool across_a, HeadLaunch& l, hipStream_t st) {
   if (output == kHeadStatistics)

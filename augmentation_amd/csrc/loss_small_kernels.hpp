@@ -53,28 +53,14 @@ __global__ __launch_bounds__(256) void loss_join_kernel(JoinArgs p) {
   p.losses[row] = loss;
 }
 
-// scale[0] brings the largest finite |dloss| to `to`, scale[1] back.  Rounded to
-// 16 bits as they are, the gradients of a mean loss would all be off by the
-// rounding of 1 / rows, the same way (8192 rows of bf16: 3.0e-3 of dx against
-// 1.9e-3, of which 1.7e-3 is dx's own rounding); and fp16 holds those of classes
-// of small probability only if they are large.
+// find_scale's numbers for many rows, which not every work-group shall read.
 __global__ __launch_bounds__(1024) void loss_scale_kernel(const float* dlosses, int64_t stride,
                                                           int64_t rows, float to, float* scale) {
   __shared__ uint32_t s_top[16];
-  uint32_t top = 0;
-  for (int64_t i = threadIdx.x; i < rows; i += 1024) {
-    const uint32_t v = __builtin_bit_cast(uint32_t, dlosses[i * stride]) & 0x7FFFFFFFu;
-    if (v < 0x7F800000u) top = max(top, v);
-  }
-  top = group_max<64>(top);
-  if ((threadIdx.x & 63u) == 0) s_top[threadIdx.x >> 6] = top;
-  __syncthreads();
+  const Scale s = find_scale<1024>(dlosses, stride, rows, to, s_top);
   if (threadIdx.x != 0) return;
-  for (int w = 0; w < 16; ++w) top = max(top, s_top[w]);
-  // numbers so small that the inverse would overflow are scaled by less
-  const float largest = fmaxf(__builtin_bit_cast(float, top), 0x1p-100f);
-  scale[0] = to / largest;
-  scale[1] = largest / to;
+  scale[0] = s.up;
+  scale[1] = s.down;
 }
 
 // out = RN_T(scale[1] * the sum of `splits` products in fp32): a thread takes

@@ -433,7 +433,7 @@ int fn_linear_cross_entropy(const void* x_dev, int64_t x_stride, const void* wei
 
 /*
  * fn_linear_cross_entropy_backward -- the gradients.  dlosses are the gradients
- * of the losses, a stride apart (0: one number for all rows).  With
+ * of the losses, dlosses_stride apart: 1, or 0 for one number for all rows.  With
  *   g[t, v] = dloss[t] (exp(z[t, v] - lse[t]) - (1 - smoothing) [v = y_t]
  *                       - smoothing / classes)     (0 in an ignored row):
  *   dx = g weight, dweight = g^T x, rounded to dtype; dbias[v] = sum_t g[t, v]

@@ -38,9 +38,20 @@ void launch_norm_k(const fn::LayerArgs& a, hipStream_t st) {
       <<<(unsigned)std::min<int64_t>(groups, 1 << 20), kBlock, 0, st>>>(a);
 }
 
+// The rows' shape, as the other norm's but for two: a second reduction and bias
+// and mean beside the weight leave fewer wavefronts room (us with 64 / 128 threads
+// a row: 3001x2243 fp32 12.5 / 10.9, 12000x2240 bf16 with a residual 48 / 43,
+// 12000x2000 40 / 38; 12000x1500 31.2 / 31.5).  fp32 rows beyond 16,384 elements do
+// not fit.
+RowShape norm_shape(int32_t width, bool wide_type) {
+  if (width > 1536 && width <= 2048) return {2048, 128, 2};
+  if (width > 2048 && width <= 2560) return {2560, 128, 3};
+  return row_shape(width, wide_type ? 16384 : 32768);
+}
+
 template <typename T, bool kDrop>
 void launch_norm(const fn::LayerArgs& a, hipStream_t st) {
-  const RowShape s = row_shape(a.width, sizeof(T) == 4 ? 16384 : 32768);
+  const RowShape s = norm_shape(a.width, sizeof(T) == 4);
   switch (shape_key(s.threads, s.chunks)) {
     case shape_key(1, 0): return launch_norm_k<T, kDrop, 1, 1, true>(a, st);
     case shape_key(1, 1): return launch_norm_k<T, kDrop, 1, 1>(a, st);
@@ -53,8 +64,8 @@ void launch_norm(const fn::LayerArgs& a, hipStream_t st) {
     case shape_key(32, 3): return launch_norm_k<T, kDrop, 32, 3>(a, st);
     case shape_key(64, 2): return launch_norm_k<T, kDrop, 64, 2>(a, st);
     case shape_key(64, 3): return launch_norm_k<T, kDrop, 64, 3>(a, st);
-    case shape_key(64, 4): return launch_norm_k<T, kDrop, 64, 4>(a, st);
-    case shape_key(64, 5): return launch_norm_k<T, kDrop, 64, 5>(a, st);
+    case shape_key(128, 2): return launch_norm_k<T, kDrop, 128, 2>(a, st);
+    case shape_key(128, 3): return launch_norm_k<T, kDrop, 128, 3>(a, st);
     case shape_key(256, 2): return launch_norm_k<T, kDrop, 256, 2>(a, st);
     case shape_key(256, 3): return launch_norm_k<T, kDrop, 256, 3>(a, st);
     case shape_key(512, 2): return launch_norm_k<T, kDrop, 512, 2>(a, st);

@@ -23,7 +23,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("fn_api.hip", "q8_api.hip", "layer_api.hip",
                                                    "loss_api.hip", "loss_fp32.hip",
-                                                   "loss_fp16.hip", "loss_bf16.hip")]
+                                                   "loss_fp16.hip", "loss_bf16.hip",
+                                                   "loss_parts.hip")]
 HEADERS = [os.path.join(HERE, "csrc", h) for h in ("fn_host.hpp", "fn_device.hpp",
                                                    "fn_kernels.hpp", "fn_rows_host.hpp",
                                                    "row_kernels.hpp", "product_kernels.hpp",

@@ -69,7 +69,13 @@ void launch_norm(const fn::LayerArgs& a, hipStream_t st) {
     case shape_key(256, 2): return launch_norm_k<T, kDrop, 256, 2>(a, st);
     case shape_key(256, 3): return launch_norm_k<T, kDrop, 256, 3>(a, st);
     case shape_key(512, 2): return launch_norm_k<T, kDrop, 512, 2>(a, st);
-    case shape_key(512, 4): return launch_norm_k<T, kDrop, 512, 4>(a, st);
+    case shape_key(512, 4):
+      // 6000x12344 bf16 with a residual: 141 us against 154; 3000x12344 fp32 126
+      // against 119
+      if constexpr (sizeof(T) == 2)
+        return launch_norm_k<T, kDrop, 1024, 2>(a, st);
+      else
+        return launch_norm_k<T, kDrop, 512, 4>(a, st);
     case shape_key(1024, 4):
       if constexpr (sizeof(T) == 2) return launch_norm_k<T, kDrop, 1024, 4>(a, st);
     default:

@@ -37,16 +37,26 @@ struct Choice {
   double cost = 0.0;  // us
 };
 
-// The time of a tile of 256, 128 and 64 rows and columns for 4,096 bytes of the
-// contraction, us.
+// What the matrix instructions take: bytes of an element, passes over the
+// contraction and parts of an operand (Fp32Parts).
+struct Elements {
+  int64_t size;
+  int passes, parts;
+};
+
+Elements elements_of(int64_t type_bytes, bool split) {
+  return split ? Elements{2, fn::HeadType<fn::Fp32Parts>::kPasses, 3} : Elements{type_bytes, 1, 1};
+}
+
+// The time of a tile for 4,096 bytes of the contraction, us.
 double tile_time(int tile, int64_t e) {
-  constexpr double kTimes[2][3] = {{57.0, 17.3, 6.3}, {220.0, 56.0, 14.5}};
+  constexpr double kTimes[2][fn::kHeadTiles] = {{57.0, 17.3, 6.3, 5.0}, {285.0, 72.0, 18.0, 6.0}};
   return kTimes[e == 4][tile];
 }
 
 int64_t tiles_of(int tile, int64_t M, int64_t N) {
-  const int64_t size = fn::kHeadTileSizes[tile];
-  return ((M + size - 1) / size) * ((N + size - 1) / size);
+  const int64_t m = fn::kHeadTileM[tile], n = fn::kHeadTileN[tile];
+  return ((M + m - 1) / m) * ((N + n - 1) / n);
 }
 
 // `tiles` on the device, each with `bytes` of the contraction.
@@ -58,17 +68,19 @@ int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 // The tile and the splits of the contraction for M x N outputs and K elements
 // of it, by the time they would take.
-Choice choose(int64_t M, int64_t N, int64_t K, int64_t e, bool splittable) {
+Choice choose(int64_t M, int64_t N, int64_t K, const Elements& t, bool splittable,
+              bool few_rows = true) {
+  const int64_t e = t.size;
   const int64_t stage = fn::kStageRow / e;
   Choice best;
   best.cost = 1e300;
-  for (int tile = 0; tile < 3; ++tile) {
+  for (int tile = 0; tile < (few_rows && M <= 16 ? 4 : 3); ++tile) {
     const int64_t tiles = tiles_of(tile, M, N);
     if (tiles >= (int64_t)1 << 22) continue;  // 2^32 threads to a launch
     for (int splits = 1; splits <= 64; splits *= 2) {
       if (splits > 1 && (!splittable || K < 8 * stage * splits || tiles * splits > 4 * kUnits)) break;
       const int64_t K_split = std::max(round_up((K + splits - 1) / splits, stage), stage);
-      double cost = 3.0 + rounds_time(tile, e, tiles * splits, K_split * e);
+      double cost = 3.0 + rounds_time(tile, e, tiles * splits, K_split * e * t.passes);
       // partial products are written and read again, in a launch of their own
       if (splits > 1) cost += 3.0 + (double)M * N * 8.0 * splits / 4e6;
       if (cost < best.cost) best = {tile, splits, K_split, cost};
@@ -89,6 +101,7 @@ struct Parts {
 
 // A call goes through its classes in pieces of the same size, but for the last.
 struct Plan {
+  bool split;  // fp32 as Fp32Parts
   bool pack_x, pack_w;
   int64_t width_packed;  // elements
   int64_t piece;         // classes
@@ -107,9 +120,13 @@ struct Plan {
   int which(int64_t count) const { return count == piece ? 0 : 1; }
 };
 
-int64_t head_tiles(const Choice& c, int64_t n) {
-  const int64_t size = fn::kHeadTileSizes[c.tile];
-  return (n + size - 1) / size;
+// Tiles along the classes of a choice for the logits, and its rows of bias_sums.
+int64_t class_tiles(const Choice& c, int64_t classes) {
+  return (classes + fn::kHeadTileN[c.tile] - 1) / fn::kHeadTileN[c.tile];
+}
+
+int64_t bias_rows_of(const Choice& c, int64_t rows) {
+  return (rows + fn::kHeadTileM[c.tile] - 1) / fn::kHeadTileM[c.tile] * fn::kHeadTileRows[c.tile];
 }
 
 // Classes of a piece, at most `most` of them: as many as give every compute unit
@@ -120,20 +137,32 @@ int64_t piece_of(int64_t rows, int64_t most) {
   return rounds > 0 ? std::max<int64_t>(rounds * kUnits / m, 1) * 256 : most;
 }
 
+// fp32 operands in parts, if six products of bf16 and the copies (ten bytes an
+// element) take less time than one of fp32 (1999x21841x1021: TIMES).
+bool worth_parts(int64_t rows, int64_t classes, int32_t width, bool backward) {
+  const double copies = 6.0 + (double)(rows + classes) * width * 10.0 / 4e6;
+  const int products = backward ? 3 : 1;
+  return copies + products * choose(rows, classes, width, elements_of(4, true), false).cost <
+         products * choose(rows, classes, width, elements_of(4, false), false).cost;
+}
+
 Plan plan_of(int64_t rows, int64_t classes, int32_t width, int64_t e, bool pack_x, bool pack_w,
              bool backward) {
   Plan p{};
-  p.pack_x = pack_x;
-  p.pack_w = pack_w;
-  p.width_packed = round_up(width, 16 / e);
-  const int64_t K = pack_x || pack_w ? p.width_packed : width;
+  p.split = e == 4 && worth_parts(rows, classes, width, backward);
+  p.pack_x = pack_x || p.split;
+  p.pack_w = pack_w || p.split;
+  const Elements t = elements_of(e, p.split);
+  const int64_t bytes = t.size * t.parts;  // of an operand's element
+  p.width_packed = round_up(width, 16 / t.size);
+  const int64_t K = p.pack_x || p.pack_w ? p.width_packed : width;
   // what a class of a piece has in the workspace: its gradients, a copy of its
   // weights
-  const int64_t per_class =
-      std::max(backward ? std::max<int64_t>(rows, 1) * e : 0, pack_w ? p.width_packed * e : 0);
+  const int64_t per_class = std::max(backward ? std::max<int64_t>(rows, 1) * bytes : 0,
+                                     p.pack_w ? p.width_packed * bytes : 0);
   int64_t most = round_up(classes, 256);
   if (per_class > 0) most = std::min(most, std::max<int64_t>(kPieceBytes / per_class / 256, 1) * 256);
-  if (backward) most = std::min(most, kMaxStrideBytes / e / 256 * 256);
+  if (backward) most = std::min(most, kMaxStrideBytes / t.size / 256 * 256);
   p.piece = classes;
   if (most < classes) {
     p.piece = piece_of(rows, most);
@@ -141,20 +170,20 @@ Plan plan_of(int64_t rows, int64_t classes, int32_t width, int64_t e, bool pack_
     // whole rounds of tiles first and the rest in smaller ones, if that is less
     const int64_t piece = piece_of(rows, classes / 256 * 256);
     if (piece > 0 && piece < classes &&
-        choose(rows, piece, K, e, false).cost + choose(rows, classes - piece, K, e, false).cost <
-            choose(rows, classes, K, e, false).cost)
+        choose(rows, piece, K, t, false).cost + choose(rows, classes - piece, K, t, false).cost <
+            choose(rows, classes, K, t, false).cost)
       p.piece = piece;
   }
   p.pieces = (classes + p.piece - 1) / p.piece;
   const int64_t counts[2] = {p.piece, p.last(classes)};
   Parts parts;
   p.scale = parts.take(8);
-  if (pack_x) p.x = parts.take(rows * p.width_packed * e);
-  if (pack_w) p.w = parts.take(p.piece * p.width_packed * e);
-  for (int k = 0; k < 2; ++k) p.logits[k] = choose(rows, counts[k], K, e, false);
+  if (p.pack_x) p.x = parts.take(rows * p.width_packed * bytes);
+  if (p.pack_w) p.w = parts.take(p.piece * p.width_packed * bytes);
+  for (int k = 0; k < 2; ++k) p.logits[k] = choose(rows, counts[k], K, t, false);
   if (!backward) {
-    p.stat_tiles = (p.pieces - 1) * head_tiles(p.logits[0], p.piece) +
-                   head_tiles(p.logits[p.which(counts[1])], counts[1]);
+    p.stat_tiles = (p.pieces - 1) * class_tiles(p.logits[0], p.piece) +
+                   class_tiles(p.logits[p.which(counts[1])], counts[1]);
     p.stats = parts.take(rows * p.stat_tiles * 8);
     p.sums = parts.take(rows * p.stat_tiles * 4);
     p.target_z = parts.take(rows * 4);
@@ -168,9 +197,9 @@ Plan plan_of(int64_t rows, int64_t classes, int32_t width, int64_t e, bool pack_
   for (int k = 0; k < 2; ++k) {
     // dx's sums of the first piece fill every split's place, a later one may
     // use fewer
-    p.dx[k] = choose(rows, width, counts[k], e, k == 0);
-    p.dw[k] = choose(counts[k], width, rows, e, true);
-    bias_rows = std::max(bias_rows, head_tiles(p.logits[k], rows) * fn::kHeadTileRows);
+    p.dx[k] = choose(rows, width, counts[k], t, k == 0);
+    p.dw[k] = choose(counts[k], width, rows, t, true, false);
+    bias_rows = std::max(bias_rows, bias_rows_of(p.logits[k], rows));
     if (p.dw[k].splits > 1) dw_rows = std::max(dw_rows, p.dw[k].splits * counts[k]);
   }
   p.sum_dx = p.pieces > 1 || p.dx[0].splits > 1;
@@ -178,14 +207,15 @@ Plan plan_of(int64_t rows, int64_t classes, int32_t width, int64_t e, bool pack_
     double least = p.dx[0].cost + p.dw[0].cost;
     for (int tile = 1; tile < 3; ++tile) {
       const int64_t tiles = tiles_of(tile, rows, width) + tiles_of(tile, classes, width);
-      const double cost = 3.0 + rounds_time(tile, e, tiles, std::max(rows, classes) * e);
+      const double cost =
+          3.0 + rounds_time(tile, t.size, tiles, std::max(rows, classes) * t.size * t.passes);
       if (tiles < (int64_t)1 << 22 && cost < least) {
         least = cost;
         p.pair_tile = tile;
       }
     }
   }
-  p.g = parts.take(rows * p.pitch * e);
+  p.g = parts.take(rows * p.pitch * bytes);
   if (p.sum_dx) p.dx_sums = parts.take(p.dx[0].splits * rows * p.sum_pitch * 4);
   if (dw_rows > 0) p.dw_sums = parts.take(dw_rows * p.sum_pitch * 4);
   p.bias_sums = parts.take(bias_rows * p.pitch * 4);
@@ -217,14 +247,19 @@ bool in_place(const void* p, int64_t stride, int32_t width, int64_t e) {
 template <typename T>
 fn::Operand operand(const void* from, int64_t stride, int64_t rows, int32_t width, int64_t copied,
                     char* copy, hipStream_t st) {
-  constexpr int64_t e = sizeof(T);
-  if (copy == nullptr) return {(const char*)from, stride * e, rows, (int64_t)width * e};
-  if (rows > 0) {
-    const dim3 grid(blocks_for(copied * e / 16, 256), (unsigned)std::min<int64_t>(rows, 65535));
+  using Element = typename fn::HeadType<T>::Operand;
+  constexpr int64_t e = sizeof(Element);
+  if (copy == nullptr) return {(const char*)from, stride * e, rows, (int64_t)width * e, 0};
+  const fn::Operand o = {copy, copied * e, rows, copied * e, rows * copied * e};
+  if (rows == 0) return o;
+  const dim3 grid(blocks_for(copied * e / 16, 256), (unsigned)std::min<int64_t>(rows, 65535));
+  if constexpr (std::is_same_v<T, fn::Fp32Parts>)
+    fn::loss_parts_kernel<<<grid, 256, 0, st>>>((const float*)from, stride, rows, width,
+                                                (Element*)copy, (int32_t)copied, rows * copied);
+  else
     fn::loss_pack_kernel<T><<<grid, 256, 0, st>>>((const T*)from, stride, rows, width, (T*)copy,
                                                   (int32_t)copied);
-  }
-  return {copy, copied * e, rows, copied * e};
+  return o;
 }
 
 struct Call {
@@ -261,11 +296,12 @@ fn::HeadArgs head_args(const Call& c, const Plan& p, const fn::Operand& x, const
 template <typename T>
 int forward(const Call& c, const Plan& p, float* losses, float* lse) {
   char* const ws = c.workspace;
+  using Given = typename fn::HeadType<T>::Output;
   const fn::Operand x = operand<T>(c.x, c.x_stride, c.rows, c.width, p.width_packed,
                                    p.pack_x ? ws + p.x : nullptr, c.st);
   for (int64_t first = 0, tile = 0; first < c.classes; first += p.piece) {
     const int64_t count = std::min(p.piece, c.classes - first);
-    const fn::Operand w = operand<T>((const T*)c.w + first * c.w_stride, c.w_stride, count, c.width,
+    const fn::Operand w = operand<T>((const Given*)c.w + first * c.w_stride, c.w_stride, count, c.width,
                                      p.width_packed, p.pack_w ? ws + p.w : nullptr, c.st);
     fn::HeadArgs a = head_args(c, p, x, w, first, count);
     a.stats = (fn::f32x2*)(ws + p.stats);
@@ -276,7 +312,7 @@ int forward(const Call& c, const Plan& p, float* losses, float* lse) {
     const Choice& choice = p.logits[p.which(count)];
     fn::launch_head<T>(fn::kHeadStatistics, false, {a, choice.tile, 1}, c.st);
     FN_TRY(launch_status("head_kernel launch"));
-    tile += head_tiles(choice, count);
+    tile += class_tiles(choice, count);
   }
   fn::JoinArgs j{};
   j.stats = (const fn::f32x2*)(ws + p.stats);
@@ -328,15 +364,16 @@ int round_sums(const float* sums, const Plan& p, int64_t split_stride, int split
 
 template <typename T>
 int backward(const Call& c, const Plan& p, const Gradients& g) {
-  constexpr int64_t e = sizeof(T);
+  using Given = typename fn::HeadType<T>::Output;
+  constexpr int64_t e = sizeof(typename fn::HeadType<T>::Operand);
   char* const ws = c.workspace;
   const fn::Operand x = operand<T>(c.x, c.x_stride, c.rows, c.width, p.width_packed,
                                    p.pack_x ? ws + p.x : nullptr, c.st);
   float* scale = nullptr;
   float scale_to = 0.0f;
-  if constexpr (sizeof(T) == 2) {
+  if constexpr (sizeof(Given) == 2) {
     scale = (float*)(ws + p.scale);
-    scale_to = std::is_same_v<T, _Float16> ? 16384.0f : 1.0f;
+    scale_to = std::is_same_v<Given, _Float16> ? 16384.0f : 1.0f;
     // few rows: each work-group of the first kernel looks for the largest
     // dloss, for less than a launch takes
     if (c.rows > kFewRows || c.rows == 0) {
@@ -350,9 +387,9 @@ int backward(const Call& c, const Plan& p, const Gradients& g) {
   for (int64_t first = 0; first < c.classes; first += p.piece) {
     const int64_t count = std::min(p.piece, c.classes - first);
     const int k = p.which(count);
-    const int32_t bias_rows = (int32_t)(head_tiles(p.logits[k], c.rows) * fn::kHeadTileRows);
+    const int32_t bias_rows = (int32_t)bias_rows_of(p.logits[k], c.rows);
     float* const bias_sums = (float*)(ws + p.bias_sums);
-    const fn::Operand w = operand<T>((const T*)c.w + first * c.w_stride, c.w_stride, count, c.width,
+    const fn::Operand w = operand<T>((const Given*)c.w + first * c.w_stride, c.w_stride, count, c.width,
                                      p.width_packed, p.pack_w ? ws + p.w : nullptr, c.st);
     if (c.rows > 0) {
       fn::HeadArgs a = head_args(c, p, x, w, first, count);
@@ -364,10 +401,12 @@ int backward(const Call& c, const Plan& p, const Gradients& g) {
       a.scale_to = scale_to;
       a.out = ws + p.g;
       a.out_stride = p.pitch;
+      a.out_part = c.rows * p.pitch;
       fn::launch_head<T>(fn::kHeadGradient, false, {a, p.logits[k].tile, 1}, c.st);
       FN_TRY(launch_status("head_kernel launch"));
     }
-    const fn::Operand gradient = {ws + p.g, p.pitch * e, c.rows, p.pitch * e};
+    const fn::Operand gradient = {ws + p.g, p.pitch * e, c.rows, p.pitch * e,
+                                  c.rows * p.pitch * e};
     fn::HeadArgs dx{}, dw{};
     dx.a = dw.a = gradient;
     dx.b = w;
@@ -378,7 +417,7 @@ int backward(const Call& c, const Plan& p, const Gradients& g) {
     dx.scale = dw.scale = scale;
     dx.out = g.dx;
     dx.out_stride = g.dx_stride;
-    T* const dw_out = (T*)g.dw + first * g.dw_stride;
+    Given* const dw_out = (Given*)g.dw + first * g.dw_stride;
     dw.out = dw_out;
     dw.out_stride = g.dw_stride;
     if (pair) {
@@ -424,13 +463,13 @@ int backward(const Call& c, const Plan& p, const Gradients& g) {
                          {dw, p.dw[k].tile, splits}, c.st);
       FN_TRY(launch_status("head_kernel launch"));
       if (splits > 1)
-        FN_TRY(round_sums<T>((const float*)(ws + p.dw_sums), p, dw.split_stride, splits, count,
+        FN_TRY(round_sums<Given>((const float*)(ws + p.dw_sums), p, dw.split_stride, splits, count,
                              c.width, scale, dw_out, g.dw_stride, c.st));
     }
   }
   if (g.dx != nullptr && p.sum_dx)
-    FN_TRY(round_sums<T>((const float*)(ws + p.dx_sums), p, c.rows * p.sum_pitch,
-                         p.dx[0].splits, c.rows, c.width, scale, (T*)g.dx, g.dx_stride, c.st));
+    FN_TRY(round_sums<Given>((const float*)(ws + p.dx_sums), p, c.rows * p.sum_pitch,
+                         p.dx[0].splits, c.rows, c.width, scale, (Given*)g.dx, g.dx_stride, c.st));
   return ok();
 }
 
@@ -481,6 +520,7 @@ FN_EXPORT int fn_linear_cross_entropy(const void* x_dev, int64_t x_stride, const
   FN_TRY(check_buffers(buffers, &dev));
   const Call c = {x_dev, x_stride, weight_dev, weight_stride, bias_dev, targets_dev, rows,
                   classes, width, smoothing, (char*)workspace_dev, (hipStream_t)stream};
+  if (plan.split) return forward<fn::Fp32Parts>(c, plan, losses_dev, lse_dev);
   if (dtype == FN_OUT_FP32) return forward<float>(c, plan, losses_dev, lse_dev);
   if (dtype == FN_OUT_FP16) return forward<_Float16>(c, plan, losses_dev, lse_dev);
   return forward<fn::BF16>(c, plan, losses_dev, lse_dev);
@@ -520,6 +560,7 @@ FN_EXPORT int fn_linear_cross_entropy_backward(
                   classes, width, smoothing, (char*)workspace_dev, (hipStream_t)stream};
   const Gradients g = {dlosses_dev, dlosses_stride, lse_dev, dx_dev, dx_stride,
                        dweight_dev, dweight_stride, dbias_dev};
+  if (plan.split) return backward<fn::Fp32Parts>(c, plan, g);
   if (dtype == FN_OUT_FP32) return backward<float>(c, plan, g);
   if (dtype == FN_OUT_FP16) return backward<_Float16>(c, plan, g);
   return backward<fn::BF16>(c, plan, g);

@@ -64,6 +64,34 @@ __device__ __forceinline__ f32x4 multiply_add(i32x4 a, i32x4 b, f32x4 c) {
   }
 }
 
+// fp32 operands as three bf16 numbers each, a = a0 + a1 + a2 with a0 = RN(a), a1 =
+// RN(a - a0), a2 = RN(a - a0 - a1): all 24 bits, and the differences are exact.
+// A product is then six products of bf16 numbers, exact in fp32 sums:
+//   a2 b0 + a0 b2 + a1 b1 + a1 b0 + a0 b1 + a0 b0,
+// the smallest first; the three left out come to 2^-24 of a b together, the
+// rounding of one product in fp32.  On the matrix cores that is 16 / 6 times the
+// rate of the fp32 instruction.  The six follow each other as one long
+// contraction.  An infinity in an operand gives NaN in every logit it reaches.
+struct Fp32Parts {};
+
+template <typename T>
+struct HeadType {
+  using Operand = T;  // what the matrix instructions take
+  using Output = T;
+  static constexpr int kPasses = 1;
+};
+
+template <>
+struct HeadType<Fp32Parts> {
+  using Operand = BF16;
+  using Output = float;
+  static constexpr int kPasses = 6;
+};
+
+// The part of each operand in a pass, two bits for each pass.
+constexpr uint32_t kPartsOfA = 2 | 0 << 2 | 1 << 4 | 1 << 6 | 0 << 8 | 0 << 10;
+constexpr uint32_t kPartsOfB = 0 | 2 << 2 | 1 << 4 | 0 << 6 | 1 << 8 | 0 << 10;
+
 // An operand of a product: `rows` rows of memory of `length` bytes each, `stride`
 // bytes apart, all multiples of 16.  Along the contraction a row of memory is a
 // row of the operand, across it an element of the contraction.
@@ -71,6 +99,13 @@ struct Operand {
   const char* p;
   int64_t stride, rows;
   int64_t length;
+  int64_t part;  // Fp32Parts: bytes from one part to the next
+};
+
+// Where in the contraction a stage begins: element k of a pass.
+struct Walk {
+  int64_t k;
+  int pass;
 };
 
 enum HeadOutput {
@@ -108,6 +143,7 @@ struct HeadArgs {
   float scale_to;
   void* out;
   int64_t out_stride;   // in elements
+  int64_t out_part;     // kHeadGradient of Fp32Parts: elements between the parts
   int64_t split_stride; // kHeadSums: elements between the splits' outputs
   bool add;             // kHeadSums: to what is there
 };
@@ -126,20 +162,23 @@ constexpr int kStageRow = 128;
 // read transposed (two reads of four elements of the contraction each: lanes
 // 4 j .. 4 j + 3 of sixteen point to sixteen elements of row j, and lane i
 // receives element i of the four rows); fp32 ones are four single reads.
-template <typename T, bool kAcross, int kRows, int kWaves, int kTiles>
+template <typename T, bool kAcross, int kRows, int kWaves, int kTiles, int kPasses, uint32_t kParts>
 struct Stager {
   static constexpr int kE = (int)sizeof(T);
-  static constexpr int kLoads = kRows / 8 / kWaves;  // of 1,024 bytes, per wavefront and stage
+  // Wavefronts that divide the loads; sixteen rows at least for each.  Where that
+  // is one, every wavefront loads it all, to the same place.
+  static constexpr int kSharers = kRows / 16 < kWaves ? kRows / 16 : kWaves;
+  static constexpr int kLoads = kRows / 8 / kSharers;  // of 1,024 bytes, per wavefront and stage
   static constexpr int kStageK = kStageRow / kE;     // elements of the contraction
   static constexpr int kRowBytes = kAcross ? kRows * kE : kStageRow;
-  static_assert(kLoads % 2 == 0, "rows per wavefront: a multiple of 16");
+  static_assert(kLoads % 2 == 0 && kWaves % kSharers == 0, "sixteen rows to a wavefront");
 
   int off[kLoads];
   int piece_byte[2];  // along: where in a row this lane's pieces are
   int at[kAcross ? kTiles : 1], at_step[2];
   const char* p;
-  int64_t stride, rows, length;
-  i32x4 resource;
+  int64_t stride, length, part;
+  int64_t bytes;  // along: of the tile's rows
 
   static __device__ __forceinline__ int swizzle(int r) {
     if constexpr (kE == 4) return 4 * ((r >> 2) & 3);
@@ -159,8 +198,9 @@ struct Stager {
   // row0: the tile's first row as an operand; tile0: the wavefront's
   __device__ __forceinline__ void start(const Operand& o, int64_t row0, int wave, int tile0) {
     const int lane = (int)(threadIdx.x & 63u);
+    wave %= kSharers;
     stride = o.stride;
-    rows = o.rows;
+    part = o.part;
     if constexpr (kAcross) {
       p = o.p + row0 * kE;
       length = o.length - row0 * kE;
@@ -186,8 +226,8 @@ struct Stager {
     } else {
       p = o.p + row0 * stride;
       length = o.length;
-      const int64_t here = min(rows - row0, (int64_t)kRows);
-      resource = make_resource(p, here > 0 ? (here - 1) * stride + length : 0);
+      const int64_t here = min(o.rows - row0, (int64_t)kRows);
+      bytes = here > 0 ? (here - 1) * stride + length : 0;
       const int sub = lane / 8;
       piece_byte[0] = 16 * staged_piece(sub, lane % 8);
       piece_byte[1] = 16 * staged_piece(8 + sub, lane % 8);
@@ -202,26 +242,28 @@ struct Stager {
     }
   }
 
-  // What the loads of the stage from element k0 of the contraction on need,
-  // which ends before k_end: elements from there on are zeros.
+  // What the loads of the stage at `w` need; its pass ends before k_end, and
+  // elements from there on are zeros.
   struct Stage {
     i32x4 resource;
     int k_byte;
     bool inside[2];
   };
 
-  __device__ __forceinline__ Stage stage(int64_t k0, int64_t k_end) const {
+  __device__ __forceinline__ Stage stage(const Walk& w, int64_t k_end) const {
     Stage s;
+    const char* from = p;
+    if constexpr (kPasses > 1) from += (int64_t)(kParts >> 2 * w.pass & 3u) * part;
     if constexpr (kAcross) {
       // rows beyond the last one lie beyond the resource
-      const int64_t left = min(k_end - k0, (int64_t)kStageK);
-      s.resource = make_resource(p + k0 * stride, left > 0 ? (left - 1) * stride + length : 0);
+      const int64_t left = min(k_end - w.k, (int64_t)kStageK);
+      s.resource = make_resource(from + w.k * stride, left > 0 ? (left - 1) * stride + length : 0);
       s.k_byte = 0;
       s.inside[0] = s.inside[1] = true;
     } else {
-      s.resource = resource;
-      s.k_byte = (int)(k0 * kE);
-      const int64_t left = (k_end - k0) * kE;
+      s.resource = make_resource(from, bytes);
+      s.k_byte = (int)(w.k * kE);
+      const int64_t left = (k_end - w.k) * kE;
       s.inside[0] = piece_byte[0] < left;
       s.inside[1] = piece_byte[1] < left;
     }
@@ -229,7 +271,7 @@ struct Stager {
   }
 
   __device__ __forceinline__ void load(const Stage& s, uint32_t lds, int wave, int i) const {
-    load_to_lds(s.resource, lds + (wave * kLoads + i) * 1024, s.inside[i & 1] ? off[i] : kOutside,
+    load_to_lds(s.resource, lds + (wave % kSharers * kLoads + i) * 1024, s.inside[i & 1] ? off[i] : kOutside,
                 s.k_byte);
   }
 
@@ -269,11 +311,13 @@ struct ValueTile {
                                                int64_t m0, int64_t n0, int64_t M, int64_t N) {
     constexpr int kE = 16 / (int)sizeof(T);  // outputs per 16-byte store
     constexpr int kLanes = 16 * kTN / kE;    // lanes along a row
-    constexpr int kRowsAtOnce = 64 / kLanes;
+    constexpr int kRowsAtOnce = 64 / kLanes < kTokens ? 64 / kLanes : kTokens;
     constexpr int kTiles = kTokens / 16;
     const int lane = (int)(threadIdx.x & 63u);
     const int64_t n = n0 + kE * (lane % kLanes);
-    const int left = (int)min(max(N - n, (int64_t)0), (int64_t)kE);
+    // (a narrow tile's rows need fewer lanes than there are)
+    const bool idle = lane / kLanes >= kRowsAtOnce;
+    const int left = idle ? 0 : (int)min(max(N - n, (int64_t)0), (int64_t)kE);
 #pragma unroll
     for (int i0 = 0; i0 < kTM; i0 += kTiles) {
 #pragma unroll
@@ -297,7 +341,8 @@ struct ValueTile {
       for (int i = 0; i < kTokens / kRowsAtOnce; ++i) {
         const int r = i * kRowsAtOnce + lane / kLanes;
         const int64_t m = m0 + 16 * i0 + r;
-        const u32x4 v = *reinterpret_cast<const u32x4*>(lds + r * kPitch + 16 * (lane % kLanes));
+        const u32x4 v = *reinterpret_cast<const u32x4*>(lds + (idle ? 0 : r) * kPitch +
+                                                        16 * (lane % kLanes));
         T* to = out + m * out_stride + n;
         if (m < M && left == kE)
           *reinterpret_cast<u32x4_any*>(to) = v;
@@ -366,9 +411,15 @@ template <typename T, int kOutput, bool kAcrossA, bool kAcrossB, int kBM, int kB
 struct HeadTile {
   static constexpr int kWaves = kWM * kWN, kTM = kBM / kWM / 16, kTN = kBN / kWN / 16;
   static constexpr int kStageBytes = (kBM + kBN) * kStageRow;
-  using StagerA = Stager<T, kAcrossA, kBM, kWaves, kTM>;
-  using StagerB = Stager<T, kAcrossB, kBN, kWaves, kTN>;
-  using Tile = ValueTile<T, kTM, kTN>;
+  using Type = HeadType<T>;
+  using Element = typename Type::Operand;
+  static constexpr int kPasses = Type::kPasses;
+  using StagerA = Stager<Element, kAcrossA, kBM, kWaves, kTM, kPasses, kPartsOfA>;
+  using StagerB = Stager<Element, kAcrossB, kBN, kWaves, kTN, kPasses, kPartsOfB>;
+  // what leaves: products in the operands' type, gradients as the next products
+  // take them
+  using Out = std::conditional_t<kOutput == kHeadGradient, Element, typename Type::Output>;
+  using Tile = ValueTile<Out, kTM, kTN>;
   static constexpr int kLoadsA = StagerA::kLoads, kLoads = kLoadsA + StagerB::kLoads;
   static constexpr int kStageK = StagerA::kStageK, kSteps = 2;
   static constexpr int kOutBytes = kWaves * Tile::kBytes;
@@ -377,7 +428,8 @@ struct HeadTile {
   // what the logits need beside: bias, lse, dlosses, targets, a word for each
   // wavefront
   static constexpr bool kSides = kOutput == kHeadStatistics || kOutput == kHeadGradient;
-  static constexpr int kSideBytes = kSides ? 4 * (kBN + 4 * kBM + 64) : 0;
+  static constexpr int kSideM = kBM < 64 ? 64 : kBM;  // loads bring 64 words
+  static constexpr int kSideBytes = kSides ? 4 * (kBN + 4 * kSideM + 64) : 0;
   static constexpr int kLds = kMainBytes + kSideBytes;
 
   // The block-th tile, the split-th part of the contraction.
@@ -399,7 +451,18 @@ struct HeadTile {
       typename StagerA::Stage a;
       typename StagerB::Stage b;
     };
-    auto next_of = [&](int64_t k0) { return Next{sa.stage(k0, k_end), sb.stage(k0, k_end)}; };
+    Walk walk = {k_begin, 0};
+    // the next stage to load
+    auto next_of = [&]() {
+      const Next next = {sa.stage(walk, k_end), sb.stage(walk, k_end)};
+      walk.k += kStageK;
+      if (kPasses > 1 && walk.k >= k_end) {
+        // (beyond the last pass comes the first element again, for nothing)
+        walk.k = k_begin;
+        ++walk.pass;
+      }
+      return next;
+    };
     auto issue = [&](int stage, int i, const Next& next) {
       const uint32_t to = lds + stage * kStageBytes;
       if (i < kLoadsA)
@@ -419,27 +482,27 @@ struct HeadTile {
     // They go first and have landed with the first stage: fetched after the last
     // product they would keep the output waiting for memory once more.
     const float* const s_bias = reinterpret_cast<const float*>(s_stages + kMainBytes);
-    const float *const s_lse = s_bias + kBN, *const s_dloss = s_lse + kBM;
-    const int64_t* const s_target = reinterpret_cast<const int64_t*>(s_dloss + kBM);
+    const float *const s_lse = s_bias + kBN, *const s_dloss = s_lse + kSideM;
+    const int64_t* const s_target = reinterpret_cast<const int64_t*>(s_dloss + kSideM);
     if constexpr (kSides) {
       auto words = [&](const void* from, int64_t first, int64_t count, int64_t size, int to) {
         // `count` words of `size` from the first one on, zeros behind them
         const int64_t here = from != nullptr ? max(count - first, (int64_t)0) : 0;
         const i32x4 r = tile_resource((const int8_t*)from + 4 * first, 0, here > 0 ? 1 : 0,
                                       (int32_t)(4 * min(here, size)));
-        for (int c = wave; c < (int)size / 64; c += kWaves)
+        for (int c = wave; c < ((int)size + 63) / 64; c += kWaves)
           load_words_to_lds(r, lds + kMainBytes + 4 * to + 256 * c, 256 * c + 4 * lane);
       };
       words(p.bias, n0, p.N, kBN, 0);
       if constexpr (kOutput == kHeadGradient) {
         words(p.lse, m0, p.M, kBM, kBN);
-        if (p.dloss_stride != 0) words(p.dlosses, m0, p.M, kBM, kBN + kBM);
+        if (p.dloss_stride != 0) words(p.dlosses, m0, p.M, kBM, kBN + kSideM);
       }
-      words(p.targets, 2 * m0, 2 * p.M, 2 * kBM, kBN + 2 * kBM);
+      words(p.targets, 2 * m0, 2 * p.M, 2 * kBM, kBN + 2 * kSideM);
     }
 #pragma unroll
     for (int s = 0; s < kStages; ++s) {
-      const Next next = next_of(k_begin + s * kStageK);
+      const Next next = next_of();
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) issue(s, i, next);
     }
@@ -448,7 +511,7 @@ struct HeadTile {
       if (p.scale_to > 0.0f) {
         scale = find_scale<64 * kWaves>(
             p.dlosses, p.dloss_stride, p.M, p.scale_to,
-            reinterpret_cast<uint32_t*>(s_stages + kMainBytes) + kBN + 4 * kBM);
+            reinterpret_cast<uint32_t*>(s_stages + kMainBytes) + kBN + 4 * kSideM);
         if (block == 0 && threadIdx.x == 0) {
           p.scale[0] = scale.up;
           p.scale[1] = scale.down;
@@ -463,7 +526,9 @@ struct HeadTile {
 #pragma unroll
     for (int i = 0; i < kTM + kTN; ++i) fetch(s_stages, 0, 0, i);
     int stage = 0;
-    for (int64_t k0 = k_begin; k0 < k_end; k0 += kStageK) {
+    const int stages =
+        k_end > k_begin ? kPasses * (int)((k_end - k_begin + kStageK - 1) / kStageK) : 0;
+    for (int left = stages; left > 0; --left) {
       const int after = stage + 1 == kStages ? 0 : stage + 1;
       static_for<kSteps>([&](auto step) {
         constexpr int k = decltype(step)::value;
@@ -480,7 +545,7 @@ struct HeadTile {
           asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
           __builtin_amdgcn_s_barrier();
           asm volatile("" ::: "memory");
-          next = next_of(k0 + kStages * kStageK);
+          next = next_of();
         }
         __builtin_amdgcn_sched_barrier(0);
         static_for<kProducts>([&](auto product) {
@@ -501,7 +566,7 @@ struct HeadTile {
           });
           __builtin_amdgcn_sched_barrier(0);
           acc[t / kTN][t % kTN] =
-              multiply_add<T>(fb[k & 1][t % kTN], fa[k & 1][t / kTN], acc[t / kTN][t % kTN]);
+              multiply_add<Element>(fb[k & 1][t % kTN], fa[k & 1][t / kTN], acc[t / kTN][t % kTN]);
           __builtin_amdgcn_sched_barrier(0);
         });
       });
@@ -538,7 +603,7 @@ struct HeadTile {
         }
     } else if constexpr (kOutput == kHeadRounded) {
       const float scale = p.scale != nullptr ? p.scale[1] : 1.0f;
-      Tile::store([&](int i, int j, int c) { return acc[i][j][c] * scale; }, own, (T*)p.out,
+      Tile::store([&](int i, int j, int c) { return acc[i][j][c] * scale; }, own, (Out*)p.out,
                   p.out_stride, m0 + m_wave, n0 + n_wave, p.M, p.N);
     } else {
       // the logits
@@ -647,8 +712,22 @@ struct HeadTile {
         }
         // to the end of the row of memory: what lies beyond the classes is zero,
         // and takes part in the next product
-        Tile::store([&](int i, int j, int c) { return acc[i][j][c]; }, own, (T*)p.out, p.out_stride,
-                    m0 + m_wave, n0 + n_wave, p.M, p.out_stride);
+        Out* out = (Out*)p.out;
+#pragma unroll 1
+        for (int part = 0; part < (kPasses > 1 ? 3 : 1); ++part, out += p.out_part) {
+          Tile::store([&](int i, int j, int c) { return acc[i][j][c]; }, own, out, p.out_stride,
+                      m0 + m_wave, n0 + n_wave, p.M, p.out_stride);
+          if constexpr (kPasses > 1) {
+            // what the part leaves of each, exactly
+#pragma unroll
+            for (int i = 0; i < kTM; ++i)
+#pragma unroll
+              for (int j = 0; j < kTN; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                  acc[i][j][c] -= bf16_to_float(float_to_bf16(acc[i][j][c]));
+          }
+        }
       }
     }
   }

@@ -8,10 +8,12 @@
 
 namespace fn {
 
-// Tiles of 256x256, 128x128 and 64x64 outputs.
-constexpr int kHeadTileSizes[3] = {256, 128, 64};
+// Rows and columns of the tiles.
+constexpr int kHeadTiles = 4;
+constexpr int kHeadTileM[kHeadTiles] = {256, 128, 64, 16};
+constexpr int kHeadTileN[kHeadTiles] = {256, 128, 64, 64};
 // rows of wavefronts in a tile, each with a row of bias_sums
-constexpr int kHeadTileRows = 2;
+constexpr int kHeadTileRows[kHeadTiles] = {2, 2, 2, 1};
 
 struct HeadLaunch {
   HeadArgs args;
@@ -22,9 +24,9 @@ struct HeadLaunch {
 template <typename T, int kOutput, bool kAcrossA, bool kAcrossB>
 void launch_head_tiles(HeadLaunch& l, hipStream_t st) {
   HeadArgs& p = l.args;
-  const int64_t size = kHeadTileSizes[l.tile];
-  p.tiles_m = (uint32_t)((p.M + size - 1) / size);
-  p.tiles_n = (uint32_t)((p.N + size - 1) / size);
+  const int64_t m = kHeadTileM[l.tile], n = kHeadTileN[l.tile];
+  p.tiles_m = (uint32_t)((p.M + m - 1) / m);
+  p.tiles_n = (uint32_t)((p.N + n - 1) / n);
   const dim3 grid(p.tiles_m * p.tiles_n, (unsigned)l.splits);
   switch (l.tile) {
     case 0:
@@ -33,8 +35,13 @@ void launch_head_tiles(HeadLaunch& l, hipStream_t st) {
     case 1:
       head_kernel<T, kOutput, kAcrossA, kAcrossB, 128, 128, 2, 2, 2><<<grid, 256, 0, st>>>(p);
       break;
-    default:
+    case 2:
       head_kernel<T, kOutput, kAcrossA, kAcrossB, 64, 64, 2, 2, 4><<<grid, 256, 0, st>>>(p);
+      break;
+    default:
+      // few rows, which only dw's operands do not have
+      if constexpr (!kAcrossA)
+        head_kernel<T, kOutput, kAcrossA, kAcrossB, 16, 64, 1, 4, 4><<<grid, 256, 0, st>>>(p);
   }
 }
 
@@ -49,7 +56,7 @@ void launch_head_pair(HeadPairArgs p, int tile, hipStream_t st);
 
 template <typename T>
 void launch_head_pair_any(HeadPairArgs& p, int tile, hipStream_t st) {
-  const int64_t size = kHeadTileSizes[tile];
+  const int64_t size = kHeadTileM[tile];
   for (HeadArgs* a : {&p.dx, &p.dw}) {
     a->tiles_m = (uint32_t)((a->M + size - 1) / size);
     a->tiles_n = (uint32_t)((a->N + size - 1) / size);

@@ -118,4 +118,36 @@ __global__ __launch_bounds__(256) void loss_pack_kernel(const T* from, int64_t s
   }
 }
 
+// The three parts of fp32 rows (see Fp32Parts), zeros at their rows' ends: a
+// thread takes eight numbers.
+__global__ __launch_bounds__(256) void loss_parts_kernel(const float* from, int64_t stride,
+                                                         int64_t rows, int32_t width, BF16* to,
+                                                         int32_t pitch, int64_t part) {
+  const int32_t c = (int32_t)(blockIdx.x * 256 + threadIdx.x) * 8;
+  if (c >= pitch) return;
+  for (int64_t m = blockIdx.y; m < rows; m += gridDim.y) {
+    const float* row = from + m * stride + c;
+    Vec8<float> v;
+    if (c + 8 <= width)
+      v.load(row);
+    else
+      v.load_some(row, width - c);
+    float left[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) left[j] = v.get(j);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      u32x4 w;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = float_to_bf16(left[2 * j]), hi = float_to_bf16(left[2 * j + 1]);
+        w[j] = lo | hi << 16;
+        left[2 * j] -= bf16_to_float(lo);
+        left[2 * j + 1] -= bf16_to_float(hi);
+      }
+      *reinterpret_cast<u32x4*>(to + k * part + m * pitch + c) = w;
+    }
+  }
+}
+
 }  // namespace fn

@@ -121,7 +121,7 @@ def check_backward(fn, x, w, y, b, smoothing, dlosses, lse, **kw):
 
 SIZES = [(1, 1, 1), (1, 10, 8), (3, 7, 5), (1, 1000, 64), (16, 64, 64), (17, 65, 72), (65, 63, 64), (64, 1000, 768),
          (200, 1003, 130), (129, 257, 100), (300, 300, 33), (513, 2000, 96), (64, 5000, 64), (5000, 60, 64),
-         (31, 4099, 520), (256, 256, 1), (1030, 1025, 264), (2, 3, 4096)]
+         (31, 4099, 520), (256, 256, 1), (1030, 1025, 264), (2, 3, 4096), (1500, 4001, 1000), (2048, 2048, 1025)]
 
 
 @pytest.mark.parametrize("t", TYPES, ids=str)

@@ -617,20 +617,11 @@ def matmul_q8(a, a_scales, b, b_scales, bias=None, out_dtype=FN_OUT_BF16, out=No
 # arguments whose gradients would be lost, and count a version for what they
 # write.
 
-def _stride_of(t, width, name) -> int:
-    return width if t.is_contiguous() else _row_stride(t, name)
-
-
 def _rows_in(t, shape, dtype, dev, width, name):
-    """(address, row stride) of an optional input of these rows."""
-    if t is None:
-        return None, 0
-    _want(t, shape, dtype, dev, name)
-    return t.data_ptr(), _stride_of(t, width, name)
-
-
-def _affine(t, width, dtype, dev, name):
-    return None if t is None else _want(t, (width,), dtype, dev, name, True).data_ptr()
+    """(address, row stride) of an input or output of these rows."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on cuda:{dev}")
+    return t.data_ptr(), width if t.is_contiguous() else _row_stride(t, name)
 
 
 def dropout(x, p, seed, first_row=0, residual=None, out=None, stream=None):
@@ -642,11 +633,15 @@ def dropout(x, p, seed, first_row=0, residual=None, out=None, stream=None):
     shape, rows, width, dev = _rows_of(x)
     dtype = x.dtype
     code = _type_code(dtype)
-    res_at, res_stride = _rows_in(residual, shape, dtype, dev, width, "residual")
-    out = _want(out, shape, dtype, dev, "out", False, stream)
-    _check(_lib.fn_dropout(x.data_ptr(), _stride_of(x, width, "x"), res_at, res_stride, rows, width,
-                           p, seed & 0xFFFFFFFFFFFFFFFF, first_row, code, out.data_ptr(),
-                           _stride_of(out, width, "out"), _stream(stream)))
+    res_at, res_stride = None, 0
+    if residual is not None:
+        res_at, res_stride = _rows_in(residual, shape, dtype, dev, width, "residual")
+    if out is None:
+        out = _empty(shape, dtype, dev, stream)
+    out_at, out_stride = _rows_in(out, shape, dtype, dev, width, "out")
+    _check(_lib.fn_dropout(
+        x.data_ptr(), width if x.is_contiguous() else _row_stride(x, "x"), res_at, res_stride, rows,
+        width, p, seed & 0xFFFFFFFFFFFFFFFF, first_row, code, out_at, out_stride, _stream(stream)))
     _increment_version((out,))
     return out
 
@@ -661,23 +656,31 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None, p=0.0, seed=0
     shape, rows, width, dev = _rows_of(x)
     dtype = x.dtype
     code = _type_code(dtype)
-    res_at, res_stride = _rows_in(residual, shape, dtype, dev, width, "residual")
-    sum_at, sum_stride = None, 0
+    weight_at = bias_at = res_at = sum_at = None
+    res_stride = sum_stride = 0
+    if weight is not None:
+        weight_at = _want(weight, (width,), dtype, dev, "weight", True).data_ptr()
+    if bias is not None:
+        bias_at = _want(bias, (width,), dtype, dev, "bias", True).data_ptr()
+    if residual is not None:
+        res_at, res_stride = _rows_in(residual, shape, dtype, dev, width, "residual")
     summed = residual is not None or p > 0
     if summed:
-        sum_out = _want(sum_out, shape, dtype, dev, "sum_out", False, stream)
-        sum_at, sum_stride = sum_out.data_ptr(), _stride_of(sum_out, width, "sum_out")
+        if sum_out is None:
+            sum_out = _empty(shape, dtype, dev, stream)
+        sum_at, sum_stride = _rows_in(sum_out, shape, dtype, dev, width, "sum_out")
     elif sum_out is not None:
         raise ValueError("sum_out without a residual and dropout")
-    out = _want(out, shape, dtype, dev, "out", False, stream)
-    mean = _want(mean, shape[:-1], torch.float32, dev, "mean", True, stream)
-    rstd = _want(rstd, shape[:-1], torch.float32, dev, "rstd", True, stream)
+    if out is None:
+        out = _empty(shape, dtype, dev, stream)
+    out_at, out_stride = _rows_in(out, shape, dtype, dev, width, "out")
+    lead = shape[:-1]
+    mean = _want(mean, lead, torch.float32, dev, "mean", True, stream)
+    rstd = _want(rstd, lead, torch.float32, dev, "rstd", True, stream)
     _check(_lib.fn_layer_norm(
-        x.data_ptr(), _stride_of(x, width, "x"), res_at, res_stride,
-        _affine(weight, width, dtype, dev, "weight"), _affine(bias, width, dtype, dev, "bias"), rows,
-        width, eps, p, seed & 0xFFFFFFFFFFFFFFFF, first_row, code, sum_at, sum_stride,
-        out.data_ptr(), _stride_of(out, width, "out"), mean.data_ptr(), rstd.data_ptr(),
-        _stream(stream)))
+        x.data_ptr(), width if x.is_contiguous() else _row_stride(x, "x"), res_at, res_stride,
+        weight_at, bias_at, rows, width, eps, p, seed & 0xFFFFFFFFFFFFFFFF, first_row, code, sum_at,
+        sum_stride, out_at, out_stride, mean.data_ptr(), rstd.data_ptr(), _stream(stream)))
     _increment_version((out, mean, rstd, sum_out) if summed else (out, mean, rstd))
     return out, mean, rstd, sum_out if summed else x
 
@@ -712,17 +715,24 @@ def layer_norm_backward(dout, h, weight, mean, rstd, dsum=None, p=0.0, seed=0, f
     dout, h or dsum.  Without a workspace one is allocated for the call."""
     _refuse_gradients(dout, h, weight, mean, rstd, dsum, dh, dx, dweight, dbias)
     shape, rows, width, dev = _rows_of(h)
-    dtype = h.dtype
+    dtype, lead = h.dtype, shape[:-1]
     code = _type_code(dtype)
-    _want(dout, shape, dtype, dev, "dout")
-    _want(mean, shape[:-1], torch.float32, dev, "mean", True)
-    _want(rstd, shape[:-1], torch.float32, dev, "rstd", True)
-    dsum_at, dsum_stride = _rows_in(dsum, shape, dtype, dev, width, "dsum")
-    dh = _want(dh, shape, dtype, dev, "dh", False, stream)
-    dx_at, dx_stride = None, 0
+    dout_at, dout_stride = _rows_in(dout, shape, dtype, dev, width, "dout")
+    _want(mean, lead, torch.float32, dev, "mean", True)
+    _want(rstd, lead, torch.float32, dev, "rstd", True)
+    weight_at = dsum_at = dx_at = None
+    dsum_stride = dx_stride = 0
+    if weight is not None:
+        weight_at = _want(weight, (width,), dtype, dev, "weight", True).data_ptr()
+    if dsum is not None:
+        dsum_at, dsum_stride = _rows_in(dsum, shape, dtype, dev, width, "dsum")
+    if dh is None:
+        dh = _empty(shape, dtype, dev, stream)
+    dh_at, dh_stride = _rows_in(dh, shape, dtype, dev, width, "dh")
     if p > 0:
-        dx = _want(dx, shape, dtype, dev, "dx", False, stream)
-        dx_at, dx_stride = dx.data_ptr(), _stride_of(dx, width, "dx")
+        if dx is None:
+            dx = _empty(shape, dtype, dev, stream)
+        dx_at, dx_stride = _rows_in(dx, shape, dtype, dev, width, "dx")
     elif dx is not None:
         raise ValueError("dx without dropout: dh is the gradient of x")
     dweight = _want(dweight, (width,), torch.float32, dev, "dweight", True, stream)
@@ -730,14 +740,17 @@ def layer_norm_backward(dout, h, weight, mean, rstd, dsum=None, p=0.0, seed=0, f
     given = workspace is not None
     workspace, at, size = _workspace(workspace, _layer_workspace_bytes(rows, width), dev, stream)
     _check(_lib.fn_layer_norm_backward(
-        dout.data_ptr(), _stride_of(dout, width, "dout"), h.data_ptr(), _stride_of(h, width, "h"),
-        _affine(weight, width, dtype, dev, "weight"), mean.data_ptr(), rstd.data_ptr(), dsum_at,
-        dsum_stride, rows, width, p, seed & 0xFFFFFFFFFFFFFFFF, first_row, code, dh.data_ptr(),
-        _stride_of(dh, width, "dh"), dx_at, dx_stride, dweight.data_ptr(), dbias.data_ptr(), at,
-        size, _stream(stream)))
-    _increment_version([t for t in (dh, dx, dweight, dbias, workspace if given else None)
-                        if t is not None])
-    return dh, dh if dx is None else dx, dweight, dbias
+        dout_at, dout_stride, h.data_ptr(), width if h.is_contiguous() else _row_stride(h, "h"),
+        weight_at, mean.data_ptr(), rstd.data_ptr(), dsum_at, dsum_stride, rows, width, p,
+        seed & 0xFFFFFFFFFFFFFFFF, first_row, code, dh_at, dh_stride, dx_at, dx_stride,
+        dweight.data_ptr(), dbias.data_ptr(), at, size, _stream(stream)))
+    written = [dh, dweight, dbias]
+    if p > 0:
+        written.append(dx)
+    if given:
+        written.append(workspace)
+    _increment_version(written)
+    return dh, dx if p > 0 else dh, dweight, dbias
 
 
 # --------------------- tensor helpers: the linear head's softmax cross entropy
@@ -746,36 +759,39 @@ _head_workspace_bytes = functools.lru_cache(maxsize=256)(fn_linear_cross_entropy
 
 
 def _head(x, weight, targets, bias):
-    """What both passes check and pass of their inputs."""
+    """What both passes check of their inputs: shape, rows, classes, width, type
+    code, device; address, stride and place of x, then of the weight."""
     shape, rows, width, dev = _rows_of(x)
     dtype = x.dtype
     code = _type_code(dtype)
-    if weight.dim() != 2 or weight.shape[0] < 1:
+    classes = weight.shape[0] if weight.dim() == 2 else 0
+    if classes < 1:
         raise ValueError("weight must be a (classes, width) tensor")
-    classes = weight.shape[0]
-    _want(weight, (classes, width), dtype, dev, "weight")
+    w_at, w_stride = _rows_in(weight, (classes, width), dtype, dev, width, "weight")
     _want(targets, shape[:-1], torch.int64, dev, "targets", True)
     if bias is not None:
         _want(bias, (classes,), torch.float32, dev, "bias", True)
-    return (shape, rows, classes, width, dev, code, _stride_of(x, width, "x"),
-            _stride_of(weight, width, "weight"))
+    x_at, x_stride = x.data_ptr(), width if x.is_contiguous() else _row_stride(x, "x")
+    e = x.element_size()
+    return (shape, rows, classes, width, code, dev, x_at, x_stride,
+            _in_place(x_at, x_stride * e, width * e), w_at, w_stride,
+            _in_place(w_at, w_stride * e, width * e))
 
 
-def _in_place(t, stride, width) -> bool:
-    """Whether the library reads these rows where they are."""
-    e = t.element_size()
-    return ((t.data_ptr() | stride * e | width * e) % 16 == 0 and stride >= width
-            and stride * e < 2**23)
+def _in_place(at, stride, width) -> bool:
+    """Whether the library reads rows where they are (strides in bytes)."""
+    return (at | stride | width) % 16 == 0 and width <= stride < 2**23
 
 
 def linear_cross_entropy_workspace(x, weight, backward=False) -> torch.Tensor:
     """A workspace for linear_cross_entropy on operands of these sizes and
     places, or for its backward pass."""
-    _, rows, width, dev = _rows_of(x)
-    return torch.empty(_head_workspace_bytes(
-        rows, weight.shape[0], width, _type_code(x.dtype), _in_place(x, _stride_of(x, width, "x"), width),
-        _in_place(weight, _stride_of(weight, width, "weight"), width), backward), dtype=torch.uint8,
-        device=x.device)
+    _, rows, width, _ = _rows_of(x)
+    e = x.element_size()
+    places = [_in_place(t.data_ptr(), e * (width if t.is_contiguous() else _row_stride(t, name)),
+                        e * width) for t, name in ((x, "x"), (weight, "weight"))]
+    return torch.empty(_head_workspace_bytes(rows, weight.shape[0], width, _type_code(x.dtype),
+                                             *places, backward), dtype=torch.uint8, device=x.device)
 
 
 def linear_cross_entropy(x, weight, targets, bias=None, smoothing=0.0, losses=None, lse=None,
@@ -786,17 +802,18 @@ def linear_cross_entropy(x, weight, targets, bias=None, smoothing=0.0, losses=No
     0..classes-1: ignored).  Returns (losses, lse), fp32 of that shape.  Without
     a workspace one is allocated for the call."""
     _refuse_gradients(x, weight, bias, losses, lse)
-    shape, rows, classes, width, dev, code, x_stride, w_stride = _head(x, weight, targets, bias)
-    losses = _want(losses, shape[:-1], torch.float32, dev, "losses", True, stream)
-    lse = _want(lse, shape[:-1], torch.float32, dev, "lse", True, stream)
+    (shape, rows, classes, width, code, dev, x_at, x_stride, x_place, w_at, w_stride,
+     w_place) = _head(x, weight, targets, bias)
+    lead = shape[:-1]
+    losses = _want(losses, lead, torch.float32, dev, "losses", True, stream)
+    lse = _want(lse, lead, torch.float32, dev, "lse", True, stream)
     given = workspace is not None
-    workspace, at, size = _workspace(workspace, _head_workspace_bytes(
-        rows, classes, width, code, _in_place(x, x_stride, width), _in_place(weight, w_stride, width),
-        False), dev, stream)
+    workspace, at, size = _workspace(
+        workspace, _head_workspace_bytes(rows, classes, width, code, x_place, w_place, False), dev,
+        stream)
     _check(_lib.fn_linear_cross_entropy(
-        x.data_ptr(), x_stride, weight.data_ptr(), w_stride,
-        None if bias is None else bias.data_ptr(), targets.data_ptr(), rows, classes, width,
-        smoothing, code, losses.data_ptr(), lse.data_ptr(), at, size, _stream(stream)))
+        x_at, x_stride, w_at, w_stride, None if bias is None else bias.data_ptr(),
+        targets.data_ptr(), rows, classes, width, smoothing, code, losses.data_ptr(), lse.data_ptr(), at, size, _stream(stream)))
     _increment_version((losses, lse, workspace) if given else (losses, lse))
     return losses, lse
 
@@ -810,25 +827,28 @@ def linear_cross_entropy_backward(dlosses, x, weight, targets, lse, bias=None, s
     operands' dtype (None if not wanted), dbias is fp32 (None without a bias).
     Without a workspace one is allocated for the call."""
     _refuse_gradients(dlosses, x, weight, lse, bias, dx, dweight, dbias)
-    shape, rows, classes, width, dev, code, x_stride, w_stride = _head(x, weight, targets, bias)
+    (shape, rows, classes, width, code, dev, x_at, x_stride, x_place, w_at, w_stride,
+     w_place) = _head(x, weight, targets, bias)
     dtype, lead = x.dtype, shape[:-1]
     _want(dlosses, lead, torch.float32, dev, "dlosses")
     _want(lse, lead, torch.float32, dev, "lse", True)
     dloss_stride = 1
     if not dlosses.is_contiguous():
-        if any(dlosses.stride()):
+        if any(step for step, n in zip(dlosses.stride(), lead) if n > 1):
             raise ValueError("dlosses must be contiguous or one number expanded")
         dloss_stride = 0
     dx_at = dw_at = None
     dx_stride = dw_stride = 0
     if want_dx:
-        dx = _want(dx, shape, dtype, dev, "dx", False, stream)
-        dx_at, dx_stride = dx.data_ptr(), _stride_of(dx, width, "dx")
+        if dx is None:
+            dx = _empty(shape, dtype, dev, stream)
+        dx_at, dx_stride = _rows_in(dx, shape, dtype, dev, width, "dx")
     elif dx is not None:
         raise ValueError("dx is given and not wanted")
     if want_dweight:
-        dweight = _want(dweight, (classes, width), dtype, dev, "dweight", False, stream)
-        dw_at, dw_stride = dweight.data_ptr(), _stride_of(dweight, width, "dweight")
+        if dweight is None:
+            dweight = _empty((classes, width), dtype, dev, stream)
+        dw_at, dw_stride = _rows_in(dweight, (classes, width), dtype, dev, width, "dweight")
     elif dweight is not None:
         raise ValueError("dweight is given and not wanted")
     if bias is not None:
@@ -836,13 +856,13 @@ def linear_cross_entropy_backward(dlosses, x, weight, targets, lse, bias=None, s
     elif dbias is not None:
         raise ValueError("dbias without a bias")
     given = workspace is not None
-    workspace, at, size = _workspace(workspace, _head_workspace_bytes(
-        rows, classes, width, code, _in_place(x, x_stride, width), _in_place(weight, w_stride, width),
-        True), dev, stream)
+    workspace, at, size = _workspace(
+        workspace, _head_workspace_bytes(rows, classes, width, code, x_place, w_place, True), dev,
+        stream)
     _check(_lib.fn_linear_cross_entropy_backward(
-        dlosses.data_ptr(), dloss_stride, x.data_ptr(), x_stride, weight.data_ptr(), w_stride,
-        None if bias is None else bias.data_ptr(), targets.data_ptr(), lse.data_ptr(), rows, classes,
-        width, smoothing, code, dx_at, dx_stride, dw_at, dw_stride,
+        dlosses.data_ptr(), dloss_stride, x_at, x_stride, w_at, w_stride,
+        None if bias is None else bias.data_ptr(), targets.data_ptr(), lse.data_ptr(), rows,
+        classes, width, smoothing, code, dx_at, dx_stride, dw_at, dw_stride,
         None if dbias is None else dbias.data_ptr(), at, size, _stream(stream)))
     _increment_version([t for t in (dx, dweight, dbias, workspace if given else None)
                         if t is not None])

@@ -25,6 +25,8 @@ constexpr int64_t kUnits = 256;
 // for every product to fill the device, few enough to stay in the memory-side
 // cache until both products have read it.
 constexpr int64_t kPieceBytes = (int64_t)1 << 27;
+// Weights that do not stay in the memory-side cache until the next call anyway.
+constexpr int64_t kCached = (int64_t)1 << 28;
 constexpr int64_t kFewRows = 8192;
 constexpr int32_t kMaxFeatures = 1 << 20;
 constexpr int64_t kMaxClasses = (int64_t)1 << 28;
@@ -50,7 +52,8 @@ Elements elements_of(int64_t type_bytes, bool split) {
 
 // The time of a tile for 4,096 bytes of the contraction, us.
 double tile_time(int tile, int64_t e) {
-  constexpr double kTimes[2][fn::kHeadTiles] = {{57.0, 17.3, 6.3, 5.0}, {285.0, 72.0, 18.0, 6.0}};
+  constexpr double kTimes[2][fn::kHeadTiles] = {{57.0, 17.3, 6.3, 10.0, 16.0},
+                                                {285.0, 72.0, 18.0, 11.0, 18.0}};
   return kTimes[e == 4][tile];
 }
 
@@ -67,14 +70,18 @@ double rounds_time(int tile, int64_t e, int64_t tiles, int64_t bytes) {
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 // The tile and the splits of the contraction for M x N outputs and K elements
-// of it, by the time they would take.
+// of it, by the time they would take.  Up to 16 rows have tiles of their own: the
+// wide ones where they give every compute unit one (1x50000x4096 bf16 with 64 /
+// 128 classes a tile 77 / 71 us, 1x16000x4096 30 / 33).
 Choice choose(int64_t M, int64_t N, int64_t K, const Elements& t, bool splittable,
               bool few_rows = true) {
   const int64_t e = t.size;
   const int64_t stage = fn::kStageRow / e;
   Choice best;
   best.cost = 1e300;
-  for (int tile = 0; tile < (few_rows && M <= 16 ? 4 : 3); ++tile) {
+  const bool few = few_rows && M <= 16;
+  const int first = !few ? 0 : N >= 128 * kUnits ? 4 : 3;
+  for (int tile = first; tile < (few ? first + 1 : 3); ++tile) {
     const int64_t tiles = tiles_of(tile, M, N);
     if (tiles >= (int64_t)1 << 22) continue;  // 2^32 threads to a launch
     for (int splits = 1; splits <= 64; splits *= 2) {
@@ -287,6 +294,7 @@ fn::HeadArgs head_args(const Call& c, const Plan& p, const fn::Operand& x, const
   a.K_split = p.logits[p.which(count)].K_split;
   a.bias = c.bias != nullptr ? c.bias + first : nullptr;
   a.targets = c.targets;
+  a.once = w.stride * c.classes > kCached;
   a.first_class = first;
   a.classes = c.classes;
   a.smoothing = c.smoothing;
@@ -309,11 +317,15 @@ int forward(const Call& c, const Plan& p, float* losses, float* lse) {
     a.target_z = (float*)(ws + p.target_z);
     a.stat_tiles = p.stat_tiles;
     a.first_tile = tile;
+    const bool alone = p.stat_tiles == 1;
+    a.losses = alone ? losses : nullptr;
+    a.losses_lse = lse;
     const Choice& choice = p.logits[p.which(count)];
     fn::launch_head<T>(fn::kHeadStatistics, false, {a, choice.tile, 1}, c.st);
     FN_TRY(launch_status("head_kernel launch"));
     tile += class_tiles(choice, count);
   }
+  if (p.stat_tiles == 1) return ok();
   fn::JoinArgs j{};
   j.stats = (const fn::f32x2*)(ws + p.stats);
   j.sums = c.smoothing > 0.0f ? (const float*)(ws + p.sums) : nullptr;
@@ -410,6 +422,7 @@ int backward(const Call& c, const Plan& p, const Gradients& g) {
     fn::HeadArgs dx{}, dw{};
     dx.a = dw.a = gradient;
     dx.b = w;
+    dx.once = w.stride * c.classes > kCached;
     dw.b = x;
     dx.M = dw.K = c.rows;
     dx.K = dw.M = count;

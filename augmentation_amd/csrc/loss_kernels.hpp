@@ -131,6 +131,10 @@ struct HeadArgs {
   float* sums;     // [M][stat_tiles] sums of logits, or null
   float* target_z; // [M]
   int64_t stat_tiles, first_tile;
+  // one tile has all classes: the losses and lse themselves, and no statistics
+  float* losses;
+  float* losses_lse;
+  bool once;  // with few rows: b shall not stay in the caches
   // kHeadGradient
   const float* lse;
   const float* dlosses;
@@ -148,6 +152,18 @@ struct HeadArgs {
   bool add;             // kHeadSums: to what is there
 };
 
+// load_to_lds for what nobody reads again: past the caches (50000 rows of 8 KiB
+// 80 -> 74 us).
+__device__ __forceinline__ void load_once_to_lds(i32x4 resource, uint32_t lds, int offset, int k0) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %2, %3 offen nt lds"
+      :
+      : "s"(lds), "v"(offset), "s"(resource), "s"(k0)
+      : "memory");
+}
+
 // Bytes of a stage for each row of an operand: eight pieces of 16.  Along the
 // contraction it is a line of memory; across it, a stage is as many elements of
 // the contraction, each a row of all the tile's rows.
@@ -162,7 +178,8 @@ constexpr int kStageRow = 128;
 // read transposed (two reads of four elements of the contraction each: lanes
 // 4 j .. 4 j + 3 of sixteen point to sixteen elements of row j, and lane i
 // receives element i of the four rows); fp32 ones are four single reads.
-template <typename T, bool kAcross, int kRows, int kWaves, int kTiles, int kPasses, uint32_t kParts>
+template <typename T, bool kAcross, int kRows, int kWaves, int kTiles, int kPasses, uint32_t kParts,
+          bool kMayBeOnce>
 struct Stager {
   static constexpr int kE = (int)sizeof(T);
   // Wavefronts that divide the loads; sixteen rows at least for each.  Where that
@@ -270,9 +287,14 @@ struct Stager {
     return s;
   }
 
-  __device__ __forceinline__ void load(const Stage& s, uint32_t lds, int wave, int i) const {
-    load_to_lds(s.resource, lds + (wave % kSharers * kLoads + i) * 1024, s.inside[i & 1] ? off[i] : kOutside,
-                s.k_byte);
+  __device__ __forceinline__ void load(const Stage& s, uint32_t lds, int wave, int i,
+                                       bool once) const {
+    const uint32_t to = lds + (wave % kSharers * kLoads + i) * 1024;
+    const int from = s.inside[i & 1] ? off[i] : kOutside;
+    if (kMayBeOnce && once)
+      load_once_to_lds(s.resource, to, from, s.k_byte);
+    else
+      load_to_lds(s.resource, to, from, s.k_byte);
   }
 
   // Tile t's fragment of step k (of two).
@@ -374,6 +396,21 @@ __device__ __forceinline__ TileAt head_tile_at(uint32_t block, const HeadArgs& p
 
 constexpr float kMinusInfinity = -__builtin_inff();
 
+// A row's lse and loss from the maximum of its logits, the sum of exponentials
+// above it, the sum of the logits and the target's.
+struct LossOf {
+  float lse, loss;
+};
+
+__device__ __forceinline__ LossOf loss_of(float top, float sum, float all, bool counts, float target,
+                                          float smoothing, int64_t classes) {
+  LossOf l;
+  l.lse = top + logf(sum);
+  l.loss = counts ? l.lse - (1.0f - smoothing) * target : 0.0f;
+  if (counts && smoothing > 0.0f) l.loss -= smoothing * (all / (float)classes);
+  return l;
+}
+
 // What brings the largest finite |dloss| to `to`, and back.  Rounded to 16 bits
 // as they are, the gradients of a mean loss would all be off by the rounding of
 // 1 / rows, the same way (4096 rows of bf16: 3.0e-3 of dx against 1.7e-3, dx's
@@ -414,8 +451,10 @@ struct HeadTile {
   using Type = HeadType<T>;
   using Element = typename Type::Operand;
   static constexpr int kPasses = Type::kPasses;
-  using StagerA = Stager<Element, kAcrossA, kBM, kWaves, kTM, kPasses, kPartsOfA>;
-  using StagerB = Stager<Element, kAcrossB, kBN, kWaves, kTN, kPasses, kPartsOfB>;
+  // with few rows of a, b passes by once
+  using StagerA = Stager<Element, kAcrossA, kBM, kWaves, kTM, kPasses, kPartsOfA, false>;
+  using StagerB = Stager<Element, kAcrossB, kBN, kWaves, kTN, kPasses, kPartsOfB,
+                         kBM == 16 && kPasses == 1>;
   // what leaves: products in the operands' type, gradients as the next products
   // take them
   using Out = std::conditional_t<kOutput == kHeadGradient, Element, typename Type::Output>;
@@ -466,9 +505,9 @@ struct HeadTile {
     auto issue = [&](int stage, int i, const Next& next) {
       const uint32_t to = lds + stage * kStageBytes;
       if (i < kLoadsA)
-        sa.load(next.a, to, wave, i);
+        sa.load(next.a, to, wave, i, false);
       else
-        sb.load(next.b, to + kBM * kStageRow, wave, i - kLoadsA);
+        sb.load(next.b, to + kBM * kStageRow, wave, i - kLoadsA, p.once);
     };
     i32x4 fa[2][kTM], fb[2][kTN];
     auto fetch = [&](const int8_t* buf, int k, int slot, int i) {
@@ -488,8 +527,7 @@ struct HeadTile {
       auto words = [&](const void* from, int64_t first, int64_t count, int64_t size, int to) {
         // `count` words of `size` from the first one on, zeros behind them
         const int64_t here = from != nullptr ? max(count - first, (int64_t)0) : 0;
-        const i32x4 r = tile_resource((const int8_t*)from + 4 * first, 0, here > 0 ? 1 : 0,
-                                      (int32_t)(4 * min(here, size)));
+        const i32x4 r = StagerA::make_resource((const char*)from + 4 * first, 4 * min(here, size));
         for (int c = wave; c < ((int)size + 63) / 64; c += kWaves)
           load_words_to_lds(r, lds + kMainBytes + 4 * to + 256 * c, 256 * c + 4 * lane);
       };
@@ -620,6 +658,7 @@ struct HeadTile {
         float* s_top = reinterpret_cast<float*>(s_stages);
         float* s_sum = s_top + kWN * kBM;
         float* s_all = s_sum + kWN * kBM;
+        float* s_z = s_all + kWN * kBM;
 #pragma unroll
         for (int i = 0; i < kTM; ++i) {
           const int64_t m = m_lane + 16 * i;
@@ -655,7 +694,12 @@ struct HeadTile {
             for (int j = 0; j < kTN; ++j)
 #pragma unroll
               for (int c = 0; c < 4; ++c)
-                if (target == 16 * j + c) p.target_z[m] = acc[i][j][c];
+                if (target == 16 * j + c) {
+                  if (p.losses != nullptr)
+                    s_z[m_wave + 16 * i + (lane & 15)] = acc[i][j][c];
+                  else
+                    p.target_z[m] = acc[i][j][c];
+                }
           }
         }
         __syncthreads();
@@ -665,12 +709,21 @@ struct HeadTile {
           float top = s_top[r];
 #pragma unroll
           for (int w = 1; w < kWN; ++w) top = fmaxf(top, s_top[w * kBM + r]);
+          const float base = top == kMinusInfinity ? 0.0f : top;
           float sum = 0.0f, all = 0.0f;
 #pragma unroll
           for (int w = 0; w < kWN; ++w) {
-            const float t = s_top[w * kBM + r];
-            sum += t == kMinusInfinity ? s_sum[w * kBM + r] : s_sum[w * kBM + r] * exp_below(t - top);
+            sum += s_sum[w * kBM + r] * exp_below(s_top[w * kBM + r] - base);
             all += s_all[w * kBM + r];
+          }
+          if (p.losses != nullptr) {
+            const int64_t y = s_target[r];
+            const bool counts = y >= 0 && y < p.classes;
+            const LossOf l = loss_of(top, sum, all, counts, counts ? s_z[r] : 0.0f, p.smoothing,
+                                     p.classes);
+            p.losses_lse[m] = l.lse;
+            p.losses[m] = l.loss;
+            continue;
           }
           const int64_t at = m * p.stat_tiles + p.first_tile + tile.n;
           p.stats[at] = f32x2{top, sum};

@@ -9,11 +9,11 @@
 namespace fn {
 
 // Rows and columns of the tiles.
-constexpr int kHeadTiles = 4;
-constexpr int kHeadTileM[kHeadTiles] = {256, 128, 64, 16};
-constexpr int kHeadTileN[kHeadTiles] = {256, 128, 64, 64};
+constexpr int kHeadTiles = 5;
+constexpr int kHeadTileM[kHeadTiles] = {256, 128, 64, 16, 16};
+constexpr int kHeadTileN[kHeadTiles] = {256, 128, 64, 64, 128};
 // rows of wavefronts in a tile, each with a row of bias_sums
-constexpr int kHeadTileRows[kHeadTiles] = {2, 2, 2, 1};
+constexpr int kHeadTileRows[kHeadTiles] = {2, 2, 2, 1, 1};
 
 struct HeadLaunch {
   HeadArgs args;
@@ -38,10 +38,14 @@ void launch_head_tiles(HeadLaunch& l, hipStream_t st) {
     case 2:
       head_kernel<T, kOutput, kAcrossA, kAcrossB, 64, 64, 2, 2, 4><<<grid, 256, 0, st>>>(p);
       break;
-    default:
-      // few rows, which only dw's operands do not have
+    // few rows, which only dw's operands do not have
+    case 3:
       if constexpr (!kAcrossA)
         head_kernel<T, kOutput, kAcrossA, kAcrossB, 16, 64, 1, 4, 4><<<grid, 256, 0, st>>>(p);
+      break;
+    default:
+      if constexpr (!kAcrossA)
+        head_kernel<T, kOutput, kAcrossA, kAcrossB, 16, 128, 1, 4, 4><<<grid, 256, 0, st>>>(p);
   }
 }
 

@@ -26,31 +26,44 @@ __global__ __launch_bounds__(256) void loss_join_kernel(JoinArgs p) {
   const int lane = (int)(threadIdx.x & 63u);
   if (row >= p.rows) return;
   const f32x2* from = p.stats + row * p.tiles;
-  float top = kMinusInfinity, all = 0.0f;
-  for (int64_t i = lane; i < p.tiles; i += 64) top = fmaxf(top, from[i][0]);
+  const float* sums = p.sums != nullptr ? p.sums + row * p.tiles : nullptr;
+  // four tiles at a time, their loads together; a tile without anything has
+  // maximum -infinity and sum 0 (or NaN, which stays)
+  float top = kMinusInfinity, sum = 0.0f, all = 0.0f;
+  for (int64_t i = lane; i < p.tiles; i += 256) {
+    f32x2 v[4];
+    float s[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool there = i + 64 * j < p.tiles;
+      v[j] = there ? from[i + 64 * j] : f32x2{kMinusInfinity, 0.0f};
+      s[j] = there && sums != nullptr ? sums[i + 64 * j] : 0.0f;
+    }
+    const float higher = fmaxf(fmaxf(fmaxf(v[0][0], v[1][0]), fmaxf(v[2][0], v[3][0])), top);
+    const float base = higher == kMinusInfinity ? 0.0f : higher;
+    sum *= exp_below(top - base);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      sum += v[j][1] * exp_below(v[j][0] - base);
+      all += s[j];
+    }
+    top = higher;
+  }
   auto bits = [](float x) { return __builtin_bit_cast(uint32_t, x); };
-  top = __builtin_bit_cast(
+  const float higher = __builtin_bit_cast(
       float, group_fold<64>(bits(top), [&](uint32_t x, uint32_t y) {
         return bits(fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y)));
       }));
-  float sum = 0.0f;
-  for (int64_t i = lane; i < p.tiles; i += 64) {
-    const f32x2 v = from[i];
-    sum += v[0] == kMinusInfinity ? v[1] : v[1] * exp_below(v[0] - top);
-    if (p.sums != nullptr) all += p.sums[row * p.tiles + i];
-  }
-  sum = group_sum<64>(sum);
+  sum = group_sum<64>(sum * exp_below(top - (higher == kMinusInfinity ? 0.0f : higher)));
+  top = higher;
   all = group_sum<64>(all);
   if (lane != 0) return;
-  const float lse = top + logf(sum);
-  p.lse[row] = lse;
   const int64_t y = p.targets[row];
-  float loss = 0.0f;
-  if (y >= 0 && y < p.classes) {
-    loss = lse - (1.0f - p.smoothing) * p.target_z[row];
-    if (p.sums != nullptr) loss -= p.smoothing * (all / (float)p.classes);
-  }
-  p.losses[row] = loss;
+  const bool counts = y >= 0 && y < p.classes;
+  const LossOf l =
+      loss_of(top, sum, all, counts, counts ? p.target_z[row] : 0.0f, p.smoothing, p.classes);
+  p.lse[row] = l.lse;
+  p.losses[row] = l.loss;
 }
 
 // find_scale's numbers for many rows, which not every work-group shall read.

@@ -658,6 +658,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None, p=0.0, seed=0
     code = _type_code(dtype)
     weight_at = bias_at = res_at = sum_at = None
     res_stride = sum_stride = 0
+    p = _f32(p).value  # what the library sees: smaller numbers may be its zero
     if weight is not None:
         weight_at = _want(weight, (width,), dtype, dev, "weight", True).data_ptr()
     if bias is not None:
@@ -722,6 +723,7 @@ def layer_norm_backward(dout, h, weight, mean, rstd, dsum=None, p=0.0, seed=0, f
     _want(rstd, lead, torch.float32, dev, "rstd", True)
     weight_at = dsum_at = dx_at = None
     dsum_stride = dx_stride = 0
+    p = _f32(p).value
     if weight is not None:
         weight_at = _want(weight, (width,), dtype, dev, "weight", True).data_ptr()
     if dsum is not None:

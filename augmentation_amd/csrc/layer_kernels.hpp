@@ -59,26 +59,17 @@ struct DropoutArgs {
   int64_t x_stride, residual_stride, out_stride;  // in elements
   Dropout drop;
   uint32_t items;   // rows * chunks of this launch
-  uint32_t chunks;  // of a row
-  uint32_t magic, shift;  // division by chunks: see quotient
+  Division chunks;  // of a row
   int32_t width;
 };
-
-// n / d for any 32-bit n, by the upper half of a product with
-// floor(2^32 (2^l - d) / d) + 1, l = ceil(log2 d), which is 2^(32 + l) / d
-// rounded up without its top bit (Granlund and Montgomery 1994).
-__device__ __forceinline__ uint32_t quotient(uint32_t n, uint32_t magic, uint32_t shift) {
-  const uint32_t t = __umulhi(n, magic);
-  return (((n - t) >> 1) + t) >> shift;  // shift = l - 1; d = 1 takes no division
-}
 
 // A thread takes one chunk of eight elements.
 template <typename T, bool kShort>
 __global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs a) {
   const uint32_t i = blockIdx.x * 256u + threadIdx.x;
   if (i >= a.items) return;
-  const uint32_t row = a.chunks == 1 ? i : quotient(i, a.magic, a.shift);
-  const int32_t chunk = (int32_t)(i - row * a.chunks);
+  const uint32_t row = quotient(i, a.chunks);
+  const int32_t chunk = (int32_t)(i - row * a.chunks.by);
   const Chunk c = chunk_at(chunk, a.width);
   Vec8<T> x, r;
   load_chunk<kShort>(x, (const T*)a.x + (int64_t)row * a.x_stride, c);

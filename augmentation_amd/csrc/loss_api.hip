@@ -50,21 +50,38 @@ Elements elements_of(int64_t type_bytes, bool split) {
   return split ? Elements{2, fn::HeadType<fn::Fp32Parts>::kPasses, 3} : Elements{type_bytes, 1, 1};
 }
 
-// The time of a tile for 4,096 bytes of the contraction, us.
-double tile_time(int tile, int64_t e) {
-  constexpr double kTimes[2][fn::kHeadTiles] = {{57.0, 17.3, 6.3, 10.0, 16.0},
-                                                {285.0, 72.0, 18.0, 11.0, 18.0}};
-  return kTimes[e == 4][tile];
-}
-
 int64_t tiles_of(int tile, int64_t M, int64_t N) {
   const int64_t m = fn::kHeadTileM[tile], n = fn::kHeadTileN[tile];
   return ((M + m - 1) / m) * ((N + n - 1) / n);
 }
 
-// `tiles` on the device, each with `bytes` of the contraction.
-double rounds_time(int tile, int64_t e, int64_t tiles, int64_t bytes) {
-  return std::ceil((double)tiles / kUnits) * (tile_time(tile, e) * bytes / 4096.0 + 1.5);
+// The time of a product's tiles in us, from measurements on 256 compute units with
+// K of 64 to 8192: a fixed part (first loads, output) and one for every 1,000
+// elements of the contraction, where each unit has one tile or where it has more,
+// two or more of them at once; of 256x256, 128x128 and 64x64 tiles.  What memory
+// gives bounds it from below.
+enum ProductKind { kLogits = 0, kGradients = 1 };
+
+double tiles_time(int tile, ProductKind kind, const Elements& t, int64_t tiles, int64_t M,
+                  int64_t N, int64_t K) {
+  constexpr double kFixed[2][2][3] = {{{9.0, 4.0, 2.0}, {9.0, 2.6, 1.5}},
+                                      {{8.0, 2.7, 1.2}, {8.3, 2.4, 1.3}}};
+  constexpr double kFixedParts[2][2][3] = {{{20.0, 6.0, 4.0}, {20.0, 5.0, 2.5}},
+                                           {{14.0, 7.0, 3.5}, {14.0, 5.0, 2.7}}};
+  constexpr double kEach[3][2][2][3] = {
+      {{{16.6, 8.2, 3.4}, {16.2, 5.0, 2.43}}, {{18.0, 10.0, 5.0}, {18.0, 5.5, 3.1}}},
+      {{{223.0, 62.0, 18.3}, {223.0, 57.5, 15.9}}, {{230.0, 66.0, 23.5}, {230.0, 59.0, 18.0}}},
+      {{{118.0, 47.0, 23.0}, {122.0, 52.0, 15.8}}, {{137.0, 77.0, 41.0}, {137.0, 50.0, 27.0}}}};
+  const int type = t.passes > 1 ? 2 : t.size == 4 ? 1 : 0;
+  const double memory = (double)(M + N) * K * t.size * t.parts / 5.4e6, rounds = (double)tiles / kUnits;
+  if (tile >= 3) {
+    // few rows: up to four narrow or two wide tiles at once
+    const double each = 2.0 + (tile == 3 ? 6.3e-3 : 8e-3) * K * (t.size == 4 ? 2 : 1);
+    return std::max(each * std::ceil(rounds / (tile == 3 ? 4 : 2)), memory);
+  }
+  const int more = tiles > kUnits;
+  const double fixed = type == 2 ? kFixedParts[kind][more][tile] : kFixed[kind][more][tile];
+  return std::max(std::ceil(rounds) * (fixed + kEach[type][kind][more][tile] * 1e-3 * K), memory);
 }
 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
@@ -73,10 +90,9 @@ int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 // of it, by the time they would take.  Up to 16 rows have tiles of their own: the
 // wide ones where they give every compute unit one (1x50000x4096 bf16 with 64 /
 // 128 classes a tile 77 / 71 us, 1x16000x4096 30 / 33).
-Choice choose(int64_t M, int64_t N, int64_t K, const Elements& t, bool splittable,
+Choice choose(ProductKind kind, int64_t M, int64_t N, int64_t K, const Elements& t, bool splittable,
               bool few_rows = true) {
-  const int64_t e = t.size;
-  const int64_t stage = fn::kStageRow / e;
+  const int64_t stage = fn::kStageRow / t.size;
   Choice best;
   best.cost = 1e300;
   const bool few = few_rows && M <= 16;
@@ -87,9 +103,9 @@ Choice choose(int64_t M, int64_t N, int64_t K, const Elements& t, bool splittabl
     for (int splits = 1; splits <= 64; splits *= 2) {
       if (splits > 1 && (!splittable || K < 8 * stage * splits || tiles * splits > 4 * kUnits)) break;
       const int64_t K_split = std::max(round_up((K + splits - 1) / splits, stage), stage);
-      double cost = 3.0 + rounds_time(tile, e, tiles * splits, K_split * e * t.passes);
+      double cost = 3.0 + tiles_time(tile, kind, t, tiles * splits, M, N, K_split);
       // partial products are written and read again, in a launch of their own
-      if (splits > 1) cost += 3.0 + (double)M * N * 8.0 * splits / 4e6;
+      if (splits > 1) cost += 4.0 + 0.1 * splits + (double)M * N * 8.0 * splits / 4e6;
       if (cost < best.cost) best = {tile, splits, K_split, cost};
     }
   }
@@ -145,12 +161,17 @@ int64_t piece_of(int64_t rows, int64_t most) {
 }
 
 // fp32 operands in parts, if six products of bf16 and the copies (ten bytes an
-// element) take less time than one of fp32 (1999x21841x1021: TIMES).
+// element) take less time than one of fp32 (1999x21841x1021: 490 us against 730).
 bool worth_parts(int64_t rows, int64_t classes, int32_t width, bool backward) {
-  const double copies = 6.0 + (double)(rows + classes) * width * 10.0 / 4e6;
-  const int products = backward ? 3 : 1;
-  return copies + products * choose(rows, classes, width, elements_of(4, true), false).cost <
-         products * choose(rows, classes, width, elements_of(4, false), false).cost;
+  double cost[2] = {0.0, 6.0 + (double)(rows + classes) * width * 10.0 / 4e6};
+  for (int split = 0; split < 2; ++split) {
+    const Elements t = elements_of(4, split);
+    cost[split] += choose(kLogits, rows, classes, width, t, false).cost;
+    if (backward)
+      cost[split] += choose(kGradients, rows, width, classes, t, true).cost +
+                     choose(kGradients, classes, width, rows, t, true, false).cost;
+  }
+  return cost[1] < cost[0];
 }
 
 Plan plan_of(int64_t rows, int64_t classes, int32_t width, int64_t e, bool pack_x, bool pack_w,
@@ -177,8 +198,8 @@ Plan plan_of(int64_t rows, int64_t classes, int32_t width, int64_t e, bool pack_
     // whole rounds of tiles first and the rest in smaller ones, if that is less
     const int64_t piece = piece_of(rows, classes / 256 * 256);
     if (piece > 0 && piece < classes &&
-        choose(rows, piece, K, t, false).cost + choose(rows, classes - piece, K, t, false).cost <
-            choose(rows, classes, K, t, false).cost)
+        choose(kLogits, rows, piece, K, t, false).cost + choose(kLogits, rows, classes - piece, K, t, false).cost <
+            choose(kLogits, rows, classes, K, t, false).cost)
       p.piece = piece;
   }
   p.pieces = (classes + p.piece - 1) / p.piece;
@@ -187,7 +208,7 @@ Plan plan_of(int64_t rows, int64_t classes, int32_t width, int64_t e, bool pack_
   p.scale = parts.take(8);
   if (p.pack_x) p.x = parts.take(rows * p.width_packed * bytes);
   if (p.pack_w) p.w = parts.take(p.piece * p.width_packed * bytes);
-  for (int k = 0; k < 2; ++k) p.logits[k] = choose(rows, counts[k], K, t, false);
+  for (int k = 0; k < 2; ++k) p.logits[k] = choose(kLogits, rows, counts[k], K, t, false);
   if (!backward) {
     p.stat_tiles = (p.pieces - 1) * class_tiles(p.logits[0], p.piece) +
                    class_tiles(p.logits[p.which(counts[1])], counts[1]);
@@ -204,8 +225,8 @@ Plan plan_of(int64_t rows, int64_t classes, int32_t width, int64_t e, bool pack_
   for (int k = 0; k < 2; ++k) {
     // dx's sums of the first piece fill every split's place, a later one may
     // use fewer
-    p.dx[k] = choose(rows, width, counts[k], t, k == 0);
-    p.dw[k] = choose(counts[k], width, rows, t, true, false);
+    p.dx[k] = choose(kGradients, rows, width, counts[k], t, k == 0);
+    p.dw[k] = choose(kGradients, counts[k], width, rows, t, true, false);
     bias_rows = std::max(bias_rows, bias_rows_of(p.logits[k], rows));
     if (p.dw[k].splits > 1) dw_rows = std::max(dw_rows, p.dw[k].splits * counts[k]);
   }
@@ -213,11 +234,16 @@ Plan plan_of(int64_t rows, int64_t classes, int32_t width, int64_t e, bool pack_
   if (p.pieces == 1 && rows > 0) {
     double least = p.dx[0].cost + p.dw[0].cost;
     for (int tile = 1; tile < 3; ++tile) {
-      const int64_t tiles = tiles_of(tile, rows, width) + tiles_of(tile, classes, width);
+      const int64_t dx = tiles_of(tile, rows, width), dw = tiles_of(tile, classes, width);
+      if (dx + dw >= (int64_t)1 << 22) continue;
+      // side by side: as if all were of either kind, by their share
       const double cost =
-          3.0 + rounds_time(tile, t.size, tiles, std::max(rows, classes) * t.size * t.passes);
-      if (tiles < (int64_t)1 << 22 && cost < least) {
-        least = cost;
+          3.0 + (dx * tiles_time(tile, kGradients, t, dx + dw, rows, width, classes) +
+                 dw * tiles_time(tile, kGradients, t, dx + dw, classes, width, rows)) /
+                    (dx + dw);
+      const double longest = 3.0 + tiles_time(tile, kGradients, t, 1, 1, 1, std::max(rows, classes));
+      if (std::max(cost, longest) < least) {
+        least = std::max(cost, longest);
         p.pair_tile = tile;
       }
     }
@@ -258,14 +284,21 @@ fn::Operand operand(const void* from, int64_t stride, int64_t rows, int32_t widt
   constexpr int64_t e = sizeof(Element);
   if (copy == nullptr) return {(const char*)from, stride * e, rows, (int64_t)width * e, 0};
   const fn::Operand o = {copy, copied * e, rows, copied * e, rows * copied * e};
-  if (rows == 0) return o;
-  const dim3 grid(blocks_for(copied * e / 16, 256), (unsigned)std::min<int64_t>(rows, 65535));
-  if constexpr (std::is_same_v<T, fn::Fp32Parts>)
-    fn::loss_parts_kernel<<<grid, 256, 0, st>>>((const float*)from, stride, rows, width,
-                                                (Element*)copy, (int32_t)copied, rows * copied);
-  else
-    fn::loss_pack_kernel<T><<<grid, 256, 0, st>>>((const T*)from, stride, rows, width, (T*)copy,
-                                                  (int32_t)copied);
+  using Given = typename fn::HeadType<T>::Output;
+  const fn::Division pieces = fn::division_by((uint32_t)(copied * e / 16));
+  // at most 2^31 threads to a launch
+  const int64_t most = ((int64_t)1 << 31) / pieces.by;
+  for (int64_t row = 0; row < rows; row += most) {
+    const uint32_t items = (uint32_t)(std::min(most, rows - row) * pieces.by);
+    const Given* x = (const Given*)from + row * stride;
+    Element* to = (Element*)copy + row * copied;
+    if constexpr (std::is_same_v<T, fn::Fp32Parts>)
+      fn::loss_parts_kernel<<<blocks_for(items, 256), 256, 0, st>>>(x, stride, items, pieces, width,
+                                                                    to, rows * copied);
+    else
+      fn::loss_pack_kernel<T><<<blocks_for(items, 256), 256, 0, st>>>(x, stride, items, pieces,
+                                                                      width, to);
+  }
   return o;
 }
 
@@ -366,12 +399,17 @@ struct Gradients {
 template <typename T>
 int round_sums(const float* sums, const Plan& p, int64_t split_stride, int splits, int64_t rows,
                int32_t width, const float* scale, T* out, int64_t out_stride, hipStream_t st) {
-  if (rows == 0) return FN_OK;
-  const dim3 grid(blocks_for(((int64_t)width + 3) / 4, 256),
-                  (unsigned)std::min<int64_t>(rows, 65535));
-  fn::loss_round_kernel<T><<<grid, 256, 0, st>>>(sums, p.sum_pitch, split_stride, splits, rows,
-                                                 width, scale, out, out_stride);
-  return launch_status("loss_round_kernel launch");
+  const fn::Division vectors = fn::division_by((uint32_t)((width + 3) / 4));
+  // at most 2^31 threads to a launch
+  const int64_t most = ((int64_t)1 << 31) / vectors.by;
+  for (int64_t row = 0; row < rows; row += most) {
+    const uint32_t items = (uint32_t)(std::min(most, rows - row) * vectors.by);
+    fn::loss_round_kernel<T><<<blocks_for(items, 256), 256, 0, st>>>(
+        sums + row * p.sum_pitch, p.sum_pitch, split_stride, splits, items, vectors, width, scale,
+        out + row * out_stride, out_stride);
+    FN_TRY(launch_status("loss_round_kernel launch"));
+  }
+  return FN_OK;
 }
 
 template <typename T>

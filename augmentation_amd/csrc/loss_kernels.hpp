@@ -46,6 +46,12 @@ __device__ __forceinline__ float exp_below(float v) {
   return v < -200.0f ? 0.0f : __builtin_fmaf(e, r * kLn2, e);
 }
 
+// The same without the correction: off by 2^-24 |v| log2(e) relative.  For sums, in
+// which large |v| count little, and for what is rounded to 16 bits.
+__device__ __forceinline__ float exp_roughly(float v) {
+  return __builtin_amdgcn_exp2f(v * 0x1.715476p+0f);
+}
+
 // A fragment is 16 bytes of a lane: eight 16-bit numbers or four fp32 ones of
 // one row, of the contraction's 32 or 16 that a step takes.
 template <typename T>
@@ -644,33 +650,56 @@ struct HeadTile {
       Tile::store([&](int i, int j, int c) { return acc[i][j][c] * scale; }, own, (Out*)p.out,
                   p.out_stride, m0 + m_wave, n0 + n_wave, p.M, p.N);
     } else {
-      // the logits
+      // The logits.  What follows is 128 elements a lane in the largest tile, so it
+      // counts by the instruction: bias, the edge of the classes and targets are
+      // looked at only where there are any (8192x50000x4096 bf16 TIMES).
+      if (p.bias != nullptr) {
 #pragma unroll
-      for (int j = 0; j < kTN; ++j)
+        for (int j = 0; j < kTN; ++j)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float bias = s_bias[n_wave + 4 * (lane >> 4) + 16 * j + c];
+          for (int c = 0; c < 4; ++c) {
+            const float bias = s_bias[n_wave + 4 * (lane >> 4) + 16 * j + c];
 #pragma unroll
-          for (int i = 0; i < kTM; ++i) acc[i][j][c] += bias;
-        }
+            for (int i = 0; i < kTM; ++i) acc[i][j][c] += bias;
+          }
+      }
+      const bool edge = n0 + kBN > p.N;
       if constexpr (kOutput == kHeadStatistics) {
         // of the work-group's rows in each column of wavefronts
         float* s_top = reinterpret_cast<float*>(s_stages);
         float* s_sum = s_top + kWN * kBM;
         float* s_all = s_sum + kWN * kBM;
         float* s_z = s_all + kWN * kBM;
+        const int slot = (wave % kWN) * kBM + m_wave + (lane & 15);
+        if (p.smoothing > 0.0f) {
 #pragma unroll
-        for (int i = 0; i < kTM; ++i) {
-          const int64_t m = m_lane + 16 * i;
-          float top = kMinusInfinity, all = 0.0f;
+          for (int i = 0; i < kTM; ++i) {
+            float all = 0.0f;
+#pragma unroll
+            for (int j = 0; j < kTN; ++j)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) all += 16 * j + c < columns ? acc[i][j][c] : 0.0f;
+            all = fold_row(all, [](float x, float y) { return x + y; });
+            if ((lane >> 4) == 0) s_all[slot + 16 * i] = all;
+          }
+        }
+        if (edge) {
 #pragma unroll
           for (int j = 0; j < kTN; ++j)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              if (16 * j + c < columns) {
-                top = fmaxf(top, acc[i][j][c]);
-                all += acc[i][j][c];
-              }
+#pragma unroll
+              for (int i = 0; i < kTM; ++i)
+                acc[i][j][c] = 16 * j + c < columns ? acc[i][j][c] : kMinusInfinity;
+        }
+#pragma unroll
+        for (int i = 0; i < kTM; ++i) {
+          const int64_t m = m_lane + 16 * i;
+          float top = kMinusInfinity;
+#pragma unroll
+          for (int j = 0; j < kTN; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) top = fmaxf(top, acc[i][j][c]);
           top = fold_row(top, [](float x, float y) { return fmaxf(x, y); });
           // a row of which nothing is left has no exponentials
           const float base = top == kMinusInfinity ? 0.0f : top;
@@ -678,18 +707,14 @@ struct HeadTile {
 #pragma unroll
           for (int j = 0; j < kTN; ++j)
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              sum += 16 * j + c < columns ? exp_below(acc[i][j][c] - base) : 0.0f;
+            for (int c = 0; c < 4; ++c) sum += exp_roughly(acc[i][j][c] - base);
           sum = fold_row(sum, [](float x, float y) { return x + y; });
-          if (p.sums != nullptr) all = fold_row(all, [](float x, float y) { return x + y; });
           if ((lane >> 4) == 0) {
-            const int at = (wave % kWN) * kBM + m_wave + 16 * i + (lane & 15);
-            s_top[at] = top;
-            s_sum[at] = sum;
-            s_all[at] = all;
+            s_top[slot + 16 * i] = top;
+            s_sum[slot + 16 * i] = sum;
           }
-          if (m < p.M) {
-            const int target = target_of(s_target[m_wave + 16 * i + (lane & 15)]);
+          const int target = m < p.M ? target_of(s_target[m_wave + 16 * i + (lane & 15)]) : -1;
+          if (__any(target >= 0)) {
 #pragma unroll
             for (int j = 0; j < kTN; ++j)
 #pragma unroll
@@ -714,7 +739,7 @@ struct HeadTile {
 #pragma unroll
           for (int w = 0; w < kWN; ++w) {
             sum += s_sum[w * kBM + r] * exp_below(s_top[w * kBM + r] - base);
-            all += s_all[w * kBM + r];
+            if (p.smoothing > 0.0f) all += s_all[w * kBM + r];
           }
           if (p.losses != nullptr) {
             const int64_t y = s_target[r];
@@ -731,6 +756,8 @@ struct HeadTile {
         }
       } else {
         const float even = p.smoothing / (float)p.classes;
+        // what is rounded to 16 bits needs no exponential of 24
+        constexpr bool kRoughly = sizeof(typename Type::Output) == 2;
 #pragma unroll
         for (int i = 0; i < kTM; ++i) {
           const int64_t m = m_lane + 16 * i;
@@ -744,10 +771,29 @@ struct HeadTile {
           for (int j = 0; j < kTN; ++j)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              float g = exp_below(acc[i][j][c] - lse) - even;
-              if (target == 16 * j + c) g -= 1.0f - p.smoothing;
-              acc[i][j][c] = counts && 16 * j + c < columns ? g * dloss : 0.0f;
+              const float v = acc[i][j][c] - lse;
+              acc[i][j][c] = (kRoughly ? exp_roughly(v) : exp_below(v)) - even;
             }
+          if (__any(target >= 0)) {
+#pragma unroll
+            for (int j = 0; j < kTN; ++j)
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                if (target == 16 * j + c) acc[i][j][c] -= 1.0f - p.smoothing;
+          }
+#pragma unroll
+          for (int j = 0; j < kTN; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[i][j][c] = counts ? acc[i][j][c] * dloss : 0.0f;
+        }
+        if (edge) {
+#pragma unroll
+          for (int j = 0; j < kTN; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int i = 0; i < kTM; ++i)
+                acc[i][j][c] = 16 * j + c < columns ? acc[i][j][c] : 0.0f;
         }
         if (p.bias_sums != nullptr) {
           // a wavefront's rows, then the sixteen lanes that hold a column

@@ -81,85 +81,86 @@ __global__ __launch_bounds__(1024) void loss_scale_kernel(const float* dlosses, 
 template <typename T>
 __global__ __launch_bounds__(256) void loss_round_kernel(const float* sums, int64_t pitch,
                                                          int64_t split_stride, int splits,
-                                                         int64_t rows, int64_t width,
-                                                         const float* scale, T* out,
+                                                         uint32_t items, Division vectors,
+                                                         int32_t width, const float* scale, T* out,
                                                          int64_t out_stride) {
-  const int64_t n = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (n >= width) return;
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  if (i >= items) return;
+  const uint32_t m = quotient(i, vectors);
+  const int32_t n = 4 * (int32_t)(i - m * vectors.by);
   const float by = scale != nullptr ? scale[1] : 1.0f;
-  for (int64_t m = blockIdx.y; m < rows; m += gridDim.y) {
-    const float* from = sums + m * pitch + n;
-    f32x4 v = *reinterpret_cast<const f32x4*>(from);
-    for (int s = 1; s < splits; ++s)
-      v += *reinterpret_cast<const f32x4*>(from + s * split_stride);
-    T* to = out + m * out_stride + n;
+  const float* from = sums + m * pitch + n;
+  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 16
+  for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4*>(from + s * split_stride);
+  T* to = out + m * out_stride + n;
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (n + c < width) {
-        if constexpr (sizeof(T) == 4)
-          to[c] = v[c] * by;
-        else
-          reinterpret_cast<uint16_t*>(to)[c] = (uint16_t)two_halves<T>(v[c] * by, 0.0f);
-      }
-  }
+  for (int c = 0; c < 4; ++c)
+    if (n + c < width) {
+      if constexpr (sizeof(T) == 4)
+        to[c] = v[c] * by;
+      else
+        reinterpret_cast<uint16_t*>(to)[c] = (uint16_t)two_halves<T>(v[c] * by, 0.0f);
+    }
 }
 
 // Rows of any alignment to rows of whole 16-byte pieces, zeros at their ends: a
 // thread takes a piece.
 template <typename T>
-__global__ __launch_bounds__(256) void loss_pack_kernel(const T* from, int64_t stride, int64_t rows,
-                                                        int32_t width, T* to, int32_t pitch) {
+__global__ __launch_bounds__(256) void loss_pack_kernel(const T* from, int64_t stride,
+                                                        uint32_t items, Division pieces,
+                                                        int32_t width, T* to) {
   constexpr int kE = 16 / (int)sizeof(T);
-  const int32_t c = (int32_t)(blockIdx.x * 256 + threadIdx.x) * kE;
-  if (c >= pitch) return;
-  for (int64_t m = blockIdx.y; m < rows; m += gridDim.y) {
-    const T* row = from + m * stride;
-    u32x4 v = {0, 0, 0, 0};
-    if (c + kE <= width) {
-      v = *reinterpret_cast<const u32x4_any*>(row + c);
-    } else {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  if (i >= items) return;
+  const uint32_t m = quotient(i, pieces);
+  const int32_t c = kE * (int32_t)(i - m * pieces.by);
+  const T* row = from + m * stride;
+  u32x4 v = {0, 0, 0, 0};
+  if (c + kE <= width) {
+    v = *reinterpret_cast<const u32x4_any*>(row + c);
+  } else {
 #pragma unroll
-      for (int j = 0; j < kE; ++j)
-        if (c + j < width) {
-          if constexpr (sizeof(T) == 4)
-            v[j] = __builtin_bit_cast(uint32_t, row[c + j]);
-          else
-            v[j >> 1] |= (uint32_t)__builtin_bit_cast(uint16_t, row[c + j]) << (16 * (j & 1));
-        }
-    }
-    *reinterpret_cast<u32x4*>(to + m * pitch + c) = v;
+    for (int j = 0; j < kE; ++j)
+      if (c + j < width) {
+        if constexpr (sizeof(T) == 4)
+          v[j] = __builtin_bit_cast(uint32_t, row[c + j]);
+        else
+          v[j >> 1] |= (uint32_t)__builtin_bit_cast(uint16_t, row[c + j]) << (16 * (j & 1));
+      }
   }
+  *reinterpret_cast<u32x4*>(to + (int64_t)i * kE) = v;
 }
 
 // The three parts of fp32 rows (see Fp32Parts), zeros at their rows' ends: a
 // thread takes eight numbers.
 __global__ __launch_bounds__(256) void loss_parts_kernel(const float* from, int64_t stride,
-                                                         int64_t rows, int32_t width, BF16* to,
-                                                         int32_t pitch, int64_t part) {
-  const int32_t c = (int32_t)(blockIdx.x * 256 + threadIdx.x) * 8;
-  if (c >= pitch) return;
-  for (int64_t m = blockIdx.y; m < rows; m += gridDim.y) {
-    const float* row = from + m * stride + c;
-    Vec8<float> v;
-    if (c + 8 <= width)
-      v.load(row);
-    else
-      v.load_some(row, width - c);
-    float left[8];
+                                                         uint32_t items, Division pieces,
+                                                         int32_t width, BF16* to, int64_t part) {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  if (i >= items) return;
+  const uint32_t m = quotient(i, pieces);
+  const int32_t c = 8 * (int32_t)(i - m * pieces.by);
+  const float* row = from + m * stride + c;
+  Vec8<float> v;
+  if (c + 8 <= width)
+    v.load(row);
+  else
+    v.load_some(row, width - c);
+  float left[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) left[j] = v.get(j);
+  for (int j = 0; j < 8; ++j) left[j] = v.get(j);
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      u32x4 w;
+  for (int k = 0; k < 3; ++k) {
+    u32x4 w;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t lo = float_to_bf16(left[2 * j]), hi = float_to_bf16(left[2 * j + 1]);
-        w[j] = lo | hi << 16;
-        left[2 * j] -= bf16_to_float(lo);
-        left[2 * j + 1] -= bf16_to_float(hi);
-      }
-      *reinterpret_cast<u32x4*>(to + k * part + m * pitch + c) = w;
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t lo = float_to_bf16(left[2 * j]), hi = float_to_bf16(left[2 * j + 1]);
+      w[j] = lo | hi << 16;
+      left[2 * j] -= bf16_to_float(lo);
+      left[2 * j + 1] -= bf16_to_float(hi);
     }
+    *reinterpret_cast<u32x4*>(to + k * part + (int64_t)i * 8) = w;
   }
 }
 

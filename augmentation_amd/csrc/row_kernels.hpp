@@ -48,6 +48,25 @@ struct RowArgs {
   float eps;
 };
 
+// n / by for any 32-bit n, from the upper half of its product with
+// floor(2^32 (2^l - by) / by) + 1, l = ceil(log2 by), which is 2^(32 + l) / by
+// rounded up without its top bit (Granlund and Montgomery 1994).
+struct Division {
+  uint32_t by, magic, shift;  // shift = l - 1; by = 1 takes no division
+};
+
+inline Division division_by(uint32_t by) {
+  if (by <= 1) return {1, 0, 0};
+  const int l = 32 - __builtin_clz(by - 1);
+  return {by, (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << l) - by)) / by + 1),
+          (uint32_t)(l - 1)};
+}
+
+__device__ __forceinline__ uint32_t quotient(uint32_t n, const Division& d) {
+  const uint32_t t = __umulhi(n, d.magic);
+  return d.by == 1 ? n : (((n - t) >> 1) + t) >> d.shift;
+}
+
 // ------------------------------------------------------------- vector access
 // Eight consecutive elements, at any alignment of the element's size: the
 // hardware's global loads and stores take unaligned addresses.  Rows are met

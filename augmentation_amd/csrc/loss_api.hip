@@ -74,10 +74,12 @@ double tiles_time(int tile, ProductKind kind, const Elements& t, int64_t tiles, 
       {{{118.0, 47.0, 23.0}, {122.0, 52.0, 15.8}}, {{137.0, 77.0, 41.0}, {137.0, 50.0, 27.0}}}};
   const int type = t.passes > 1 ? 2 : t.size == 4 ? 1 : 0;
   const double memory = (double)(M + N) * K * t.size * t.parts / 5.4e6, rounds = (double)tiles / kUnits;
-  if (tile >= 3) {
-    // few rows: up to four narrow or two wide tiles at once
-    const double each = 2.0 + (tile == 3 ? 6.3e-3 : 8e-3) * K * (t.size == 4 ? 2 : 1);
-    return std::max(each * std::ceil(rounds / (tile == 3 ? 4 : 2)), memory);
+  if (tile == 4) return std::max((2.0 + 8e-3 * K * (t.size == 4 ? 2 : 1)) * std::ceil(rounds / 2), memory);
+  if (tile == 3) {
+    constexpr double kNarrow[3][3] = {{4.0, 2.4, 2.3}, {10.5, 6.3, 7.0}, {19.0, 13.5, 14.0}};
+    const bool groups = fn::in_groups(tile, tiles, K);
+    const double each = kNarrow[type][groups ? 1 : tiles > kUnits ? 2 : 0] * 1e-3 * K;
+    return std::max(std::ceil(rounds) * ((groups ? 3.5 : 1.5) + each), memory);
   }
   const int more = tiles > kUnits;
   const double fixed = type == 2 ? kFixedParts[kind][more][tile] : kFixed[kind][more][tile];
@@ -87,18 +89,20 @@ double tiles_time(int tile, ProductKind kind, const Elements& t, int64_t tiles, 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 // The tile and the splits of the contraction for M x N outputs and K elements
-// of it, by the time they would take.  Up to 16 rows have tiles of their own: the
-// wide ones where they give every compute unit one (1x50000x4096 bf16 with 64 /
-// 128 classes a tile 77 / 71 us, 1x16000x4096 30 / 33).
+// of it, by the time they would take.  Up to 16 rows have tiles of 16: the wide
+// ones where they give every compute unit one (1x50000x4096 bf16 with 64 / 128
+// classes a tile 77 / 71 us, 1x16000x4096 30 / 33); more rows have the narrow ones
+// where they are few.  `few_rows`: whether there are kernels for those.
 Choice choose(ProductKind kind, int64_t M, int64_t N, int64_t K, const Elements& t, bool splittable,
               bool few_rows = true) {
   const int64_t stage = fn::kStageRow / t.size;
   Choice best;
   best.cost = 1e300;
   const bool few = few_rows && M <= 16;
-  const int first = !few ? 0 : N >= 128 * kUnits ? 4 : 3;
-  for (int tile = first; tile < (few ? first + 1 : 3); ++tile) {
+  const int first = !few ? 0 : N >= 128 * kUnits ? 4 : 3, last = few ? first : few_rows ? 3 : 2;
+  for (int tile = first; tile <= last; ++tile) {
     const int64_t tiles = tiles_of(tile, M, N);
+    if (tile == 3 && !few && tiles > kUnits) continue;
     if (tiles >= (int64_t)1 << 22) continue;  // 2^32 threads to a launch
     for (int splits = 1; splits <= 64; splits *= 2) {
       if (splits > 1 && (!splittable || K < 8 * stage * splits || tiles * splits > 4 * kUnits)) break;

@@ -449,8 +449,14 @@ __device__ __forceinline__ Scale find_scale(const float* dlosses, int64_t stride
 // stages of 128 bytes of the contraction on their way, as in
 // product_tile_kernel: between the products of a step stand, one at a time, the
 // reads of the next step's fragments and the loads of a later stage.
+//
+// kGroups: sets of wavefronts that divide the contraction, each with stages of its
+// own; their sums are joined in LDS.  A small tile's stage is a chain of waits
+// (barrier, reads, products) several times as long as its products, and where a
+// compute unit has one tile alone, others shall fill them (16x64 tiles of 8192
+// elements, one to a unit, with one group / four: bf16 34 / 24 us, fp32 90 / 57).
 template <typename T, int kOutput, bool kAcrossA, bool kAcrossB, int kBM, int kBN, int kWM, int kWN,
-          int kStages>
+          int kStages, int kGroups = 1>
 struct HeadTile {
   static constexpr int kWaves = kWM * kWN, kTM = kBM / kWM / 16, kTN = kBN / kWN / 16;
   static constexpr int kStageBytes = (kBM + kBN) * kStageRow;
@@ -468,8 +474,10 @@ struct HeadTile {
   static constexpr int kLoadsA = StagerA::kLoads, kLoads = kLoadsA + StagerB::kLoads;
   static constexpr int kStageK = StagerA::kStageK, kSteps = 2;
   static constexpr int kOutBytes = kWaves * Tile::kBytes;
+  static constexpr int kGroupBytes = kStages * kStageBytes;
   static constexpr int kMainBytes =
-      kStages * kStageBytes > kOutBytes ? kStages * kStageBytes : kOutBytes;
+      kGroups * kGroupBytes > kOutBytes ? kGroups * kGroupBytes : kOutBytes;
+  static constexpr int kThreads = 64 * kWaves * kGroups;
   // what the logits need beside: bias, lse, dlosses, targets, a word for each
   // wavefront
   static constexpr bool kSides = kOutput == kHeadStatistics || kOutput == kHeadGradient;
@@ -481,17 +489,28 @@ struct HeadTile {
   static __device__ __forceinline__ void run(const HeadArgs& p, uint32_t block, uint32_t split,
                                              int8_t* s_stages) {
     const int lane = (int)(threadIdx.x & 63u);
-    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int wave_of_all = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int wave = wave_of_all % kWaves, group = wave_of_all / kWaves;
+    const bool first_group = kGroups == 1 || group == 0;
 
     const TileAt tile = head_tile_at(block, p);
     const int64_t m0 = (int64_t)tile.m * kBM, n0 = (int64_t)tile.n * kBN;
-    const int64_t k_begin = (int64_t)split * p.K_split;
+    // the split's part of the contraction and the group's part of that: the same
+    // number of stages for every group, zeros beyond k_end
+    int64_t k_begin = (int64_t)split * p.K_split;
     const int64_t k_end = min(k_begin + p.K_split, p.K);
+    const int pass_stages =
+        k_end > k_begin
+            ? (int)((k_end - k_begin + kGroups * kStageK - 1) / (kGroups * kStageK))
+            : 0;
+    k_begin += (int64_t)group * pass_stages * kStageK;
+    const int64_t pass_end = k_begin + (int64_t)pass_stages * kStageK;
     StagerA sa;
     StagerB sb;
     sa.start(p.a, m0, wave, (wave / kWN) * kTM);
     sb.start(p.b, n0, wave, (wave % kWN) * kTN);
     const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)s_stages;
+    int8_t* const s_group = s_stages + group * kGroupBytes;
     struct Next {
       typename StagerA::Stage a;
       typename StagerB::Stage b;
@@ -501,7 +520,7 @@ struct HeadTile {
     auto next_of = [&]() {
       const Next next = {sa.stage(walk, k_end), sb.stage(walk, k_end)};
       walk.k += kStageK;
-      if (kPasses > 1 && walk.k >= k_end) {
+      if (kPasses > 1 && walk.k >= pass_end) {
         // (beyond the last pass comes the first element again, for nothing)
         walk.k = k_begin;
         ++walk.pass;
@@ -509,7 +528,7 @@ struct HeadTile {
       return next;
     };
     auto issue = [&](int stage, int i, const Next& next) {
-      const uint32_t to = lds + stage * kStageBytes;
+      const uint32_t to = lds + group * kGroupBytes + stage * kStageBytes;
       if (i < kLoadsA)
         sa.load(next.a, to, wave, i, false);
       else
@@ -529,7 +548,7 @@ struct HeadTile {
     const float* const s_bias = reinterpret_cast<const float*>(s_stages + kMainBytes);
     const float *const s_lse = s_bias + kBN, *const s_dloss = s_lse + kSideM;
     const int64_t* const s_target = reinterpret_cast<const int64_t*>(s_dloss + kSideM);
-    if constexpr (kSides) {
+    if (kSides && first_group) {
       auto words = [&](const void* from, int64_t first, int64_t count, int64_t size, int to) {
         // `count` words of `size` from the first one on, zeros behind them
         const int64_t here = from != nullptr ? max(count - first, (int64_t)0) : 0;
@@ -553,7 +572,7 @@ struct HeadTile {
     Scale scale = {1.0f, 1.0f};
     if constexpr (kOutput == kHeadGradient) {
       if (p.scale_to > 0.0f) {
-        scale = find_scale<64 * kWaves>(
+        scale = find_scale<kThreads>(
             p.dlosses, p.dloss_stride, p.M, p.scale_to,
             reinterpret_cast<uint32_t*>(s_stages + kMainBytes) + kBN + 4 * kSideM);
         if (block == 0 && threadIdx.x == 0) {
@@ -568,18 +587,16 @@ struct HeadTile {
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < kTM + kTN; ++i) fetch(s_stages, 0, 0, i);
+    for (int i = 0; i < kTM + kTN; ++i) fetch(s_group, 0, 0, i);
     int stage = 0;
-    const int stages =
-        k_end > k_begin ? kPasses * (int)((k_end - k_begin + kStageK - 1) / kStageK) : 0;
-    for (int left = stages; left > 0; --left) {
+    for (int left = kPasses * pass_stages; left > 0; --left) {
       const int after = stage + 1 == kStages ? 0 : stage + 1;
       static_for<kSteps>([&](auto step) {
         constexpr int k = decltype(step)::value;
         constexpr bool kLast = k + 1 == kSteps;
         constexpr int kProducts = kTM * kTN, kReads = kTM + kTN, kNewLoads = kLast ? kLoads : 0;
         constexpr int kOthers = kReads + kNewLoads;
-        const int8_t* from = s_stages + (kLast ? after : stage) * kStageBytes;
+        const int8_t* from = s_group + (kLast ? after : stage) * kStageBytes;
         Next next;
         if constexpr (kLast) {
           // this wavefront's loads of the next stage have landed and its reads
@@ -620,6 +637,30 @@ struct HeadTile {
     // again
     wait_loads<0>();
     __syncthreads();
+    if constexpr (kGroups > 1) {
+      // in the groups' order
+      static_assert((kGroups - 1) * kWaves * kTM * kTN * 1024 <= kMainBytes, "room for the sums");
+      f32x4* s_sums = reinterpret_cast<f32x4*>(s_stages) + wave * kTM * kTN * 64 + lane;
+      constexpr int kOfGroup = kWaves * kTM * kTN * 64;
+      if (!first_group) {
+#pragma unroll
+        for (int i = 0; i < kTM; ++i)
+#pragma unroll
+          for (int j = 0; j < kTN; ++j)
+            s_sums[(group - 1) * kOfGroup + (i * kTN + j) * 64] = acc[i][j];
+      }
+      __syncthreads();
+      if (first_group) {
+#pragma unroll
+        for (int g = 1; g < kGroups; ++g)
+#pragma unroll
+          for (int i = 0; i < kTM; ++i)
+#pragma unroll
+            for (int j = 0; j < kTN; ++j)
+              acc[i][j] += s_sums[(g - 1) * kOfGroup + (i * kTN + j) * 64];
+      }
+      __syncthreads();
+    }
 
     const int m_wave = (wave / kWN) * kTM * 16, n_wave = (wave % kWN) * kTN * 16;
     const int64_t m_lane = m0 + m_wave + (lane & 15), n_lane = n0 + n_wave + 4 * (lane >> 4);
@@ -633,6 +674,7 @@ struct HeadTile {
     };
 
     if constexpr (kOutput == kHeadSums) {
+      if (!first_group) return;
       float* out = (float*)p.out + (int64_t)split * p.split_stride;
 #pragma unroll
       for (int i = 0; i < kTM; ++i)
@@ -646,6 +688,7 @@ struct HeadTile {
           }
         }
     } else if constexpr (kOutput == kHeadRounded) {
+      if (!first_group) return;
       const float scale = p.scale != nullptr ? p.scale[1] : 1.0f;
       Tile::store([&](int i, int j, int c) { return acc[i][j][c] * scale; }, own, (Out*)p.out,
                   p.out_stride, m0 + m_wave, n0 + n_wave, p.M, p.N);
@@ -653,7 +696,7 @@ struct HeadTile {
       // The logits.  What follows is 128 elements a lane in the largest tile, so it
       // counts by the instruction: bias, the edge of the classes and targets are
       // looked at only where there are any (8192x50000x4096 bf16 TIMES).
-      if (p.bias != nullptr) {
+      if (p.bias != nullptr && first_group) {
 #pragma unroll
         for (int j = 0; j < kTN; ++j)
 #pragma unroll
@@ -671,64 +714,66 @@ struct HeadTile {
         float* s_all = s_sum + kWN * kBM;
         float* s_z = s_all + kWN * kBM;
         const int slot = (wave % kWN) * kBM + m_wave + (lane & 15);
-        if (p.smoothing > 0.0f) {
+        if (first_group) {
+          if (p.smoothing > 0.0f) {
 #pragma unroll
-          for (int i = 0; i < kTM; ++i) {
-            float all = 0.0f;
+            for (int i = 0; i < kTM; ++i) {
+              float all = 0.0f;
 #pragma unroll
-            for (int j = 0; j < kTN; ++j)
+              for (int j = 0; j < kTN; ++j)
 #pragma unroll
-              for (int c = 0; c < 4; ++c) all += 16 * j + c < columns ? acc[i][j][c] : 0.0f;
-            all = fold_row(all, [](float x, float y) { return x + y; });
-            if ((lane >> 4) == 0) s_all[slot + 16 * i] = all;
+                for (int c = 0; c < 4; ++c) all += 16 * j + c < columns ? acc[i][j][c] : 0.0f;
+              all = fold_row(all, [](float x, float y) { return x + y; });
+              if ((lane >> 4) == 0) s_all[slot + 16 * i] = all;
+            }
           }
-        }
-        if (edge) {
-#pragma unroll
-          for (int j = 0; j < kTN; ++j)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int i = 0; i < kTM; ++i)
-                acc[i][j][c] = 16 * j + c < columns ? acc[i][j][c] : kMinusInfinity;
-        }
-#pragma unroll
-        for (int i = 0; i < kTM; ++i) {
-          const int64_t m = m_lane + 16 * i;
-          float top = kMinusInfinity;
-#pragma unroll
-          for (int j = 0; j < kTN; ++j)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) top = fmaxf(top, acc[i][j][c]);
-          top = fold_row(top, [](float x, float y) { return fmaxf(x, y); });
-          // a row of which nothing is left has no exponentials
-          const float base = top == kMinusInfinity ? 0.0f : top;
-          float sum = 0.0f;
-#pragma unroll
-          for (int j = 0; j < kTN; ++j)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) sum += exp_roughly(acc[i][j][c] - base);
-          sum = fold_row(sum, [](float x, float y) { return x + y; });
-          if ((lane >> 4) == 0) {
-            s_top[slot + 16 * i] = top;
-            s_sum[slot + 16 * i] = sum;
-          }
-          const int target = m < p.M ? target_of(s_target[m_wave + 16 * i + (lane & 15)]) : -1;
-          if (__any(target >= 0)) {
+          if (edge) {
 #pragma unroll
             for (int j = 0; j < kTN; ++j)
 #pragma unroll
               for (int c = 0; c < 4; ++c)
-                if (target == 16 * j + c) {
-                  if (p.losses != nullptr)
-                    s_z[m_wave + 16 * i + (lane & 15)] = acc[i][j][c];
-                  else
-                    p.target_z[m] = acc[i][j][c];
-                }
+#pragma unroll
+                for (int i = 0; i < kTM; ++i)
+                  acc[i][j][c] = 16 * j + c < columns ? acc[i][j][c] : kMinusInfinity;
+          }
+#pragma unroll
+          for (int i = 0; i < kTM; ++i) {
+            const int64_t m = m_lane + 16 * i;
+            float top = kMinusInfinity;
+#pragma unroll
+            for (int j = 0; j < kTN; ++j)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) top = fmaxf(top, acc[i][j][c]);
+            top = fold_row(top, [](float x, float y) { return fmaxf(x, y); });
+            // a row of which nothing is left has no exponentials
+            const float base = top == kMinusInfinity ? 0.0f : top;
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < kTN; ++j)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) sum += exp_roughly(acc[i][j][c] - base);
+            sum = fold_row(sum, [](float x, float y) { return x + y; });
+            if ((lane >> 4) == 0) {
+              s_top[slot + 16 * i] = top;
+              s_sum[slot + 16 * i] = sum;
+            }
+            const int target = m < p.M ? target_of(s_target[m_wave + 16 * i + (lane & 15)]) : -1;
+            if (__any(target >= 0)) {
+#pragma unroll
+              for (int j = 0; j < kTN; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                  if (target == 16 * j + c) {
+                    if (p.losses != nullptr)
+                      s_z[m_wave + 16 * i + (lane & 15)] = acc[i][j][c];
+                    else
+                      p.target_z[m] = acc[i][j][c];
+                  }
+            }
           }
         }
         __syncthreads();
-        for (int r = (int)threadIdx.x; r < kBM; r += 64 * kWaves) {
+        for (int r = (int)threadIdx.x; r < kBM; r += kThreads) {
           const int64_t m = m0 + r;
           if (m >= p.M) break;
           float top = s_top[r];
@@ -755,6 +800,7 @@ struct HeadTile {
           if (p.sums != nullptr) p.sums[at] = all;
         }
       } else {
+        if (!first_group) return;
         const float even = p.smoothing / (float)p.classes;
         // what is rounded to 16 bits needs no exponential of 24
         constexpr bool kRoughly = sizeof(typename Type::Output) == 2;
@@ -833,9 +879,9 @@ struct HeadTile {
 };
 
 template <typename T, int kOutput, bool kAcrossA, bool kAcrossB, int kBM, int kBN, int kWM, int kWN,
-          int kStages>
-__global__ __launch_bounds__(64 * kWM * kWN, 2) void head_kernel(HeadArgs p) {
-  using Head = HeadTile<T, kOutput, kAcrossA, kAcrossB, kBM, kBN, kWM, kWN, kStages>;
+          int kStages, int kGroups = 1>
+__global__ __launch_bounds__(64 * kWM * kWN * kGroups, 2) void head_kernel(HeadArgs p) {
+  using Head = HeadTile<T, kOutput, kAcrossA, kAcrossB, kBM, kBN, kWM, kWN, kStages, kGroups>;
   __shared__ __align__(1024) int8_t s_stages[Head::kLds];
   Head::run(p, blockIdx.x, blockIdx.y, s_stages);
 }
@@ -852,10 +898,10 @@ struct HeadPairArgs {
   float* dbias;
 };
 
-template <typename T, int kBM, int kBN, int kWM, int kWN, int kStages>
-__global__ __launch_bounds__(64 * kWM * kWN, 2) void head_pair_kernel(HeadPairArgs p) {
-  using Dx = HeadTile<T, kHeadRounded, false, true, kBM, kBN, kWM, kWN, kStages>;
-  using Dw = HeadTile<T, kHeadRounded, true, true, kBM, kBN, kWM, kWN, kStages>;
+template <typename T, int kBM, int kBN, int kWM, int kWN, int kStages, int kGroups = 1>
+__global__ __launch_bounds__(64 * kWM * kWN * kGroups, 2) void head_pair_kernel(HeadPairArgs p) {
+  using Dx = HeadTile<T, kHeadRounded, false, true, kBM, kBN, kWM, kWN, kStages, kGroups>;
+  using Dw = HeadTile<T, kHeadRounded, true, true, kBM, kBN, kWM, kWN, kStages, kGroups>;
   __shared__ __align__(1024) int8_t s_stages[Dx::kLds > Dw::kLds ? Dx::kLds : Dw::kLds];
   if (blockIdx.x < p.dx_blocks) {
     Dx::run(p.dx, blockIdx.x, 0, s_stages);
@@ -863,7 +909,7 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void head_pair_kernel(HeadPairAr
     Dw::run(p.dw, blockIdx.x - p.dx_blocks, 0, s_stages);
   } else {
     // 64 classes: a wavefront takes every kWaves-th row of partial sums
-    constexpr int kWaves = kWM * kWN;
+    constexpr int kWaves = kWM * kWN * kGroups;
     float* s_sum = reinterpret_cast<float*>(s_stages);
     const int lane = (int)(threadIdx.x & 63u), wave = (int)(threadIdx.x >> 6);
     const int64_t n = (int64_t)(blockIdx.x - p.dx_blocks - p.dw_blocks) * 64 + lane;

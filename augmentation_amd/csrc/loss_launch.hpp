@@ -21,6 +21,13 @@ struct HeadLaunch {
   int splits;  // of the contraction
 };
 
+// Whether a 16x64 tile's contraction is divided between groups: where no compute
+// unit of 256 has a second tile, and it is long enough (512 elements of bf16 6.1
+// us with one group, 6.5 with four; 1024 8.0 / 7.5).
+inline bool in_groups(int tile, int64_t tiles, int64_t K) {
+  return tile == 3 && tiles <= 256 && K >= 768;
+}
+
 template <typename T, int kOutput, bool kAcrossA, bool kAcrossB>
 void launch_head_tiles(HeadLaunch& l, hipStream_t st) {
   HeadArgs& p = l.args;
@@ -38,10 +45,14 @@ void launch_head_tiles(HeadLaunch& l, hipStream_t st) {
     case 2:
       head_kernel<T, kOutput, kAcrossA, kAcrossB, 64, 64, 2, 2, 4><<<grid, 256, 0, st>>>(p);
       break;
-    // few rows, which only dw's operands do not have
+    // few rows, which only dw's operands do not have; or few tiles
     case 3:
-      if constexpr (!kAcrossA)
-        head_kernel<T, kOutput, kAcrossA, kAcrossB, 16, 64, 1, 4, 4><<<grid, 256, 0, st>>>(p);
+      if constexpr (!kAcrossA) {
+        if (in_groups(3, (int64_t)grid.x * grid.y, p.K_split))
+          head_kernel<T, kOutput, kAcrossA, kAcrossB, 16, 64, 1, 4, 3, 4><<<grid, 1024, 0, st>>>(p);
+        else
+          head_kernel<T, kOutput, kAcrossA, kAcrossB, 16, 64, 1, 4, 4><<<grid, 256, 0, st>>>(p);
+      }
       break;
     default:
       if constexpr (!kAcrossA)

@@ -280,30 +280,51 @@ bool in_place(const void* p, int64_t stride, int32_t width, int64_t e) {
          stride >= width && stride * e <= kMaxStrideBytes;
 }
 
-// An operand of the call: where it lies, or its copy.
+// An operand of the call: where it lies, or the place of its copy, which is still
+// to be made.
+struct Placed {
+  fn::Operand operand;
+  fn::Copy copy;
+  int64_t rows;  // to copy
+};
+
 template <typename T>
-fn::Operand operand(const void* from, int64_t stride, int64_t rows, int32_t width, int64_t copied,
-                    char* copy, hipStream_t st) {
-  using Element = typename fn::HeadType<T>::Operand;
-  constexpr int64_t e = sizeof(Element);
-  if (copy == nullptr) return {(const char*)from, stride * e, rows, (int64_t)width * e, 0};
-  const fn::Operand o = {copy, copied * e, rows, copied * e, rows * copied * e};
-  using Given = typename fn::HeadType<T>::Output;
-  const fn::Division pieces = fn::division_by((uint32_t)(copied * e / 16));
-  // at most 2^31 threads to a launch
-  const int64_t most = ((int64_t)1 << 31) / pieces.by;
-  for (int64_t row = 0; row < rows; row += most) {
-    const uint32_t items = (uint32_t)(std::min(most, rows - row) * pieces.by);
-    const Given* x = (const Given*)from + row * stride;
-    Element* to = (Element*)copy + row * copied;
-    if constexpr (std::is_same_v<T, fn::Fp32Parts>)
-      fn::loss_parts_kernel<<<blocks_for(items, 256), 256, 0, st>>>(x, stride, items, pieces, width,
-                                                                    to, rows * copied);
-    else
-      fn::loss_pack_kernel<T><<<blocks_for(items, 256), 256, 0, st>>>(x, stride, items, pieces,
-                                                                      width, to);
+Placed place(const void* from, int64_t stride, int64_t rows, int32_t width, int64_t copied,
+             char* copy) {
+  constexpr int64_t e = sizeof(typename fn::HeadType<T>::Operand);
+  if (copy == nullptr) return {{(const char*)from, stride * e, rows, (int64_t)width * e, 0}, {}, 0};
+  fn::Copy c{};
+  c.from = from;
+  c.stride = stride;
+  c.to = copy;
+  c.part = rows * copied;
+  c.pieces = fn::division_by((uint32_t)(copied * e / 16));
+  c.width = width;
+  return {{copy, copied * e, rows, copied * e, rows * copied * e}, c, rows};
+}
+
+// Makes the copies of one or two operands, at most 2^30 pieces of each in a launch.
+template <typename T>
+int make_copies(Placed a, Placed b, hipStream_t st) {
+  while (a.rows > 0 || b.rows > 0) {
+    unsigned groups = 0;
+    for (Placed* p : {&a, &b}) {
+      const int64_t pieces = std::max<int64_t>(p->copy.pieces.by, 1);
+      const int64_t count = std::min(p->rows, std::max<int64_t>(((int64_t)1 << 30) / pieces, 1));
+      p->copy.items = (uint32_t)(count * pieces);
+      if (count == 0) p->copy.items = 0;
+      groups += blocks_for(p->copy.items, 256);
+    }
+    fn::loss_copy_kernel<T><<<groups, 256, 0, st>>>(a.copy, b.copy);
+    FN_TRY(launch_status("loss_copy_kernel launch"));
+    for (Placed* p : {&a, &b}) {
+      const int64_t count = p->copy.items / std::max(p->copy.pieces.by, 1u);
+      p->copy.from = (const typename fn::HeadType<T>::Output*)p->copy.from + count * p->copy.stride;
+      p->copy.to = (char*)p->copy.to + (int64_t)p->copy.items * 16;
+      p->rows -= count;
+    }
   }
-  return o;
+  return FN_OK;
 }
 
 struct Call {
@@ -342,13 +363,15 @@ template <typename T>
 int forward(const Call& c, const Plan& p, float* losses, float* lse) {
   char* const ws = c.workspace;
   using Given = typename fn::HeadType<T>::Output;
-  const fn::Operand x = operand<T>(c.x, c.x_stride, c.rows, c.width, p.width_packed,
-                                   p.pack_x ? ws + p.x : nullptr, c.st);
+  Placed x = place<T>(c.x, c.x_stride, c.rows, c.width, p.width_packed,
+                      p.pack_x ? ws + p.x : nullptr);
   for (int64_t first = 0, tile = 0; first < c.classes; first += p.piece) {
     const int64_t count = std::min(p.piece, c.classes - first);
-    const fn::Operand w = operand<T>((const Given*)c.w + first * c.w_stride, c.w_stride, count, c.width,
-                                     p.width_packed, p.pack_w ? ws + p.w : nullptr, c.st);
-    fn::HeadArgs a = head_args(c, p, x, w, first, count);
+    const Placed w = place<T>((const Given*)c.w + first * c.w_stride, c.w_stride, count, c.width,
+                              p.width_packed, p.pack_w ? ws + p.w : nullptr);
+    FN_TRY(make_copies<T>(x, w, c.st));
+    x.rows = 0;
+    fn::HeadArgs a = head_args(c, p, x.operand, w.operand, first, count);
     a.stats = (fn::f32x2*)(ws + p.stats);
     a.sums = c.smoothing > 0.0f ? (float*)(ws + p.sums) : nullptr;
     a.target_z = (float*)(ws + p.target_z);
@@ -421,8 +444,8 @@ int backward(const Call& c, const Plan& p, const Gradients& g) {
   using Given = typename fn::HeadType<T>::Output;
   constexpr int64_t e = sizeof(typename fn::HeadType<T>::Operand);
   char* const ws = c.workspace;
-  const fn::Operand x = operand<T>(c.x, c.x_stride, c.rows, c.width, p.width_packed,
-                                   p.pack_x ? ws + p.x : nullptr, c.st);
+  Placed x = place<T>(c.x, c.x_stride, c.rows, c.width, p.width_packed,
+                      p.pack_x ? ws + p.x : nullptr);
   float* scale = nullptr;
   float scale_to = 0.0f;
   if constexpr (sizeof(Given) == 2) {
@@ -443,10 +466,12 @@ int backward(const Call& c, const Plan& p, const Gradients& g) {
     const int k = p.which(count);
     const int32_t bias_rows = (int32_t)bias_rows_of(p.logits[k], c.rows);
     float* const bias_sums = (float*)(ws + p.bias_sums);
-    const fn::Operand w = operand<T>((const Given*)c.w + first * c.w_stride, c.w_stride, count, c.width,
-                                     p.width_packed, p.pack_w ? ws + p.w : nullptr, c.st);
+    const Placed w = place<T>((const Given*)c.w + first * c.w_stride, c.w_stride, count, c.width,
+                              p.width_packed, p.pack_w ? ws + p.w : nullptr);
+    FN_TRY(make_copies<T>(x, w, c.st));
+    x.rows = 0;
     if (c.rows > 0) {
-      fn::HeadArgs a = head_args(c, p, x, w, first, count);
+      fn::HeadArgs a = head_args(c, p, x.operand, w.operand, first, count);
       a.lse = g.lse;
       a.dlosses = g.dlosses;
       a.dloss_stride = g.dloss_stride;
@@ -463,9 +488,9 @@ int backward(const Call& c, const Plan& p, const Gradients& g) {
                                   c.rows * p.pitch * e};
     fn::HeadArgs dx{}, dw{};
     dx.a = dw.a = gradient;
-    dx.b = w;
-    dx.once = w.stride * c.classes > kCached;
-    dw.b = x;
+    dx.b = w.operand;
+    dx.once = w.operand.stride * c.classes > kCached;
+    dw.b = x.operand;
     dx.M = dw.K = c.rows;
     dx.K = dw.M = count;
     dx.N = dw.N = c.width;

@@ -104,63 +104,77 @@ __global__ __launch_bounds__(256) void loss_round_kernel(const float* sums, int6
     }
 }
 
-// Rows of any alignment to rows of whole 16-byte pieces, zeros at their ends: a
-// thread takes a piece.
+// A copy of an operand: rows of any alignment to rows of whole 16-byte pieces, zeros
+// at their ends; fp32 in three parts (see Fp32Parts).
+struct Copy {
+  const void* from;
+  int64_t stride;  // in elements
+  void* to;
+  int64_t part;     // in elements
+  uint32_t items;   // pieces of this launch
+  Division pieces;  // of a row
+  int32_t width;
+};
+
 template <typename T>
-__global__ __launch_bounds__(256) void loss_pack_kernel(const T* from, int64_t stride,
-                                                        uint32_t items, Division pieces,
-                                                        int32_t width, T* to) {
-  constexpr int kE = 16 / (int)sizeof(T);
-  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
-  if (i >= items) return;
-  const uint32_t m = quotient(i, pieces);
-  const int32_t c = kE * (int32_t)(i - m * pieces.by);
-  const T* row = from + m * stride;
-  u32x4 v = {0, 0, 0, 0};
-  if (c + kE <= width) {
-    v = *reinterpret_cast<const u32x4_any*>(row + c);
-  } else {
+__device__ __forceinline__ void copy_piece(const Copy& a, uint32_t i) {
+  using Element = typename HeadType<T>::Operand;
+  using Given = typename HeadType<T>::Output;
+  constexpr int kE = 16 / (int)sizeof(Element);
+  const uint32_t m = quotient(i, a.pieces);
+  const int32_t c = kE * (int32_t)(i - m * a.pieces.by);
+  const Given* row = (const Given*)a.from + m * a.stride + c;
+  Element* to = (Element*)a.to + (int64_t)i * kE;
+  if constexpr (HeadType<T>::kPasses > 1) {
+    Vec8<float> v;
+    if (c + 8 <= a.width)
+      v.load(row);
+    else
+      v.load_some(row, a.width - c);
+    float left[8];
 #pragma unroll
-    for (int j = 0; j < kE; ++j)
-      if (c + j < width) {
-        if constexpr (sizeof(T) == 4)
-          v[j] = __builtin_bit_cast(uint32_t, row[c + j]);
-        else
-          v[j >> 1] |= (uint32_t)__builtin_bit_cast(uint16_t, row[c + j]) << (16 * (j & 1));
+    for (int j = 0; j < 8; ++j) left[j] = v.get(j);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      u32x4 w;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = float_to_bf16(left[2 * j]), hi = float_to_bf16(left[2 * j + 1]);
+        w[j] = lo | hi << 16;
+        left[2 * j] -= bf16_to_float(lo);
+        left[2 * j + 1] -= bf16_to_float(hi);
       }
+      *reinterpret_cast<u32x4*>(to + k * a.part) = w;
+    }
+  } else {
+    u32x4 v = {0, 0, 0, 0};
+    if (c + kE <= a.width) {
+      v = *reinterpret_cast<const u32x4_any*>(row);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kE; ++j)
+        if (c + j < a.width) {
+          if constexpr (sizeof(Given) == 4)
+            v[j] = __builtin_bit_cast(uint32_t, row[j]);
+          else
+            v[j >> 1] |= (uint32_t)__builtin_bit_cast(uint16_t, row[j]) << (16 * (j & 1));
+        }
+    }
+    *reinterpret_cast<u32x4*>(to) = v;
   }
-  *reinterpret_cast<u32x4*>(to + (int64_t)i * kE) = v;
 }
 
-// The three parts of fp32 rows (see Fp32Parts), zeros at their rows' ends: a
-// thread takes eight numbers.
-__global__ __launch_bounds__(256) void loss_parts_kernel(const float* from, int64_t stride,
-                                                         uint32_t items, Division pieces,
-                                                         int32_t width, BF16* to, int64_t part) {
-  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
-  if (i >= items) return;
-  const uint32_t m = quotient(i, pieces);
-  const int32_t c = 8 * (int32_t)(i - m * pieces.by);
-  const float* row = from + m * stride + c;
-  Vec8<float> v;
-  if (c + 8 <= width)
-    v.load(row);
-  else
-    v.load_some(row, width - c);
-  float left[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) left[j] = v.get(j);
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    u32x4 w;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t lo = float_to_bf16(left[2 * j]), hi = float_to_bf16(left[2 * j + 1]);
-      w[j] = lo | hi << 16;
-      left[2 * j] -= bf16_to_float(lo);
-      left[2 * j + 1] -= bf16_to_float(hi);
-    }
-    *reinterpret_cast<u32x4*>(to + k * part + (int64_t)i * 8) = w;
+// Both operands' copies in one launch (a's work-groups first): a thread takes a
+// piece.
+template <typename T>
+__global__ __launch_bounds__(256) void loss_copy_kernel(Copy a, Copy b) {
+  const uint32_t groups = (a.items + 255u) / 256u;
+  if (blockIdx.x < groups) {
+    const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+    if (i < a.items) copy_piece<T>(a, i);
+  } else {
+    const uint32_t i = (blockIdx.x - groups) * 256u + threadIdx.x;
+    if (i < b.items) copy_piece<T>(b, i);
   }
 }
 

@@ -7,7 +7,9 @@ same pass (page "(11) FusedNormalization", tech-renaissance.cn/blog/?p=487).
 
 Next to it stand the operators of a model's 8-bit linear layer: the RMS norm
 of x + residual with 8-bit output, its gradients, the quantisation of rows and
-the product of 8-bit codes.
+the product of 8-bit codes.  And those of a network in training, with their
+gradients: dropout, the layer norm of residual + dropout(x), and the softmax cross
+entropy of a linear head, whose logits are not kept.
 
 The work runs in the hand-written HIP kernels of ``libfn.so`` (built from
 ``csrc/``).  ``augmentation_amd.binding`` exposes the library's C entry

@@ -815,7 +815,8 @@ def linear_cross_entropy(x, weight, targets, bias=None, smoothing=0.0, losses=No
         stream)
     _check(_lib.fn_linear_cross_entropy(
         x_at, x_stride, w_at, w_stride, None if bias is None else bias.data_ptr(),
-        targets.data_ptr(), rows, classes, width, smoothing, code, losses.data_ptr(), lse.data_ptr(), at, size, _stream(stream)))
+        targets.data_ptr(), rows, classes, width, smoothing, code, losses.data_ptr(),
+        lse.data_ptr(), at, size, _stream(stream)))
     _increment_version((losses, lse, workspace) if given else (losses, lse))
     return losses, lse
 

@@ -113,10 +113,13 @@ BackwardPlan plan_backward(int64_t rows, int32_t width) {
     const int64_t at_once = p.shape.threads <= 64 ? 256 / p.shape.threads : 1;
     const int64_t groups = (rows + at_once - 1) / at_once;
     p.partials = (int32_t)std::min<int64_t>(groups, width <= 1024 ? 512 : 256);
-    // so few rows that one work-group's sums are the gradients: it does a few
-    // groups of rows in less time than the second launch takes (52x65 bf16 16 ->
-    // 11 us a call)
-    p.direct = groups >= 1 && groups <= 6;
+    // So few rows that one work-group's sums are the gradients: a few groups of
+    // rows take it less time than the second launch does, which makes 12.4 us of
+    // a call.  6 groups: 9.8 us at 512 to 4,096 columns (with one or two chunks
+    // a thread), 13.6 at 2,048 (four), 17.2 at 2,560 (five; 3 groups 11.0), 11.9
+    // at 8,192; 16,384 columns: 2 rows 9.8 (fp32 14.9), 3 rows 12.3 (19.4).
+    const int most = width > 8192 ? 2 : std::min(6, 12 / std::max(1, p.shape.chunks));
+    p.direct = groups >= 1 && groups <= most;
     if (p.direct) p.partials = 1;
     p.bytes = p.direct ? 0 : (int64_t)p.partials * p.pitch * 8;
     p.bytes = (p.bytes + 15) / 16 * 16;
@@ -310,7 +313,8 @@ FN_EXPORT int fn_layer_norm_backward(
   fn::LayerBackwardArgs a{};
   FN_TRY(dropout_of(dropout_p, seed, first_row, rows, &a.drop));
   if ((dropout_p > 0.0f) != (dx_dev != nullptr) && rows > 0)
-    return fail(FN_EINVAL, "dx_dev comes with dropout, and only then (else dh is the gradient of x)");
+    return fail(FN_EINVAL,
+                "dx_dev comes with dropout, and only then (else dh is the gradient of x)");
   const BackwardPlan plan = plan_backward(rows, width);
   if (workspace_bytes < plan.bytes)
     return fail(FN_EINVAL, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes,

@@ -73,8 +73,12 @@ double tiles_time(int tile, ProductKind kind, const Elements& t, int64_t tiles, 
       {{{223.0, 62.0, 18.3}, {223.0, 57.5, 15.9}}, {{230.0, 66.0, 23.5}, {230.0, 59.0, 18.0}}},
       {{{118.0, 47.0, 23.0}, {122.0, 52.0, 15.8}}, {{137.0, 77.0, 41.0}, {137.0, 50.0, 27.0}}}};
   const int type = t.passes > 1 ? 2 : t.size == 4 ? 1 : 0;
-  const double memory = (double)(M + N) * K * t.size * t.parts / 5.4e6, rounds = (double)tiles / kUnits;
-  if (tile == 4) return std::max((2.0 + 8e-3 * K * (t.size == 4 ? 2 : 1)) * std::ceil(rounds / 2), memory);
+  const double memory = (double)(M + N) * K * t.size * t.parts / 5.4e6;
+  const double rounds = (double)tiles / kUnits;
+  if (tile == 4) {
+    const double each = 8e-3 * K * (t.size == 4 ? 2 : 1);
+    return std::max(std::ceil(rounds / 2) * (2.0 + each), memory);
+  }
   if (tile == 3) {
     constexpr double kNarrow[3][3] = {{4.0, 2.4, 2.3}, {10.5, 6.3, 7.0}, {19.0, 13.5, 14.0}};
     const bool groups = fn::in_groups(tile, tiles, K);
@@ -105,7 +109,8 @@ Choice choose(ProductKind kind, int64_t M, int64_t N, int64_t K, const Elements&
     if (tile == 3 && !few && tiles > kUnits) continue;
     if (tiles >= (int64_t)1 << 22) continue;  // 2^32 threads to a launch
     for (int splits = 1; splits <= 64; splits *= 2) {
-      if (splits > 1 && (!splittable || K < 8 * stage * splits || tiles * splits > 4 * kUnits)) break;
+      if (splits > 1 && (!splittable || K < 8 * stage * splits || tiles * splits > 4 * kUnits))
+        break;
       const int64_t K_split = std::max(round_up((K + splits - 1) / splits, stage), stage);
       double cost = 3.0 + tiles_time(tile, kind, t, tiles * splits, M, N, K_split);
       // partial products are written and read again, in a launch of their own
@@ -193,7 +198,8 @@ Plan plan_of(int64_t rows, int64_t classes, int32_t width, int64_t e, bool pack_
   const int64_t per_class = std::max(backward ? std::max<int64_t>(rows, 1) * bytes : 0,
                                      p.pack_w ? p.width_packed * bytes : 0);
   int64_t most = round_up(classes, 256);
-  if (per_class > 0) most = std::min(most, std::max<int64_t>(kPieceBytes / per_class / 256, 1) * 256);
+  if (per_class > 0)
+    most = std::min(most, std::max<int64_t>(kPieceBytes / per_class / 256, 1) * 256);
   if (backward) most = std::min(most, kMaxStrideBytes / t.size / 256 * 256);
   p.piece = classes;
   if (most < classes) {
@@ -201,9 +207,8 @@ Plan plan_of(int64_t rows, int64_t classes, int32_t width, int64_t e, bool pack_
   } else if (!backward) {
     // whole rounds of tiles first and the rest in smaller ones, if that is less
     const int64_t piece = piece_of(rows, classes / 256 * 256);
-    if (piece > 0 && piece < classes &&
-        choose(kLogits, rows, piece, K, t, false).cost + choose(kLogits, rows, classes - piece, K, t, false).cost <
-            choose(kLogits, rows, classes, K, t, false).cost)
+    auto cost = [&](int64_t count) { return choose(kLogits, rows, count, K, t, false).cost; };
+    if (piece > 0 && piece < classes && cost(piece) + cost(classes - piece) < cost(classes))
       p.piece = piece;
   }
   p.pieces = (classes + p.piece - 1) / p.piece;
@@ -245,7 +250,8 @@ Plan plan_of(int64_t rows, int64_t classes, int32_t width, int64_t e, bool pack_
           3.0 + (dx * tiles_time(tile, kGradients, t, dx + dw, rows, width, classes) +
                  dw * tiles_time(tile, kGradients, t, dx + dw, classes, width, rows)) /
                     (dx + dw);
-      const double longest = 3.0 + tiles_time(tile, kGradients, t, 1, 1, 1, std::max(rows, classes));
+      const double longest =
+          3.0 + tiles_time(tile, kGradients, t, 1, 1, 1, std::max(rows, classes));
       if (std::max(cost, longest) < least) {
         least = std::max(cost, longest);
         p.pair_tile = tile;
@@ -276,8 +282,8 @@ int check_head(int64_t rows, int64_t classes, int32_t width, int32_t dtype) {
 
 // Rows that the kernels can read where they are.
 bool in_place(const void* p, int64_t stride, int32_t width, int64_t e) {
-  return ((uintptr_t)p | (uint64_t)(stride * e) | (uint64_t)(width * e)) % 16 == 0 &&
-         stride >= width && stride * e <= kMaxStrideBytes;
+  return stride >= width && stride <= kMaxStrideBytes / e &&
+         ((uintptr_t)p | (uint64_t)(stride * e) | (uint64_t)(width * e)) % 16 == 0;
 }
 
 // An operand of the call: where it lies, or the place of its copy, which is still
@@ -568,9 +574,15 @@ FN_EXPORT int fn_linear_cross_entropy_workspace(int64_t rows, int64_t classes, i
                                                 int64_t* bytes) {
   FN_TRY(check_head(rows, classes, width, dtype));
   if (bytes == nullptr) return fail(FN_EINVAL, "bytes is NULL");
-  *bytes = plan_of(rows, classes, width, type_bytes(dtype), !in_place_x, !in_place_weight,
-                   backward_pass != 0)
-               .bytes;
+  // what may turn out to lie in place after all has a plan of its own
+  *bytes = 0;
+  for (int copied = 0; copied < 4; ++copied) {
+    const bool pack_x = copied & 1, pack_w = copied & 2;
+    if ((pack_x && in_place_x) || (pack_w && in_place_weight)) continue;
+    *bytes = std::max(*bytes, plan_of(rows, classes, width, type_bytes(dtype), pack_x, pack_w,
+                                      backward_pass != 0)
+                                  .bytes);
+  }
   return ok();
 }
 

@@ -15,6 +15,13 @@
 // second time is a third of the backward pass; what is not kept is T x V
 // logits.
 //
+// Large calls are bound by the matrix cores, whose clock sinks to 1.8 GHz at full
+// load and which work 67% of it: 8192x50000x4096 bf16 2.45 ms, 1.37 PFLOP/s (a
+// library product of that shape alone, its logits written, 2.61 ms); gradients of
+// 4096x50000x4096 4.0 ms, 1.26 PFLOP/s.  Few rows are bound by the bytes of the
+// weights: 1x50000x4096 bf16 74 us, 5.5 TB/s.  Small calls by their launches:
+// gradients of 1024x1000x768 fp16 20.6 us in two.
+//
 // One kernel serves the three products.  They differ in how their operands lie:
 // "along" the contraction (x and w in the logits, g in dx: a row of memory is
 // a row of the operand) or "across" it (w in dx, g and x in dw: a row of memory
@@ -77,7 +84,8 @@ __device__ __forceinline__ f32x4 multiply_add(i32x4 a, i32x4 b, f32x4 c) {
 // the smallest first; the three left out come to 2^-24 of a b together, the
 // rounding of one product in fp32.  On the matrix cores that is 16 / 6 times the
 // rate of the fp32 instruction.  The six follow each other as one long
-// contraction.  An infinity in an operand gives NaN in every logit it reaches.
+// contraction.  An infinity in an operand gives NaN in every logit it reaches, and
+// so does a number that rounds to one (of 2^128 - 2^119 and more).
 struct Fp32Parts {};
 
 template <typename T>
@@ -315,7 +323,8 @@ struct Stager {
       return v;
     } else {
       typedef __attribute__((address_space(3))) i16x4 Lds;
-      const auto* q = (const __attribute__((address_space(3))) int8_t*)buf + at[t] + 32 * k * kRowBytes;
+      const auto* q =
+          (const __attribute__((address_space(3))) int8_t*)buf + at[t] + 32 * k * kRowBytes;
       const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds*)q));
       const u32x2 hi = __builtin_bit_cast(
           u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds*)(q + 4 * kRowBytes)));
@@ -408,8 +417,9 @@ struct LossOf {
   float lse, loss;
 };
 
-__device__ __forceinline__ LossOf loss_of(float top, float sum, float all, bool counts, float target,
-                                          float smoothing, int64_t classes) {
+__device__ __forceinline__ LossOf loss_of(float top, float sum, float all, bool counts,
+                                          float target, float smoothing,
+                                          int64_t classes) {
   LossOf l;
   l.lse = top + logf(sum);
   l.loss = counts ? l.lse - (1.0f - smoothing) * target : 0.0f;
@@ -695,7 +705,7 @@ struct HeadTile {
     } else {
       // The logits.  What follows is 128 elements a lane in the largest tile, so it
       // counts by the instruction: bias, the edge of the classes and targets are
-      // looked at only where there are any (8192x50000x4096 bf16 TIMES).
+      // looked at only where there are any (8192x50000x4096 bf16 2.55 -> 2.45 ms).
       if (p.bias != nullptr && first_group) {
 #pragma unroll
         for (int j = 0; j < kTN; ++j)

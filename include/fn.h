@@ -17,8 +17,9 @@
  *     fraction and log aspect ratio, rounding, acceptance, corner).
  * The page runs this per image on CPU threads; here one call processes a
  * whole batch on one GPU.  The operators of a model's 8-bit linear layer
- * follow at the end: a norm that quantises, row quantisation, the product of
- * the codes and the norm's gradients.
+ * follow: a norm that quantises, row quantisation, the product of the codes and
+ * the norm's gradients.  Then those of a network in training: dropout, layer norm
+ * and the softmax cross entropy of a linear head, each with its gradients.
  *
  * Conventions for every entry point:
  *   - Pointers named *_dev are device memory (hipMalloc or a PyTorch CUDA
@@ -402,10 +403,15 @@ int fn_layer_norm_backward_workspace(int64_t rows, int32_t width, int64_t* bytes
 /*   lse[t]  = log(sum_v exp(z[t, v])),                                       */
 /*   loss[t] = lse[t] - (1 - smoothing) z[t, y_t] - smoothing mean_v z[t, v]. */
 /* targets are 64-bit; a row whose target y_t lies outside 0..classes-1 (-100, */
-/* say) is ignored: its loss and its gradients are zero.  smoothing lies in    */
-/* [0, 1].  A class of bias -infinity is left out: probability 0, and a loss   */
-/* of +infinity for rows that want it.  A row with a NaN or +infinity among    */
-/* its logits, or all classes left out, has a NaN loss.                        */
+/* say) is ignored: its loss and its gradients are zero, whatever its logits   */
+/* (but its features still meet dweight's zeros, so they have to be finite).   */
+/* smoothing lies in [0, 1].  A class of bias -infinity is left out:           */
+/* probability 0, and a loss of +infinity for rows that want it.  A row with a */
+/* NaN or +infinity among its logits, or all classes left out, has a NaN loss. */
+/*                                                                            */
+/* In large fp32 products an operand is taken as three bf16 numbers, which     */
+/* hold all of its digits if it is 2^-100 or more; one that is infinite, or    */
+/* that bf16 rounds to infinity, gives NaN logits.                             */
 /*                                                                            */
 /* Speed only: operands are read in place if in_place(x), which is that the    */
 /* base, the stride and the width are multiples of 16 bytes and the stride is  */

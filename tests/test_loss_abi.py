@@ -88,6 +88,19 @@ def test_workspace_sizes(b):
     assert size(8192, 50000, 4096, 3, 1, 1, 0) < 8192 * 50000 * 2 / 30
 
 
+def test_a_workspace_for_copies_is_enough_in_place(b):
+    size = b.fn_linear_cross_entropy_workspace
+    for rows in (0, 1, 16, 17, 300, 5000, 2**17):
+        for classes in (1, 64, 1000, 2**17, 2**18):
+            for width in (8, 512, 4096, 2**16):
+                for dtype in (0, 1):
+                    for backward in (0, 1):
+                        a = (rows, classes, width, dtype)
+                        both, x, w, none = (size(*a, i, j, backward) for i, j in
+                                            ((1, 1), (1, 0), (0, 1), (0, 0)))
+                        assert both <= min(x, w) and max(x, w) <= none
+
+
 def calls(b):
     """(name, function, its float arguments)."""
     x, w, s, c = torch.ones(4, 8), torch.ones(5, 8), torch.ones(4), torch.ones(5)

@@ -457,9 +457,9 @@ int backward(const Call& c, const Plan& p, const Gradients& g) {
   if constexpr (sizeof(Given) == 2) {
     scale = (float*)(ws + p.scale);
     scale_to = std::is_same_v<Given, _Float16> ? 16384.0f : 1.0f;
-    // few rows: each work-group of the first kernel looks for the largest
-    // dloss, for less than a launch takes
-    if (c.rows > kFewRows || c.rows == 0) {
+    // few dlosses: each work-group of the first kernel looks for the largest one,
+    // for less than a launch takes
+    if (c.rows == 0 || (c.rows > kFewRows && g.dloss_stride != 0)) {
       fn::loss_scale_kernel<<<1, 1024, 0, c.st>>>(g.dlosses, g.dloss_stride, c.rows, scale_to,
                                                   scale);
       FN_TRY(launch_status("loss_scale_kernel launch"));

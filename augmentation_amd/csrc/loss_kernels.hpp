@@ -441,9 +441,17 @@ template <int kThreads>
 __device__ __forceinline__ Scale find_scale(const float* dlosses, int64_t stride, int64_t rows,
                                             float to, uint32_t* s_top) {
   uint32_t top = 0;
-  for (int64_t i = threadIdx.x; i < rows; i += kThreads) {
-    const uint32_t v = __builtin_bit_cast(uint32_t, dlosses[i * stride]) & 0x7FFFFFFFu;
-    if (v < 0x7F800000u) top = max(top, v);
+  if (stride == 0) rows = min(rows, (int64_t)1);
+  // four loads at a time on their way
+  for (int64_t i = threadIdx.x; i < rows; i += 4 * kThreads) {
+    uint32_t v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t at = min(i + j * kThreads, rows - 1);
+      v[j] = __builtin_bit_cast(uint32_t, dlosses[at * stride]) & 0x7FFFFFFFu;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = max(top, v[j] < 0x7F800000u ? v[j] : 0u);
   }
   top = group_max<64>(top);
   if ((threadIdx.x & 63u) == 0) s_top[threadIdx.x >> 6] = top;
@@ -579,8 +587,14 @@ struct HeadTile {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) issue(s, i, next);
     }
+    // numbers that the output takes are read here, like the words above
     Scale scale = {1.0f, 1.0f};
+    float same_dloss = 0.0f;
+    if constexpr (kOutput == kHeadRounded) {
+      if (p.scale != nullptr) scale.down = p.scale[1];
+    }
     if constexpr (kOutput == kHeadGradient) {
+      if (p.dloss_stride == 0) same_dloss = p.dlosses[0];
       if (p.scale_to > 0.0f) {
         scale = find_scale<kThreads>(
             p.dlosses, p.dloss_stride, p.M, p.scale_to,
@@ -699,9 +713,8 @@ struct HeadTile {
         }
     } else if constexpr (kOutput == kHeadRounded) {
       if (!first_group) return;
-      const float scale = p.scale != nullptr ? p.scale[1] : 1.0f;
-      Tile::store([&](int i, int j, int c) { return acc[i][j][c] * scale; }, own, (Out*)p.out,
-                  p.out_stride, m0 + m_wave, n0 + n_wave, p.M, p.N);
+      Tile::store([&](int i, int j, int c) { return acc[i][j][c] * scale.down; }, own,
+                  (Out*)p.out, p.out_stride, m0 + m_wave, n0 + n_wave, p.M, p.N);
     } else {
       // The logits.  What follows is 128 elements a lane in the largest tile, so it
       // counts by the instruction: bias, the edge of the classes and targets are
@@ -820,7 +833,7 @@ struct HeadTile {
           const int at = m_wave + 16 * i + (lane & 15);
           const int64_t y = s_target[at];
           const float lse = s_lse[at];
-          const float dloss = (p.dloss_stride != 0 ? s_dloss[at] : p.dlosses[0]) * scale.up;
+          const float dloss = (p.dloss_stride != 0 ? s_dloss[at] : same_dloss) * scale.up;
           const bool counts = m < p.M && y >= 0 && y < p.classes;
           const int target = target_of(y);
 #pragma unroll

@@ -15,12 +15,12 @@
 // second time is a third of the backward pass; what is not kept is T x V
 // logits.
 //
-// Large calls are bound by the matrix cores, whose clock sinks to 1.8 GHz at full
-// load and which work 67% of it: 8192x50000x4096 bf16 2.45 ms, 1.37 PFLOP/s (a
-// library product of that shape alone, its logits written, 2.61 ms); gradients of
-// 4096x50000x4096 4.0 ms, 1.26 PFLOP/s.  Few rows are bound by the bytes of the
-// weights: 1x50000x4096 bf16 74 us, 5.5 TB/s.  Small calls by their launches:
-// gradients of 1024x1000x768 fp16 20.6 us in two.
+// Large calls are bound by the matrix cores, whose clock sinks to 1.7 GHz under
+// this load and which are busy 71% of it: 8192x50000x4096 bf16 2.46 ms, 1.36
+// PFLOP/s (a library product of that shape alone, its logits written, 2.61 ms);
+// gradients of 4096x50000x4096 4.0 ms, 1.26 PFLOP/s.  Few rows are bound by the
+// bytes of the weights: 1x50000x4096 bf16 74 us, 5.6 TB/s.  Small calls by their
+// launches: gradients of 1024x1000x768 fp16 19.8 us in two.
 //
 // One kernel serves the three products.  They differ in how their operands lie:
 // "along" the contraction (x and w in the logits, g in dx: a row of memory is

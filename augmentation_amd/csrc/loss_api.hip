@@ -28,6 +28,7 @@ constexpr int64_t kPieceBytes = (int64_t)1 << 27;
 // Weights that do not stay in the memory-side cache until the next call anyway.
 constexpr int64_t kCached = (int64_t)1 << 28;
 constexpr int64_t kFewRows = 8192;
+constexpr int kMostSplits = 64;
 constexpr int32_t kMaxFeatures = 1 << 20;
 constexpr int64_t kMaxClasses = (int64_t)1 << 28;
 // a stage's rows times the stride within the 31-bit offsets of a resource
@@ -97,7 +98,7 @@ int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 // ones where they give every compute unit one (1x50000x4096 bf16 with 64 / 128
 // classes a tile 77 / 71 us, 1x16000x4096 30 / 33); more rows have the narrow ones
 // where they are few.  `few_rows`: whether there are kernels for those.
-Choice choose(ProductKind kind, int64_t M, int64_t N, int64_t K, const Elements& t, bool splittable,
+Choice choose(ProductKind kind, int64_t M, int64_t N, int64_t K, const Elements& t, int most_splits,
               bool few_rows = true) {
   const int64_t stage = fn::kStageRow / t.size;
   Choice best;
@@ -108,9 +109,8 @@ Choice choose(ProductKind kind, int64_t M, int64_t N, int64_t K, const Elements&
     const int64_t tiles = tiles_of(tile, M, N);
     if (tile == 3 && !few && tiles > kUnits) continue;
     if (tiles >= (int64_t)1 << 22) continue;  // 2^32 threads to a launch
-    for (int splits = 1; splits <= 64; splits *= 2) {
-      if (splits > 1 && (!splittable || K < 8 * stage * splits || tiles * splits > 4 * kUnits))
-        break;
+    for (int splits = 1; splits <= most_splits; splits *= 2) {
+      if (splits > 1 && (K < 8 * stage * splits || tiles * splits > 4 * kUnits)) break;
       const int64_t K_split = std::max(round_up((K + splits - 1) / splits, stage), stage);
       double cost = 3.0 + tiles_time(tile, kind, t, tiles * splits, M, N, K_split);
       // partial products are written and read again, in a launch of their own
@@ -175,10 +175,10 @@ bool worth_parts(int64_t rows, int64_t classes, int32_t width, bool backward) {
   double cost[2] = {0.0, 6.0 + (double)(rows + classes) * width * 10.0 / 4e6};
   for (int split = 0; split < 2; ++split) {
     const Elements t = elements_of(4, split);
-    cost[split] += choose(kLogits, rows, classes, width, t, false).cost;
+    cost[split] += choose(kLogits, rows, classes, width, t, 1).cost;
     if (backward)
-      cost[split] += choose(kGradients, rows, width, classes, t, true).cost +
-                     choose(kGradients, classes, width, rows, t, true, false).cost;
+      cost[split] += choose(kGradients, rows, width, classes, t, kMostSplits).cost +
+                     choose(kGradients, classes, width, rows, t, kMostSplits, false).cost;
   }
   return cost[1] < cost[0];
 }
@@ -207,7 +207,7 @@ Plan plan_of(int64_t rows, int64_t classes, int32_t width, int64_t e, bool pack_
   } else if (!backward) {
     // whole rounds of tiles first and the rest in smaller ones, if that is less
     const int64_t piece = piece_of(rows, classes / 256 * 256);
-    auto cost = [&](int64_t count) { return choose(kLogits, rows, count, K, t, false).cost; };
+    auto cost = [&](int64_t count) { return choose(kLogits, rows, count, K, t, 1).cost; };
     if (piece > 0 && piece < classes && cost(piece) + cost(classes - piece) < cost(classes))
       p.piece = piece;
   }
@@ -217,7 +217,7 @@ Plan plan_of(int64_t rows, int64_t classes, int32_t width, int64_t e, bool pack_
   p.scale = parts.take(8);
   if (p.pack_x) p.x = parts.take(rows * p.width_packed * bytes);
   if (p.pack_w) p.w = parts.take(p.piece * p.width_packed * bytes);
-  for (int k = 0; k < 2; ++k) p.logits[k] = choose(kLogits, rows, counts[k], K, t, false);
+  for (int k = 0; k < 2; ++k) p.logits[k] = choose(kLogits, rows, counts[k], K, t, 1);
   if (!backward) {
     p.stat_tiles = (p.pieces - 1) * class_tiles(p.logits[0], p.piece) +
                    class_tiles(p.logits[p.which(counts[1])], counts[1]);
@@ -232,10 +232,10 @@ Plan plan_of(int64_t rows, int64_t classes, int32_t width, int64_t e, bool pack_
   p.pair_tile = -1;
   int64_t bias_rows = 0, dw_rows = 0;
   for (int k = 0; k < 2; ++k) {
-    // dx's sums of the first piece fill every split's place, a later one may
-    // use fewer
-    p.dx[k] = choose(kGradients, rows, width, counts[k], t, k == 0);
-    p.dw[k] = choose(kGradients, counts[k], width, rows, t, true, false);
+    // dx's sums of the first piece fill every split's place; the last one may use
+    // fewer, but no others (1024x129280x384 fp16: 723 us without any, 505)
+    p.dx[k] = choose(kGradients, rows, width, counts[k], t, k == 0 ? kMostSplits : p.dx[0].splits);
+    p.dw[k] = choose(kGradients, counts[k], width, rows, t, kMostSplits, false);
     bias_rows = std::max(bias_rows, bias_rows_of(p.logits[k], rows));
     if (p.dw[k].splits > 1) dw_rows = std::max(dw_rows, p.dw[k].splits * counts[k]);
   }
@@ -516,6 +516,7 @@ int backward(const Call& c, const Plan& p, const Gradients& g) {
       both.pitch = p.pitch;
       both.bias_rows = bias_rows;
       both.dbias = g.dbias;
+      both.dw_first = dw.K > dx.K;
       fn::launch_head_pair<T>(both, p.pair_tile, c.st);
       return launch_status("head_pair_kernel launch");
     }

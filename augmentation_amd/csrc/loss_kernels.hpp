@@ -910,11 +910,13 @@ __global__ __launch_bounds__(64 * kWM * kWN * kGroups, 2) void head_kernel(HeadA
 }
 
 // Both products with g in one launch, for sizes where one alone leaves compute
-// units idle, and the sums of dbias: work-groups 0 .. dx_blocks - 1 have tiles of
-// dx, the next dw_blocks of dw, the others 64 classes each.
+// units idle, and the sums of dbias: first the tiles of the product with the longer
+// contraction, so that none of them starts late, then the other's; the last
+// work-groups have 64 classes each.
 struct HeadPairArgs {
   HeadArgs dx, dw;
   uint32_t dx_blocks, dw_blocks;
+  bool dw_first;
   const float* bias_sums;  // [bias_rows][pitch]
   int64_t pitch;
   int32_t bias_rows;
@@ -926,16 +928,17 @@ __global__ __launch_bounds__(64 * kWM * kWN * kGroups, 2) void head_pair_kernel(
   using Dx = HeadTile<T, kHeadRounded, false, true, kBM, kBN, kWM, kWN, kStages, kGroups>;
   using Dw = HeadTile<T, kHeadRounded, true, true, kBM, kBN, kWM, kWN, kStages, kGroups>;
   __shared__ __align__(1024) int8_t s_stages[Dx::kLds > Dw::kLds ? Dx::kLds : Dw::kLds];
-  if (blockIdx.x < p.dx_blocks) {
-    Dx::run(p.dx, blockIdx.x, 0, s_stages);
-  } else if (blockIdx.x < p.dx_blocks + p.dw_blocks) {
-    Dw::run(p.dw, blockIdx.x - p.dx_blocks, 0, s_stages);
+  const uint32_t tiles = p.dx_blocks + p.dw_blocks, first = p.dw_first ? p.dw_blocks : p.dx_blocks;
+  if (blockIdx.x < tiles && (blockIdx.x < first) != p.dw_first) {
+    Dx::run(p.dx, blockIdx.x - (p.dw_first ? first : 0u), 0, s_stages);
+  } else if (blockIdx.x < tiles) {
+    Dw::run(p.dw, blockIdx.x - (p.dw_first ? 0u : first), 0, s_stages);
   } else {
     // 64 classes: a wavefront takes every kWaves-th row of partial sums
     constexpr int kWaves = kWM * kWN * kGroups;
     float* s_sum = reinterpret_cast<float*>(s_stages);
     const int lane = (int)(threadIdx.x & 63u), wave = (int)(threadIdx.x >> 6);
-    const int64_t n = (int64_t)(blockIdx.x - p.dx_blocks - p.dw_blocks) * 64 + lane;
+    const int64_t n = (int64_t)(blockIdx.x - tiles) * 64 + lane;
     float sum = 0.0f;
     if (n < p.dw.M)
       for (int32_t r = wave; r < p.bias_rows; r += kWaves) sum += p.bias_sums[r * p.pitch + n];

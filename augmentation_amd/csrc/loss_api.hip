@@ -61,18 +61,21 @@ int64_t tiles_of(int tile, int64_t M, int64_t N) {
 // elements of the contraction, where each unit has one tile or where it has more,
 // two or more of them at once; of 256x256, 128x128 and 64x64 tiles.  What memory
 // gives bounds it from below.
-enum ProductKind { kLogits = 0, kGradients = 1 };
+// kStoredLogits: logits whose gradients are stored, in three parts where operands
+// have them, which 256x256 tiles cannot do beside their products (1024x65536x384 fp32
+// with 256x256 / 128x128 tiles 1421 / 1266 us in all).
+enum ProductKind { kLogits = 0, kGradients = 1, kStoredLogits = 2 };
 
 double tiles_time(int tile, ProductKind kind, const Elements& t, int64_t tiles, int64_t M,
                   int64_t N, int64_t K) {
   constexpr double kFixed[2][2][3] = {{{9.0, 4.0, 2.0}, {9.0, 2.6, 1.5}},
                                       {{8.0, 2.7, 1.2}, {8.3, 2.4, 1.3}}};
-  constexpr double kFixedParts[2][2][3] = {{{20.0, 6.0, 4.0}, {20.0, 5.0, 2.5}},
+  constexpr double kFixedParts[2][2][3] = {{{9.0, 6.0, 4.0}, {9.0, 5.0, 2.5}},
                                            {{14.0, 7.0, 3.5}, {14.0, 5.0, 2.7}}};
   constexpr double kEach[3][2][2][3] = {
       {{{16.6, 8.2, 3.4}, {16.2, 5.0, 2.43}}, {{18.0, 10.0, 5.0}, {18.0, 5.5, 3.1}}},
       {{{223.0, 62.0, 18.3}, {223.0, 57.5, 15.9}}, {{230.0, 66.0, 23.5}, {230.0, 59.0, 18.0}}},
-      {{{118.0, 47.0, 23.0}, {122.0, 52.0, 15.8}}, {{137.0, 77.0, 41.0}, {137.0, 50.0, 27.0}}}};
+      {{{118.0, 60.0, 23.0}, {122.0, 52.0, 15.8}}, {{137.0, 77.0, 41.0}, {137.0, 50.0, 27.0}}}};
   const int type = t.passes > 1 ? 2 : t.size == 4 ? 1 : 0;
   const double memory = (double)(M + N) * K * t.size * t.parts / 5.4e6;
   const double rounds = (double)tiles / kUnits;
@@ -87,7 +90,10 @@ double tiles_time(int tile, ProductKind kind, const Elements& t, int64_t tiles, 
     return std::max(std::ceil(rounds) * ((groups ? 3.5 : 1.5) + each), memory);
   }
   const int more = tiles > kUnits;
-  const double fixed = type == 2 ? kFixedParts[kind][more][tile] : kFixed[kind][more][tile];
+  const bool stored = kind == kStoredLogits;
+  if (stored) kind = kLogits;
+  double fixed = type == 2 ? kFixedParts[kind][more][tile] : kFixed[kind][more][tile];
+  if (stored && type == 2 && tile == 0) fixed += 56.0;
   return std::max(std::ceil(rounds) * (fixed + kEach[type][kind][more][tile] * 1e-3 * K), memory);
 }
 
@@ -170,12 +176,15 @@ int64_t piece_of(int64_t rows, int64_t most) {
 }
 
 // fp32 operands in parts, if six products of bf16 and the copies (ten bytes an
-// element) take less time than one of fp32 (1999x21841x1021: 490 us against 730).
+// element) take less time than one of fp32 (1999x21841x1021: 465 us against 730;
+// 1024x65536x64 78 / 92).  The parts of the gradients of the logits do not stay in
+// the memory-side cache (gradients of 1024x65536x384 1280 / 1226, x1024 2420 / 2977).
 bool worth_parts(int64_t rows, int64_t classes, int32_t width, bool backward) {
   double cost[2] = {0.0, 6.0 + (double)(rows + classes) * width * 10.0 / 4e6};
+  if (backward) cost[1] += (double)rows * classes * 3.5e-6;
   for (int split = 0; split < 2; ++split) {
     const Elements t = elements_of(4, split);
-    cost[split] += choose(kLogits, rows, classes, width, t, 1).cost;
+    cost[split] += choose(backward ? kStoredLogits : kLogits, rows, classes, width, t, 1).cost;
     if (backward)
       cost[split] += choose(kGradients, rows, width, classes, t, kMostSplits).cost +
                      choose(kGradients, classes, width, rows, t, kMostSplits, false).cost;
@@ -217,7 +226,8 @@ Plan plan_of(int64_t rows, int64_t classes, int32_t width, int64_t e, bool pack_
   p.scale = parts.take(8);
   if (p.pack_x) p.x = parts.take(rows * p.width_packed * bytes);
   if (p.pack_w) p.w = parts.take(p.piece * p.width_packed * bytes);
-  for (int k = 0; k < 2; ++k) p.logits[k] = choose(kLogits, rows, counts[k], K, t, 1);
+  const ProductKind kind = backward ? kStoredLogits : kLogits;
+  for (int k = 0; k < 2; ++k) p.logits[k] = choose(kind, rows, counts[k], K, t, 1);
   if (!backward) {
     p.stat_tiles = (p.pieces - 1) * class_tiles(p.logits[0], p.piece) +
                    class_tiles(p.logits[p.which(counts[1])], counts[1]);

@@ -20,7 +20,7 @@
 // PFLOP/s (a library product of that shape alone, its logits written, 2.61 ms);
 // gradients of 4096x50000x4096 4.0 ms, 1.26 PFLOP/s.  Few rows are bound by the
 // bytes of the weights: 1x50000x4096 bf16 74 us, 5.6 TB/s.  Small calls by their
-// launches: gradients of 1024x1000x768 fp16 19.8 us in two.
+// launches: gradients of 1024x1000x768 fp16 19.3 us in two.
 //
 // One kernel serves the three products.  They differ in how their operands lie:
 // "along" the contraction (x and w in the logits, g in dx: a row of memory is

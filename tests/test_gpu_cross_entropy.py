@@ -144,6 +144,13 @@ def test_classes_in_pieces(fn, rows, classes, width, t):
     check_backward(fn, x, w, y, b, 0.1, torch.full((rows,), 1 / rows, device="cuda"), lse)
 
 
+def test_large_fp32_products_in_pieces(fn):
+    """Operands in three parts, whose pieces are added up."""
+    x, w, y, b = head(5, 5000, 10001, 1021, torch.float32)
+    _, lse = check_forward(fn, x, w, y, b, 0.1)
+    check_backward(fn, x, w, y, b, 0.1, torch.full((5000,), 1 / 5000, device="cuda"), lse)
+
+
 def test_a_constant_loss_gradient_may_be_expanded(fn):
     x, w, y, b = head(1, 300, 500, 128, torch.bfloat16)
     losses, lse = fn.linear_cross_entropy(x, w, y, bias=b)

@@ -478,8 +478,8 @@ int backward(const Call& c, const Plan& p, const Gradients& g) {
     // few dlosses: each work-group of the first kernel looks for the largest one,
     // for less than a launch takes
     if (c.rows == 0 || (c.rows > kFewRows && g.dloss_stride != 0)) {
-      fn::loss_scale_kernel<<<1, 1024, 0, c.st>>>(g.dlosses, g.dloss_stride, c.rows, scale_to,
-                                                  scale);
+      fn::loss_scale_kernel<<<1, 1024, 0, c.st>>>(g.dlosses, g.dloss_stride, c.targets, c.classes,
+                                                  c.rows, scale_to, scale);
       FN_TRY(launch_status("loss_scale_kernel launch"));
       scale_to = 0.0f;
     }

@@ -427,31 +427,37 @@ __device__ __forceinline__ LossOf loss_of(float top, float sum, float all, bool 
   return l;
 }
 
-// What brings the largest finite |dloss| to `to`, and back.  Rounded to 16 bits
-// as they are, the gradients of a mean loss would all be off by the rounding of
-// 1 / rows, the same way (4096 rows of bf16: 3.0e-3 of dx against 1.7e-3, dx's
-// own rounding); and fp16 holds those of classes of small probability only if
-// they are large.
+// What brings the largest finite |dloss| of the rows that count to `to`, and back.
+// Rounded to 16 bits as they are, the gradients of a mean loss would all be off by
+// the rounding of 1 / rows, the same way (4096 rows of bf16: 3.0e-3 of dx against
+// 1.7e-3, dx's own rounding); and fp16 holds those of classes of small probability
+// only if they are large.  An ignored row's gradients are zeros, and its dloss may
+// be anything: it has no say.
 struct Scale {
   float up, down;
 };
 
-// By all threads of the work-group; s_top: a word for each wavefront.
+// By all threads of the work-group; s_top: a word for each wavefront.  Of a dloss
+// for all rows (stride 0) no target is looked at.
 template <int kThreads>
-__device__ __forceinline__ Scale find_scale(const float* dlosses, int64_t stride, int64_t rows,
+__device__ __forceinline__ Scale find_scale(const float* dlosses, int64_t stride,
+                                            const int64_t* targets, int64_t classes, int64_t rows,
                                             float to, uint32_t* s_top) {
   uint32_t top = 0;
   if (stride == 0) rows = min(rows, (int64_t)1);
   // four loads at a time on their way
   for (int64_t i = threadIdx.x; i < rows; i += 4 * kThreads) {
     uint32_t v[4];
+    int64_t y[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int64_t at = min(i + j * kThreads, rows - 1);
       v[j] = __builtin_bit_cast(uint32_t, dlosses[at * stride]) & 0x7FFFFFFFu;
+      y[j] = stride != 0 ? targets[at] : 0;
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) top = max(top, v[j] < 0x7F800000u ? v[j] : 0u);
+    for (int j = 0; j < 4; ++j)
+      top = max(top, v[j] < 0x7F800000u && (uint64_t)y[j] < (uint64_t)classes ? v[j] : 0u);
   }
   top = group_max<64>(top);
   if ((threadIdx.x & 63u) == 0) s_top[threadIdx.x >> 6] = top;
@@ -597,7 +603,7 @@ struct HeadTile {
       if (p.dloss_stride == 0) same_dloss = p.dlosses[0];
       if (p.scale_to > 0.0f) {
         scale = find_scale<kThreads>(
-            p.dlosses, p.dloss_stride, p.M, p.scale_to,
+            p.dlosses, p.dloss_stride, p.targets, p.classes, p.M, p.scale_to,
             reinterpret_cast<uint32_t*>(s_stages + kMainBytes) + kBN + 4 * kSideM);
         if (block == 0 && threadIdx.x == 0) {
           p.scale[0] = scale.up;

@@ -68,9 +68,10 @@ __global__ __launch_bounds__(256) void loss_join_kernel(JoinArgs p) {
 
 // find_scale's numbers for many rows, which not every work-group shall read.
 __global__ __launch_bounds__(1024) void loss_scale_kernel(const float* dlosses, int64_t stride,
+                                                          const int64_t* targets, int64_t classes,
                                                           int64_t rows, float to, float* scale) {
   __shared__ uint32_t s_top[16];
-  const Scale s = find_scale<1024>(dlosses, stride, rows, to, s_top);
+  const Scale s = find_scale<1024>(dlosses, stride, targets, classes, rows, to, s_top);
   if (threadIdx.x != 0) return;
   scale[0] = s.up;
   scale[1] = s.down;

@@ -447,9 +447,10 @@ int fn_linear_cross_entropy(const void* x_dev, int64_t x_stride, const void* wei
  * again, a piece of the classes at a time, and g is rounded to dtype before its
  * products, as the matrix instructions take it (dbias comes before that); the
  * sums are fp32, in an order that the sizes alone fix (no atomics).  In 16-bit
- * types g is scaled so that the largest finite |dloss| is 1 (bf16) or 2^14
- * (fp16, where probabilities down to 2^-28 then keep all their digits in rows of
- * that dloss), and its products back.  rows = 0 writes zeros.
+ * types g is scaled so that the largest finite |dloss| of a row that counts is 1
+ * (bf16) or 2^14 (fp16, where probabilities down to 2^-28 then keep all their
+ * digits in rows of that dloss), and its products back; an ignored row's dloss may
+ * be anything.  rows = 0 writes zeros.
  */
 int fn_linear_cross_entropy_backward(
     const float* dlosses_dev, int64_t dlosses_stride, const void* x_dev, int64_t x_stride,

@@ -412,7 +412,9 @@ __device__ __forceinline__ TileAt head_tile_at(uint32_t block, const HeadArgs& p
 constexpr float kMinusInfinity = -__builtin_inff();
 
 // A row's lse and loss from the maximum of its logits, the sum of exponentials
-// above it, the sum of the logits and the target's.
+// above it, the sum of the logits and the target's.  The loss is made of differences
+// from the maximum, not of lse, whose rounding is that of a number of the logits'
+// size (logits near 20: steps of 2e-6, where a loss may be 1e-5).
 struct LossOf {
   float lse, loss;
 };
@@ -422,8 +424,12 @@ __device__ __forceinline__ LossOf loss_of(float top, float sum, float all, bool 
                                           int64_t classes) {
   LossOf l;
   l.lse = top + logf(sum);
-  l.loss = counts ? l.lse - (1.0f - smoothing) * target : 0.0f;
-  if (counts && smoothing > 0.0f) l.loss -= smoothing * (all / (float)classes);
+  l.loss = 0.0f;
+  if (counts) {
+    float below = (1.0f - smoothing) * (top - target);
+    if (smoothing > 0.0f) below += smoothing * (top - all / (float)classes);
+    l.loss = below + logf(sum);
+  }
   return l;
 }
 

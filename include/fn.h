@@ -426,8 +426,9 @@ int fn_layer_norm_backward_workspace(int64_t rows, int32_t width, int64_t* bytes
 
 /*
  * fn_linear_cross_entropy -- the losses and lse (which the backward pass takes),
- * `rows` fp32 numbers each.  Sums are fp32, in an order that the sizes alone
- * fix.  workspace_dev: at least fn_linear_cross_entropy_workspace(...) bytes,
+ * `rows` fp32 numbers each.  A loss is computed from differences from the largest
+ * logit, not from lse, and keeps digits that a number of the logits' size has not.
+ * Sums are fp32, in an order that the sizes alone fix.  workspace_dev: at least fn_linear_cross_entropy_workspace(...) bytes,
  * 16-byte aligned, that no other call in flight uses.
  */
 int fn_linear_cross_entropy(const void* x_dev, int64_t x_stride, const void* weight_dev,

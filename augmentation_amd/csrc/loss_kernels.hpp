@@ -426,7 +426,8 @@ __device__ __forceinline__ LossOf loss_of(float top, float sum, float all, bool 
   l.lse = top + logf(sum);
   l.loss = 0.0f;
   if (counts) {
-    float below = (1.0f - smoothing) * (top - target);
+    // (where the target has no part, it may be infinitely low)
+    float below = smoothing < 1.0f ? (1.0f - smoothing) * (top - target) : 0.0f;
     if (smoothing > 0.0f) below += smoothing * (top - all / (float)classes);
     l.loss = below + logf(sum);
   }

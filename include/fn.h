@@ -406,8 +406,9 @@ int fn_layer_norm_backward_workspace(int64_t rows, int32_t width, int64_t* bytes
 /* say) is ignored: its loss and its gradients are zero, whatever its logits   */
 /* (but its features still meet dweight's zeros, so they have to be finite).   */
 /* smoothing lies in [0, 1].  A class of bias -infinity is left out:           */
-/* probability 0, and a loss of +infinity for rows that want it.  A row with a */
-/* NaN or +infinity among its logits, or all classes left out, has a NaN loss. */
+/* probability 0, and a loss of +infinity for rows that want it (with smoothing */
+/* every row does).  A row with a NaN or +infinity among its logits, or all     */
+/* classes left out, has a NaN loss.                                           */
 /*                                                                            */
 /* In large fp32 products an operand is taken as three bf16 numbers, which     */
 /* hold all of its digits if it is 2^-100 or more; one that is infinite, or    */

@@ -66,3 +66,26 @@ def test_a_smoothed_loss_too(fn, rows, classes):
         tol = (1.5 * classes + EXP) * U + 2 * U * total.log() + 4 * U * (spread.double().abs() + spread.double().abs().mean() + ref.abs())
         tol = tol + 0.25 * (classes + 2) * U * zd.abs().mean()
         assert ((losses.double() - ref[y]).abs() <= tol[y]).all(), shift
+
+
+@pytest.mark.parametrize("t", TYPES, ids=str)
+@pytest.mark.parametrize("rows,classes", [(5, 5), (40, 60), (300, 2000)])
+def test_a_class_left_out_of_a_loss_that_is_all_smoothing(fn, rows, classes, t):
+    """With smoothing 1 the target's own logit has no part in the loss: whether the
+    target is left out or another class, every row's loss is infinite, not NaN, and
+    the gradients are p - 1 / V."""
+    x, w = zero_head(rows, classes, t)
+    b = torch.zeros(classes, device="cuda")
+    y = torch.arange(rows, device="cuda") % classes
+    losses, lse = fn.linear_cross_entropy(x, w, y, bias=b, smoothing=1.0)
+    want = torch.log(torch.tensor(float(classes), dtype=torch.float64)).item()
+    assert ((losses.double() - want).abs() <= (1.5 * classes + EXP) * U + 4 * U * want).all()
+    b[0] = -float("inf")
+    y[-1] = -1  # ignored
+    losses, lse = fn.linear_cross_entropy(x, w, y, bias=b, smoothing=1.0)
+    assert (losses[:-1] == float("inf")).all() and losses[-1] == 0
+    _, _, db = fn.linear_cross_entropy_backward(torch.ones(rows, device="cuda"), x, w, y, lse, bias=b, smoothing=1.0)
+    p = torch.full((classes,), 1 / (classes - 1), dtype=torch.float64, device="cuda")
+    p[0] = 0
+    tol = (rows - 1) * U * ((1.5 * classes + EXP + 4 * want) * p + (rows + 8) / classes)
+    assert ((db.double() - (rows - 1) * (p - 1 / classes)).abs() <= tol).all()

@@ -18,12 +18,60 @@ using namespace fnhost;
 
 // ------------------------------------------------------------- row kernels
 
+// Whether many wide fp32 rows are read past the caches: 2^23 elements and more (few
+// rows stay in the memory-side cache: gradients of 500x8192 16.8 us past it, 15.7),
+// by the threads of a row and how many of them are at work.  In us, past the caches /
+// through them:
+//   gradients  512x2 (rows to 8,192) 8192x8192 150 / 175, 9000x6720 142 / 159,
+//              8192x8185 162 / 173; 256x3 (to 6,144) 12000x5120 140 / 147,
+//              11000x6001 160 / 166, but 16384x4100 173 / 165; 256x2 and 512x4 (to
+//              4,096 and 16,384) on whole cache lines 16384x4096 with dsum 202 / 214,
+//              4096x16384 165 / 183, but 16384x4095 166 / 155, 4096x13440 142 / 138;
+//   codes      256x2 to 512x2 on whole lines 16384x4096 56 / 59, 8192x8192 55.6 / 59.2,
+//              but 16384x4100 63.5 / 57.5, 4096x14336 55 / 53;
+//   norms with a residual  512x4 4096x16384 205 / 247, 4096x15001 196 / 205, but
+//              6000x12288 228 / 215; 1024x4 2000x32768 227 / 246.
+// All others are faster through the caches, norms by up to a third.
+bool many_rows(int64_t rows, int32_t width) { return rows >= ((int64_t)1 << 23) / width; }
+
+// Whether a matrix's rows are whole cache lines (or there is none).
+bool on_lines(const void* p, int64_t stride, int64_t e) {
+  return p == nullptr || ((uintptr_t)p | (uint64_t)(stride * e)) % 128 == 0;
+}
+
+template <int kMode, int kThreads, int kChunks>
+bool once_rows(const fn::RowArgs& a) {
+  if (!many_rows(a.rows, a.width)) return false;
+  if constexpr (kMode == fn::kRowQuantize) return on_lines(a.x, a.x_stride, 4);
+  return a.residual != nullptr && a.width >= (kThreads == 1024 ? 0 : 7 * kThreads * kChunks);
+}
+
+template <int kThreads, int kChunks>
+bool once_backward(const fn::BackwardArgs& a) {
+  if (!many_rows(a.rows, a.width)) return false;
+  if (kThreads == 512 && kChunks == 2) return true;
+  if (kThreads == 256 && kChunks == 3) return a.width >= 5 * 8 * 256 * 3 / 6;
+  return a.width >= 7 * kThreads * kChunks && on_lines(a.dout, a.dout_stride, 4) &&
+         on_lines(a.h, a.h_stride, 4) && on_lines(a.dsum, a.dsum_stride, 4);
+}
+
 template <typename T, int kMode, int kThreads, int kChunks, bool kShort = false>
 void launch_rows_k(const fn::RowArgs& a, hipStream_t st) {
   constexpr int kBlock = fn::rows_block<kThreads>(), kRows = kBlock / kThreads;
   const int64_t groups = (a.rows + kRows - 1) / kRows;
-  fn::rows_kernel<T, kMode, kThreads, kChunks, kShort>
-      <<<(unsigned)std::min<int64_t>(groups, 1 << 20), kBlock, 0, st>>>(a);
+  const unsigned grid = (unsigned)std::min<int64_t>(groups, 1 << 20);
+  // codes 256x2 to 512x2, norms 512x4 and 1024x4
+  constexpr bool kMayBeOnce =
+      sizeof(T) == 4 &&
+      ((kMode == fn::kRowQuantize && kThreads >= 256 && kThreads * kChunks <= 1024) ||
+       (kMode == fn::kRowNorm && kThreads * kChunks >= 2048));
+  if constexpr (kMayBeOnce) {
+    if (once_rows<kMode, kThreads, kChunks>(a)) {
+      fn::rows_kernel<T, kMode, kThreads, kChunks, kShort, true><<<grid, kBlock, 0, st>>>(a);
+      return;
+    }
+  }
+  fn::rows_kernel<T, kMode, kThreads, kChunks, kShort><<<grid, kBlock, 0, st>>>(a);
 }
 
 template <typename T, int kMode>
@@ -164,8 +212,15 @@ BackwardPlan plan_backward(int64_t rows, int32_t width) {
 
 template <typename T, int kThreads, int kChunks, bool kShort = false>
 void launch_backward_k(const fn::BackwardArgs& a, hipStream_t st) {
-  fn::rows_backward_kernel<T, kThreads, kChunks, kShort>
-      <<<(unsigned)a.partials, fn::rows_block<kThreads>(), 0, st>>>(a);
+  constexpr int kBlock = fn::rows_block<kThreads>();
+  const unsigned grid = (unsigned)a.partials;
+  if constexpr (sizeof(T) == 4 && kThreads >= 256) {
+    if (once_backward<kThreads, kChunks>(a)) {
+      fn::rows_backward_kernel<T, kThreads, kChunks, kShort, true><<<grid, kBlock, 0, st>>>(a);
+      return;
+    }
+  }
+  fn::rows_backward_kernel<T, kThreads, kChunks, kShort><<<grid, kBlock, 0, st>>>(a);
 }
 
 template <typename T>

@@ -71,10 +71,12 @@ __device__ __forceinline__ uint32_t quotient(uint32_t n, const Division& d) {
 // Eight consecutive elements, at any alignment of the element's size: the
 // hardware's global loads and stores take unaligned addresses.  Rows are met
 // once, so both are non-temporal (16384x8192 bf16: norm 182 -> 173 us, to
-// codes 159 -> 149 us, backward 191 -> 179 us).  Not the loads of fp32: a lane's
+// codes 159 -> 149 us, backward 191 -> 179 us).  Not all loads of fp32: a lane's
 // eight numbers are two loads, whose lines the second one finds in the cache only
 // if they may stay there (layer norm of 3001x2243 21.3 -> 12.5 us, 12000x1000 with a
-// residual 49 -> 36).
+// residual 49 -> 36); but many wide rows are faster past the caches (load_once: the
+// rows, not the weight, which every work-group reads; see once_rows and
+// once_backward).
 
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
@@ -101,6 +103,10 @@ struct Vec8<float> {
   __device__ __forceinline__ void load(const float* p) {
     a = *reinterpret_cast<const u32x4_any*>(p);
     b = *reinterpret_cast<const u32x4_any*>(p + 4);
+  }
+  __device__ __forceinline__ void load_once(const float* p) {
+    a = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
+    b = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p + 4));
   }
   __device__ __forceinline__ void load_some(const float* p, int n) {
 #pragma unroll
@@ -234,11 +240,14 @@ __device__ __forceinline__ Chunk chunk_at(int32_t c, int32_t width, int32_t shif
   return {at, min(first - at, 8), first < 0 ? 7 : width - first};
 }
 
-// kShort: rows of fewer than eight elements (chunk 0 is all there is)
-template <bool kShort, typename T>
+// kShort: rows of fewer than eight elements (chunk 0 is all there is); kOnce: fp32
+// that shall not stay in the caches
+template <bool kShort, bool kOnce = false, typename T>
 __device__ __forceinline__ void load_chunk(Vec8<T>& v, const T* row, const Chunk& c) {
   if constexpr (kShort)
     v.load_some(row, c.left);
+  else if constexpr (kOnce)
+    v.load_once(row + c.at);
   else
     v.load(row + c.at);
 }
@@ -413,7 +422,7 @@ constexpr int rows_block() {
   return kThreads <= 64 ? 256 : kThreads;
 }
 
-template <typename T, int kMode, int kThreads, int kChunks, bool kShort = false>
+template <typename T, int kMode, int kThreads, int kChunks, bool kShort = false, bool kOnce = false>
 __global__ __launch_bounds__(rows_block<kThreads>()) void rows_kernel(RowArgs a) {
   constexpr int kRows = rows_block<kThreads>() / kThreads;
   const int lane = (int)threadIdx.x % kThreads;
@@ -443,12 +452,12 @@ __global__ __launch_bounds__(rows_block<kThreads>()) void rows_kernel(RowArgs a)
     const T* x = (const T*)a.x + row * a.x_stride;
     Vec8<T> h[kChunks];
 #pragma unroll
-    for (int k = 0; k < kChunks; ++k) load_chunk<kShort>(h[k], x, c[k]);
+    for (int k = 0; k < kChunks; ++k) load_chunk<kShort, kOnce>(h[k], x, c[k]);
     if (add) {
       const T* r = (const T*)a.residual + row * a.residual_stride;
       Vec8<T> v[kChunks];
 #pragma unroll
-      for (int k = 0; k < kChunks; ++k) load_chunk<kShort>(v[k], r, c[k]);
+      for (int k = 0; k < kChunks; ++k) load_chunk<kShort, kOnce>(v[k], r, c[k]);
 #pragma unroll
       for (int k = 0; k < kChunks; ++k) {
         float t[8];
@@ -626,7 +635,7 @@ __device__ __forceinline__ void backward_chunk(const Vec8<T>& d, const Vec8<T>& 
 // Layout of threads and rows as in rows_kernel.  A work-group takes every
 // gridDim.x-th group of rows and keeps its columns' sums of dout n in
 // registers until the end: one row of partial sums per work-group.
-template <typename T, int kThreads, int kChunks, bool kShort = false>
+template <typename T, int kThreads, int kChunks, bool kShort = false, bool kOnce = false>
 __global__ __launch_bounds__(rows_block<kThreads>()) void rows_backward_kernel(BackwardArgs a) {
   constexpr int kRows = rows_block<kThreads>() / kThreads;
   const int lane = (int)threadIdx.x % kThreads;
@@ -667,13 +676,13 @@ __global__ __launch_bounds__(rows_block<kThreads>()) void rows_backward_kernel(B
     r.rstd = a.rstd[row];
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
-      load_chunk<kShort>(r.d[k], pd, c[k]);
-      load_chunk<kShort>(r.h[k], ph, c[k]);
+      load_chunk<kShort, kOnce>(r.d[k], pd, c[k]);
+      load_chunk<kShort, kOnce>(r.h[k], ph, c[k]);
     }
     if (add) {
       const T* ps = (const T*)a.dsum + row * a.dsum_stride;
 #pragma unroll
-      for (int k = 0; k < kChunks; ++k) load_chunk<kShort>(r.s[k], ps, c[k]);
+      for (int k = 0; k < kChunks; ++k) load_chunk<kShort, kOnce>(r.s[k], ps, c[k]);
     } else {
 #pragma unroll
       for (int k = 0; k < kChunks; ++k) r.s[k].zero();

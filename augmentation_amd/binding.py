@@ -828,6 +828,7 @@ def linear_cross_entropy_backward(dlosses, x, weight, targets, lse, bias=None, s
     dlosses of linear_cross_entropy's losses (fp32 of their shape, one number
     expanded included) and the lse that it returned.  dx and dweight are of the
     operands' dtype (None if not wanted), dbias is fp32 (None without a bias).
+    The last bits of each may depend on whether dx and dweight are both wanted.
     Without a workspace one is allocated for the call."""
     _refuse_gradients(dlosses, x, weight, lse, bias, dx, dweight, dbias)
     (shape, rows, classes, width, code, dev, x_at, x_stride, x_place, w_at, w_stride,

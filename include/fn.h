@@ -414,10 +414,12 @@ int fn_layer_norm_backward_workspace(int64_t rows, int32_t width, int64_t* bytes
 /* hold all of its digits if it is 2^-100 or more; one that is infinite, or    */
 /* that bf16 rounds to infinity, gives NaN logits.                             */
 /*                                                                            */
-/* Speed only: operands are read in place if in_place(x), which is that the    */
-/* base, the stride and the width are multiples of 16 bytes and the stride is  */
-/* at least the width and below 2^23 bytes; others are copied to the          */
-/* workspace first.                                                           */
+/* Operands are read in place if in_place(x), which is that the base, the      */
+/* stride and the width are multiples of 16 bytes and the stride is at least   */
+/* the width and below 2^23 bytes; others are copied to the workspace first.   */
+/* For x this is a matter of speed only.  A weight that is copied may be taken */
+/* in other pieces than one in place, and the sums in another order: the       */
+/* results then differ by the rounding of the sums.                            */
 /*                                                                            */
 /* Errors: FN_EINVAL as for the other matrices, for classes or width < 1,      */
 /* smoothing outside [0, 1] or a workspace that is too short; FN_EOVERFLOW     */
@@ -429,8 +431,9 @@ int fn_layer_norm_backward_workspace(int64_t rows, int32_t width, int64_t* bytes
  * fn_linear_cross_entropy -- the losses and lse (which the backward pass takes),
  * `rows` fp32 numbers each.  A loss is computed from differences from the largest
  * logit, not from lse, and keeps digits that a number of the logits' size has not.
- * Sums are fp32, in an order that the sizes alone fix.  workspace_dev: at least fn_linear_cross_entropy_workspace(...) bytes,
- * 16-byte aligned, that no other call in flight uses.
+ * Sums are fp32, in an order that the sizes, the type and whether weight is read
+ * in place fix.  workspace_dev: at least fn_linear_cross_entropy_workspace(...)
+ * bytes, 16-byte aligned, that no other call in flight uses.
  */
 int fn_linear_cross_entropy(const void* x_dev, int64_t x_stride, const void* weight_dev,
                             int64_t weight_stride, const float* bias_dev,
@@ -448,7 +451,8 @@ int fn_linear_cross_entropy(const void* x_dev, int64_t x_stride, const void* wei
  * in fp32.  All are overwritten; each may be NULL.  The logits are computed
  * again, a piece of the classes at a time, and g is rounded to dtype before its
  * products, as the matrix instructions take it (dbias comes before that); the
- * sums are fp32, in an order that the sizes alone fix (no atomics).  In 16-bit
+ * sums are fp32, in an order that the sizes, the type, whether weight is read in
+ * place and whether both dx and dweight are wanted fix (no atomics).  In 16-bit
  * types g is scaled so that the largest finite |dloss| of a row that counts is 1
  * (bf16) or 2^14 (fp16, where probabilities down to 2^-28 then keep all their
  * digits in rows of that dloss), and its products back; an ignored row's dloss may

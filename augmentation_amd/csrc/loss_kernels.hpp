@@ -20,7 +20,7 @@
 // PFLOP/s (a library product of that shape alone, its logits written, 2.61 ms);
 // gradients of 4096x50000x4096 4.0 ms, 1.26 PFLOP/s.  Few rows are bound by the
 // bytes of the weights: 1x50000x4096 bf16 74 us, 5.6 TB/s.  Small calls by their
-// launches: gradients of 1024x1000x768 fp16 19.3 us in two.
+// launches: gradients of 1024x1000x768 fp16 19.5 us in two.
 //
 // One kernel serves the three products.  They differ in how their operands lie:
 // "along" the contraction (x and w in the logits, g in dx: a row of memory is
@@ -53,8 +53,10 @@ __device__ __forceinline__ float exp_below(float v) {
   return v < -200.0f ? 0.0f : __builtin_fmaf(e, r * kLn2, e);
 }
 
-// The same without the correction: off by 2^-24 |v| log2(e) relative.  For sums, in
-// which large |v| count little, and for what is rounded to 16 bits.
+// The same without the correction, two instructions for six: off by 2^-24 |v| log2(e)
+// relative, about as much as a logit of size |v| is by one of its roundings.  For sums,
+// those of fp32 too, in which a term is off by 2^-24 log2(e) |v| exp(v) then, no more
+// than 0.54 2^-24 of the largest term, and for what is rounded to 16 bits.
 __device__ __forceinline__ float exp_roughly(float v) {
   return __builtin_amdgcn_exp2f(v * 0x1.715476p+0f);
 }
@@ -731,7 +733,8 @@ struct HeadTile {
     } else {
       // The logits.  What follows is 128 elements a lane in the largest tile, so it
       // counts by the instruction: bias, the edge of the classes and targets are
-      // looked at only where there are any (8192x50000x4096 bf16 2.55 -> 2.45 ms).
+      // looked at only where there are any (8192x50000x4096 bf16 2.55 -> 2.45 ms);
+      // but smoothing's sum of the logits selects by the edge in every tile.
       if (p.bias != nullptr && first_group) {
 #pragma unroll
         for (int j = 0; j < kTN; ++j)

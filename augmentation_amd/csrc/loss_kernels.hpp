@@ -144,7 +144,7 @@ struct HeadArgs {
   float smoothing;
   // kHeadStatistics: [M][stat_tiles] maxima and sums, from tile first_tile on
   f32x2* stats;
-  float* sums;     // [M][stat_tiles] sums of logits, or null
+  float* sums;     // [M][stat_tiles] sums of logits / classes, or null
   float* target_z; // [M]
   int64_t stat_tiles, first_tile;
   // one tile has all classes: the losses and lse themselves, and no statistics
@@ -414,23 +414,22 @@ __device__ __forceinline__ TileAt head_tile_at(uint32_t block, const HeadArgs& p
 constexpr float kMinusInfinity = -__builtin_inff();
 
 // A row's lse and loss from the maximum of its logits, the sum of exponentials
-// above it, the sum of the logits and the target's.  The loss is made of differences
+// above it, the mean of the logits and the target's.  The loss is made of differences
 // from the maximum, not of lse, whose rounding is that of a number of the logits'
 // size (logits near 20: steps of 2e-6, where a loss may be 1e-5).
 struct LossOf {
   float lse, loss;
 };
 
-__device__ __forceinline__ LossOf loss_of(float top, float sum, float all, bool counts,
-                                          float target, float smoothing,
-                                          int64_t classes) {
+__device__ __forceinline__ LossOf loss_of(float top, float sum, float mean, bool counts,
+                                          float target, float smoothing) {
   LossOf l;
   l.lse = top + logf(sum);
   l.loss = 0.0f;
   if (counts) {
     // (where the target has no part, it may be infinitely low)
     float below = smoothing < 1.0f ? (1.0f - smoothing) * (top - target) : 0.0f;
-    if (smoothing > 0.0f) below += smoothing * (top - all / (float)classes);
+    if (smoothing > 0.0f) below += smoothing * (top - mean);
     l.loss = below + logf(sum);
   }
   return l;
@@ -755,13 +754,17 @@ struct HeadTile {
         const int slot = (wave % kWN) * kBM + m_wave + (lane & 15);
         if (first_group) {
           if (p.smoothing > 0.0f) {
+            // the mean's share: a sum would overflow where classes are masked by the
+            // lowest number
+            const float share = 1.0f / (float)p.classes;
 #pragma unroll
             for (int i = 0; i < kTM; ++i) {
               float all = 0.0f;
 #pragma unroll
               for (int j = 0; j < kTN; ++j)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) all += 16 * j + c < columns ? acc[i][j][c] : 0.0f;
+                for (int c = 0; c < 4; ++c)
+                  all = __builtin_fmaf(16 * j + c < columns ? acc[i][j][c] : 0.0f, share, all);
               all = fold_row(all, [](float x, float y) { return x + y; });
               if ((lane >> 4) == 0) s_all[slot + 16 * i] = all;
             }
@@ -828,8 +831,8 @@ struct HeadTile {
           if (p.losses != nullptr) {
             const int64_t y = s_target[r];
             const bool counts = y >= 0 && y < p.classes;
-            const LossOf l = loss_of(top, sum, all, counts, counts ? s_z[r] : 0.0f, p.smoothing,
-                                     p.classes);
+            const LossOf l =
+                loss_of(top, sum, all, counts, counts ? s_z[r] : 0.0f, p.smoothing);
             p.losses_lse[m] = l.lse;
             p.losses[m] = l.loss;
             continue;

@@ -61,7 +61,7 @@ __global__ __launch_bounds__(256) void loss_join_kernel(JoinArgs p) {
   const int64_t y = p.targets[row];
   const bool counts = y >= 0 && y < p.classes;
   const LossOf l =
-      loss_of(top, sum, all, counts, counts ? p.target_z[row] : 0.0f, p.smoothing, p.classes);
+      loss_of(top, sum, all, counts, counts ? p.target_z[row] : 0.0f, p.smoothing);
   p.lse[row] = l.lse;
   p.losses[row] = l.loss;
 }

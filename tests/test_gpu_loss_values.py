@@ -89,3 +89,24 @@ def test_a_class_left_out_of_a_loss_that_is_all_smoothing(fn, rows, classes, t):
     p[0] = 0
     tol = (rows - 1) * U * ((1.5 * classes + EXP + 4 * want) * p + (rows + 8) / classes)
     assert ((db.double() - (rows - 1) * (p - 1 / classes)).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("rows,classes,out", [(5, 10, 3), (40, 60, 8), (3, 700, 100), (300, 2000, 1999)])
+def test_classes_masked_by_the_lowest_number(fn, rows, classes, out):
+    """Several logits of the lowest finite number: their mean is one, though their sum
+    is not.  The mean is off by (V + 4) u of the logits' mean size, a loss by that
+    share of it and its own few u."""
+    x, w = zero_head(rows, classes, torch.float32)
+    b = torch.linspace(-1, 1, classes, device="cuda")
+    b[:out] = torch.finfo(torch.float32).min
+    y = out + torch.arange(rows, device="cuda") % (classes - out)
+    for smoothing in (0.0, 0.125):
+        losses, lse = fn.linear_cross_entropy(x, w, y, bias=b, smoothing=smoothing)
+        bd = b.double()
+        ref = torch.logsumexp(bd, 0) - (1 - smoothing) * bd[y] - smoothing * bd.mean()
+        tol = (1.5 * classes + EXP + 16) * U + smoothing * (classes + 4) * U * bd.abs().mean() + 8 * U * ref.abs()
+        assert torch.isfinite(losses).all() and ((losses.double() - ref).abs() <= tol).all()
+        grads = fn.linear_cross_entropy_backward(torch.ones(rows, device="cuda"), x, w, y, lse, bias=b, smoothing=smoothing)
+        assert all(torch.isfinite(v).all() for v in grads)
+        want = rows * smoothing / classes
+        assert ((grads[2][:out].double() + want).abs() <= (rows + 8) * U * want).all()
